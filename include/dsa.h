@@ -29,7 +29,7 @@
  *     such a call are unspecified.
  *   - Limits of the indexer calls: H in {4, 8, 16, 32, 64}; D in {64, 128}; 1 <= topk <= 2048;
  *     0 <= T, N < 2^31.  Other values return DSA_ERR_UNSUPPORTED (not an undefined result).
- *     dsa_quantize_k and dsa_sparse_attn state their own limits.
+ *     dsa_quantize_k, dsa_sparse_attn and the calls on the 4-bit cache state their own limits.
  *
  * Output conventions (TileLang README, "Top-k Selector"; DeepSeek V4.1 model page,
  * sparse_attn_kernel, where an index of -1 marks "no key"):
@@ -284,6 +284,131 @@ DSA_API dsa_status dsa_sparse_attn_bwd(const uint16_t* q, const uint16_t* kv, co
                                        const int32_t* idx, const uint16_t* out, const float* lse,
                                        const uint16_t* dout, int T, int N, int H, int D, int K, float scale,
                                        float* dq, float* dkv, float* dsink, void* stream);
+
+/*
+ * ---- The 4-bit paged kv cache -------------------------------------------------------------
+ *
+ * dsa_quantize_kv4 writes kv rows (key = value, as dsa_sparse_attn takes them) in 4 bits into pages,
+ * dsa_sparse_attn_kv4 attends over them, dsa_dequantize_kv4 reads them back, and the page calls branch,
+ * grow, free, compact and copy.  (The pages this library follows have no counterpart of these.)
+ *
+ * A row x of D values is held as x[d] ~= r * s[d / 16] * c[d]:
+ *     c[d]  an e2m1 code (4 bits: sign, then 0, .5, 1, 1.5, 2, 3, 4, 6; even d in the low half of its byte)
+ *     s[g]  an e4m3 scale for each 16 values (no sign, no NaN)
+ *     r     an fp32 scale of the row, between 2^-100 and 2^117
+ * A page of page_rows rows is codes [page_rows][D / 2], then group scales [page_rows][D / 16], then row
+ * scales float [page_rows]: dsa_kv4_page_bytes(page_rows, D) bytes, a multiple of 16.
+ *
+ *   cache      uint8 [P][page bytes], 16-byte aligned
+ *   table      int32 [R][M]: the pages of R sequences, row pos of sequence r being row
+ *              pos % page_rows of page table[r][pos / page_rows].  Any value outside [0, P) is no page.
+ *   D in {64, 128, 256, 512}, page_rows a power of two in [16, 256], M * page_rows < 2^31
+ *              (DSA_ERR_UNSUPPORTED otherwise).
+ * One table serves the caches of all layers; a page may stand in several rows (shared).
+ */
+
+/* dsa_kv4_page_bytes -- bytes of a page (0 for an unsupported page_rows or D). */
+DSA_API size_t dsa_kv4_page_bytes(int page_rows, int D);
+
+/*
+ * dsa_quantize_kv4 -- writes row i of kv as row pos[i] of sequence seq[i].  A row whose place is not
+ * mapped (seq outside [0, R), pos outside [0, M * page_rows), no page) is left out.  Per row:
+ *     r   = the smallest power of two >= 2^-100 with max|x| <= 6 * 448 * r
+ *     s_g = max over the group of |x| / (6 r), to the nearest e4m3 value, ties to even
+ *     c_d = x_d / (r s_g) to the nearest e2m1 value, ties to even, beyond 6 to 6; 0 where s_g is 0
+ * each rounding that of the exact quotient (-0 codes keep the sign of x_d).
+ *
+ *   kv         bf16 (uint16 bits) [N][D], finite values; 16-byte aligned
+ *   seq, pos   int32 [N]; the same place at most once (else the rows may end up mixed)
+ */
+DSA_API dsa_status dsa_quantize_kv4(const uint16_t* kv, const int32_t* seq, const int32_t* pos, int N, int D,
+                                    uint8_t* cache, int P, int page_rows, const int32_t* table, int R, int M,
+                                    void* stream);
+
+/*
+ * dsa_dequantize_kv4 -- row pos[i] of sequence seq[i] as bf16: r s c, exact for rows that
+ * dsa_quantize_kv4 wrote (otherwise rounded to the nearest bf16; next to the largest bf16 a scale that was
+ * rounded up can take values past it, which come back as infinities).  A place that is not mapped gives zeros.
+ *   kv   bf16 (uint16 bits) [N][D]   OUTPUT, 16-byte aligned
+ */
+DSA_API dsa_status dsa_dequantize_kv4(const uint8_t* cache, int P, int page_rows, const int32_t* table, int R, int M,
+                                      const int32_t* seq, const int32_t* pos, int N, int D, uint16_t* kv,
+                                      void* stream);
+
+/*
+ * dsa_sparse_attn_kv4 -- dsa_sparse_attn over the 4-bit paged cache: for token t and head h, over the
+ * entries of idx[t, :], entry v naming row v - start[t] of sequence seq[t],
+ *     x_j = scale * sum_d q[t,h,d] kv[j,d],   out[t,h,:] = sum_j e^{x_j} kv[j,:] / ( sum_j e^{x_j} + e^{sink[h]} )
+ * An entry that is negative, lies before start[t] or behind the sequence's table row, or whose page is not
+ * mapped is skipped (its memory is not read); a token without entries gets zeros and an lse of its sink (-inf
+ * without one).  With dsa_index_topk, start[t] = ks[t] when the keys of seq[t] are packed from ks[t] on.
+ * Weights enter the weighted sum as fp16 (q too, exactly except for values 2^29 below the token's
+ * largest); products accumulate in fp32.
+ *
+ *   q          bf16 [T][H][D], 16-byte aligned
+ *   seq        int32 [T];  start  int32 [T] or NULL (0)
+ *   attn_sink  float [H] or NULL;  idx  int32 [T][K];  scale  softmax scale
+ *   out        bf16 [T][H][D]   OUTPUT
+ *   lse        float [T][H] or NULL   OUTPUT, as dsa_sparse_attn's
+ * H >= 1.  No workspace; deterministic.
+ */
+DSA_API dsa_status dsa_sparse_attn_kv4(const uint16_t* q, const uint8_t* cache, int P, int page_rows,
+                                       const int32_t* table, int R, int M, const int32_t* seq, const int32_t* start,
+                                       const float* attn_sink, const int32_t* idx, int T, int H, int D, int K,
+                                       float scale, uint16_t* out, float* lse, void* stream);
+
+/*
+ * The page calls share one state: a table [R][M] as above and ref int32 [P], the number of table entries
+ * that name each page.  A page whose count is not positive is free.  All results are whole numbers
+ * that do not depend on scheduling.
+ *
+ * dsa_fork_pages -- branching and freeing: table_out[r] = table[parent[r]], no pages (-1) where
+ * parent[r] is outside [0, R); ref follows the entries that change.  parent[r] = r keeps a sequence, -1 frees
+ * it, another row makes it share that row's pages (dsa_reserve_pages separates them when one is written).
+ * table_out must not overlap table (DSA_ERR_INVALID_ARG).
+ */
+DSA_API dsa_status dsa_fork_pages(const int32_t* table, const int32_t* parent, int R, int M, int P, int32_t* ref,
+                                  int32_t* table_out, void* stream);
+
+/*
+ * dsa_reserve_pages -- before rows [begin[r], end[r]) of each sequence r are written (begin >= end: none;
+ * clamped to [0, M * page_rows)): every page they cover becomes mapped and the sequence's own.  By the table and
+ * counts as they are at the call, a page that is missing, or whose count is above 1, is replaced by a free
+ * page (a missing one mapped to it): the k-th such place, in the order of (r, page), takes the k-th lowest free page.  The
+ * rows that a replaced page holds outside [begin, end) have to come along: dsa_copy_pages(cache, src, dst)
+ * with the lists below does that, for each cache that follows the table, before the pages are written.
+ *   src, dst   int32 [2 R]  OUTPUT: entries 2 r and 2 r + 1 are the first and the last page of r's span
+ *              where they are replaced and not wholly covered, else -1
+ *   lacking    int32 [1]    OUTPUT: 0, or by how many pages the free ones fall short; then nothing
+ *              else changes and the lists are all -1
+ *   workspace  dsa_reserve_pages_workspace_size(P) bytes, 4-byte aligned (DSA_ERR_WORKSPACE); its contents on
+ *              entry do not matter; two calls running at the same time must not share it
+ */
+DSA_API size_t dsa_reserve_pages_workspace_size(int P);
+DSA_API dsa_status dsa_reserve_pages(int32_t* table, int32_t* ref, const int32_t* begin, const int32_t* end, int R,
+                                     int M, int P, int page_rows, int32_t* src, int32_t* dst, int32_t* lacking,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dsa_compact_pages -- with L pages in use, renames pages so that these are [0, L): the k-th used page at or
+ * above L becomes the k-th free page below L.  table and ref follow (an entry that names no used page becomes
+ * -1, counts below 0 become 0); dsa_copy_pages(cache, src, dst) moves the rows of each cache.
+ *   src, dst   int32 [P / 2]  OUTPUT: the pages that move, in ascending order, then -1
+ *   n_live     int32 [1]      OUTPUT: L
+ *   workspace  dsa_compact_pages_workspace_size(P) bytes, as above
+ */
+DSA_API size_t dsa_compact_pages_workspace_size(int P);
+DSA_API dsa_status dsa_compact_pages(int32_t* table, int32_t* ref, int R, int M, int P, int32_t* src, int32_t* dst,
+                                     int32_t* n_live, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dsa_copy_pages -- pages[dst[i]] = pages[src[i]] for the n entries whose two ids lie in [0, P); others
+ * are skipped.  `pages` is any array of P pages of page_bytes bytes (a multiple of 16, else
+ * DSA_ERR_UNSUPPORTED; 16-byte aligned): a 4-bit cache, or index keys and their scales kept in the same pages.
+ * The copies have no order: a page must not be both a source and a destination, nor twice a destination.
+ */
+DSA_API dsa_status dsa_copy_pages(void* pages, size_t page_bytes, int P, const int32_t* src, const int32_t* dst, int n,
+                                  void* stream);
 
 /*
  * dsa_check_bounded_wait -- failure-detection self-check (no counterpart in the method's

@@ -792,6 +792,12 @@ dsa_status dsa_check_bounded_wait(uint64_t* wait_ns, void* stream) {
 }  // extern "C"
 
 namespace dsa {
+bool device_facts(DeviceFacts* f) {
+  const DeviceInfo* d = device_info();
+  if (!d) return false;
+  *f = DeviceFacts{d->sms, d->max_smem, d->err};
+  return true;
+}
 int max_dynamic_smem() {
   const DeviceInfo* d = device_info();
   return d ? d->max_smem : 0;

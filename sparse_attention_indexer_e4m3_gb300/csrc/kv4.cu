@@ -1,0 +1,76 @@
+// The 4-bit paged cache's codec and page calls: launchers (their own translation unit).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "kv4_codec_kernel.cuh"
+#include "launch.h"
+#include "pages_kernel.cuh"
+
+namespace dsa {
+
+namespace {
+
+template <int D>
+int codec_grid(int N) {
+  const int64_t rows_per_cta = static_cast<int64_t>(kKv4CodecThreads / 32) * (32 / (D / kKv4Group)) * kRowSets;
+  return static_cast<int>(std::min<int64_t>((N + rows_per_cta - 1) / rows_per_cta, 1 << 20));
+}
+
+}  // namespace
+
+#define DSA_KV4_BY_D(D, CALL)             \
+  switch (D) {                            \
+    case 64: CALL(64); break;             \
+    case 128: CALL(128); break;           \
+    case 256: CALL(256); break;           \
+    case 512: CALL(512); break;           \
+    default: return cudaErrorInvalidValue; \
+  }
+
+cudaError_t launch_kv4_write(int D, const uint16_t* x, int N, const int32_t* seq, const int32_t* pos, const Kv4Pool& c,
+                             cudaStream_t stream) {
+#define DSA_CALL(DD) kv4_write_kernel<DD><<<codec_grid<DD>(N), kKv4CodecThreads, 0, stream>>>(x, N, seq, pos, c)
+  DSA_KV4_BY_D(D, DSA_CALL)
+#undef DSA_CALL
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv4_read(int D, uint16_t* out, int N, const int32_t* seq, const int32_t* pos, const Kv4Pool& c,
+                            cudaStream_t stream) {
+#define DSA_CALL(DD) kv4_read_kernel<DD><<<codec_grid<DD>(N), kKv4CodecThreads, 0, stream>>>(out, N, seq, pos, c)
+  DSA_KV4_BY_D(D, DSA_CALL)
+#undef DSA_CALL
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_fork(const int32_t* table, const int32_t* parent, int R, int M, int P, int32_t* ref,
+                              int32_t* out, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(std::min((M + 255) / 256, 1 << 16)), static_cast<unsigned>(std::min(R, 65535)));
+  pages_fork_kernel<<<grid, 256, 0, stream>>>(table, parent, R, M, P, ref, out);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_reserve(const ReserveArgs& a, cudaStream_t stream) {
+  pages_reserve_kernel<<<kPagesCluster, kPagesThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_compact(const CompactArgs& a, int32_t* table, int64_t entries, cudaStream_t stream) {
+  pages_compact_kernel<<<kPagesCluster, kPagesThreads, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || entries == 0) return e;
+  const int grid = static_cast<int>(std::min<int64_t>((entries + 255) / 256, 1 << 16));
+  pages_relabel_kernel<<<grid, 256, 0, stream>>>(table, entries, a.P, a.remap);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_copy(uint8_t* pages, int64_t page_bytes, int P, const int32_t* src, const int32_t* dst, int n,
+                              int sms, cudaStream_t stream) {
+  const int64_t pieces = (page_bytes + kCopyPiece - 1) / kCopyPiece;
+  const int grid = static_cast<int>(std::min<int64_t>(n * pieces, static_cast<int64_t>(sms) * 8));
+  pages_copy_kernel<<<grid, kCopyThreads, 0, stream>>>(pages, page_bytes, P, src, dst, n, static_cast<int>(pieces));
+  return cudaGetLastError();
+}
+
+}  // namespace dsa

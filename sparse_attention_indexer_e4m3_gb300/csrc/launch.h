@@ -16,6 +16,10 @@ struct PlanArgs;
 struct AttnParams;
 struct AttnBwdParams;
 struct KresParams;
+struct AttnKv4Params;
+struct Kv4Pool;
+struct ReserveArgs;
+struct CompactArgs;
 
 // Index kernel for head dimension 128 / 64; `fused` selects the fused index + top-k mode.
 cudaError_t launch_index_d128(int H, bool fused, int grid, size_t smem, cudaStream_t stream, const CUtensorMap& kmap,
@@ -52,6 +56,33 @@ int sparse_attn_tc_smem(int D);
 // persistent CTAs over the query rows; dkv and dsink must be zeroed first.
 cudaError_t launch_sparse_attn_bwd_tc(int D, int grid, const AttnBwdParams& p, unsigned* err, cudaStream_t stream);
 int sparse_attn_bwd_tc_smem(int D);
+
+// 4-bit paged cache: N rows of D (64, 128, 256 or 512) bf16 values into their pages and back.
+cudaError_t launch_kv4_write(int D, const uint16_t* x, int N, const int32_t* seq, const int32_t* pos, const Kv4Pool& c,
+                             cudaStream_t stream);
+cudaError_t launch_kv4_read(int D, uint16_t* out, int N, const int32_t* seq, const int32_t* pos, const Kv4Pool& c,
+                            cudaStream_t stream);
+// Page tables: rows from their parents, pages for rows about to be written, live pages to the front, copies.
+cudaError_t launch_pages_fork(const int32_t* table, const int32_t* parent, int R, int M, int P, int32_t* ref,
+                              int32_t* out, cudaStream_t stream);
+cudaError_t launch_pages_reserve(const ReserveArgs& a, cudaStream_t stream);
+cudaError_t launch_pages_compact(const CompactArgs& a, int32_t* table, int64_t entries, cudaStream_t stream);
+cudaError_t launch_pages_copy(uint8_t* pages, int64_t page_bytes, int P, const int32_t* src, const int32_t* dst, int n,
+                              int sms, cudaStream_t stream);
+// Sparse attention over the 4-bit paged cache (D in {64, 128, 256, 512}); `shares` CTAs of a cluster
+// share a unit's list.
+constexpr int kKv4Block = 128;  // list entries per block
+cudaError_t launch_sparse_attn_kv4(int D, int grid, int shares, const AttnKv4Params& p, unsigned* err,
+                                   cudaStream_t stream);
+int sparse_attn_kv4_smem(int D);
+
+// Facts of the current device that the entry points need; false on a CUDA error.
+struct DeviceFacts {
+  int sms;
+  int max_smem;
+  unsigned* err;  // the device error word
+};
+bool device_facts(DeviceFacts* f);
 
 // Largest dynamic shared memory a CTA of this device may use (bytes).
 int max_dynamic_smem();
