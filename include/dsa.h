@@ -348,7 +348,7 @@ DSA_API dsa_status dsa_dequantize_kv4(const uint8_t* cache, int P, int page_rows
  *   q          bf16 [T][H][D], 16-byte aligned
  *   seq        int32 [T];  start  int32 [T] or NULL (0)
  *   attn_sink  float [H] or NULL;  idx  int32 [T][K];  scale  softmax scale
- *   out        bf16 [T][H][D]   OUTPUT
+ *   out        bf16 [T][H][D], 16-byte aligned   OUTPUT
  *   lse        float [T][H] or NULL   OUTPUT, as dsa_sparse_attn's
  * H >= 1.  No workspace; deterministic.
  */

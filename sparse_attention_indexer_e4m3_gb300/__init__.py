@@ -53,6 +53,8 @@ def library_path() -> str:
 def load():
     """Load libdsa_gb300.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -117,20 +119,32 @@ def load():
     return _lib
 
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_ptr(stream) -> int:
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
+    if stream is not None:
+        return int(stream.cuda_stream)
+    c = _torch()._C  # the current stream's handle, without a Stream object around it
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _dev(t, name, dtypes):
     torch = _torch()
+    try:
+        if t.dtype in dtypes and t.is_cuda and t.is_contiguous():
+            return t
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype == torch.float8_e4m3fn:
@@ -146,7 +160,7 @@ def _dev(t, name, dtypes):
 
 def _shape(t, name, shape):
     """Raise unless tensor t has exactly this shape (caller buffers are never written past)."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -439,10 +453,15 @@ def _new(shape, dtype, like, stream):
 
 def _on_current_device(*tensors):
     """Raise unless every tensor given lies on the current CUDA device, on which the call launches."""
-    torch = _torch()
+    now = -1
     for t in tensors:
-        if t is not None and t.is_cuda and t.get_device() != torch.cuda.current_device():
-            raise ValueError("tensors must be on the current CUDA device")
+        if t is not None:
+            d = t.get_device()
+            if d != now and d >= 0:
+                if now < 0:
+                    now = _torch()._C._cuda_getDevice()
+                if d != now:
+                    raise ValueError("tensors must be on the current CUDA device")
 
 
 def _pool(cache, table, D: int):
@@ -550,20 +569,25 @@ def _tables(table, ref):
     return table, ref, table.shape[0], table.shape[1], ref.shape[0]
 
 
-def _int_out(t, name, n, like, stream):
+def _lists(n, src, dst, one, name, scratch_ints, workspace, like, stream):
+    """The outputs src [n], dst [n] and one [1] and the workspace of a page call: the caller's where given,
+    else views of one new allocation."""
     torch = _torch()
-    if t is None:
-        t = _new((n,), torch.int32, like, stream)
-    t = _dev(t, name, (torch.int32,))
-    _shape(t, name, (n,))
-    return t
-
-
-def _scratch(nbytes, workspace, like, stream):
-    torch = _torch()
-    if workspace is None:
-        workspace = _new((nbytes,), torch.uint8, like, stream)
-    return _dev(workspace, "workspace", (torch.uint8,))
+    if src is not None or dst is not None or one is not None or workspace is not None:
+        i32 = (torch.int32,)
+        src = _dev(_new((n,), torch.int32, like, stream) if src is None else src, "src", i32)
+        dst = _dev(_new((n,), torch.int32, like, stream) if dst is None else dst, "dst", i32)
+        one = _dev(_new((1,), torch.int32, like, stream) if one is None else one, name, i32)
+        if workspace is None:
+            workspace = _new((4 * scratch_ints,), torch.uint8, like, stream)
+        workspace = _dev(workspace, "workspace", (torch.uint8,))
+        _shape(src, "src", (n,))
+        _shape(dst, "dst", (n,))
+        _shape(one, name, (1,))
+        _on_current_device(src, dst, one, workspace)
+        return src, dst, one, workspace.data_ptr(), workspace.numel()
+    src, dst, one, ws = _new((2 * n + 1 + scratch_ints,), torch.int32, like, stream).split_with_sizes((n, n, 1, scratch_ints))
+    return src, dst, one, ws.data_ptr(), 4 * scratch_ints
 
 
 def fork_pages(table, parent, ref, table_out=None, stream=None):
@@ -598,13 +622,10 @@ def reserve_pages(table, ref, begin, end, page_rows: int, src=None, dst=None, la
     end = _dev(end, "end", (torch.int32,))
     _shape(begin, "begin", (R,))
     _shape(end, "end", (R,))
-    src = _int_out(src, "src", 2 * R, table, stream)
-    dst = _int_out(dst, "dst", 2 * R, table, stream)
-    lacking = _int_out(lacking, "lacking", 1, table, stream)
-    ws = _scratch(8 * P, workspace, table, stream)
-    _on_current_device(table, ref, begin, end, src, dst, lacking, ws)
+    _on_current_device(table, ref, begin, end)
+    src, dst, lacking, ws, nws = _lists(2 * R, src, dst, lacking, "lacking", 2 * P, workspace, table, stream)
     _check(load().dsa_reserve_pages(table.data_ptr(), ref.data_ptr(), begin.data_ptr(), end.data_ptr(), R, M, P, page_rows,
-                                    src.data_ptr(), dst.data_ptr(), lacking.data_ptr(), ws.data_ptr(), ws.numel(),
+                                    src.data_ptr(), dst.data_ptr(), lacking.data_ptr(), ws, nws,
                                     _stream_ptr(stream)), "dsa_reserve_pages")
     return src, dst, lacking
 
@@ -617,13 +638,10 @@ def compact_pages(table, ref, src=None, dst=None, n_live=None, workspace=None, s
     """Rename the pages in use to the lowest ones (table and ref in place).  Returns (src, dst, n_live):
     copy_pages(cache, src, dst) moves the rows (int32 [P // 2], -1 = none); n_live (int32 [1]) pages are in use."""
     table, ref, R, M, P = _tables(table, ref)
-    src = _int_out(src, "src", P // 2, table, stream)
-    dst = _int_out(dst, "dst", P // 2, table, stream)
-    n_live = _int_out(n_live, "n_live", 1, table, stream)
-    ws = _scratch(4 * P, workspace, table, stream)
-    _on_current_device(table, ref, src, dst, n_live, ws)
+    _on_current_device(table, ref)
+    src, dst, n_live, ws, nws = _lists(P // 2, src, dst, n_live, "n_live", P, workspace, table, stream)
     _check(load().dsa_compact_pages(table.data_ptr(), ref.data_ptr(), R, M, P, src.data_ptr(), dst.data_ptr(),
-                                    n_live.data_ptr(), ws.data_ptr(), ws.numel(), _stream_ptr(stream)),
+                                    n_live.data_ptr(), ws, nws, _stream_ptr(stream)),
            "dsa_compact_pages")
     return src, dst, n_live
 

@@ -16,7 +16,7 @@ cudaError_t launch_d(int grid, int shares, const AttnKv4Params& p, unsigned* err
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(static_cast<unsigned>(grid));
-  c.blockDim = dim3(kTcAttnThreads);
+  c.blockDim = dim3(kKv4Threads);
   c.dynamicSmemBytes = smem;
   c.stream = stream;
   cudaLaunchAttribute attr = {};

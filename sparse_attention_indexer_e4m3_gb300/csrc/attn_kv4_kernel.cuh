@@ -12,16 +12,18 @@
 //
 // A unit is (token, group of up to 64 heads, share of the token's list); a cluster of S CTAs shares
 // one list and joins its S partial results through distributed shared memory, so a call with few tokens still
-// uses most SMs and needs no second launch.  One CTA per SM, 512 threads, per block of 128 entries:
-//   gather   (warps 12-15) looks the entries' pages up, converts the rows' codes to fp16 values and
-//                          writes them as D / 64 chunks of [128 keys x 128 bytes], 128-byte swizzled; a
-//                          masked entry becomes a row of zeros (its memory is not read);
+// uses most SMs and needs no second launch.  One CTA per SM, 640 threads, per block of 128 entries:
+//   scout    (warps 1-3)   find the unit's blocks and, up to six blocks ahead, its entries' pages and row scales;
+//   convert  (warps 12-19) the rows' codes to fp16 values, as D / 64 chunks of [128 keys x 128 bytes], 128-byte
+//                          swizzled; a masked entry becomes a row of zeros (its memory is not read); and the
+//                          unit's q to fp16;
 //   score    (warp 0)      S^T = V . Q^T: M = 128 keys, N = 64 heads, K = D (tcgen05.mma kind::f16);
 //   softmax  (warps 4-11)  thread = (key, 32 heads): weights as fp16 rows P[key][head]; the running
 //                          bound m moves only when exceeded by more than 2^8;
 //   weighted (warp 0)      O^T += V^T . P^T: M = 128 output dims (D / 128 tiles), N = 64, K = 128 keys.
-// The gather refills a tile of 128 dims as soon as the weighted sum has read it; its global loads for the
-// next block are in flight while it waits.
+// A tile of 128 dims is converted anew as soon as the weighted sum has read it; the global loads of the next
+// block are in flight while its tiles are waited for.  Up to D = 256 two blocks fit, and the score product of
+// the next block is issued before the weighted sum of the last, so the softmax runs beside it.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -35,29 +37,41 @@ namespace dsa {
 // Row scales outside this range are clamped (the quantiser writes 2^-100 to 2^117).
 constexpr float kKv4MinScale = 7.888609052210118e-31f;  // 2^-100
 
+constexpr int kKv4Threads = 640;
+constexpr int kKv4ConvThreads = 256;
+constexpr int kKv4ConvWarps = kKv4ConvThreads / 32;
+constexpr int kKv4SoftWarps = kTcSoftThreads / 32;
+constexpr int kKv4Scouts = 3;             // scout warps; one of them looks up every third block
+constexpr int kKv4Slots = 2 * kKv4Scouts; // blocks whose entries are looked up ahead (a slot is always one scout's)
+constexpr int kKv4Shares = 8;             // most CTAs that share a list
+constexpr float kKv4NoBound = -1e30f;     // bound of a head without keys so far
+
 template <int D>
 struct AttnKv4Layout {
+  static constexpr int kStages = D <= 256 ? 2 : 1;              // kv blocks held
   static constexpr int kChunks = D / 64;                        // chunks of a row in the score product
   static constexpr int kTiles = D >= 128 ? D / 128 : 1;         // output tiles (D = 64: half of one is zero)
   static constexpr int kChunkBytes = kTcAttnKeys * 128;
+  static constexpr int kStageBytes = 2 * kTiles * kChunkBytes;
   static constexpr int kQChunkBytes = kTcAttnHeads * 128;
   static constexpr int kKv = 0;
-  static constexpr int kQ = kKv + 2 * kTiles * kChunkBytes;
+  static constexpr int kQ = kKv + kStages * kStageBytes;
   static constexpr int kP = kQ + kChunks * kQChunkBytes;        // fp16 [128 keys][64 heads]
-  static constexpr int kEnt = kP + kTcAttnKeys * 128;           // int2 [2][128]: page, row in the page
-  static constexpr int kScl = kEnt + 2 * kTcAttnKeys * 8;       // float [2][128]: row scale, 0 = masked
-  static constexpr int kRed = kScl + 2 * kTcAttnKeys * 4;       // float [4][64] cross-warp scratch
+  static constexpr int kEnt = kP + kTcAttnKeys * 128;           // int2 [slots][128]: page, row in the page
+  static constexpr int kScl = kEnt + kKv4Slots * kTcAttnKeys * 8;  // float [slots][128]: row scale, 0 = masked
+  static constexpr int kRed = kScl + kKv4Slots * kTcAttnKeys * 4;  // float [4][64] cross-warp scratch
   static constexpr int kMax = kRed + 4 * kTcAttnHeads * 4;      // float [64] running bound (log2 units)
   static constexpr int kAlpha = kMax + kTcAttnHeads * 4;        // float [64] rescale / output factors
   static constexpr int kSum = kAlpha + kTcAttnHeads * 4;        // float [64] denominators (of this share)
-  static constexpr int kJoin = kSum + kTcAttnHeads * 4;         // float [8][64] factors of the shares
-  static constexpr int kMisc = kJoin + 8 * kTcAttnHeads * 4;    // int [32]
+  static constexpr int kJoin = kSum + kTcAttnHeads * 4;         // float [shares][64] factors of the shares
+  static constexpr int kMisc = kJoin + kKv4Shares * kTcAttnHeads * 4;  // int [32]
   static constexpr int kBar = kMisc + 128;
-  static constexpr int kNumBars = 10 + 2 * kTiles;
+  static constexpr int kNumBars = 14 + 2 * kKv4Slots + 2 * kStages * kTiles;
   static constexpr int kSmem = kBar + kNumBars * 8 + 1024;      // + alignment slack
-  // the joined shares' partial outputs, fp32 [D][64], take the place of the kv block
-  static_assert(D * kTcAttnHeads * 4 <= 2 * kTiles * kChunkBytes, "partial outputs fit the kv block");
-  static constexpr int kTmemCols = kTiles == 1 ? 128 : (kTiles == 2 ? 256 : 512);
+  // the joined shares' partial outputs, fp32 [64][D], take the place of the kv blocks
+  static_assert(D * kTcAttnHeads * 4 <= kStages * kStageBytes, "partial outputs fit the kv blocks");
+  // tensor memory: S^T (one per stage) from column 0, O^T tile m from column 64 (kStages + m)
+  static constexpr int kTmemCols = kStages + kTiles <= 4 ? 256 : 512;
 };
 
 // Instruction descriptor, kind::f16 with fp16 operands and an fp32 accumulator.
@@ -66,15 +80,45 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Index of the 16-byte piece of dim d's row that holds heads [4 u, 4 u + 4) of the partial outputs: the
-// pieces of neighbouring dims fall on different banks.
-__device__ __forceinline__ uint32_t join_at(int d, int u) { return static_cast<uint32_t>(d * 16 + (u ^ (d & 15))); }
+// One thread of the (converged) warp: 1 there, 0 elsewhere.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+
+// tcgen05.mma kind::f16 and commit, issued where `on` is set.  The whole warp runs the issue loop, so that
+// addresses and descriptors stay warp-uniform; a loop that one thread runs alone took 80 to 120 cycles per
+// product instead of the tensor core's 52 to 63.
+template <bool kAcc>
+__device__ __forceinline__ void mma_f16_if(uint32_t on, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc = 1u) {
+  if constexpr (kAcc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, 1, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(on)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(on), "r"(acc)
+        : "memory");
+  }
+}
+__device__ __forceinline__ void mma_commit_if(uint32_t on, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(on)
+      : "memory");
+}
 
 // Output factor of a head whose weights' bound is m (log2 units) and whose denominator, in units of
 // 2^m, is l without the sink; writes the natural log of the whole denominator where lse is given.  0 for
-// a head without keys and sink.  The larger of bound and sink is the unit, so neither overflows.
+// a head without keys (m = kKv4NoBound) and sink.  The larger of bound and sink is the unit, so neither overflows.
 __device__ __forceinline__ float softmax_factor(float m, float l, const float* sink, int h, float* lse) {
-  const bool keys = m != -INFINITY;
+  const bool keys = m != kKv4NoBound;
   float f = keys ? 1.f : 0.f, unit = m;
   if (!keys) l = 0.f;
   if (sink != nullptr) {
@@ -98,11 +142,12 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float f) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kTcAttnThreads, 1) sparse_attn_kv4_kernel(const AttnKv4Params p, int shares,
-                                                                            unsigned* err) {
+__global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const AttnKv4Params p, int shares,
+                                                                         unsigned* err) {
   using L = AttnKv4Layout<D>;
   constexpr int kCh = L::kChunks;
   constexpr int kTi = L::kTiles;
+  constexpr int kSt = L::kStages;
   extern __shared__ __align__(1024) uint8_t kv4_attn_smem[];
   uint8_t* smem = kv4_attn_smem + ((1024u - (smem_addr(kv4_attn_smem) & 1023u)) & 1023u);
   uint8_t* kv_s = smem + L::kKv;
@@ -115,23 +160,25 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1) sparse_attn_kv4_kernel(cons
   float* alpha_s = reinterpret_cast<float*>(smem + L::kAlpha);
   float* sum_s = reinterpret_cast<float*>(smem + L::kSum);
   float* join_s = reinterpret_cast<float*>(smem + L::kJoin);
-  // [0] blocks of the unit in flight, [1] the bits of its q factor, [2] / [3] their copies for the softmax
-  // warps, [4] / [5] for the gather warps, [8..15] the gather warps' partial results
+  // [0, 1] blocks of the units in flight, [2, 3] the bits of their q factors, [8..15] the convert warps' maxima
   volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMisc);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  uint64_t* q_full = bars + 0;
-  uint64_t* q_empty = bars + 1;
-  uint64_t* s_full = bars + 2;
+  // (a barrier that its waiters may lag behind by more than a phase is a pair, or one per stage)
+  uint64_t* q_full = bars + 0;  // [2]
+  uint64_t* q_empty = bars + 2;
   uint64_t* p_full = bars + 3;
   uint64_t* pv_done = bars + 4;
   uint64_t* o_empty = bars + 5;
-  uint64_t* tok_full = bars + 6;  // one unit in flight between the gather and the rest
-  uint64_t* tok_empty = bars + 7;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8);
+  uint64_t* unit_full = bars + 6;   // [2]
+  uint64_t* unit_empty = bars + 8;  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 10);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint64_t* kv_full = bars + 9;
-  uint64_t* kv_empty = kv_full + kTi;
-  uint64_t* drain = kv_empty + kTi;
+  uint64_t* drain = bars + 11;
+  uint64_t* s_full = bars + 12;  // [stage]
+  uint64_t* ent_full = bars + 14;
+  uint64_t* ent_empty = ent_full + kKv4Slots;
+  uint64_t* kv_full = ent_empty + kKv4Slots;  // [stage][tile]
+  uint64_t* kv_empty = kv_full + kSt * kTi;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -141,25 +188,29 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1) sparse_attn_kv4_kernel(cons
   const int unit0 = static_cast<int>(blockIdx.x) / shares;
   const int unit_step = static_cast<int>(gridDim.x) / shares;
 
-  // q rows past the group's heads, and the upper half of a 64-dim row's tile, stay zero
-  for (int i = threadIdx.x; i < kCh * L::kQChunkBytes / 16; i += kTcAttnThreads)
-    reinterpret_cast<uint4*>(q_s)[i] = make_uint4(0u, 0u, 0u, 0u);
-  if constexpr (D == 64) {
-    for (int i = threadIdx.x; i < L::kChunkBytes / 16; i += kTcAttnThreads)
-      reinterpret_cast<uint4*>(kv_s + L::kChunkBytes)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if constexpr (D == 64) {  // the upper half of a 64-dim row's tile stays zero
+    for (int s = 0; s < kSt; ++s)
+      for (int i = threadIdx.x; i < L::kChunkBytes / 16; i += kKv4Threads)
+        reinterpret_cast<uint4*>(kv_s + s * L::kStageBytes + L::kChunkBytes)[i] = make_uint4(0u, 0u, 0u, 0u);
   }
   if (threadIdx.x == 0) {
-    mbar_init(q_full, kTcGatherThreads);
     mbar_init(q_empty, 1);
-    mbar_init(s_full, 1);
-    mbar_init(p_full, kTcSoftThreads);
+    mbar_init(p_full, kKv4SoftWarps);
     mbar_init(pv_done, 1);
-    mbar_init(o_empty, kTcSoftThreads);
-    mbar_init(tok_full, 1);
-    mbar_init(tok_empty, 2);  // the MMA issuer and the softmax warps
-    for (int m = 0; m < kTi; ++m) {
-      mbar_init(&kv_full[m], kTcGatherThreads);
-      mbar_init(&kv_empty[m], 1);
+    mbar_init(o_empty, kKv4SoftWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], kKv4ConvWarps);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&unit_full[i], 1);
+      mbar_init(&unit_empty[i], 1 + kKv4SoftWarps + kKv4ConvWarps);
+    }
+    for (int i = 0; i < kKv4Slots; ++i) {
+      mbar_init(&ent_full[i], 32);
+      mbar_init(&ent_empty[i], kKv4SoftWarps + kKv4ConvWarps);
+    }
+    for (int i = 0; i < kSt * kTi; ++i) {
+      mbar_init(&kv_full[i], kKv4ConvWarps);
+      mbar_init(&kv_empty[i], 1);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -175,121 +226,111 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1) sparse_attn_kv4_kernel(cons
   tc_fence_after_sync();
   const uint32_t tbase = *tmem_slot;
   const uint32_t s_tmem = tbase;
-  const uint32_t o_tmem = tbase + 64;
+  const uint32_t o_tmem = tbase + 64 * kSt;
+  // this CTA's blocks of a unit whose list has `all` of them
+  const auto first_block = [&](int all, int s) { return static_cast<int>(static_cast<int64_t>(all) * s / shares); };
+  const int rows = 1 << p.pool.log_rows;
+  const int64_t page_bytes = static_cast<int64_t>(rows) * kv4_row_bytes(D);
 
   if (warp >= 12) {
-    // ------------------------------------------------------------------ gather
-    const int gtid = threadIdx.x - 384;
-    const int rows = 1 << p.pool.log_rows;
-    const int64_t page_bytes = static_cast<int64_t>(rows) * kv4_row_bytes(D);
-    // Thread gtid converts, of every tile, the 32 dims [32 part, 32 part + 32) of rows gtid / 4 + 32 k.
-    const int part = gtid & 3;
-    const int row0 = gtid >> 2;
+    // ------------------------------------------------------------------ convert
+    const int ctid = threadIdx.x - 384;
+    // Thread ctid converts, of every tile, the 32 dims [32 part, 32 part + 32) of rows ctid / 4 and ctid / 4 + 64.
+    const int part = ctid & 3;
+    const int row0 = ctid >> 2;
     const bool has_part = D >= 128 || part < 2;
+    uint4 raw[kTi][2];
+    uint32_t grp[kTi][2];
+    // the codes and group scales of block gb
+    const auto load = [&](uint32_t gb) {
+      const uint32_t slot = gb % kKv4Slots;
+      mbar_wait(&ent_full[slot], (gb / kKv4Slots) & 1u, abort_flag, err, 0x43);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int2 ent = ent_s[slot * kTcAttnKeys + row0 + 64 * k];
+        const uint8_t* base = p.pool.cache + max(ent.x, 0) * page_bytes;
+        const uint8_t* codes = base + ent.y * (D / 2) + part * 16;
+        const uint8_t* scales = base + rows * (D / 2) + ent.y * (D / kKv4Group) + part * 2;
+#pragma unroll
+        for (int m = 0; m < kTi; ++m) {
+          raw[m][k] = make_uint4(0u, 0u, 0u, 0u);
+          grp[m][k] = 0u;
+          if (ent.x >= 0 && has_part) {
+            raw[m][k] = __ldg(reinterpret_cast<const uint4*>(codes + m * 64));
+            grp[m][k] = __ldg(reinterpret_cast<const uint16_t*>(scales + m * 8));
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ent_empty[slot]);
+    };
     uint32_t gb = 0;  // blocks of this CTA so far
     int n = 0;        // units of this CTA so far
     for (int u = unit0; u < units; u += unit_step, ++n) {
       const int t = u / p.groups;
       const int h0 = (u % p.groups) * kTcAttnHeads;
       const int nh = min(kTcAttnHeads, H - h0);
-      const int32_t* list = p.idx + static_cast<int64_t>(t) * p.K;
-      const int seq = __ldg(p.seq + t);
-      const int start = p.start != nullptr ? __ldg(p.start + t) : 0;
-      // blocks to walk: up to the last entry that names a row
-      int last = -1;
-      for (int j = gtid; j < p.K; j += kTcGatherThreads)
-        if (__ldg(list + j) >= 0) last = j;
-      last = __reduce_max_sync(0xffffffffu, last);
-      if (lane == 0) misc[8 + (warp - 12)] = last;
-      named_bar_sync(kTcGatherBar, kTcGatherThreads);
-      const int nball = (max(max(misc[8], misc[9]), max(misc[10], misc[11])) + kTcAttnKeys) / kTcAttnKeys;
-      const int blk0 = static_cast<int>(static_cast<int64_t>(nball) * share / shares);
-      const int nb = static_cast<int>(static_cast<int64_t>(nball) * (share + 1) / shares) - blk0;
-      // the unit's q as fp16 once the previous unit's score products are done
-      if (n > 0) mbar_wait(q_empty, static_cast<uint32_t>(n - 1) & 1u, abort_flag, err, 0x41);
+      // the unit's q as fp16
       float f = 1.0f;
+      int nb = 0;
+      const uint16_t* q = p.q + (static_cast<int64_t>(t) * H + h0) * D;
+      constexpr int kPieces = kTcAttnHeads * (D / 8) / kKv4ConvThreads;  // 16-byte pieces of a thread
       for (int pass = 0; pass < 2; ++pass) {
         uint32_t top = 0u;
-        const uint16_t* q = p.q + (static_cast<int64_t>(t) * H + h0) * D;
-#pragma unroll 4
-        for (int i = gtid; i < kTcAttnHeads * (D / 8); i += kTcGatherThreads) {
-          const int h = i / (D / 8), pc = i % (D / 8);
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (h < nh) v = __ldg(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * D) + pc);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint4 v[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int at = ctid + i * kKv4ConvThreads;
+          const int h = at / (D / 8), pc = at % (D / 8);
+          v[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (h < nh) v[i] = __ldg(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * D) + pc);
+        }
+        if (pass == 0) {  // the unit's blocks; q's place once the previous unit's score products are done
+          mbar_wait(&unit_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x44);
+          nb = misc[n & 1];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
+          if (n > 0) mbar_wait(q_empty, static_cast<uint32_t>(n - 1) & 1u, abort_flag, err, 0x41);
+        }
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int at = ctid + i * kKv4ConvThreads;
+          const int h = at / (D / 8), pc = at % (D / 8);
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-          *reinterpret_cast<uint4*>(q_s + (pc / 8) * L::kQChunkBytes + swz128(h, (pc % 8) * 16)) =
-              make_uint4(bf16x2_to_f16x2(v.x, f), bf16x2_to_f16x2(v.y, f), bf16x2_to_f16x2(v.z, f), bf16x2_to_f16x2(v.w, f));
+          *reinterpret_cast<uint4*>(q_s + (pc / 8) * L::kQChunkBytes + swz128(h, (pc % 8) * 16)) = make_uint4(
+              bf16x2_to_f16x2(w[0], f), bf16x2_to_f16x2(w[1], f), bf16x2_to_f16x2(w[2], f), bf16x2_to_f16x2(w[3], f));
         }
         if (pass == 1) break;
         top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) misc[12 + (warp - 12)] = static_cast<int>(top);
-        named_bar_sync(kTcGatherBar, kTcGatherThreads);
-        const int e = (max(max(misc[12], misc[13]), max(misc[14], misc[15])) >> 7) - 127;  // exponent of the largest
+        if (lane == 0) misc[8 + (warp - 12)] = static_cast<int>(top);
+        named_bar_sync(kTcGatherBar, kKv4ConvThreads);
+        int all = 0;
+#pragma unroll
+        for (int i = 0; i < kKv4ConvWarps; ++i) all = max(all, misc[8 + i]);
+        named_bar_sync(kTcGatherBar, kKv4ConvThreads);
+        const int e = (all >> 7) - 127;  // exponent of the largest
         if (e >= 0 && e < 15) break;
         if (e < -126 || e > 127) break;  // zeros (or less than the least normal number), or not finite
         f = __int_as_float((127 + min(13 - e, 126)) << 23);  // the largest lands in [2^13, 2^14)
       }
-      if (gtid == 0) {
-        mbar_wait(tok_empty, (static_cast<uint32_t>(n) & 1u) ^ 1u, abort_flag, err, 0x40);
-        misc[0] = nb;
-        misc[1] = __float_as_int(f);
-        mbar_arrive(tok_full);
-      }
+      if (ctid == 0) misc[2 + (n & 1)] = __float_as_int(f);
       fence_proxy_async_shared();
-      mbar_arrive(q_full);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[n & 1]);
+      if (nb > 0) load(gb);
 
-      // entry of key gtid of block b, and its row scale
-      const auto lookup = [&](int b, int2& ent, float& r) {
-        const int j = (blk0 + b) * kTcAttnKeys + gtid;
-        const int v = b < nb && j < p.K ? __ldg(list + j) : -1;
-        const int64_t pos = static_cast<int64_t>(v) - start;
-        const int page = v >= 0 && pos >= 0 && pos < INT32_MAX ? kv4_page(p.pool, seq, static_cast<int>(pos)) : -1;
-        ent = make_int2(page, static_cast<int>(pos) & (rows - 1));
-        r = 0.0f;
-        if (page >= 0)
-          r = __ldg(reinterpret_cast<const float*>(p.pool.cache + page * page_bytes + rows * (D / 2 + D / kKv4Group)) + ent.y);
-      };
-      uint4 raw[kTi][4];
-      uint32_t grp[kTi][4];
-      const auto load = [&](uint32_t slot) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int2 ent = ent_s[(slot & 1u) * kTcAttnKeys + row0 + 32 * k];
-          const uint8_t* base = p.pool.cache + max(ent.x, 0) * page_bytes;
-          const uint8_t* codes = base + ent.y * (D / 2) + part * 16;
-          const uint8_t* scales = base + rows * (D / 2) + ent.y * (D / kKv4Group) + part * 2;
-#pragma unroll
-          for (int m = 0; m < kTi; ++m) {
-            raw[m][k] = make_uint4(0u, 0u, 0u, 0u);
-            grp[m][k] = 0u;
-            if (ent.x >= 0 && has_part) {
-              raw[m][k] = __ldg(reinterpret_cast<const uint4*>(codes + m * 64));
-              grp[m][k] = __ldg(reinterpret_cast<const uint16_t*>(scales + m * 8));
-            }
-          }
-        }
-      };
-      int2 ent;
-      float r;
-      lookup(0, ent, r);
-      if (nb > 0) {
-        ent_s[(gb & 1u) * kTcAttnKeys + gtid] = ent;
-        scl_s[(gb & 1u) * kTcAttnKeys + gtid] = ent.x >= 0 ? fmaxf(r, kKv4MinScale) : 0.0f;
-        named_bar_sync(kTcGatherBar, kTcGatherThreads);
-        load(gb);
-      }
       for (int b = 0; b < nb; ++b, ++gb) {
-        lookup(b + 1, ent, r);
+        const int st = static_cast<int>(gb % kSt);
 #pragma unroll
         for (int m = 0; m < kTi; ++m) {
-          if (gb > 0) mbar_wait(&kv_empty[m], (gb - 1) & 1u, abort_flag, err, 0x42);
+          if (gb >= kSt) mbar_wait(&kv_empty[st * kTi + m], (gb / kSt - 1) & 1u, abort_flag, err, 0x42);
           if (has_part) {
-            uint8_t* chunk = kv_s + (2 * m + (part >> 1)) * L::kChunkBytes;
+            uint8_t* chunk = kv_s + st * L::kStageBytes + (2 * m + (part >> 1)) * L::kChunkBytes;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int row = row0 + 32 * k;
+            for (int k = 0; k < 2; ++k) {
+              const int row = row0 + 64 * k;
               const uint32_t s2 = e4m3x2_to_f16x2(grp[m][k]);
               const uint32_t w[4] = {raw[m][k].x, raw[m][k].y, raw[m][k].z, raw[m][k].w};
 #pragma unroll
@@ -306,77 +347,161 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1) sparse_attn_kv4_kernel(cons
             }
           }
           fence_proxy_async_shared();
-          mbar_arrive(&kv_full[m]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&kv_full[st * kTi + m]);
         }
-        // the next block's entries: the softmax of block gb - 1, whose slot this is, is finished, since
-        // the weighted sum of that block, awaited above, followed it
-        if (b + 1 < nb) {
-          ent_s[((gb + 1) & 1u) * kTcAttnKeys + gtid] = ent;
-          scl_s[((gb + 1) & 1u) * kTcAttnKeys + gtid] = ent.x >= 0 ? fmaxf(r, kKv4MinScale) : 0.0f;
-          named_bar_sync(kTcGatherBar, kTcGatherThreads);
-          load(gb + 1);
+        if (b + 1 < nb) load(gb + 1);
+      }
+    }
+  } else if (warp >= 1 && warp <= kKv4Scouts) {
+    // ------------------------------------------------------------------ scout
+    uint32_t gb = 0;
+    int n = 0;
+    for (int u = unit0; u < units; u += unit_step, ++n) {
+      const int t = u / p.groups;
+      const int32_t* list = p.idx + static_cast<int64_t>(t) * p.K;
+      const int seq = __ldg(p.seq + t);
+      const int start = p.start != nullptr ? __ldg(p.start + t) : 0;
+      // blocks to walk: up to the last entry that names a row, looked for from the end
+      int last = -1;
+      for (int j0 = (p.K - 1) / 256 * 256; j0 >= 0 && last < 0; j0 -= 256) {
+        int v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = j0 + 32 * i + lane < p.K ? __ldg(list + j0 + 32 * i + lane) : -1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (v[i] >= 0) last = j0 + 32 * i + lane;
+        last = __reduce_max_sync(0xffffffffu, last);
+      }
+      const int all = (last + kTcAttnKeys) / kTcAttnKeys;
+      const int blk0 = first_block(all, share);
+      const int nb = first_block(all, share + 1) - blk0;
+      if (warp == 1) {
+        if (n > 1) mbar_wait(&unit_empty[n & 1], static_cast<uint32_t>((n >> 1) - 1) & 1u, abort_flag, err, 0x40);
+        if (lane == 0) {
+          misc[n & 1] = nb;
+          mbar_arrive(&unit_full[n & 1]);
         }
+      }
+      for (int b = 0; b < nb; ++b, ++gb) {
+        if (static_cast<int>(gb % kKv4Scouts) != warp - 1) continue;
+        const uint32_t slot = gb % kKv4Slots;
+        int2 ent[4];
+        float r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = (blk0 + b) * kTcAttnKeys + 32 * i + lane;
+          ent[i].x = j < p.K ? __ldg(list + j) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t pos = static_cast<int64_t>(ent[i].x) - start;
+          const bool some = ent[i].x >= 0 && pos >= 0 && pos < INT32_MAX;
+          ent[i] = make_int2(some ? kv4_page(p.pool, seq, static_cast<int>(pos)) : -1, static_cast<int>(pos) & (rows - 1));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          r[i] = 0.0f;
+          if (ent[i].x >= 0)
+            r[i] = fmaxf(__ldg(reinterpret_cast<const float*>(p.pool.cache + ent[i].x * page_bytes +
+                                                              rows * (D / 2 + D / kKv4Group)) + ent[i].y), kKv4MinScale);
+        }
+        if (gb >= kKv4Slots) mbar_wait(&ent_empty[slot], (gb / kKv4Slots - 1) & 1u, abort_flag, err, 0x45);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ent_s[slot * kTcAttnKeys + 32 * i + lane] = ent[i];
+          scl_s[slot * kTcAttnKeys + 32 * i + lane] = r[i];
+        }
+        mbar_arrive(&ent_full[slot]);
       }
     }
   } else if (warp == 0) {
-    // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t id_qk = idesc_f16(kTcAttnKeys, kTcAttnHeads, false, false);
-      const uint32_t id_pv = idesc_f16(128, kTcAttnHeads, true, true);
-      const uint64_t kv_k = desc_sw128(smem_addr(kv_s), 16, 1024);               // K-major: keys x dims
-      const uint64_t q_k = desc_sw128(smem_addr(q_s), 16, 1024);                 // K-major: heads x dims
-      const uint64_t kv_mn = desc_sw128(smem_addr(kv_s), L::kChunkBytes, 1024);  // MN-major: dims x keys
-      const uint64_t p_mn = desc_sw128(smem_addr(p_s), 16384, 1024);             // MN-major: heads x keys
-      uint32_t gb = 0;
-      int n = 0;
-      bool ok = true;
-      for (int u = unit0; ok && u < units; u += unit_step, ++n) {
-        if (!mbar_wait(tok_full, static_cast<uint32_t>(n) & 1u, abort_flag, err, 0x50)) break;
-        const int nb = misc[0];
-        mbar_arrive(tok_empty);
-        if (!mbar_wait(q_full, static_cast<uint32_t>(n) & 1u, abort_flag, err, 0x51)) break;
-        for (int b = 0; b < nb; ++b, ++gb) {
-          for (int c = 0; c < kCh; ++c) {
-            if ((c & 1) == 0) {
-              if (!mbar_wait(&kv_full[c / 2], gb & 1u, abort_flag, err, 0x53)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after_sync();
-            }
+    // ------------------------------------------------------------------ MMA issuer (the whole warp, one thread elected)
+    const uint32_t on = elect_one();
+    const auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, site)) != 0;
+    };
+    constexpr uint32_t id_qk = idesc_f16(kTcAttnKeys, kTcAttnHeads, false, false);
+    constexpr uint32_t id_pv = idesc_f16(128, kTcAttnHeads, true, true);
+    const uint64_t kv_k = desc_sw128(smem_addr(kv_s), 16, 1024);               // K-major: keys x dims
+    const uint64_t q_k = desc_sw128(smem_addr(q_s), 16, 1024);                 // K-major: heads x dims
+    const uint64_t kv_mn = desc_sw128(smem_addr(kv_s), L::kChunkBytes, 1024);  // MN-major: dims x keys
+    const uint64_t p_mn = desc_sw128(smem_addr(p_s), 16384, 1024);             // MN-major: heads x keys
+    // S^T of block gb over D / 16 steps; chunk c holds dims [64 c, 64 c + 64)
+    const auto score = [&](uint32_t gb) -> bool {
+      const uint32_t st = gb % kSt;
+      const uint64_t a = kv_k + st * (L::kStageBytes >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16(s_tmem, kv_k + ((c * L::kChunkBytes + kk * 32) >> 4), q_k + ((c * L::kQChunkBytes + kk * 32) >> 4),
-                       id_qk, (c | kk) ? 1u : 0u);
-          }
-          if (!ok) break;
-          mma_commit(s_full);
-          if (!mbar_wait(p_full, gb & 1u, abort_flag, err, 0x54)) {
-            ok = false;
-            break;
-          }
-          // the unit's first weighted sum overwrites O: the previous unit's output must be read
-          if (b == 0 && n > 0 && !mbar_wait(o_empty, static_cast<uint32_t>(n - 1) & 1u, abort_flag, err, 0x52)) {
-            ok = false;
-            break;
-          }
+      for (int c = 0; c < kCh; ++c) {
+        if ((c & 1) == 0) {
+          if (!wait(&kv_full[st * kTi + c / 2], (gb / kSt) & 1u, 0x53)) return false;
           tc_fence_after_sync();
-          for (int m = 0; m < kTi; ++m) {
-#pragma unroll
-            for (int ks = 0; ks < kTcAttnKeys / 16; ++ks)
-              mma_bf16(o_tmem + 64 * m, kv_mn + ((2 * m * L::kChunkBytes + ks * 16 * 128) >> 4),
-                       p_mn + ((ks * 16 * 128) >> 4), id_pv, (b > 0 || ks > 0) ? 1u : 0u);
-            mma_commit(&kv_empty[m]);
-          }
-          mma_commit(pv_done);
         }
-        if (!ok) break;
-        mma_commit(q_empty);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t ad = a + ((c * L::kChunkBytes + kk * 32) >> 4), bd = q_k + ((c * L::kQChunkBytes + kk * 32) >> 4);
+          if (c == 0 && kk == 0)
+            mma_f16_if<false>(on, s_tmem + 64 * st, ad, bd, id_qk, 0u);
+          else
+            mma_f16_if<true>(on, s_tmem + 64 * st, ad, bd, id_qk);
+        }
       }
-      // every MMA issued by this thread has completed once `drain` flips
-      mma_commit(drain);
-      mbar_wait_drain(drain, 0);
+      mma_commit_if(on, &s_full[st]);
+      return true;
+    };
+    uint32_t gb = 0;
+    int n = 0;
+    bool ok = true;
+    for (int u = unit0; ok && u < units; u += unit_step, ++n) {
+      if (!wait(&unit_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, 0x50)) break;
+      const int nb = __shfl_sync(0xffffffffu, misc[n & 1], 0);
+      if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
+      __syncwarp();
+      if (!wait(&q_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, 0x51)) break;
+      if (nb > 0 && !score(gb)) break;
+      for (int b = 0; b < nb; ++b, ++gb) {
+        if (kSt > 1 && b + 1 < nb && !score(gb + 1)) {
+          ok = false;
+          break;
+        }
+        if (!wait(p_full, gb & 1u, 0x54)) {
+          ok = false;
+          break;
+        }
+        // the unit's first weighted sum overwrites O: the previous unit's output must be read
+        if (b == 0 && n > 0 && !wait(o_empty, static_cast<uint32_t>(n - 1) & 1u, 0x52)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t st = gb % kSt;
+        const uint64_t a = kv_mn + st * (L::kStageBytes >> 4);
+        const uint32_t more = b > 0 ? 1u : 0u;
+#pragma unroll
+        for (int m = 0; m < kTi; ++m) {
+#pragma unroll
+          for (int ks = 0; ks < kTcAttnKeys / 16; ++ks) {
+            const uint64_t ad = a + ((2 * m * L::kChunkBytes + ks * 16 * 128) >> 4), bd = p_mn + ((ks * 16 * 128) >> 4);
+            if (ks == 0)
+              mma_f16_if<false>(on, o_tmem + 64 * m, ad, bd, id_pv, more);
+            else
+              mma_f16_if<true>(on, o_tmem + 64 * m, ad, bd, id_pv);
+          }
+          mma_commit_if(on, &kv_empty[st * kTi + m]);
+        }
+        mma_commit_if(on, pv_done);
+        if (kSt == 1 && b + 1 < nb && !score(gb + 1)) {
+          ok = false;
+          break;
+        }
+      }
+      if (!ok) break;
+      mma_commit_if(on, q_empty);
     }
+    // every MMA issued by this thread has completed once `drain` flips
+    mma_commit_if(on, drain);
+    mbar_wait_drain(drain, 0);
+    __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ softmax and output
     const int etid = threadIdx.x - 128;
@@ -391,42 +516,51 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1) sparse_attn_kv4_kernel(cons
       const int t = u / p.groups;
       const int h0 = (u % p.groups) * kTcAttnHeads;
       const int nh = min(kTcAttnHeads, H - h0);
-      if (etid == 0) {
-        mbar_wait(tok_full, static_cast<uint32_t>(n) & 1u, abort_flag, err, 0x60);
-        misc[2] = misc[0];
-        misc[3] = misc[1];
-        mbar_arrive(tok_empty);
-      }
-      if (etid < kTcAttnHeads) max_s[etid] = -INFINITY;
+      mbar_wait(&unit_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x60);
+      const int nb = misc[n & 1];
+      mbar_wait(&q_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x66);  // the q factor
+      const float to_log2 = p.scale * 1.4426950408889634f / __int_as_float(misc[2 + (n & 1)]);
+      if (etid < kTcAttnHeads) max_s[etid] = kKv4NoBound;
 #pragma unroll
       for (int h = 0; h < kTcHalfHeads; ++h) lsum[h] = 0.f;
       named_bar_sync(kTcEpiBar, kTcSoftThreads);
-      const int nb = misc[2];
-      const float to_log2 = p.scale * 1.4426950408889634f / __int_as_float(misc[3]);
+      if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
       for (int b = 0; b < nb; ++b, ++gb) {
-        mbar_wait(&kv_full[0], gb & 1u, abort_flag, err, 0x65);  // the block's row scales
-        const float rs = scl_s[(gb & 1u) * kTcAttnKeys + r];
+        const uint32_t slot = gb % kKv4Slots;
+        mbar_wait(&ent_full[slot], (gb / kKv4Slots) & 1u, abort_flag, err, 0x65);
+        const float rs = scl_s[slot * kTcAttnKeys + r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ent_empty[slot]);
         const bool valid = rs > 0.f;
-        const float a = to_log2 * rs;                       // score to log2 units
-        const float lr = valid ? log2f(rs) : -INFINITY;     // a masked key's weight is 0
+        const float a = to_log2 * rs;                    // score to log2 units
+        const float lr = valid ? log2f(rs) : -INFINITY;  // a masked key's weight is 0
         const float inv = valid ? 1.0f / rs : 0.f;
-        mbar_wait(s_full, gb & 1u, abort_flag, err, 0x61);
+        const uint32_t s_at = s_tmem + 64 * (gb % kSt) + lane_off + hb;
+        mbar_wait(&s_full[gb % kSt], (gb / kSt) & 1u, abort_flag, err, 0x61);
         tc_fence_after_sync();
         float x[kTcHalfHeads];
-        tmem_ld_x32_sync(s_tmem + lane_off + hb, x);
+        // exponents relative to the running bounds
+        const auto exponents = [&]() {
+          tmem_ld_x32_sync(s_at, x);
 #pragma unroll
-        for (int h = 0; h < kTcHalfHeads; ++h) x[h] = fmaf(x[h], a, lr);
-        // does a value exceed its head's running bound by more than 2^8 (or is it the first)?
-        bool exceed = false;
+          for (int h = 0; h < kTcHalfHeads; h += 4) {
+            const float4 mv = *reinterpret_cast<const float4*>(max_s + hb + h);
+            x[h] = fmaf(x[h], a, lr) - mv.x;
+            x[h + 1] = fmaf(x[h + 1], a, lr) - mv.y;
+            x[h + 2] = fmaf(x[h + 2], a, lr) - mv.z;
+            x[h + 3] = fmaf(x[h + 3], a, lr) - mv.w;
+          }
+        };
+        exponents();
+        // does one exceed its bound by more than 2^8 (or is it a head's first)?
+        float over = x[0];
 #pragma unroll
-        for (int h = 0; h < kTcHalfHeads; h += 4) {
-          const float4 mv = *reinterpret_cast<const float4*>(max_s + hb + h);
-          exceed |= (x[h] > mv.x + kTcLazyLog2) | (x[h + 1] > mv.y + kTcLazyLog2) | (x[h + 2] > mv.z + kTcLazyLog2) |
-                    (x[h + 3] > mv.w + kTcLazyLog2);
-        }
-        const bool raise = bar_or(kTcEpiBar, kTcSoftThreads, exceed);
-        if (raise) {
-          // (the reduction consumes x; the scores are read again from tensor memory below)
+        for (int h = 1; h < kTcHalfHeads; ++h) over = fmaxf(over, x[h]);
+        if (bar_or(kTcEpiBar, kTcSoftThreads, over > kTcLazyLog2)) {
+          // the largest exponents per head across the 128 keys (the reduction consumes x)
+          tmem_ld_x32_sync(s_at, x);
+#pragma unroll
+          for (int h = 0; h < kTcHalfHeads; ++h) x[h] = fmaf(x[h], a, lr);
           xpose_reduce32(x, lane, [](float a2, float c) { return fmaxf(a2, c); });
           red_s[quarter * kTcAttnHeads + hb + lane] = x[0];
           named_bar_sync(kTcEpiBar, kTcSoftThreads);
@@ -435,7 +569,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1) sparse_attn_kv4_kernel(cons
                                    fmaxf(red_s[2 * kTcAttnHeads + etid], red_s[3 * kTcAttnHeads + etid]));
             const float mo = max_s[etid];
             const float mn = (bm > mo + kTcLazyLog2) ? bm : mo;
-            alpha_s[etid] = (mo == -INFINITY || mn == mo) ? 1.f : exp2f(mo - mn);
+            alpha_s[etid] = (mo == kKv4NoBound || mn == mo) ? 1.f : exp2f(mo - mn);
             max_s[etid] = mn;
           }
           named_bar_sync(kTcEpiBar, kTcSoftThreads);
@@ -465,9 +599,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1) sparse_attn_kv4_kernel(cons
             }
             tmem_wait_st();
           }
-          tmem_ld_x32_sync(s_tmem + lane_off + hb, x);
-#pragma unroll
-          for (int h = 0; h < kTcHalfHeads; ++h) x[h] = fmaf(x[h], a, lr);
+          exponents();
         }
         // weights, written into the fp16 row P[key r] once the previous block's weighted sum has read P
         if (gb > 0) mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x63);
@@ -475,26 +607,19 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1) sparse_attn_kv4_kernel(cons
         for (int hh = 0; hh < kTcHalfHeads; hh += 8) {
           uint32_t pk[4];
 #pragma unroll
-          for (int q2 = 0; q2 < 2; ++q2) {
-            const float4 mv = *reinterpret_cast<const float4*>(max_s + hb + hh + 4 * q2);
-            const float mu[4] = {mv.x, mv.y, mv.z, mv.w};
-            float e[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int h = hh + 4 * q2 + i;
-              e[i] = exp2_approx(x[h] - (mu[i] == -INFINITY ? 0.f : mu[i]));
-              lsum[h] = fmaf(e[i], inv, lsum[h]);
-            }
-            const __half2 lo = __floats2half2_rn(e[0], e[1]);
-            const __half2 hi = __floats2half2_rn(e[2], e[3]);
-            pk[2 * q2] = *reinterpret_cast<const uint32_t*>(&lo);
-            pk[2 * q2 + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+          for (int i = 0; i < 4; ++i) {
+            const float e0 = exp2_approx(x[hh + 2 * i]), e1 = exp2_approx(x[hh + 2 * i + 1]);
+            lsum[hh + 2 * i] = fmaf(e0, inv, lsum[hh + 2 * i]);
+            lsum[hh + 2 * i + 1] = fmaf(e1, inv, lsum[hh + 2 * i + 1]);
+            const __half2 w = __floats2half2_rn(e0, e1);
+            pk[i] = *reinterpret_cast<const uint32_t*>(&w);
           }
           *reinterpret_cast<uint4*>(p_s + swz128(r, 2 * (hb + hh))) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
         fence_proxy_async_shared();
         tc_fence_before_sync();
-        mbar_arrive(p_full);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
       }
       // end of the unit: denominators (partial sums across the 128 keys)
       xpose_reduce32(lsum, lane, [](float a2, float c) { return a2 + c; });
@@ -530,8 +655,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1) sparse_attn_kv4_kernel(cons
           }
           if (shares > 1) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 4)
-              reinterpret_cast<float4*>(kv_s)[join_at(d, (hb + c + j) / 4)] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            for (int j = 0; j < 16; ++j) reinterpret_cast<float*>(kv_s)[(hb + c + j) * D + d] = o[j];
           } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -545,8 +669,9 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1) sparse_attn_kv4_kernel(cons
         }
       }
       tc_fence_before_sync();
-      mbar_arrive(o_empty);
-      named_bar_sync(kTcEpiBar, kTcSoftThreads);  // alpha_s, max_s and misc are rewritten by the next unit
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_empty);
+      named_bar_sync(kTcEpiBar, kTcSoftThreads);  // alpha_s and max_s are rewritten by the next unit
     }
   }
 
@@ -559,47 +684,59 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1) sparse_attn_kv4_kernel(cons
     const int nh = min(kTcAttnHeads, H - h0);
     if (threadIdx.x < kTcAttnHeads) {
       const int h = threadIdx.x;
-      float m[8], l[8];
-      float top = -INFINITY;
-      for (int i = 0; i < shares; ++i) {
-        m[i] = ld_cluster_f32(smem_addr(max_s + h), i);
-        l[i] = ld_cluster_f32(smem_addr(sum_s + h), i);
-        top = fmaxf(top, m[i]);
+      float m[kKv4Shares], l[kKv4Shares];
+      float top = kKv4NoBound;
+#pragma unroll
+      for (int i = 0; i < kKv4Shares; ++i) {
+        m[i] = kKv4NoBound;
+        l[i] = 0.f;
+        if (i < shares) {
+          m[i] = ld_cluster_f32(smem_addr(max_s + h), i);
+          l[i] = ld_cluster_f32(smem_addr(sum_s + h), i);
+        }
       }
+#pragma unroll
+      for (int i = 0; i < kKv4Shares; ++i) top = fmaxf(top, m[i]);
       float sum = 0.f;
-      for (int i = 0; i < shares; ++i) {
-        m[i] = m[i] == -INFINITY ? 0.f : exp2f(m[i] - top);
+#pragma unroll
+      for (int i = 0; i < kKv4Shares; ++i) {
+        m[i] = m[i] == kKv4NoBound ? 0.f : exp2f(m[i] - top);
         sum = fmaf(l[i], m[i], sum);
       }
       float f = 0.f;
       if (h < nh)
         f = softmax_factor(top, sum, p.sink, h0 + h,
                            p.lse != nullptr && share == 0 ? p.lse + static_cast<int64_t>(t) * H + h0 + h : nullptr);
-      for (int i = 0; i < shares; ++i) join_s[i * kTcAttnHeads + h] = m[i] * f;
+#pragma unroll
+      for (int i = 0; i < kKv4Shares; ++i) join_s[i * kTcAttnHeads + h] = m[i] * f;
     }
     __syncthreads();
-    // this CTA's dims, four heads at a time
-    const int per = D / shares;
+    // this CTA's share of the group's [64][D] outputs, four dims at a time: a warp reads 512 contiguous bytes of
+    // each partial (with lanes on different rows the remote reads took ten times as long)
+    const int per = kTcAttnHeads * D / 4 / shares;
     uint16_t* out = p.out + (static_cast<int64_t>(t) * H + h0) * D;
-    for (int i = threadIdx.x; i < per * 16; i += kTcAttnThreads) {
-      const int d = share * per + i % per;
-      const int uu = i / per;
-      if (4 * uu >= nh) continue;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int k = 0; k < shares; ++k) {
-        const float4 v = ld_cluster_f4(smem_addr(kv_s) + join_at(d, uu) * 16, k);
-        const float4 f = *reinterpret_cast<const float4*>(join_s + k * kTcAttnHeads + 4 * uu);
-        acc[0] = fmaf(v.x, f.x, acc[0]);
-        acc[1] = fmaf(v.y, f.y, acc[1]);
-        acc[2] = fmaf(v.z, f.z, acc[2]);
-        acc[3] = fmaf(v.w, f.w, acc[3]);
-      }
+    for (int i = share * per + threadIdx.x; i < (share + 1) * per; i += kKv4Threads) {
+      const int h = i / (D / 4);
+      if (h >= nh) break;
+      float4 v[kKv4Shares];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (4 * uu + j < nh) {
-          const __nv_bfloat16 ob = __float2bfloat16_rn(acc[j]);
-          out[static_cast<int64_t>(4 * uu + j) * D + d] = *reinterpret_cast<const uint16_t*>(&ob);
-        }
+      for (int k = 0; k < kKv4Shares; ++k) {
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < shares) v[k] = ld_cluster_f4(smem_addr(kv_s) + i * 16, k);
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kKv4Shares; ++k) {
+        const float f = k < shares ? join_s[k * kTcAttnHeads + h] : 0.f;
+        acc.x = fmaf(v[k].x, f, acc.x);
+        acc.y = fmaf(v[k].y, f, acc.y);
+        acc.z = fmaf(v[k].z, f, acc.z);
+        acc.w = fmaf(v[k].w, f, acc.w);
+      }
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(i) * 4);
+      dst[0] = *reinterpret_cast<const uint32_t*>(&lo);
+      dst[1] = *reinterpret_cast<const uint32_t*>(&hi);
     }
     cluster_sync_all();  // no CTA leaves while another reads its partial outputs
   }

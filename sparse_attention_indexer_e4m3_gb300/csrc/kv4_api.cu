@@ -81,7 +81,7 @@ dsa_status dsa_sparse_attn_kv4(const uint16_t* q, const uint8_t* cache, int P, i
   if (st != DSA_OK) return st;
   if (T < 0 || H < 1 || K < 0) return DSA_ERR_INVALID_ARG;
   if (T == 0) return DSA_OK;
-  if (!q || !aligned(q, 16) || !out || !aligned(out, 2) || !seq || !aligned(seq, 4)) return DSA_ERR_INVALID_ARG;
+  if (!q || !aligned(q, 16) || !out || !aligned(out, 16) || !seq || !aligned(seq, 4)) return DSA_ERR_INVALID_ARG;
   if (K > 0 && (!idx || !aligned(idx, 4))) return DSA_ERR_INVALID_ARG;
   if ((start && !aligned(start, 4)) || (attn_sink && !aligned(attn_sink, 4)) || (lse && !aligned(lse, 4)))
     return DSA_ERR_INVALID_ARG;
