@@ -12,13 +12,13 @@
 //
 // A unit is (token, group of up to 64 heads, share of the token's list); a cluster of S CTAs shares
 // one list and joins its S partial results through distributed shared memory, so a call with few tokens still
-// uses most SMs and needs no second launch.  One CTA per SM, 640 threads, per block of 128 entries:
+// uses most SMs and needs no second launch.  One CTA per SM, 896 threads, per block of 128 entries:
 //   scout    (warps 1-3)   find the unit's blocks and, up to six blocks ahead, its entries' pages and row scales;
-//   convert  (warps 12-19) the rows' codes to fp16 values, as D / 64 chunks of [128 keys x 128 bytes], 128-byte
+//   convert  (warps 20-27) the rows' codes to fp16 values, as D / 64 chunks of [128 keys x 128 bytes], 128-byte
 //                          swizzled; a masked entry becomes a row of zeros (its memory is not read); and the
 //                          unit's q to fp16;
 //   score    (warp 0)      S^T = V . Q^T: M = 128 keys, N = 64 heads, K = D (tcgen05.mma kind::f16);
-//   softmax  (warps 4-11)  thread = (key, 32 heads): weights as fp16 rows P[key][head]; the running
+//   softmax  (warps 4-19)  thread = (key, 16 heads): weights as fp16 rows P[key][head]; the running
 //                          bound m moves only when exceeded by more than 2^8;
 //   weighted (warp 0)      O^T += V^T . P^T: M = 128 output dims (D / 128 tiles), N = 64, K = 128 keys.
 // A tile of 128 dims is converted anew as soon as the weighted sum has read it; the global loads of the next
@@ -37,10 +37,13 @@ namespace dsa {
 // Row scales outside this range are clamped (the quantiser writes 2^-100 to 2^117).
 constexpr float kKv4MinScale = 7.888609052210118e-31f;  // 2^-100
 
-constexpr int kKv4Threads = 640;
+constexpr int kKv4SoftHeads = 16;         // heads of a softmax thread
+constexpr int kKv4SoftThreads = kTcAttnKeys * kTcAttnHeads / kKv4SoftHeads;
+constexpr int kKv4SoftWarps = kKv4SoftThreads / 32;
+constexpr int kKv4FirstConv = 4 + kKv4SoftWarps;  // warps 0-3 issue and scout, then softmax, then convert
 constexpr int kKv4ConvThreads = 256;
 constexpr int kKv4ConvWarps = kKv4ConvThreads / 32;
-constexpr int kKv4SoftWarps = kTcSoftThreads / 32;
+constexpr int kKv4Threads = 32 * (kKv4FirstConv + kKv4ConvWarps);
 constexpr int kKv4Scouts = 3;             // scout warps; one of them looks up every third block
 constexpr int kKv4Slots = 2 * kKv4Scouts; // blocks whose entries are looked up ahead (a slot is always one scout's)
 constexpr int kKv4Shares = 8;             // most CTAs that share a list
@@ -51,6 +54,7 @@ struct AttnKv4Layout {
   static constexpr int kStages = D <= 256 ? 2 : 1;              // kv blocks held
   static constexpr int kChunks = D / 64;                        // chunks of a row in the score product
   static constexpr int kTiles = D >= 128 ? D / 128 : 1;         // output tiles (D = 64: half of one is zero)
+  static constexpr int kTileWarps = kTiles > 1 ? kKv4ConvWarps / 2 : kKv4ConvWarps;  // warps that convert a tile
   static constexpr int kChunkBytes = kTcAttnKeys * 128;
   static constexpr int kStageBytes = 2 * kTiles * kChunkBytes;
   static constexpr int kQChunkBytes = kTcAttnHeads * 128;
@@ -66,7 +70,7 @@ struct AttnKv4Layout {
   static constexpr int kJoin = kSum + kTcAttnHeads * 4;         // float [shares][64] factors of the shares
   static constexpr int kMisc = kJoin + kKv4Shares * kTcAttnHeads * 4;  // int [32]
   static constexpr int kBar = kMisc + 128;
-  static constexpr int kNumBars = 14 + 2 * kKv4Slots + 2 * kStages * kTiles;
+  static constexpr int kNumBars = 15 + 2 * kKv4Slots + 2 * kStages * kTiles;
   static constexpr int kSmem = kBar + kNumBars * 8 + 1024;      // + alignment slack
   // the joined shares' partial outputs, fp32 [64][D], take the place of the kv blocks
   static_assert(D * kTcAttnHeads * 4 <= kStages * kStageBytes, "partial outputs fit the kv blocks");
@@ -112,6 +116,45 @@ __device__ __forceinline__ void mma_commit_if(uint32_t on, uint64_t* bar) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
       "r"(on)
       : "memory");
+}
+
+// Two fp32 lanes in one register pair.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Reduces 16 values per lane (one of each of 16 heads) across the warp's 32 lanes, by recursive halving:
+// afterwards v[0] holds head lane / 2.
+template <class Op>
+__device__ __forceinline__ void xpose_reduce16(float (&v)[16], int lane, Op op) {
+#pragma unroll
+  for (int half = 8, off = 16; half >= 1; half >>= 1, off >>= 1) {
+    const bool up = (lane & off) != 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i < half) {
+        const float send = up ? v[i] : v[i + half];
+        const float keep = up ? v[i + half] : v[i];
+        v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, off));
+      }
+    }
+  }
+  v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
 // Output factor of a head whose weights' bound is m (log2 units) and whose denominator, in units of
@@ -160,7 +203,8 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   float* alpha_s = reinterpret_cast<float*>(smem + L::kAlpha);
   float* sum_s = reinterpret_cast<float*>(smem + L::kSum);
   float* join_s = reinterpret_cast<float*>(smem + L::kJoin);
-  // [0, 1] blocks of the units in flight, [2, 3] the bits of their q factors, [8..15] the convert warps' maxima
+  // [0, 1] blocks of the units in flight, [2, 3] the bits of their q factors, [8..15] the convert warps' maxima,
+  // [16..18] by block modulo 3: a bound has to be raised
   volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMisc);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   // (a barrier that its waiters may lag behind by more than a phase is a pair, or one per stage)
@@ -175,7 +219,8 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint64_t* drain = bars + 11;
   uint64_t* s_full = bars + 12;  // [stage]
-  uint64_t* ent_full = bars + 14;
+  uint64_t* checked = bars + 14;
+  uint64_t* ent_full = bars + 15;
   uint64_t* ent_empty = ent_full + kKv4Slots;
   uint64_t* kv_full = ent_empty + kKv4Slots;  // [stage][tile]
   uint64_t* kv_empty = kv_full + kSt * kTi;
@@ -195,6 +240,8 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   }
   if (threadIdx.x == 0) {
     mbar_init(q_empty, 1);
+    mbar_init(checked, kKv4SoftWarps);
+    misc[16] = misc[17] = misc[18] = 0;
     mbar_init(p_full, kKv4SoftWarps);
     mbar_init(pv_done, 1);
     mbar_init(o_empty, kKv4SoftWarps);
@@ -209,7 +256,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       mbar_init(&ent_empty[i], kKv4SoftWarps + kKv4ConvWarps);
     }
     for (int i = 0; i < kSt * kTi; ++i) {
-      mbar_init(&kv_full[i], kKv4ConvWarps);
+      mbar_init(&kv_full[i], L::kTileWarps);
       mbar_init(&kv_empty[i], 1);
     }
     mbar_init(drain, 1);
@@ -232,32 +279,38 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   const int rows = 1 << p.pool.log_rows;
   const int64_t page_bytes = static_cast<int64_t>(rows) * kv4_row_bytes(D);
 
-  if (warp >= 12) {
+  if (warp >= kKv4FirstConv) {
     // ------------------------------------------------------------------ convert
-    const int ctid = threadIdx.x - 384;
-    // Thread ctid converts, of every tile, the 32 dims [32 part, 32 part + 32) of rows ctid / 4 and ctid / 4 + 64.
+    const int ctid = threadIdx.x - 32 * kKv4FirstConv;
+    // From two tiles on, half of the warps converts the even tiles and half the odd ones, so that a tile's waits
+    // and fences pass beside the other's conversion.  A thread converts, of each of its tiles, the 32 dims
+    // [32 part, 32 part + 32) of kItems rows.
     const int part = ctid & 3;
-    const int row0 = ctid >> 2;
+    const int grp_tile = kTi > 1 ? (warp - kKv4FirstConv) / L::kTileWarps : 0;  // its first tile
+    const int row0 = (ctid % (32 * L::kTileWarps)) >> 2;
+    constexpr int kRowStep = 8 * L::kTileWarps;
+    constexpr int kItems = kTcAttnKeys / kRowStep;
+    constexpr int kMine = kTi > 1 ? kTi / 2 : 1;  // its tiles: grp_tile + 2 i
     const bool has_part = D >= 128 || part < 2;
-    uint4 raw[kTi][2];
-    uint32_t grp[kTi][2];
-    // the codes and group scales of block gb
+    // The codes and group scales of the next block are in flight while its tiles are waited for.
+    uint4 raw[kMine][kItems];
+    uint32_t grp[kMine][kItems];
     const auto load = [&](uint32_t gb) {
       const uint32_t slot = gb % kKv4Slots;
       mbar_wait(&ent_full[slot], (gb / kKv4Slots) & 1u, abort_flag, err, 0x43);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int2 ent = ent_s[slot * kTcAttnKeys + row0 + 64 * k];
+      for (int k = 0; k < kItems; ++k) {
+        const int2 ent = ent_s[slot * kTcAttnKeys + row0 + kRowStep * k];
         const uint8_t* base = p.pool.cache + max(ent.x, 0) * page_bytes;
-        const uint8_t* codes = base + ent.y * (D / 2) + part * 16;
-        const uint8_t* scales = base + rows * (D / 2) + ent.y * (D / kKv4Group) + part * 2;
+        const uint8_t* codes = base + ent.y * (D / 2) + part * 16 + grp_tile * 64;
+        const uint8_t* scales = base + rows * (D / 2) + ent.y * (D / kKv4Group) + part * 2 + grp_tile * 8;
 #pragma unroll
-        for (int m = 0; m < kTi; ++m) {
-          raw[m][k] = make_uint4(0u, 0u, 0u, 0u);
-          grp[m][k] = 0u;
+        for (int i = 0; i < kMine; ++i) {
+          raw[i][k] = make_uint4(0u, 0u, 0u, 0u);
+          grp[i][k] = 0u;
           if (ent.x >= 0 && has_part) {
-            raw[m][k] = __ldg(reinterpret_cast<const uint4*>(codes + m * 64));
-            grp[m][k] = __ldg(reinterpret_cast<const uint16_t*>(scales + m * 8));
+            raw[i][k] = __ldg(reinterpret_cast<const uint4*>(codes + i * 128));
+            grp[i][k] = __ldg(reinterpret_cast<const uint16_t*>(scales + i * 16));
           }
         }
       }
@@ -275,36 +328,40 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       int nb = 0;
       const uint16_t* q = p.q + (static_cast<int64_t>(t) * H + h0) * D;
       constexpr int kPieces = kTcAttnHeads * (D / 8) / kKv4ConvThreads;  // 16-byte pieces of a thread
+      constexpr int kBatch = kPieces < 4 ? kPieces : 4;
       for (int pass = 0; pass < 2; ++pass) {
         uint32_t top = 0u;
-        uint4 v[kPieces];
+#pragma unroll 1
+        for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
+          uint4 v[kBatch];
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int at = ctid + i * kKv4ConvThreads;
-          const int h = at / (D / 8), pc = at % (D / 8);
-          v[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (h < nh) v[i] = __ldg(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * D) + pc);
-        }
-        if (pass == 0) {  // the unit's blocks; q's place once the previous unit's score products are done
-          mbar_wait(&unit_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x44);
-          nb = misc[n & 1];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
-          if (n > 0) mbar_wait(q_empty, static_cast<uint32_t>(n - 1) & 1u, abort_flag, err, 0x41);
-        }
+          for (int i = 0; i < kBatch; ++i) {
+            const int at = ctid + (i0 + i) * kKv4ConvThreads;
+            const int h = at / (D / 8), pc = at % (D / 8);
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (h < nh) v[i] = __ldg(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * D) + pc);
+          }
+          if (pass == 0 && i0 == 0) {  // the unit's blocks; q's place once the previous unit's scores are done
+            mbar_wait(&unit_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x44);
+            nb = misc[n & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
+            if (n > 0) mbar_wait(q_empty, static_cast<uint32_t>(n - 1) & 1u, abort_flag, err, 0x41);
+          }
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int at = ctid + i * kKv4ConvThreads;
-          const int h = at / (D / 8), pc = at % (D / 8);
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          for (int i = 0; i < kBatch; ++i) {
+            const int at = ctid + (i0 + i) * kKv4ConvThreads;
+            const int h = at / (D / 8), pc = at % (D / 8);
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-          *reinterpret_cast<uint4*>(q_s + (pc / 8) * L::kQChunkBytes + swz128(h, (pc % 8) * 16)) = make_uint4(
-              bf16x2_to_f16x2(w[0], f), bf16x2_to_f16x2(w[1], f), bf16x2_to_f16x2(w[2], f), bf16x2_to_f16x2(w[3], f));
+            for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+            *reinterpret_cast<uint4*>(q_s + (pc / 8) * L::kQChunkBytes + swz128(h, (pc % 8) * 16)) = make_uint4(
+                bf16x2_to_f16x2(w[0], f), bf16x2_to_f16x2(w[1], f), bf16x2_to_f16x2(w[2], f), bf16x2_to_f16x2(w[3], f));
+          }
         }
         if (pass == 1) break;
         top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) misc[8 + (warp - 12)] = static_cast<int>(top);
+        if (lane == 0) misc[8 + (warp - kKv4FirstConv)] = static_cast<int>(top);
         named_bar_sync(kTcGatherBar, kKv4ConvThreads);
         int all = 0;
 #pragma unroll
@@ -320,30 +377,32 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[n & 1]);
       if (nb > 0) load(gb);
-
       for (int b = 0; b < nb; ++b, ++gb) {
         const int st = static_cast<int>(gb % kSt);
 #pragma unroll
-        for (int m = 0; m < kTi; ++m) {
-          if (gb >= kSt) mbar_wait(&kv_empty[st * kTi + m], (gb / kSt - 1) & 1u, abort_flag, err, 0x42);
-          if (has_part) {
-            uint8_t* chunk = kv_s + st * L::kStageBytes + (2 * m + (part >> 1)) * L::kChunkBytes;
+        for (int i = 0; i < kMine; ++i) {
+          const int m = grp_tile + 2 * i;
+          uint8_t* chunk = kv_s + st * L::kStageBytes + (2 * m + (part >> 1)) * L::kChunkBytes;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int row = row0 + 64 * k;
-              const uint32_t s2 = e4m3x2_to_f16x2(grp[m][k]);
-              const uint32_t w[4] = {raw[m][k].x, raw[m][k].y, raw[m][k].z, raw[m][k].w};
+          for (int k = 0; k < kItems; ++k) {
+            const int row = row0 + kRowStep * k;
+            const uint32_t s2 = e4m3x2_to_f16x2(grp[i][k]);
+            const uint32_t w[4] = {raw[i][k].x, raw[i][k].y, raw[i][k].z, raw[i][k].w};
+            uint4 o[4];
 #pragma unroll
-              for (int i0 = 0; i0 < 4; ++i0) {
-                // the two chunks' threads take their pieces in different order: no bank conflicts
-                const int i = (part & 2) ? (i0 ^ 2) : i0;
-                const uint32_t wi = (part & 2) ? w[i0 ^ 2] : w[i0];
-                const uint32_t s = (i & 2) ? __byte_perm(s2, s2, 0x3232) : __byte_perm(s2, s2, 0x1010);
-                uint32_t v[4];
-                e2m1x8_to_f16x2(wi, v);
-                *reinterpret_cast<uint4*>(chunk + swz128(row, (part & 1) * 64 + i * 16)) =
-                    make_uint4(hmul2(v[0], s), hmul2(v[1], s), hmul2(v[2], s), hmul2(v[3], s));
-              }
+            for (int j0 = 0; j0 < 4; ++j0) {
+              // the two chunks' threads take their pieces in different order: no bank conflicts
+              const uint32_t wj = (part & 2) ? w[j0 ^ 2] : w[j0];
+              const uint32_t s = ((part & 2) ? (j0 ^ 2) : j0) & 2 ? __byte_perm(s2, s2, 0x3232) : __byte_perm(s2, s2, 0x1010);
+              uint32_t v[4];
+              e2m1x8_to_f16x2(wj, v);
+              o[j0] = make_uint4(hmul2(v[0], s), hmul2(v[1], s), hmul2(v[2], s), hmul2(v[3], s));
+            }
+            if (k == 0 && gb >= kSt) mbar_wait(&kv_empty[st * kTi + m], (gb / kSt - 1) & 1u, abort_flag, err, 0x42);
+            if (has_part) {
+#pragma unroll
+              for (int j0 = 0; j0 < 4; ++j0)
+                *reinterpret_cast<uint4*>(chunk + swz128(row, (part & 1) * 64 + ((part & 2) ? (j0 ^ 2) : j0) * 16)) = o[j0];
             }
           }
           fence_proxy_async_shared();
@@ -353,7 +412,212 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
         if (b + 1 < nb) load(gb + 1);
       }
     }
-  } else if (warp >= 1 && warp <= kKv4Scouts) {
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ softmax and output
+    const int etid = threadIdx.x - 128;
+    const int quarter = warp & 3;                     // tensor-memory lane quarter
+    const int hb = ((warp - 4) >> 2) * kKv4SoftHeads;  // this thread's heads [hb, hb + 16)
+    const int r = quarter * 32 + lane;                // key of the block (score rows) / dim of a tile (output rows)
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    uint32_t gb = 0;
+    int n = 0;
+    uint32_t checks = 0;  // blocks of this CTA whose bounds were checked
+    uint64_t lsum[kKv4SoftHeads / 2];
+    for (int u = unit0; u < units; u += unit_step, ++n) {
+      const int t = u / p.groups;
+      const int h0 = (u % p.groups) * kTcAttnHeads;
+      const int nh = min(kTcAttnHeads, H - h0);
+      mbar_wait(&unit_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x60);
+      const int nb = misc[n & 1];
+      mbar_wait(&q_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x66);  // the q factor
+      const float to_log2 = p.scale * 1.4426950408889634f / __int_as_float(misc[2 + (n & 1)]);
+      if (etid < kTcAttnHeads) max_s[etid] = kKv4NoBound;
+#pragma unroll
+      for (int h = 0; h < kKv4SoftHeads / 2; ++h) lsum[h] = 0ull;
+      named_bar_sync(kTcEpiBar, kKv4SoftThreads);
+      if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
+      for (int b = 0; b < nb; ++b, ++gb) {
+        const uint32_t slot = gb % kKv4Slots;
+        mbar_wait(&ent_full[slot], (gb / kKv4Slots) & 1u, abort_flag, err, 0x65);
+        const float rs = scl_s[slot * kTcAttnKeys + r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ent_empty[slot]);
+        const bool valid = rs > 0.f;
+        const float a = to_log2 * rs;                    // score to log2 units
+        const float lr = valid ? log2f(rs) : -INFINITY;  // a masked key's weight is 0
+        const float inv = valid ? 1.0f / rs : 0.f;
+        const uint64_t a2 = pack_f32x2(a, a), lr2 = pack_f32x2(lr, lr), inv2 = pack_f32x2(inv, inv);
+        const uint32_t s_at = s_tmem + 64 * (gb % kSt) + lane_off + hb;
+        mbar_wait(&s_full[gb % kSt], (gb / kSt) & 1u, abort_flag, err, 0x61);
+        tc_fence_after_sync();
+        float x[kKv4SoftHeads];
+        // exponents relative to the running bounds
+        const auto exponents = [&]() {
+          const uint64_t minus = pack_f32x2(-1.f, -1.f);
+          tmem_ld_x16(s_at, x);
+          tmem_wait_ld_regs16(x);
+#pragma unroll
+          for (int h = 0; h < kKv4SoftHeads; h += 4) {
+            const float4 mv = *reinterpret_cast<const float4*>(max_s + hb + h);
+            unpack_f32x2(fma_f32x2(pack_f32x2(mv.x, mv.y), minus, fma_f32x2(pack_f32x2(x[h], x[h + 1]), a2, lr2)), x[h], x[h + 1]);
+            unpack_f32x2(fma_f32x2(pack_f32x2(mv.z, mv.w), minus, fma_f32x2(pack_f32x2(x[h + 2], x[h + 3]), a2, lr2)), x[h + 2],
+                         x[h + 3]);
+          }
+        };
+        // weights, written into the fp16 row P[key r]; x keeps them
+        const auto weights = [&]() {
+#pragma unroll
+          for (int hh = 0; hh < kKv4SoftHeads; hh += 8) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[hh + 2 * i] = exp2_approx(x[hh + 2 * i]);
+              x[hh + 2 * i + 1] = exp2_approx(x[hh + 2 * i + 1]);
+              const __half2 w = __floats2half2_rn(x[hh + 2 * i], x[hh + 2 * i + 1]);
+              pk[i] = *reinterpret_cast<const uint32_t*>(&w);
+            }
+            *reinterpret_cast<uint4*>(p_s + swz128(r, 2 * (hb + hh))) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+        };
+        // A unit's first block sets the bounds.  After that the weights are formed with the bounds as they are,
+        // while the warps tell one another whether an exponent exceeds its bound by more than 2^8; if one
+        // does, which is rare, the bounds are raised and the weights formed again.
+        bool raise = b == 0;
+        if (!raise) {
+          exponents();
+          float over = x[0];
+#pragma unroll
+          for (int h = 1; h + 1 < kKv4SoftHeads; h += 2) over = max3(over, x[h], x[h + 1]);
+          over = fmaxf(over, x[kKv4SoftHeads - 1]);
+          if (__any_sync(0xffffffffu, over > kTcLazyLog2) && lane == 0) misc[16 + checks % 3] = 1;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(checked);
+          mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x63);  // the previous weighted sum has read P
+          weights();
+          mbar_wait(checked, checks & 1u, abort_flag, err, 0x67);
+          raise = misc[16 + checks % 3] != 0;
+          ++checks;
+          // this flag's next use but one: every warp has read it (two blocks ago), none sets it before the next check
+          if (etid == 0) misc[16 + (checks + 1) % 3] = 0;
+        }
+        if (raise) {
+          // the largest exponents per head across the 128 keys (the reduction consumes x)
+          tmem_ld_x16(s_at, x);
+          tmem_wait_ld_regs16(x);
+#pragma unroll
+          for (int h = 0; h < kKv4SoftHeads; ++h) x[h] = fmaf(x[h], a, lr);
+          xpose_reduce16(x, lane, [](float v, float w) { return fmaxf(v, w); });
+          if ((lane & 1) == 0) red_s[quarter * kTcAttnHeads + hb + (lane >> 1)] = x[0];
+          named_bar_sync(kTcEpiBar, kKv4SoftThreads);
+          if (etid < kTcAttnHeads) {
+            const float bm = fmaxf(fmaxf(red_s[etid], red_s[kTcAttnHeads + etid]),
+                                   fmaxf(red_s[2 * kTcAttnHeads + etid], red_s[3 * kTcAttnHeads + etid]));
+            const float mo = max_s[etid];
+            const float mn = (bm > mo + kTcLazyLog2) ? bm : mo;
+            alpha_s[etid] = (mo == kKv4NoBound || mn == mo) ? 1.f : exp2f(mo - mn);
+            max_s[etid] = mn;
+          }
+          named_bar_sync(kTcEpiBar, kKv4SoftThreads);
+          if (b > 0) {
+            // sums and output accumulators of earlier blocks follow the new bound (this thread: its dim row r
+            // of every tile, its 16 head columns)
+#pragma unroll
+            for (int h = 0; h < kKv4SoftHeads; h += 2)
+              lsum[h / 2] = fma_f32x2(lsum[h / 2], pack_f32x2(alpha_s[hb + h], alpha_s[hb + h + 1]), 0ull);
+            tc_fence_after_sync();
+#pragma unroll 1
+            for (int m = 0; m < kTi; ++m) {
+              tmem_ld_x16(o_tmem + lane_off + 64 * m + hb, x);
+              tmem_wait_ld_regs16(x);
+#pragma unroll
+              for (int j = 0; j < kKv4SoftHeads; ++j) x[j] *= alpha_s[hb + j];
+              tmem_st_x16(o_tmem + lane_off + 64 * m + hb, x);
+            }
+            tmem_wait_st();
+          } else if (gb > 0) {
+            mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x62);
+          }
+          exponents();
+          weights();
+        }
+        fence_proxy_async_shared();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+#pragma unroll
+        for (int h = 0; h < kKv4SoftHeads; h += 2) lsum[h / 2] = fma_f32x2(pack_f32x2(x[h], x[h + 1]), inv2, lsum[h / 2]);
+      }
+      // end of the unit: denominators (partial sums across the 128 keys)
+      {
+        float l[kKv4SoftHeads];
+#pragma unroll
+        for (int h = 0; h < kKv4SoftHeads; h += 2) unpack_f32x2(lsum[h / 2], l[h], l[h + 1]);
+        xpose_reduce16(l, lane, [](float v, float w) { return v + w; });
+        if ((lane & 1) == 0) red_s[quarter * kTcAttnHeads + hb + (lane >> 1)] = l[0];
+      }
+      named_bar_sync(kTcEpiBar, kKv4SoftThreads);
+      if (etid < kTcAttnHeads) {
+        const float l = (red_s[etid] + red_s[kTcAttnHeads + etid]) + (red_s[2 * kTcAttnHeads + etid] + red_s[3 * kTcAttnHeads + etid]);
+        if (shares > 1) {
+          sum_s[etid] = l;
+        } else if (etid < nh) {
+          alpha_s[etid] = softmax_factor(max_s[etid], l, p.sink, h0 + etid,
+                                         p.lse != nullptr ? p.lse + static_cast<int64_t>(t) * H + h0 + etid : nullptr);
+        }
+      }
+      named_bar_sync(kTcEpiBar, kKv4SoftThreads);
+      if (nb > 0) {
+        mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x64);
+        tc_fence_after_sync();
+      }
+      uint16_t* out = p.out + (static_cast<int64_t>(t) * H + h0) * D;
+      const bool row = D >= 128 || quarter < 2;  // (the upper half of a 64-dim row's tile is padding)
+      for (int m = 0; m < kTi; ++m) {
+        float o[kKv4SoftHeads];
+        if (nb > 0 && row) {
+          tmem_ld_x16(o_tmem + lane_off + 64 * m + hb, o);
+          tmem_wait_ld_regs16(o);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kKv4SoftHeads; ++j) o[j] = 0.f;
+        }
+        if (shares > 1) {
+          if (row) {
+#pragma unroll
+            for (int j = 0; j < kKv4SoftHeads; ++j) reinterpret_cast<float*>(kv_s)[(hb + j) * D + 128 * m + r] = o[j];
+          }
+          continue;
+        }
+        // through P's place, as [head pair][dim] words: then 16-byte stores of 8 dims of a head
+        uint32_t* tile = reinterpret_cast<uint32_t*>(p_s);
+#pragma unroll
+        for (int j = 0; j < kKv4SoftHeads; j += 2) {
+          const float2 f = *reinterpret_cast<const float2*>(alpha_s + hb + j);
+          const __nv_bfloat162 w = __floats2bfloat162_rn(o[j] * f.x, o[j + 1] * f.y);
+          tile[(hb + j) / 2 * 128 + r] = *reinterpret_cast<const uint32_t*>(&w);
+        }
+        named_bar_sync(kTcEpiBar, kKv4SoftThreads);
+        {
+          const int pair = etid / 16, d8 = (etid & 15) * 8;
+          const uint4 lo = *reinterpret_cast<const uint4*>(tile + pair * 128 + d8);
+          const uint4 hi = *reinterpret_cast<const uint4*>(tile + pair * 128 + d8 + 4);
+          uint16_t* dst = out + static_cast<int64_t>(2 * pair) * D + 128 * m + d8;
+          if (2 * pair < nh && d8 < D)
+            *reinterpret_cast<uint4*>(dst) = make_uint4(__byte_perm(lo.x, lo.y, 0x5410), __byte_perm(lo.z, lo.w, 0x5410),
+                                                        __byte_perm(hi.x, hi.y, 0x5410), __byte_perm(hi.z, hi.w, 0x5410));
+          if (2 * pair + 1 < nh && d8 < D)
+            *reinterpret_cast<uint4*>(dst + D) = make_uint4(__byte_perm(lo.x, lo.y, 0x7632), __byte_perm(lo.z, lo.w, 0x7632),
+                                                            __byte_perm(hi.x, hi.y, 0x7632), __byte_perm(hi.z, hi.w, 0x7632));
+        }
+        named_bar_sync(kTcEpiBar, kKv4SoftThreads);  // the next tile, or the next unit's P, takes the place
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_empty);
+      named_bar_sync(kTcEpiBar, kKv4SoftThreads);  // alpha_s and max_s are rewritten by the next unit
+    }
+  } else {
+    if (warp >= 1) {
     // ------------------------------------------------------------------ scout
     uint32_t gb = 0;
     int n = 0;
@@ -372,6 +636,12 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
         for (int i = 0; i < 8; ++i)
           if (v[i] >= 0) last = j0 + 32 * i + lane;
         last = __reduce_max_sync(0xffffffffu, last);
+      }
+      if (warp == 2) {  // the unit's q into L2: its loads come when the previous unit's scores are done
+        const int nh = min(kTcAttnHeads, H - (u % p.groups) * kTcAttnHeads);
+        const uint16_t* q = p.q + (static_cast<int64_t>(t) * H + (u % p.groups) * kTcAttnHeads) * D;
+        for (int i = lane; i < nh * (D / 64); i += 32)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + static_cast<int64_t>(i) * 64));
       }
       const int all = (last + kTcAttnKeys) / kTcAttnKeys;
       const int blk0 = first_block(all, share);
@@ -415,7 +685,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
         mbar_arrive(&ent_full[slot]);
       }
     }
-  } else if (warp == 0) {
+    } else {
     // ------------------------------------------------------------------ MMA issuer (the whole warp, one thread elected)
     const uint32_t on = elect_one();
     const auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
@@ -459,10 +729,14 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       __syncwarp();
       if (!wait(&q_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, 0x51)) break;
       if (nb > 0 && !score(gb)) break;
+      if (nb <= 1) mma_commit_if(on, q_empty);  // (after the unit's last score product)
       for (int b = 0; b < nb; ++b, ++gb) {
-        if (kSt > 1 && b + 1 < nb && !score(gb + 1)) {
-          ok = false;
-          break;
+        if (kSt > 1 && b + 1 < nb) {
+          if (!score(gb + 1)) {
+            ok = false;
+            break;
+          }
+          if (b + 2 == nb) mma_commit_if(on, q_empty);
         }
         if (!wait(p_full, gb & 1u, 0x54)) {
           ok = false;
@@ -490,188 +764,19 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
           mma_commit_if(on, &kv_empty[st * kTi + m]);
         }
         mma_commit_if(on, pv_done);
-        if (kSt == 1 && b + 1 < nb && !score(gb + 1)) {
-          ok = false;
-          break;
+        if (kSt == 1 && b + 1 < nb) {
+          if (!score(gb + 1)) {
+            ok = false;
+            break;
+          }
+          if (b + 2 == nb) mma_commit_if(on, q_empty);
         }
       }
-      if (!ok) break;
-      mma_commit_if(on, q_empty);
     }
     // every MMA issued by this thread has completed once `drain` flips
     mma_commit_if(on, drain);
     mbar_wait_drain(drain, 0);
     __syncwarp();
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------------ softmax and output
-    const int etid = threadIdx.x - 128;
-    const int quarter = warp & 3;                     // tensor-memory lane quarter
-    const int hb = ((warp - 4) >> 2) * kTcHalfHeads;  // this thread's heads [hb, hb + 32)
-    const int r = quarter * 32 + lane;                // key of the block (score rows) / dim of a tile (output rows)
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    uint32_t gb = 0;
-    int n = 0;
-    float lsum[kTcHalfHeads];
-    for (int u = unit0; u < units; u += unit_step, ++n) {
-      const int t = u / p.groups;
-      const int h0 = (u % p.groups) * kTcAttnHeads;
-      const int nh = min(kTcAttnHeads, H - h0);
-      mbar_wait(&unit_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x60);
-      const int nb = misc[n & 1];
-      mbar_wait(&q_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x66);  // the q factor
-      const float to_log2 = p.scale * 1.4426950408889634f / __int_as_float(misc[2 + (n & 1)]);
-      if (etid < kTcAttnHeads) max_s[etid] = kKv4NoBound;
-#pragma unroll
-      for (int h = 0; h < kTcHalfHeads; ++h) lsum[h] = 0.f;
-      named_bar_sync(kTcEpiBar, kTcSoftThreads);
-      if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
-      for (int b = 0; b < nb; ++b, ++gb) {
-        const uint32_t slot = gb % kKv4Slots;
-        mbar_wait(&ent_full[slot], (gb / kKv4Slots) & 1u, abort_flag, err, 0x65);
-        const float rs = scl_s[slot * kTcAttnKeys + r];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ent_empty[slot]);
-        const bool valid = rs > 0.f;
-        const float a = to_log2 * rs;                    // score to log2 units
-        const float lr = valid ? log2f(rs) : -INFINITY;  // a masked key's weight is 0
-        const float inv = valid ? 1.0f / rs : 0.f;
-        const uint32_t s_at = s_tmem + 64 * (gb % kSt) + lane_off + hb;
-        mbar_wait(&s_full[gb % kSt], (gb / kSt) & 1u, abort_flag, err, 0x61);
-        tc_fence_after_sync();
-        float x[kTcHalfHeads];
-        // exponents relative to the running bounds
-        const auto exponents = [&]() {
-          tmem_ld_x32_sync(s_at, x);
-#pragma unroll
-          for (int h = 0; h < kTcHalfHeads; h += 4) {
-            const float4 mv = *reinterpret_cast<const float4*>(max_s + hb + h);
-            x[h] = fmaf(x[h], a, lr) - mv.x;
-            x[h + 1] = fmaf(x[h + 1], a, lr) - mv.y;
-            x[h + 2] = fmaf(x[h + 2], a, lr) - mv.z;
-            x[h + 3] = fmaf(x[h + 3], a, lr) - mv.w;
-          }
-        };
-        exponents();
-        // does one exceed its bound by more than 2^8 (or is it a head's first)?
-        float over = x[0];
-#pragma unroll
-        for (int h = 1; h < kTcHalfHeads; ++h) over = fmaxf(over, x[h]);
-        if (bar_or(kTcEpiBar, kTcSoftThreads, over > kTcLazyLog2)) {
-          // the largest exponents per head across the 128 keys (the reduction consumes x)
-          tmem_ld_x32_sync(s_at, x);
-#pragma unroll
-          for (int h = 0; h < kTcHalfHeads; ++h) x[h] = fmaf(x[h], a, lr);
-          xpose_reduce32(x, lane, [](float a2, float c) { return fmaxf(a2, c); });
-          red_s[quarter * kTcAttnHeads + hb + lane] = x[0];
-          named_bar_sync(kTcEpiBar, kTcSoftThreads);
-          if (etid < kTcAttnHeads) {
-            const float bm = fmaxf(fmaxf(red_s[etid], red_s[kTcAttnHeads + etid]),
-                                   fmaxf(red_s[2 * kTcAttnHeads + etid], red_s[3 * kTcAttnHeads + etid]));
-            const float mo = max_s[etid];
-            const float mn = (bm > mo + kTcLazyLog2) ? bm : mo;
-            alpha_s[etid] = (mo == kKv4NoBound || mn == mo) ? 1.f : exp2f(mo - mn);
-            max_s[etid] = mn;
-          }
-          named_bar_sync(kTcEpiBar, kTcSoftThreads);
-          bool rescale = false;
-#pragma unroll
-          for (int h = 0; h < kTcHalfHeads; ++h) {
-            const float al = alpha_s[hb + h];
-            lsum[h] *= al;
-            rescale |= al != 1.f;
-          }
-          // the output accumulators of earlier blocks follow the new bound (this thread: its dim row r
-          // of every tile, its 32 head columns)
-          rescale = bar_or(kTcEpiBar, kTcSoftThreads, rescale);
-          if (b > 0 && rescale) {
-            mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x62);
-            tc_fence_after_sync();
-            for (int m = 0; m < kTi; ++m) {
-#pragma unroll
-              for (int c = 0; c < kTcHalfHeads; c += 16) {
-                float o[16];
-                tmem_ld_x16(o_tmem + lane_off + 64 * m + hb + c, o);
-                tmem_wait_ld_regs16(o);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] *= alpha_s[hb + c + j];
-                tmem_st_x16(o_tmem + lane_off + 64 * m + hb + c, o);
-              }
-            }
-            tmem_wait_st();
-          }
-          exponents();
-        }
-        // weights, written into the fp16 row P[key r] once the previous block's weighted sum has read P
-        if (gb > 0) mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x63);
-#pragma unroll
-        for (int hh = 0; hh < kTcHalfHeads; hh += 8) {
-          uint32_t pk[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float e0 = exp2_approx(x[hh + 2 * i]), e1 = exp2_approx(x[hh + 2 * i + 1]);
-            lsum[hh + 2 * i] = fmaf(e0, inv, lsum[hh + 2 * i]);
-            lsum[hh + 2 * i + 1] = fmaf(e1, inv, lsum[hh + 2 * i + 1]);
-            const __half2 w = __floats2half2_rn(e0, e1);
-            pk[i] = *reinterpret_cast<const uint32_t*>(&w);
-          }
-          *reinterpret_cast<uint4*>(p_s + swz128(r, 2 * (hb + hh))) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        }
-        fence_proxy_async_shared();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
-      }
-      // end of the unit: denominators (partial sums across the 128 keys)
-      xpose_reduce32(lsum, lane, [](float a2, float c) { return a2 + c; });
-      red_s[quarter * kTcAttnHeads + hb + lane] = lsum[0];
-      named_bar_sync(kTcEpiBar, kTcSoftThreads);
-      if (etid < kTcAttnHeads) {
-        const float l = (red_s[etid] + red_s[kTcAttnHeads + etid]) + (red_s[2 * kTcAttnHeads + etid] + red_s[3 * kTcAttnHeads + etid]);
-        if (shares > 1) {
-          sum_s[etid] = l;
-        } else if (etid < nh) {
-          alpha_s[etid] = softmax_factor(max_s[etid], l, p.sink, h0 + etid,
-                                         p.lse != nullptr ? p.lse + static_cast<int64_t>(t) * H + h0 + etid : nullptr);
-        }
-      }
-      named_bar_sync(kTcEpiBar, kTcSoftThreads);
-      if (nb > 0) {
-        mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x64);
-        tc_fence_after_sync();
-      }
-      uint16_t* out = p.out + (static_cast<int64_t>(t) * H + h0) * D;
-      for (int m = 0; m < kTi; ++m) {
-        const int d = 128 * m + r;
-        if (D == 64 && quarter >= 2) break;  // (warp-uniform: the tile's upper half is padding)
-#pragma unroll
-        for (int c = 0; c < kTcHalfHeads; c += 16) {
-          float o[16];
-          if (nb > 0) {
-            tmem_ld_x16(o_tmem + lane_off + 64 * m + hb + c, o);
-            tmem_wait_ld_regs16(o);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = 0.f;
-          }
-          if (shares > 1) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) reinterpret_cast<float*>(kv_s)[(hb + c + j) * D + d] = o[j];
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int h = hb + c + j;
-              if (h < nh) {
-                const __nv_bfloat16 ob = __float2bfloat16_rn(o[j] * alpha_s[h]);
-                out[static_cast<int64_t>(h) * D + d] = *reinterpret_cast<const uint16_t*>(&ob);
-              }
-            }
-          }
-        }
-      }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(o_empty);
-      named_bar_sync(kTcEpiBar, kTcSoftThreads);  // alpha_s and max_s are rewritten by the next unit
     }
   }
 
