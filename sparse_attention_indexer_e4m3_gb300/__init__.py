@@ -1,7 +1,7 @@
 """GB300-native FP8 lightning indexer and exact top-k selector.
 
 Python binding of the C ABI in ``include/dsa.h`` (library ``libdsa_gb300.so``, built in-tree by
-``sparse_attention_indexer_e4m3_gb300.build``).  This module only marshals arguments: it checks
+``sparse_attention_indexer_e4m3_gb300.build``; the 4-bit cache's calls marshal natively, ``_marshal.so``).  This module only marshals arguments: it checks
 torch tensors, passes their device pointers and the current CUDA stream, and raises
 ``DsaError`` on a non-OK status.  Every step of the computation runs in the library's kernels;
 there is no fallback path.  If the library has not been built, every call raises.
@@ -12,6 +12,7 @@ there is no fallback path.  If the library has not been built, every call raises
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 
@@ -91,24 +92,10 @@ def load():
             lib.dsa_sparse_attn.restype = i
             lib.dsa_kv4_page_bytes.argtypes = [i, i]
             lib.dsa_kv4_page_bytes.restype = sz
-            lib.dsa_quantize_kv4.argtypes = [p, p, p, i, i, p, i, i, p, i, i, p]
-            lib.dsa_quantize_kv4.restype = i
-            lib.dsa_dequantize_kv4.argtypes = [p, i, i, p, i, i, p, p, i, i, p, p]
-            lib.dsa_dequantize_kv4.restype = i
-            lib.dsa_sparse_attn_kv4.argtypes = [p, p, i, i, p, i, i, p, p, p, p, i, i, i, i, ctypes.c_float, p, p, p]
-            lib.dsa_sparse_attn_kv4.restype = i
-            lib.dsa_fork_pages.argtypes = [p, p, i, i, i, p, p, p]
-            lib.dsa_fork_pages.restype = i
             lib.dsa_reserve_pages_workspace_size.argtypes = [i]
             lib.dsa_reserve_pages_workspace_size.restype = sz
-            lib.dsa_reserve_pages.argtypes = [p, p, p, p, i, i, i, i, p, p, p, p, sz, p]
-            lib.dsa_reserve_pages.restype = i
             lib.dsa_compact_pages_workspace_size.argtypes = [i]
             lib.dsa_compact_pages_workspace_size.restype = sz
-            lib.dsa_compact_pages.argtypes = [p, p, i, i, i, p, p, p, p, sz, p]
-            lib.dsa_compact_pages.restype = i
-            lib.dsa_copy_pages.argtypes = [p, sz, i, p, p, i, p]
-            lib.dsa_copy_pages.restype = i
             lib.dsa_check_bounded_wait.argtypes = [p, p]
             lib.dsa_check_bounded_wait.restype = i
             lib.dsa_status_string.argtypes = [i]
@@ -442,85 +429,38 @@ def kv4_page_bytes(page_rows: int, D: int) -> int:
     return int(load().dsa_kv4_page_bytes(page_rows, D))
 
 
-def _new(shape, dtype, like, stream):
-    """An output or workspace on like's device; kept for `stream` where the call runs on another
-    stream than the current one (the allocator would otherwise hand it out again too early)."""
-    t = _torch().empty(shape, dtype=dtype, device=like.device)
-    if stream is not None and t.is_cuda:
-        t.record_stream(stream)
-    return t
+_calls = None  # the module _marshal, once loaded and bound
 
 
-def _on_current_device(*tensors):
-    """Raise unless every tensor given lies on the current CUDA device, on which the call launches."""
-    now = -1
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d != now and d >= 0:
-                if now < 0:
-                    now = _torch()._C._cuda_getDevice()
-                if d != now:
-                    raise ValueError("tensors must be on the current CUDA device")
-
-
-def _pool(cache, table, D: int):
-    """Checked cache [P, page bytes] and table [R, M]: (cache, table, P, page_rows, R, M)."""
-    torch = _torch()
-    cache = _dev(cache, "cache", (torch.uint8,))
-    table = _dev(table, "table", (torch.int32,))
-    if cache.dim() != 2 or table.dim() != 2:
-        raise ValueError("cache must be [P, page bytes] and table [R, M]")
-    if D not in SUPPORTED_KV4_D:
-        raise ValueError(f"D must be one of {SUPPORTED_KV4_D}")
-    row = D // 2 + D // 16 + 4
-    rows = cache.shape[1] // row
-    if cache.shape[1] != rows * row or rows < 16 or rows > 256 or rows & (rows - 1):
-        raise ValueError(f"cache pages of {cache.shape[1]} bytes hold no power of two in [16, 256] of rows of D = {D}")
-    return cache, table, cache.shape[0], rows, table.shape[0], table.shape[1]
-
-
-def _places(seq, pos, n: int):
-    torch = _torch()
-    seq = _dev(seq, "seq", (torch.int32,))
-    pos = _dev(pos, "pos", (torch.int32,))
-    _shape(seq, "seq", (n,))
-    _shape(pos, "pos", (n,))
-    return seq, pos
+def _native():
+    """The native argument marshalling of the calls below, bound to the loaded library."""
+    global _calls
+    if _calls is None:
+        lib, torch = load(), _torch()
+        path = os.path.join(_HERE, "_marshal.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m sparse_attention_indexer_e4m3_gb300.build`")
+        m = importlib.import_module(__name__ + "._marshal")
+        if m.torch_version != torch.__version__.split("+")[0]:
+            raise RuntimeError(f"_marshal.so was built for torch {m.torch_version}, not {torch.__version__}: build it again")
+        names = ("quantize_kv4", "dequantize_kv4", "sparse_attn_kv4", "fork_pages", "reserve_pages",
+                 "reserve_pages_workspace_size", "compact_pages", "compact_pages_workspace_size", "copy_pages")
+        m.bind(tuple(ctypes.cast(getattr(lib, "dsa_" + n), ctypes.c_void_p).value for n in names), DsaError)
+        _calls = m
+    return _calls
 
 
 def quantize_kv4(kv, cache, table, seq, pos, stream=None):
     """Write bf16 rows kv [N, D] in 4 bits into the paged cache (uint8 [P, kv4_page_bytes]): row i as
     row pos[i] of sequence seq[i], whose pages are table[seq[i]] (int32 [R, M], -1 = none); rows
     whose place is not mapped are left out.  Returns cache."""
-    torch = _torch()
-    kv = _dev(kv, "kv", (torch.bfloat16,))
-    if kv.dim() != 2:
-        raise ValueError("kv must be [N, D]")
-    N, D = kv.shape
-    cache, table, P, rows, R, M = _pool(cache, table, D)
-    seq, pos = _places(seq, pos, N)
-    _on_current_device(kv, cache, table, seq, pos)
-    _check(load().dsa_quantize_kv4(kv.data_ptr(), seq.data_ptr(), pos.data_ptr(), N, D, cache.data_ptr(), P, rows,
-                                   table.data_ptr(), R, M, _stream_ptr(stream)), "dsa_quantize_kv4")
-    return cache
+    return (_calls or _native()).quantize_kv4(kv, cache, table, seq, pos, stream)
 
 
 def dequantize_kv4(cache, table, seq, pos, D: int, out=None, stream=None):
     """Rows pos[i] of sequences seq[i] of the 4-bit paged cache as bf16 [N, D] (zeros where no page is
     mapped)."""
-    torch = _torch()
-    cache, table, P, rows, R, M = _pool(cache, table, D)
-    N = seq.shape[0] if seq.dim() == 1 else -1
-    seq, pos = _places(seq, pos, N)
-    if out is None:
-        out = _new((N, D), torch.bfloat16, cache, stream)
-    out = _dev(out, "out", (torch.bfloat16,))
-    _shape(out, "out", (N, D))
-    _on_current_device(cache, table, seq, pos, out)
-    _check(load().dsa_dequantize_kv4(cache.data_ptr(), P, rows, table.data_ptr(), R, M, seq.data_ptr(), pos.data_ptr(),
-                                     N, D, out.data_ptr(), _stream_ptr(stream)), "dsa_dequantize_kv4")
-    return out
+    return (_calls or _native()).dequantize_kv4(cache, table, seq, pos, D, out, stream)
 
 
 def sparse_attn_kv4(q, cache, table, seq, idx, start=None, attn_sink=None, scale=None, out=None, lse=None, stream=None):
@@ -528,83 +468,13 @@ def sparse_attn_kv4(q, cache, table, seq, idx, start=None, attn_sink=None, scale
     naming row v - start[t] of sequence seq[t] (start int32 [T], default 0; negative or unmapped entries
     are skipped); attn_sink fp32 [H] or None, scale default 1 / sqrt(D).  Returns bf16 [T, H, D]; with
     lse (fp32 [T, H]) given, also writes the natural log of each softmax denominator into it."""
-    torch = _torch()
-    q = _dev(q, "q", (torch.bfloat16,))
-    idx = _dev(idx, "idx", (torch.int32,))
-    if q.dim() != 3 or idx.dim() != 2 or idx.shape[0] != q.shape[0]:
-        raise ValueError("shapes: q [T, H, D], idx [T, K]")
-    T, H, D = q.shape
-    cache, table, P, rows, R, M = _pool(cache, table, D)
-    seq = _dev(seq, "seq", (torch.int32,))
-    _shape(seq, "seq", (T,))
-    if start is not None:
-        start = _dev(start, "start", (torch.int32,))
-        _shape(start, "start", (T,))
-    if attn_sink is not None:
-        attn_sink = _dev(attn_sink, "attn_sink", (torch.float32,))
-        _shape(attn_sink, "attn_sink", (H,))
-    if out is None:
-        out = _new((T, H, D), torch.bfloat16, q, stream)
-    out = _dev(out, "out", (torch.bfloat16,))
-    _shape(out, "out", (T, H, D))
-    if lse is not None:
-        lse = _dev(lse, "lse", (torch.float32,))
-        _shape(lse, "lse", (T, H))
-    _on_current_device(q, cache, table, seq, idx, start, attn_sink, out, lse)
-    sc = float(scale) if scale is not None else 1.0 / float(D) ** 0.5
-    _check(load().dsa_sparse_attn_kv4(q.data_ptr(), cache.data_ptr(), P, rows, table.data_ptr(), R, M, seq.data_ptr(),
-                                      None if start is None else start.data_ptr(),
-                                      None if attn_sink is None else attn_sink.data_ptr(), idx.data_ptr(), T, H, D,
-                                      idx.shape[1], sc, out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                      _stream_ptr(stream)), "dsa_sparse_attn_kv4")
-    return out
-
-
-def _tables(table, ref):
-    torch = _torch()
-    table = _dev(table, "table", (torch.int32,))
-    ref = _dev(ref, "ref", (torch.int32,))
-    if table.dim() != 2 or ref.dim() != 1:
-        raise ValueError("table must be [R, M] and ref [P]")
-    return table, ref, table.shape[0], table.shape[1], ref.shape[0]
-
-
-def _lists(n, src, dst, one, name, scratch_ints, workspace, like, stream):
-    """The outputs src [n], dst [n] and one [1] and the workspace of a page call: the caller's where given,
-    else views of one new allocation."""
-    torch = _torch()
-    if src is not None or dst is not None or one is not None or workspace is not None:
-        i32 = (torch.int32,)
-        src = _dev(_new((n,), torch.int32, like, stream) if src is None else src, "src", i32)
-        dst = _dev(_new((n,), torch.int32, like, stream) if dst is None else dst, "dst", i32)
-        one = _dev(_new((1,), torch.int32, like, stream) if one is None else one, name, i32)
-        if workspace is None:
-            workspace = _new((4 * scratch_ints,), torch.uint8, like, stream)
-        workspace = _dev(workspace, "workspace", (torch.uint8,))
-        _shape(src, "src", (n,))
-        _shape(dst, "dst", (n,))
-        _shape(one, name, (1,))
-        _on_current_device(src, dst, one, workspace)
-        return src, dst, one, workspace.data_ptr(), workspace.numel()
-    src, dst, one, ws = _new((2 * n + 1 + scratch_ints,), torch.int32, like, stream).split_with_sizes((n, n, 1, scratch_ints))
-    return src, dst, one, ws.data_ptr(), 4 * scratch_ints
+    return (_calls or _native()).sparse_attn_kv4(q, cache, table, seq, idx, start, attn_sink, scale, out, lse, stream)
 
 
 def fork_pages(table, parent, ref, table_out=None, stream=None):
     """New page table (int32 [R, M]) whose row r is table[parent[r]] (-1: the row is freed); the page
     counts ref (int32 [P]) follow in place.  table_out must not overlap table."""
-    torch = _torch()
-    table, ref, R, M, P = _tables(table, ref)
-    parent = _dev(parent, "parent", (torch.int32,))
-    _shape(parent, "parent", (R,))
-    if table_out is None:
-        table_out = _new((R, M), torch.int32, table, stream)
-    table_out = _dev(table_out, "table_out", (torch.int32,))
-    _shape(table_out, "table_out", (R, M))
-    _on_current_device(table, parent, ref, table_out)
-    _check(load().dsa_fork_pages(table.data_ptr(), parent.data_ptr(), R, M, P, ref.data_ptr(), table_out.data_ptr(),
-                                 _stream_ptr(stream)), "dsa_fork_pages")
-    return table_out
+    return (_calls or _native()).fork_pages(table, parent, ref, table_out, stream)
 
 
 def reserve_pages_workspace_size(P: int) -> int:
@@ -616,18 +486,7 @@ def reserve_pages(table, ref, begin, end, page_rows: int, src=None, dst=None, la
     the sequence a page of its own where one is shared (table and ref in place).  Returns (src, dst, lacking):
     copy_pages(cache, src, dst) brings along what the replaced pages hold (int32 [2 R], -1 = none), and
     lacking (int32 [1]) is 0 or by how many pages the pool falls short (then nothing changed)."""
-    torch = _torch()
-    table, ref, R, M, P = _tables(table, ref)
-    begin = _dev(begin, "begin", (torch.int32,))
-    end = _dev(end, "end", (torch.int32,))
-    _shape(begin, "begin", (R,))
-    _shape(end, "end", (R,))
-    _on_current_device(table, ref, begin, end)
-    src, dst, lacking, ws, nws = _lists(2 * R, src, dst, lacking, "lacking", 2 * P, workspace, table, stream)
-    _check(load().dsa_reserve_pages(table.data_ptr(), ref.data_ptr(), begin.data_ptr(), end.data_ptr(), R, M, P, page_rows,
-                                    src.data_ptr(), dst.data_ptr(), lacking.data_ptr(), ws, nws,
-                                    _stream_ptr(stream)), "dsa_reserve_pages")
-    return src, dst, lacking
+    return (_calls or _native()).reserve_pages(table, ref, begin, end, page_rows, src, dst, lacking, workspace, stream)
 
 
 def compact_pages_workspace_size(P: int) -> int:
@@ -637,32 +496,13 @@ def compact_pages_workspace_size(P: int) -> int:
 def compact_pages(table, ref, src=None, dst=None, n_live=None, workspace=None, stream=None):
     """Rename the pages in use to the lowest ones (table and ref in place).  Returns (src, dst, n_live):
     copy_pages(cache, src, dst) moves the rows (int32 [P // 2], -1 = none); n_live (int32 [1]) pages are in use."""
-    table, ref, R, M, P = _tables(table, ref)
-    _on_current_device(table, ref)
-    src, dst, n_live, ws, nws = _lists(P // 2, src, dst, n_live, "n_live", P, workspace, table, stream)
-    _check(load().dsa_compact_pages(table.data_ptr(), ref.data_ptr(), R, M, P, src.data_ptr(), dst.data_ptr(),
-                                    n_live.data_ptr(), ws, nws, _stream_ptr(stream)),
-           "dsa_compact_pages")
-    return src, dst, n_live
+    return (_calls or _native()).compact_pages(table, ref, src, dst, n_live, workspace, stream)
 
 
 def copy_pages(pages, src, dst, stream=None):
     """pages[dst[i]] = pages[src[i]] in place for the entries whose two ids name pages (src, dst int32 [n]);
     pages is any contiguous tensor [P, ...] whose pages take a multiple of 16 bytes.  Returns pages."""
-    torch = _torch()
-    pages = _dev(pages, "pages", (pages.dtype,) if isinstance(pages, torch.Tensor) else ())
-    src = _dev(src, "src", (torch.int32,))
-    dst = _dev(dst, "dst", (torch.int32,))
-    if pages.dim() < 2 or src.dim() != 1:
-        raise ValueError("shapes: pages [P, ...], src [n], dst [n]")
-    _shape(dst, "dst", tuple(src.shape))
-    P = pages.shape[0]
-    if P == 0:
-        return pages
-    _on_current_device(pages, src, dst)
-    _check(load().dsa_copy_pages(pages.data_ptr(), pages.numel() // P * pages.element_size(), P, src.data_ptr(),
-                                 dst.data_ptr(), src.shape[0], _stream_ptr(stream)), "dsa_copy_pages")
-    return pages
+    return (_calls or _native()).copy_pages(pages, src, dst, stream)
 
 
 def check_bounded_wait(stream=None):

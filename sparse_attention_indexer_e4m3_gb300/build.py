@@ -1,4 +1,5 @@
-"""Builds the CUDA library libdsa_gb300.so in-tree for sm_103a (GB300).
+"""Builds the CUDA library libdsa_gb300.so in-tree for sm_103a (GB300), and the native argument
+marshalling _marshal.so of the 4-bit cache's calls against the installed torch (g++).
 
 Plain nvcc, no CMake: each translation unit under csrc/ compiles in parallel to an object,
 then one shared library is linked.  The CUDA runtime is linked statically, so the library
@@ -7,10 +8,12 @@ depends only on the driver.  Usage: ``python -m sparse_attention_indexer_e4m3_gb
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -18,6 +21,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libdsa_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+MARSHAL_PATH = os.path.join(HERE, "_marshal.so")
 
 SOURCES = ["dsa_api.cu", "index_d128.cu", "index_d64.cu", "kres_d128.cu", "kres_d64.cu", "select_kernels.cu", "attn.cu", "attn_bwd.cu", "attn_kv4.cu", "kv4.cu",
            "kv4_api.cu"]
@@ -41,10 +45,26 @@ def _deps() -> list[str]:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not (os.path.exists(LIB_PATH) and os.path.exists(MARSHAL_PATH)):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(MARSHAL_PATH))
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _compile_marshal(cc: str) -> None:
+    """g++ of marshal.cpp against the installed torch's headers and libraries."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")
+    tmp = MARSHAL_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
+           "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", cuda, os.path.join(CSRC, "marshal.cpp"), "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
@@ -67,8 +87,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(_compile_marshal, cc)
         objs = list(ex.map(compile_one, SOURCES))
+        marshal.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -2,6 +2,9 @@
 // with the others).
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <cstdint>
+
 #include "attn_kv4_kernel.cuh"
 #include "launch.h"
 
@@ -12,8 +15,16 @@ namespace {
 template <int D>
 cudaError_t launch_d(int grid, int shares, const AttnKv4Params& p, unsigned* err, cudaStream_t stream) {
   constexpr int smem = AttnKv4Layout<D>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(sparse_attn_kv4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // once per device (setting it again, from another thread too, changes nothing)
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(set.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(sparse_attn_kv4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(static_cast<unsigned>(grid));
   c.blockDim = dim3(kKv4Threads);

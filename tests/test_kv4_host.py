@@ -1,6 +1,6 @@
 """The 4-bit paged cache without a GPU: the reference of its tests against hand-made values and torch's
-e4m3, the C ABI's synchronous refusals, and the binding's checks of arguments (the library replaced by a
-stub, CPU tensors standing in for device ones)."""
+e4m3, the C ABI's synchronous refusals, and the binding's checks of arguments on CPU tensors, which get as far as the
+device check."""
 import ctypes
 
 import numpy as np
@@ -56,7 +56,17 @@ def lib():
     from sparse_attention_indexer_e4m3_gb300 import build
 
     build.build()
-    return dsa.load()
+    lib = ctypes.CDLL(dsa.library_path())
+    p, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    lib.dsa_quantize_kv4.argtypes = [p, p, p, i, i, p, i, i, p, i, i, p]
+    lib.dsa_dequantize_kv4.argtypes = [p, i, i, p, i, i, p, p, i, i, p, p]
+    lib.dsa_sparse_attn_kv4.argtypes = [p, p, i, i, p, i, i, p, p, p, p, i, i, i, i, ctypes.c_float, p, p, p]
+    lib.dsa_fork_pages.argtypes = [p, p, i, i, i, p, p, p]
+    lib.dsa_reserve_pages.argtypes = [p, p, p, p, i, i, i, i, p, p, p, p, sz, p]
+    lib.dsa_reserve_pages_workspace_size.restype = lib.dsa_compact_pages_workspace_size.restype = sz
+    lib.dsa_compact_pages.argtypes = [p, p, i, i, i, p, p, p, p, sz, p]
+    lib.dsa_copy_pages.argtypes = [p, sz, i, p, p, i, p]
+    return lib
 
 
 @pytest.fixture(scope="module")
@@ -142,29 +152,6 @@ T, H, D, K, P, B, R, M = 6, 5, 128, 7, 9, 32, 3, 4
 i32, bf16 = torch.int32, torch.bfloat16
 
 
-@pytest.fixture()
-def stub(monkeypatch):
-    calls = []
-
-    class Lib:
-        def __getattr__(self, name):
-            return lambda *args: calls.append(name) or 0
-
-    def dev(t, name, dtypes):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(name)
-        if t.dtype not in dtypes:
-            raise TypeError(name)
-        if not t.is_contiguous():
-            raise ValueError(name)
-        return t
-
-    monkeypatch.setattr(dsa, "load", lambda: Lib())
-    monkeypatch.setattr(dsa, "_dev", dev)
-    monkeypatch.setattr(dsa, "_stream_ptr", lambda s: 0)
-    return calls
-
-
 def z(*shape, t=i32):
     return torch.zeros(shape, dtype=t)
 
@@ -172,20 +159,20 @@ def z(*shape, t=i32):
 CACHE = lambda: z(P, K4.page_bytes(B, D), t=torch.uint8)  # noqa: E731
 
 
-def test_binding_reaches_the_library(stub):
-    dsa.quantize_kv4(z(T, D, t=bf16), CACHE(), z(R, M), z(T), z(T))
-    assert dsa.dequantize_kv4(CACHE(), z(R, M), z(T), z(T), D).shape == (T, D)
-    out = dsa.sparse_attn_kv4(z(T, H, D, t=bf16), CACHE(), z(R, M), z(T), z(T, K), start=z(T), attn_sink=torch.zeros(H),
-                              lse=torch.zeros(T, H))
-    assert out.shape == (T, H, D)
-    assert dsa.fork_pages(z(R, M), z(R), z(P)).shape == (R, M)
-    src, dst, lack = dsa.reserve_pages(z(R, M), z(P), z(R), z(R), B)
-    assert src.shape == dst.shape == (2 * R,) and lack.shape == (1,)
-    src, dst, n = dsa.compact_pages(z(R, M), z(P))
-    assert src.shape == dst.shape == (P // 2,) and n.shape == (1,)
-    dsa.copy_pages(torch.zeros(P, 4, 4), z(3), z(3))
-    assert stub == ["dsa_quantize_kv4", "dsa_dequantize_kv4", "dsa_sparse_attn_kv4", "dsa_fork_pages", "dsa_reserve_pages",
-                    "dsa_compact_pages", "dsa_copy_pages"]
+@pytest.mark.parametrize("call", [
+    lambda: dsa.quantize_kv4(z(T, D, t=bf16), CACHE(), z(R, M), z(T), z(T)),
+    lambda: dsa.dequantize_kv4(CACHE(), z(R, M), z(T), z(T), D, out=z(T, D, t=bf16)),
+    lambda: dsa.sparse_attn_kv4(z(T, H, D, t=bf16), CACHE(), z(R, M), z(T), z(T, K), start=z(T), attn_sink=torch.zeros(H),
+                                lse=torch.zeros(T, H), out=z(T, H, D, t=bf16)),
+    lambda: dsa.fork_pages(z(R, M), z(R), z(P), table_out=z(R, M)),
+    lambda: dsa.reserve_pages(z(R, M), z(P), z(R), z(R), B, src=z(2 * R), dst=z(2 * R), lacking=z(1), workspace=z(99, t=torch.uint8)),
+    lambda: dsa.compact_pages(z(R, M), z(P), src=z(P // 2), dst=z(P // 2), n_live=z(1), workspace=z(99, t=torch.uint8)),
+    lambda: dsa.copy_pages(torch.zeros(P, 4, 4), z(3), z(3)),
+])
+def test_binding_accepts_shapes_and_wants_cuda(lib, call):
+    """Arguments that are right in every other respect get as far as the device check."""
+    with pytest.raises(ValueError, match="CUDA"):
+        call()
 
 
 @pytest.mark.parametrize("call", [
@@ -223,7 +210,18 @@ def test_binding_reaches_the_library(stub):
     lambda: dsa.copy_pages(CACHE(), z(3, t=torch.int64), z(3)),
     lambda: dsa.copy_pages(CACHE()[:, ::2], z(3), z(3)),
 ])
-def test_binding_refuses(stub, call):
-    with pytest.raises((ValueError, TypeError)):
+def test_binding_refuses(lib, call):
+    with pytest.raises((ValueError, TypeError)) as e:
         call()
-    assert stub == []  # nothing reached the library
+    assert "CUDA" not in str(e.value)  # refused for what is wrong, before the device is looked at
+
+
+def test_binding_refuses_what_is_no_tensor(lib):
+    with pytest.raises(TypeError):
+        dsa.quantize_kv4([1.0], CACHE(), z(R, M), z(T), z(T))
+    with pytest.raises(TypeError):
+        dsa.copy_pages(None, z(3), z(3))
+    with pytest.raises(TypeError):
+        dsa.reserve_pages(z(R, M), z(P), z(R), z(R), "64")
+    with pytest.raises(TypeError):
+        dsa.sparse_attn_kv4(z(T, H, D, t=bf16), CACHE(), z(R, M), z(T), z(T, K), scale="1")
