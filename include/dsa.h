@@ -318,7 +318,7 @@ DSA_API size_t dsa_kv4_page_bytes(int page_rows, int D);
  *     c_d = x_d / (r s_g) to the nearest e2m1 value, ties to even, beyond 6 to 6; 0 where s_g is 0
  * each rounding that of the exact quotient (-0 codes keep the sign of x_d).
  *
- *   kv         bf16 (uint16 bits) [N][D], finite values; 16-byte aligned
+ *   kv         bf16 (uint16 bits) [N][D], finite values; 32-byte aligned
  *   seq, pos   int32 [N]; the same place at most once (else the rows may end up mixed)
  */
 DSA_API dsa_status dsa_quantize_kv4(const uint16_t* kv, const int32_t* seq, const int32_t* pos, int N, int D,
@@ -329,7 +329,7 @@ DSA_API dsa_status dsa_quantize_kv4(const uint16_t* kv, const int32_t* seq, cons
  * dsa_dequantize_kv4 -- row pos[i] of sequence seq[i] as bf16: r s c, exact for rows that
  * dsa_quantize_kv4 wrote (otherwise rounded to the nearest bf16; next to the largest bf16 a scale that was
  * rounded up can take values past it, which come back as infinities).  A place that is not mapped gives zeros.
- *   kv   bf16 (uint16 bits) [N][D]   OUTPUT, 16-byte aligned
+ *   kv   bf16 (uint16 bits) [N][D]   OUTPUT, 32-byte aligned
  */
 DSA_API dsa_status dsa_dequantize_kv4(const uint8_t* cache, int P, int page_rows, const int32_t* table, int R, int M,
                                       const int32_t* seq, const int32_t* pos, int N, int D, uint16_t* kv,

@@ -12,9 +12,8 @@ namespace dsa {
 namespace {
 
 template <int D>
-int codec_grid(int N) {
-  const int64_t rows_per_cta = static_cast<int64_t>(kKv4CodecThreads / 32) * (32 / (D / kKv4Group)) * kRowSets;
-  return static_cast<int>(std::min<int64_t>((N + rows_per_cta - 1) / rows_per_cta, 1 << 20));
+unsigned codec_grid(int N) {
+  return static_cast<unsigned>((static_cast<int64_t>(N) * (D / kKv4Group) + kKv4CodecThreads - 1) / kKv4CodecThreads);
 }
 
 }  // namespace

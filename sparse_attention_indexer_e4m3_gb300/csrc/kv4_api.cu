@@ -57,7 +57,7 @@ dsa_status dsa_quantize_kv4(const uint16_t* kv, const int32_t* seq, const int32_
   if (st != DSA_OK) return st;
   if (N < 0) return DSA_ERR_INVALID_ARG;
   if (N == 0) return DSA_OK;
-  if (!kv || !aligned(kv, 16) || !seq || !aligned(seq, 4) || !pos || !aligned(pos, 4)) return DSA_ERR_INVALID_ARG;
+  if (!kv || !aligned(kv, 32) || !seq || !aligned(seq, 4) || !pos || !aligned(pos, 4)) return DSA_ERR_INVALID_ARG;
   return done(launch_kv4_write(D, kv, N, seq, pos, c, static_cast<cudaStream_t>(stream)));
 }
 
@@ -68,7 +68,7 @@ dsa_status dsa_dequantize_kv4(const uint8_t* cache, int P, int page_rows, const 
   if (st != DSA_OK) return st;
   if (N < 0) return DSA_ERR_INVALID_ARG;
   if (N == 0) return DSA_OK;
-  if (!kv || !aligned(kv, 16) || !seq || !aligned(seq, 4) || !pos || !aligned(pos, 4)) return DSA_ERR_INVALID_ARG;
+  if (!kv || !aligned(kv, 32) || !seq || !aligned(seq, 4) || !pos || !aligned(pos, 4)) return DSA_ERR_INVALID_ARG;
   return done(launch_kv4_read(D, kv, N, seq, pos, c, static_cast<cudaStream_t>(stream)));
 }
 

@@ -92,6 +92,7 @@ struct Where {
 
   // A new tensor, kept for the stream where that is not the one it is allocated for.
   at::Tensor make(at::IntArrayRef sizes, at::ScalarType type) const {
+    const at::AutoDispatchBelowADInplaceOrView below;  // nothing here is differentiated
     at::Tensor t = at::empty(sizes, at::TensorOptions().dtype(type).device(c10::Device(c10::DeviceType::CUDA, device)));
     if (given) t.record_stream(c10::cuda::getStreamFromExternal(stream, device).unwrap());
     return t;
@@ -253,8 +254,7 @@ PyObject* fork_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// The outputs src [n], dst [n] and one [1] and the workspace of a page call: the caller's where given, the others
-// views of one new allocation.
+// The outputs src [n], dst [n] and one [1] and the workspace of a page call: the caller's where given.
 struct Lists {
   at::Tensor src, dst, one, ws;
   void* workspace = nullptr;
@@ -268,26 +268,15 @@ struct Lists {
   }
   const at::Tensor* given(const at::Tensor& t) const { return t.defined() ? &t : nullptr; }
   void fill(const Where& w, int64_t n, size_t need) {
-    const int64_t ints = (src.defined() ? 0 : n) + (dst.defined() ? 0 : n) + (one.defined() ? 0 : 1);
+    // one allocation for what is left out, the workspace last
     const int64_t scratch = ws.defined() ? 0 : static_cast<int64_t>((need + 3) / 4);
-    int64_t at = 0;
-    at::Tensor all;
-    if (ints + scratch > 0) all = w.make({ints + scratch}, at::kInt);
-    const auto take = [&](at::Tensor& t, int64_t k) {
-      if (t.defined()) return;
-      t = all.narrow(0, at, k);
-      at += k;
-    };
-    take(src, n);
-    take(dst, n);
-    take(one, 1);
-    if (ws.defined()) {
-      workspace = ws.data_ptr();
-      workspace_bytes = static_cast<size_t>(ws.numel());
-    } else if (scratch > 0) {
-      workspace = ptr<int32_t>(all) + at;
-      workspace_bytes = static_cast<size_t>(scratch) * 4;
-    }
+    const at::Tensor all = w.make({2 * n + 1 + scratch}, at::kInt);
+    const at::AutoDispatchBelowADInplaceOrView below;
+    if (!src.defined()) src = all.as_strided({n}, {1}, 0);
+    if (!dst.defined()) dst = all.as_strided({n}, {1}, n);
+    if (!one.defined()) one = all.as_strided({1}, {1}, 2 * n);
+    workspace = ws.defined() ? ws.data_ptr() : (need > 0 ? ptr<int32_t>(all) + 2 * n + 1 : nullptr);
+    workspace_bytes = ws.defined() ? static_cast<size_t>(ws.numel()) : static_cast<size_t>(scratch) * 4;
   }
   PyObject* result(PyObject* const* a) const {
     PyObject* r = PyTuple_New(3);
