@@ -350,12 +350,17 @@ DSA_API dsa_status dsa_dequantize_kv4(const uint8_t* cache, int P, int page_rows
  *   attn_sink  float [H] or NULL;  idx  int32 [T][K];  scale  softmax scale
  *   out        bf16 [T][H][D], 16-byte aligned   OUTPUT
  *   lse        float [T][H] or NULL   OUTPUT, as dsa_sparse_attn's
- * H >= 1.  No workspace; deterministic.
+ *   workspace  dsa_sparse_attn_kv4_workspace_size(T, H, D, K) bytes, 16-byte aligned (may be NULL when that is 0:
+ *              with as many tokens and head groups of 64 as SMs); its contents on entry do not matter; two calls
+ *              running at the same time must not share it.  DSA_ERR_WORKSPACE if it is missing, short or misaligned
+ * H >= 1.  Deterministic.
  */
+DSA_API size_t dsa_sparse_attn_kv4_workspace_size(int T, int H, int D, int K);
 DSA_API dsa_status dsa_sparse_attn_kv4(const uint16_t* q, const uint8_t* cache, int P, int page_rows,
                                        const int32_t* table, int R, int M, const int32_t* seq, const int32_t* start,
                                        const float* attn_sink, const int32_t* idx, int T, int H, int D, int K,
-                                       float scale, uint16_t* out, float* lse, void* stream);
+                                       float scale, uint16_t* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, void* stream);
 
 /*
  * The page calls share one state: a table [R][M] as above and ref int32 [P], the number of table entries

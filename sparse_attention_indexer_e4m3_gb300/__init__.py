@@ -20,7 +20,7 @@ __all__ = [
     "DsaError", "library_path", "load", "index_score", "index_score_kres", "index_score_kres_workspace_size", "topk",
     "index_topk", "index_topk_plan", "index_topk_run", "topk_workspace_size",
     "index_topk_workspace_size", "get_device_error", "status_string", "version", "MAX_TOPK", "SUPPORTED_H",
-    "SUPPORTED_D", "kv4_page_bytes", "quantize_kv4", "dequantize_kv4", "sparse_attn_kv4", "fork_pages", "reserve_pages",
+    "SUPPORTED_D", "kv4_page_bytes", "quantize_kv4", "dequantize_kv4", "sparse_attn_kv4", "sparse_attn_kv4_workspace_size", "fork_pages", "reserve_pages",
     "reserve_pages_workspace_size", "compact_pages", "compact_pages_workspace_size", "copy_pages", "SUPPORTED_KV4_D",
 ]
 
@@ -92,6 +92,8 @@ def load():
             lib.dsa_sparse_attn.restype = i
             lib.dsa_kv4_page_bytes.argtypes = [i, i]
             lib.dsa_kv4_page_bytes.restype = sz
+            lib.dsa_sparse_attn_kv4_workspace_size.argtypes = [i, i, i, i]
+            lib.dsa_sparse_attn_kv4_workspace_size.restype = sz
             lib.dsa_reserve_pages_workspace_size.argtypes = [i]
             lib.dsa_reserve_pages_workspace_size.restype = sz
             lib.dsa_compact_pages_workspace_size.argtypes = [i]
@@ -443,7 +445,7 @@ def _native():
         m = importlib.import_module(__name__ + "._marshal")
         if m.torch_version != torch.__version__.split("+")[0]:
             raise RuntimeError(f"_marshal.so was built for torch {m.torch_version}, not {torch.__version__}: build it again")
-        names = ("quantize_kv4", "dequantize_kv4", "sparse_attn_kv4", "fork_pages", "reserve_pages",
+        names = ("quantize_kv4", "dequantize_kv4", "sparse_attn_kv4", "sparse_attn_kv4_workspace_size", "fork_pages", "reserve_pages",
                  "reserve_pages_workspace_size", "compact_pages", "compact_pages_workspace_size", "copy_pages")
         m.bind(tuple(ctypes.cast(getattr(lib, "dsa_" + n), ctypes.c_void_p).value for n in names), DsaError)
         _calls = m
@@ -463,12 +465,18 @@ def dequantize_kv4(cache, table, seq, pos, D: int, out=None, stream=None):
     return (_calls or _native()).dequantize_kv4(cache, table, seq, pos, D, out, stream)
 
 
-def sparse_attn_kv4(q, cache, table, seq, idx, start=None, attn_sink=None, scale=None, out=None, lse=None, stream=None):
+def sparse_attn_kv4_workspace_size(T: int, H: int, D: int, K: int) -> int:
+    return int(load().dsa_sparse_attn_kv4_workspace_size(T, H, D, K))
+
+
+def sparse_attn_kv4(q, cache, table, seq, idx, start=None, attn_sink=None, scale=None, out=None, lse=None, workspace=None,
+                    stream=None):
     """sparse_attn over the 4-bit paged cache: q bf16 [T, H, D]; idx int32 [T, K], entry v of token t
     naming row v - start[t] of sequence seq[t] (start int32 [T], default 0; negative or unmapped entries
     are skipped); attn_sink fp32 [H] or None, scale default 1 / sqrt(D).  Returns bf16 [T, H, D]; with
     lse (fp32 [T, H]) given, also writes the natural log of each softmax denominator into it."""
-    return (_calls or _native()).sparse_attn_kv4(q, cache, table, seq, idx, start, attn_sink, scale, out, lse, stream)
+    return (_calls or _native()).sparse_attn_kv4(q, cache, table, seq, idx, start, attn_sink, scale, out, lse, workspace,
+                                                 stream)
 
 
 def fork_pages(table, parent, ref, table_out=None, stream=None):

@@ -12,23 +12,53 @@ namespace dsa {
 
 namespace {
 
+constexpr int kDevices = 64;
+
+// Shared memory and cluster size of the kernel on the current device, set once per device (setting them again, from
+// another thread too, changes nothing), and how many clusters of `shares` CTAs the device runs at a time: 0 for a
+// size that it does not run, negative on a CUDA error.
+template <int D>
+int clusters_d(int shares) {
+  static std::atomic<int> known[kDevices][kKv4MaxShares + 1];  // by cluster size: clusters + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return -1;
+  const int have = known[dev][shares].load(std::memory_order_acquire);
+  if (have > 0) return have - 1;
+  constexpr int smem = AttnKv4Layout<D>::kSmem;
+  if (cudaFuncSetAttribute(sparse_attn_kv4_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaFuncSetAttribute(sparse_attn_kv4_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaFuncSetAttribute(sparse_attn_kv4_kernel<D, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return -1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(static_cast<unsigned>(shares));
+  c.blockDim = dim3(kKv4Threads);
+  c.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(shares);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, sparse_attn_kv4_kernel<D, true>, &c) != cudaSuccess) {
+    (void)cudaGetLastError();
+    clusters = 0;
+  }
+  known[dev][shares].store(clusters + 1, std::memory_order_release);
+  return clusters;
+}
+
 template <int D>
 cudaError_t launch_d(int grid, int shares, const AttnKv4Params& p, unsigned* err, cudaStream_t stream) {
-  constexpr int smem = AttnKv4Layout<D>::kSmem;
-  // once per device (setting it again, from another thread too, changes nothing)
-  static std::atomic<uint64_t> set{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !(set.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(sparse_attn_kv4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) set.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
-  }
+  if (clusters_d<D>(shares) < 1) return cudaErrorInvalidValue;
+  // every unit on a CTA or cluster of its own, or one CTA walking over several
+  const bool single = static_cast<int64_t>(p.T) * p.groups * shares == grid;
+  if (!single && shares > 1) return cudaErrorInvalidValue;
+  const auto kernel = single ? sparse_attn_kv4_kernel<D, true> : sparse_attn_kv4_kernel<D, false>;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(static_cast<unsigned>(grid));
   c.blockDim = dim3(kKv4Threads);
-  c.dynamicSmemBytes = smem;
+  c.dynamicSmemBytes = AttnKv4Layout<D>::kSmem;
   c.stream = stream;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -37,7 +67,7 @@ cudaError_t launch_d(int grid, int shares, const AttnKv4Params& p, unsigned* err
   attr.val.clusterDim.z = 1;
   c.attrs = &attr;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, sparse_attn_kv4_kernel<D>, p, shares, err);
+  return cudaLaunchKernelEx(&c, kernel, p, shares, err);
 }
 
 }  // namespace
@@ -49,6 +79,16 @@ int sparse_attn_kv4_smem(int D) {
     case 256: return AttnKv4Layout<256>::kSmem;
     case 512: return AttnKv4Layout<512>::kSmem;
     default: return 0;
+  }
+}
+
+int sparse_attn_kv4_clusters(int D, int shares) {
+  switch (D) {
+    case 64: return clusters_d<64>(shares);
+    case 128: return clusters_d<128>(shares);
+    case 256: return clusters_d<256>(shares);
+    case 512: return clusters_d<512>(shares);
+    default: return -1;
   }
 }
 

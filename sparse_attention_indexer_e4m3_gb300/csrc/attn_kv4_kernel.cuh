@@ -11,8 +11,8 @@
 // their rounding would otherwise be as large as the output's own.
 //
 // A unit is (token, group of up to 64 heads, share of the token's list); a cluster of S CTAs shares
-// one list and joins its S partial results through distributed shared memory, so a call with few tokens still
-// uses most SMs and needs no second launch.  One CTA per SM, 896 threads, per block of 128 entries:
+// one list and joins its S partial results, so a call with few tokens still uses most SMs and needs no second
+// launch.  One CTA per SM, 896 threads, per block of 128 entries:
 //   scout    (warps 1-3)   find the unit's blocks and, up to six blocks ahead, its entries' pages and row scales;
 //   convert  (warps 20-27) the rows' codes to fp16 values, as D / 64 chunks of [128 keys x 128 bytes], 128-byte
 //                          swizzled; a masked entry becomes a row of zeros (its memory is not read); and the
@@ -31,6 +31,7 @@
 #include "attn_tc_kernel.cuh"
 #include "cluster.cuh"
 #include "kv4.cuh"
+#include "launch.h"
 
 namespace dsa {
 
@@ -46,12 +47,13 @@ constexpr int kKv4ConvWarps = kKv4ConvThreads / 32;
 constexpr int kKv4Threads = 32 * (kKv4FirstConv + kKv4ConvWarps);
 constexpr int kKv4Scouts = 3;             // scout warps; one of them looks up every third block
 constexpr int kKv4Slots = 2 * kKv4Scouts; // blocks whose entries are looked up ahead (a slot is always one scout's)
-constexpr int kKv4Shares = 8;             // most CTAs that share a list
+constexpr int kKv4Shares = kKv4MaxShares; // most CTAs that share a list
 constexpr float kKv4NoBound = -1e30f;     // bound of a head without keys so far
 
 template <int D>
 struct AttnKv4Layout {
-  static constexpr int kStages = D <= 256 ? 2 : 1;              // kv blocks held
+  static constexpr int kStages = D <= 128 ? 4 : (D <= 256 ? 2 : 1);  // kv blocks held
+  static constexpr int kScores = kStages < 2 ? 1 : 2;           // score accumulators
   static constexpr int kChunks = D / 64;                        // chunks of a row in the score product
   static constexpr int kTiles = D >= 128 ? D / 128 : 1;         // output tiles (D = 64: half of one is zero)
   static constexpr int kTileWarps = kTiles > 1 ? kKv4ConvWarps / 2 : kKv4ConvWarps;  // warps that convert a tile
@@ -70,12 +72,10 @@ struct AttnKv4Layout {
   static constexpr int kJoin = kSum + kTcAttnHeads * 4;         // float [shares][64] factors of the shares
   static constexpr int kMisc = kJoin + kKv4Shares * kTcAttnHeads * 4;  // int [32]
   static constexpr int kBar = kMisc + 128;
-  static constexpr int kNumBars = 15 + 2 * kKv4Slots + 2 * kStages * kTiles;
+  static constexpr int kNumBars = 15 + 3 * kKv4Slots + 2 * kStages * kTiles;
   static constexpr int kSmem = kBar + kNumBars * 8 + 1024;      // + alignment slack
-  // the joined shares' partial outputs, fp32 [64][D], take the place of the kv blocks
-  static_assert(D * kTcAttnHeads * 4 <= kStages * kStageBytes, "partial outputs fit the kv blocks");
-  // tensor memory: S^T (one per stage) from column 0, O^T tile m from column 64 (kStages + m)
-  static constexpr int kTmemCols = kStages + kTiles <= 4 ? 256 : 512;
+  // tensor memory: S^T (kScores of them) from column 0, O^T tile m from column 64 (kScores + m)
+  static constexpr int kTmemCols = kScores + kTiles <= 4 ? 256 : 512;
 };
 
 // Instruction descriptor, kind::f16 with fp16 operands and an fp32 accumulator.
@@ -184,13 +184,15 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float f) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int D>
+// kSingle: one unit per cluster, whose CTAs may share its list; else one CTA per unit, walking over the units.
+template <int D, bool kSingle>
 __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const AttnKv4Params p, int shares,
                                                                          unsigned* err) {
   using L = AttnKv4Layout<D>;
   constexpr int kCh = L::kChunks;
   constexpr int kTi = L::kTiles;
   constexpr int kSt = L::kStages;
+  constexpr int kSc = L::kScores;
   extern __shared__ __align__(1024) uint8_t kv4_attn_smem[];
   uint8_t* smem = kv4_attn_smem + ((1024u - (smem_addr(kv4_attn_smem) & 1023u)) & 1023u);
   uint8_t* kv_s = smem + L::kKv;
@@ -218,10 +220,11 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 10);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint64_t* drain = bars + 11;
-  uint64_t* s_full = bars + 12;  // [stage]
+  uint64_t* s_full = bars + 12;  // [score accumulator]
   uint64_t* checked = bars + 14;
   uint64_t* ent_full = bars + 15;
-  uint64_t* ent_empty = ent_full + kKv4Slots;
+  uint64_t* scl_full = ent_full + kKv4Slots;
+  uint64_t* ent_empty = scl_full + kKv4Slots;
   uint64_t* kv_full = ent_empty + kKv4Slots;  // [stage][tile]
   uint64_t* kv_empty = kv_full + kSt * kTi;
 
@@ -229,9 +232,9 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   const int lane = threadIdx.x & 31;
   const int H = p.H;
   const int units = p.T * p.groups;
-  const int share = static_cast<int>(blockIdx.x) % shares;
-  const int unit0 = static_cast<int>(blockIdx.x) / shares;
-  const int unit_step = static_cast<int>(gridDim.x) / shares;
+  const int share = kSingle ? static_cast<int>(blockIdx.x) % shares : 0;
+  const int unit0 = kSingle ? static_cast<int>(blockIdx.x) / shares : static_cast<int>(blockIdx.x);
+  const int unit_step = static_cast<int>(gridDim.x);
 
   if constexpr (D == 64) {  // the upper half of a 64-dim row's tile stays zero
     for (int s = 0; s < kSt; ++s)
@@ -253,6 +256,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     }
     for (int i = 0; i < kKv4Slots; ++i) {
       mbar_init(&ent_full[i], 32);
+      mbar_init(&scl_full[i], 32);
       mbar_init(&ent_empty[i], kKv4SoftWarps + kKv4ConvWarps);
     }
     for (int i = 0; i < kSt * kTi; ++i) {
@@ -273,14 +277,72 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   tc_fence_after_sync();
   const uint32_t tbase = *tmem_slot;
   const uint32_t s_tmem = tbase;
-  const uint32_t o_tmem = tbase + 64 * kSt;
+  const uint32_t o_tmem = tbase + 64 * L::kScores;
   // this CTA's blocks of a unit whose list has `all` of them
-  const auto first_block = [&](int all, int s) { return static_cast<int>(static_cast<int64_t>(all) * s / shares); };
+  const auto first_block = [&](int all, int s) { return kSingle ? static_cast<int>(static_cast<int64_t>(all) * s / shares) : all * s; };
   const int rows = 1 << p.pool.log_rows;
   const int64_t page_bytes = static_cast<int64_t>(rows) * kv4_row_bytes(D);
 
+  // q of unit n (token t, heads [h0, h0 + nh)) as fp16, by 256 threads; the place is written after free() returns.
+  const auto bring_q = [&](int tid, int n, int t, int h0, int nh, auto free) {
+    float f = 1.0f;
+    const uint16_t* q = p.q + (static_cast<int64_t>(t) * H + h0) * D;
+    constexpr int kPieces = kTcAttnHeads * (D / 8) / kKv4ConvThreads;  // 16-byte pieces of a thread
+    constexpr int kMost = kSingle ? 8 : 4;  // in flight at a time
+    constexpr int kBatch = kPieces < kMost ? kPieces : kMost;
+    for (int pass = 0; pass < 2; ++pass) {
+      uint32_t top = 0u;
+#pragma unroll 1
+      for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int at = tid + (i0 + i) * kKv4ConvThreads;
+          const int h = at / (D / 8), pc = at % (D / 8);
+          v[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (h < nh) v[i] = __ldg(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * D) + pc);
+        }
+        if (pass == 0 && i0 == 0) free();
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int at = tid + (i0 + i) * kKv4ConvThreads;
+          const int h = at / (D / 8), pc = at % (D / 8);
+          const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top = max(top, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
+          *reinterpret_cast<uint4*>(q_s + (pc / 8) * L::kQChunkBytes + swz128(h, (pc % 8) * 16)) = make_uint4(
+              bf16x2_to_f16x2(x[0], f), bf16x2_to_f16x2(x[1], f), bf16x2_to_f16x2(x[2], f), bf16x2_to_f16x2(x[3], f));
+        }
+      }
+      if (pass == 1) break;
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) misc[8 + (tid >> 5)] = static_cast<int>(top);
+      named_bar_sync(kTcGatherBar, kKv4ConvThreads);
+      int all = 0;
+#pragma unroll
+      for (int i = 0; i < kKv4ConvWarps; ++i) all = max(all, misc[8 + i]);
+      named_bar_sync(kTcGatherBar, kKv4ConvThreads);
+      const int e = (all >> 7) - 127;  // exponent of the largest
+      if (e >= 0 && e < 15) break;
+      if (e < -126 || e > 127) break;  // zeros (or less than the least normal number), or not finite
+      f = __int_as_float((127 + min(13 - e, 126)) << 23);  // the largest lands in [2^13, 2^14)
+    }
+    if (tid == 0) misc[2 + (n & 1)] = __float_as_int(f);
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_full[n & 1]);
+  };
+
   if (warp >= kKv4FirstConv) {
     // ------------------------------------------------------------------ convert
+    // blocks of unit n, once the scouts know
+    const auto take_unit = [&](int n) {
+      mbar_wait(&unit_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x44);
+      const int nb = misc[n & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
+      return nb;
+    };
     const int ctid = threadIdx.x - 32 * kKv4FirstConv;
     // From two tiles on, half of the warps converts the even tiles and half the odd ones, so that a tile's waits
     // and fences pass beside the other's conversion.  A thread converts, of each of its tiles, the 32 dims
@@ -319,63 +381,19 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     };
     uint32_t gb = 0;  // blocks of this CTA so far
     int n = 0;        // units of this CTA so far
-    for (int u = unit0; u < units; u += unit_step, ++n) {
-      const int t = u / p.groups;
-      const int h0 = (u % p.groups) * kTcAttnHeads;
-      const int nh = min(kTcAttnHeads, H - h0);
-      // the unit's q as fp16
-      float f = 1.0f;
+    for (int u = unit0; u < (kSingle ? unit0 + 1 : units); u += unit_step, ++n) {
       int nb = 0;
-      const uint16_t* q = p.q + (static_cast<int64_t>(t) * H + h0) * D;
-      constexpr int kPieces = kTcAttnHeads * (D / 8) / kKv4ConvThreads;  // 16-byte pieces of a thread
-      constexpr int kBatch = kPieces < 4 ? kPieces : 4;
-      for (int pass = 0; pass < 2; ++pass) {
-        uint32_t top = 0u;
-#pragma unroll 1
-        for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
-          uint4 v[kBatch];
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int at = ctid + (i0 + i) * kKv4ConvThreads;
-            const int h = at / (D / 8), pc = at % (D / 8);
-            v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (h < nh) v[i] = __ldg(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * D) + pc);
-          }
-          if (pass == 0 && i0 == 0) {  // the unit's blocks; q's place once the previous unit's scores are done
-            mbar_wait(&unit_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x44);
-            nb = misc[n & 1];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
-            if (n > 0) mbar_wait(q_empty, static_cast<uint32_t>(n - 1) & 1u, abort_flag, err, 0x41);
-          }
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int at = ctid + (i0 + i) * kKv4ConvThreads;
-            const int h = at / (D / 8), pc = at % (D / 8);
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-            *reinterpret_cast<uint4*>(q_s + (pc / 8) * L::kQChunkBytes + swz128(h, (pc % 8) * 16)) = make_uint4(
-                bf16x2_to_f16x2(w[0], f), bf16x2_to_f16x2(w[1], f), bf16x2_to_f16x2(w[2], f), bf16x2_to_f16x2(w[3], f));
-          }
-        }
-        if (pass == 1) break;
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) misc[8 + (warp - kKv4FirstConv)] = static_cast<int>(top);
-        named_bar_sync(kTcGatherBar, kKv4ConvThreads);
-        int all = 0;
-#pragma unroll
-        for (int i = 0; i < kKv4ConvWarps; ++i) all = max(all, misc[8 + i]);
-        named_bar_sync(kTcGatherBar, kKv4ConvThreads);
-        const int e = (all >> 7) - 127;  // exponent of the largest
-        if (e >= 0 && e < 15) break;
-        if (e < -126 || e > 127) break;  // zeros (or less than the least normal number), or not finite
-        f = __int_as_float((127 + min(13 - e, 126)) << 23);  // the largest lands in [2^13, 2^14)
+      if constexpr (kSingle) {  // (the softmax warps, idle so far, bring q)
+        nb = take_unit(0);
+      } else {
+        const int t = u / p.groups;
+        const int h0 = (u % p.groups) * kTcAttnHeads;
+        bring_q(ctid, n, t, h0, min(kTcAttnHeads, H - h0), [&]() {
+          nb = take_unit(n);
+          // q's place is free once the previous unit's score products are done
+          if (n > 0) mbar_wait(q_empty, static_cast<uint32_t>(n - 1) & 1u, abort_flag, err, 0x41);
+        });
       }
-      if (ctid == 0) misc[2 + (n & 1)] = __float_as_int(f);
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[n & 1]);
       if (nb > 0) load(gb);
       for (int b = 0; b < nb; ++b, ++gb) {
         const int st = static_cast<int>(gb % kSt);
@@ -423,7 +441,11 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     int n = 0;
     uint32_t checks = 0;  // blocks of this CTA whose bounds were checked
     uint64_t lsum[kKv4SoftHeads / 2];
-    for (int u = unit0; u < units; u += unit_step, ++n) {
+    if (kSingle && etid < kKv4ConvThreads) {
+      const int h0 = (unit0 % p.groups) * kTcAttnHeads;
+      bring_q(etid, 0, unit0 / p.groups, h0, min(kTcAttnHeads, H - h0), []() {});
+    }
+    for (int u = unit0; u < (kSingle ? unit0 + 1 : units); u += unit_step, ++n) {
       const int t = u / p.groups;
       const int h0 = (u % p.groups) * kTcAttnHeads;
       const int nh = min(kTcAttnHeads, H - h0);
@@ -438,7 +460,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
       for (int b = 0; b < nb; ++b, ++gb) {
         const uint32_t slot = gb % kKv4Slots;
-        mbar_wait(&ent_full[slot], (gb / kKv4Slots) & 1u, abort_flag, err, 0x65);
+        mbar_wait(&scl_full[slot], (gb / kKv4Slots) & 1u, abort_flag, err, 0x65);
         const float rs = scl_s[slot * kTcAttnKeys + r];
         __syncwarp();
         if (lane == 0) mbar_arrive(&ent_empty[slot]);
@@ -447,8 +469,8 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
         const float lr = valid ? log2f(rs) : -INFINITY;  // a masked key's weight is 0
         const float inv = valid ? 1.0f / rs : 0.f;
         const uint64_t a2 = pack_f32x2(a, a), lr2 = pack_f32x2(lr, lr), inv2 = pack_f32x2(inv, inv);
-        const uint32_t s_at = s_tmem + 64 * (gb % kSt) + lane_off + hb;
-        mbar_wait(&s_full[gb % kSt], (gb / kSt) & 1u, abort_flag, err, 0x61);
+        const uint32_t s_at = s_tmem + 64 * (gb % kSc) + lane_off + hb;
+        mbar_wait(&s_full[gb % kSc], (gb / kSc) & 1u, abort_flag, err, 0x61);
         tc_fence_after_sync();
         float x[kKv4SoftHeads];
         // exponents relative to the running bounds
@@ -558,7 +580,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       named_bar_sync(kTcEpiBar, kKv4SoftThreads);
       if (etid < kTcAttnHeads) {
         const float l = (red_s[etid] + red_s[kTcAttnHeads + etid]) + (red_s[2 * kTcAttnHeads + etid] + red_s[3 * kTcAttnHeads + etid]);
-        if (shares > 1) {
+        if (kSingle && shares > 1) {
           sum_s[etid] = l;
         } else if (etid < nh) {
           alpha_s[etid] = softmax_factor(max_s[etid], l, p.sink, h0 + etid,
@@ -581,10 +603,11 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
 #pragma unroll
           for (int j = 0; j < kKv4SoftHeads; ++j) o[j] = 0.f;
         }
-        if (shares > 1) {
+        if (kSingle && shares > 1) {
           if (row) {
+            float* part = p.partial + (static_cast<int64_t>(u) * shares + share) * kTcAttnHeads * D + 128 * m + r;
 #pragma unroll
-            for (int j = 0; j < kKv4SoftHeads; ++j) reinterpret_cast<float*>(kv_s)[(hb + j) * D + 128 * m + r] = o[j];
+            for (int j = 0; j < kKv4SoftHeads; ++j) __stcg(part + (hb + j) * D, o[j]);
           }
           continue;
         }
@@ -621,7 +644,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     // ------------------------------------------------------------------ scout
     uint32_t gb = 0;
     int n = 0;
-    for (int u = unit0; u < units; u += unit_step, ++n) {
+    for (int u = unit0; u < (kSingle ? unit0 + 1 : units); u += unit_step, ++n) {
       const int t = u / p.groups;
       const int32_t* list = p.idx + static_cast<int64_t>(t) * p.K;
       const int seq = __ldg(p.seq + t);
@@ -673,16 +696,16 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
         for (int i = 0; i < 4; ++i) {
           r[i] = 0.0f;
           if (ent[i].x >= 0)
-            r[i] = fmaxf(__ldg(reinterpret_cast<const float*>(p.pool.cache + ent[i].x * page_bytes +
-                                                              rows * (D / 2 + D / kKv4Group)) + ent[i].y), kKv4MinScale);
+            r[i] = __ldg(reinterpret_cast<const float*>(p.pool.cache + ent[i].x * page_bytes +
+                                                        rows * (D / 2 + D / kKv4Group)) + ent[i].y);
         }
         if (gb >= kKv4Slots) mbar_wait(&ent_empty[slot], (gb / kKv4Slots - 1) & 1u, abort_flag, err, 0x45);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ent_s[slot * kTcAttnKeys + 32 * i + lane] = ent[i];
-          scl_s[slot * kTcAttnKeys + 32 * i + lane] = r[i];
-        }
+        for (int i = 0; i < 4; ++i) ent_s[slot * kTcAttnKeys + 32 * i + lane] = ent[i];
         mbar_arrive(&ent_full[slot]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) scl_s[slot * kTcAttnKeys + 32 * i + lane] = fmaxf(r[i], ent[i].x >= 0 ? kKv4MinScale : 0.0f);
+        mbar_arrive(&scl_full[slot]);
       }
     }
     } else {
@@ -711,18 +734,18 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
         for (int kk = 0; kk < 4; ++kk) {
           const uint64_t ad = a + ((c * L::kChunkBytes + kk * 32) >> 4), bd = q_k + ((c * L::kQChunkBytes + kk * 32) >> 4);
           if (c == 0 && kk == 0)
-            mma_f16_if<false>(on, s_tmem + 64 * st, ad, bd, id_qk, 0u);
+            mma_f16_if<false>(on, s_tmem + 64 * (gb % kSc), ad, bd, id_qk, 0u);
           else
-            mma_f16_if<true>(on, s_tmem + 64 * st, ad, bd, id_qk);
+            mma_f16_if<true>(on, s_tmem + 64 * (gb % kSc), ad, bd, id_qk);
         }
       }
-      mma_commit_if(on, &s_full[st]);
+      mma_commit_if(on, &s_full[gb % kSc]);
       return true;
     };
     uint32_t gb = 0;
     int n = 0;
     bool ok = true;
-    for (int u = unit0; ok && u < units; u += unit_step, ++n) {
+    for (int u = unit0; ok && u < (kSingle ? unit0 + 1 : units); u += unit_step, ++n) {
       if (!wait(&unit_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, 0x50)) break;
       const int nb = __shfl_sync(0xffffffffu, misc[n & 1], 0);
       if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
@@ -780,8 +803,8 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     }
   }
 
-  if (shares > 1) {
-    // ------------------------------------------------------------------ join (one unit per cluster)
+  if (kSingle && shares > 1) {
+    // ------------------------------------------------------------------ join
     __syncthreads();
     cluster_sync_all();
     const int t = unit0 / p.groups;
@@ -816,34 +839,38 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       for (int i = 0; i < kKv4Shares; ++i) join_s[i * kTcAttnHeads + h] = m[i] * f;
     }
     __syncthreads();
-    // this CTA's share of the group's [64][D] outputs, four dims at a time: a warp reads 512 contiguous bytes of
-    // each partial (with lanes on different rows the remote reads took ten times as long)
+    // this CTA's share of the group's [64][D] outputs, four dims at a time.  The partial outputs pass through
+    // L2: read from the other CTAs' shared memory instead, 128 KB arrive at 13 bytes a clock (10,000 cycles at D = 512).
     const int per = kTcAttnHeads * D / 4 / shares;
+    const float4* part = reinterpret_cast<const float4*>(p.partial) + static_cast<int64_t>(unit0) * shares * kTcAttnHeads * (D / 4);
     uint16_t* out = p.out + (static_cast<int64_t>(t) * H + h0) * D;
     for (int i = share * per + threadIdx.x; i < (share + 1) * per; i += kKv4Threads) {
       const int h = i / (D / 4);
       if (h >= nh) break;
-      float4 v[kKv4Shares];
-#pragma unroll
-      for (int k = 0; k < kKv4Shares; ++k) {
-        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k < shares) v[k] = ld_cluster_f4(smem_addr(kv_s) + i * 16, k);
-      }
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < kKv4Shares; ++k) {
-        const float f = k < shares ? join_s[k * kTcAttnHeads + h] : 0.f;
-        acc.x = fmaf(v[k].x, f, acc.x);
-        acc.y = fmaf(v[k].y, f, acc.y);
-        acc.z = fmaf(v[k].z, f, acc.z);
-        acc.w = fmaf(v[k].w, f, acc.w);
+      for (int k0 = 0; k0 < kKv4Shares; k0 += 8) {
+        if (k0 >= shares) break;
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k0 + k < shares) v[k] = __ldcg(part + static_cast<int64_t>(k0 + k) * kTcAttnHeads * (D / 4) + i);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float f = k0 + k < shares ? join_s[(k0 + k) * kTcAttnHeads + h] : 0.f;
+          acc.x = fmaf(v[k].x, f, acc.x);
+          acc.y = fmaf(v[k].y, f, acc.y);
+          acc.z = fmaf(v[k].z, f, acc.z);
+          acc.w = fmaf(v[k].w, f, acc.w);
+        }
       }
       const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
-      uint32_t* dst = reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(i) * 4);
-      dst[0] = *reinterpret_cast<const uint32_t*>(&lo);
-      dst[1] = *reinterpret_cast<const uint32_t*>(&hi);
+      *reinterpret_cast<uint2*>(out + static_cast<int64_t>(i) * 4) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
-    cluster_sync_all();  // no CTA leaves while another reads its partial outputs
+    cluster_sync_all();  // no CTA leaves while another reads its bounds and sums
   }
 
   tc_fence_before_sync();

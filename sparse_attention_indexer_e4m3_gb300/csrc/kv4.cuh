@@ -39,6 +39,7 @@ struct AttnKv4Params {
   const int32_t* idx;     // [T][K]
   uint16_t* out;          // [T][H][D] bf16
   float* lse;             // [T][H] or null
+  float* partial;         // [unit][share][64][D] partial outputs where a list is shared
   int T, H, K;
   int groups;             // ceil(H / 64)
   float scale;

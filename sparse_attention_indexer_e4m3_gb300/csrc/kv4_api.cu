@@ -37,6 +37,19 @@ dsa_status check_tables(int R, int M, int P) {
   return DSA_OK;
 }
 
+// CTAs that share a unit's list: the largest power of two for which the device runs all units' clusters at once and every
+// share keeps a block of the list.
+int list_shares(int64_t units, int D, int K) {
+  const int blocks = (K + kKv4Block - 1) / kKv4Block;
+  int shares = 1;
+  while (shares < kKv4MaxShares && shares * 2 <= blocks && units <= sparse_attn_kv4_clusters(D, shares * 2)) shares *= 2;
+  return shares;
+}
+
+size_t partial_bytes(int64_t units, int shares, int D) {
+  return shares > 1 ? static_cast<size_t>(units) * shares * kTcMaxHeads * D * sizeof(float) : 0;
+}
+
 dsa_status done(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
 
 }  // namespace
@@ -72,10 +85,16 @@ dsa_status dsa_dequantize_kv4(const uint8_t* cache, int P, int page_rows, const 
   return done(launch_kv4_read(D, kv, N, seq, pos, c, static_cast<cudaStream_t>(stream)));
 }
 
+size_t dsa_sparse_attn_kv4_workspace_size(int T, int H, int D, int K) {
+  if (T <= 0 || H < 1 || K <= 0 || !kv4_d(D)) return 0;
+  const int64_t units = static_cast<int64_t>(T) * ((H + kTcMaxHeads - 1) / kTcMaxHeads);
+  return partial_bytes(units, list_shares(units, D, K), D);
+}
+
 dsa_status dsa_sparse_attn_kv4(const uint16_t* q, const uint8_t* cache, int P, int page_rows, const int32_t* table,
                                int R, int M, const int32_t* seq, const int32_t* start, const float* attn_sink,
                                const int32_t* idx, int T, int H, int D, int K, float scale, uint16_t* out, float* lse,
-                               void* stream) {
+                               void* workspace, size_t workspace_bytes, void* stream) {
   Kv4Pool c;
   const dsa_status st = check_pool(&c, cache, P, page_rows, table, R, M, D);
   if (st != DSA_OK) return st;
@@ -91,12 +110,12 @@ dsa_status dsa_sparse_attn_kv4(const uint16_t* q, const uint8_t* cache, int P, i
   DeviceFacts dev;
   if (!device_facts(&dev)) return DSA_ERR_CUDA;
   if (sparse_attn_kv4_smem(D) > dev.max_smem) return DSA_ERR_UNSUPPORTED;
-  // Fewer units than SMs: a cluster of up to 8 CTAs shares each list, as long as every share keeps a block.
-  int shares = 1;
-  const int blocks = (K + kKv4Block - 1) / kKv4Block;
-  while (shares < 8 && units * shares * 2 <= dev.sms && shares * 2 <= blocks) shares *= 2;
+  const int shares = list_shares(units, D, K);
+  if (shares > 1 && (!workspace || !aligned(workspace, 16) || workspace_bytes < partial_bytes(units, shares, D)))
+    return DSA_ERR_WORKSPACE;
   const int grid = shares > 1 ? static_cast<int>(units) * shares : static_cast<int>(std::min<int64_t>(units, dev.sms));
-  const AttnKv4Params p{q, c, seq, start, attn_sink, idx, out, lse, T, H, K, groups, scale};
+  const AttnKv4Params p{q,   c,   seq, start, attn_sink, idx,    out, lse, shares > 1 ? static_cast<float*>(workspace) : nullptr,
+                        T,   H,   K,   groups, scale};
   return done(launch_sparse_attn_kv4(D, grid, shares, p, dev.err, static_cast<cudaStream_t>(stream)));
 }
 

@@ -71,10 +71,13 @@ cudaError_t launch_pages_copy(uint8_t* pages, int64_t page_bytes, int P, const i
                               int sms, cudaStream_t stream);
 // Sparse attention over the 4-bit paged cache (D in {64, 128, 256, 512}); `shares` CTAs of a cluster
 // share a unit's list.
-constexpr int kKv4Block = 128;  // list entries per block
+constexpr int kKv4Block = 128;     // list entries per block
+constexpr int kKv4MaxShares = 16;  // most CTAs that share a list
 cudaError_t launch_sparse_attn_kv4(int D, int grid, int shares, const AttnKv4Params& p, unsigned* err,
                                    cudaStream_t stream);
 int sparse_attn_kv4_smem(int D);
+// How many clusters of `shares` of its CTAs this device runs at a time (0: none of that size; < 0: a CUDA error).
+int sparse_attn_kv4_clusters(int D, int shares);
 
 // Facts of the current device that the entry points need; false on a CUDA error.
 struct DeviceFacts {

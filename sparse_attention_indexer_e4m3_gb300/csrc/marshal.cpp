@@ -25,6 +25,7 @@ struct Entry {
   decltype(&dsa_quantize_kv4) quantize_kv4;
   decltype(&dsa_dequantize_kv4) dequantize_kv4;
   decltype(&dsa_sparse_attn_kv4) sparse_attn_kv4;
+  decltype(&dsa_sparse_attn_kv4_workspace_size) sparse_attn_kv4_workspace_size;
   decltype(&dsa_fork_pages) fork_pages;
   decltype(&dsa_reserve_pages) reserve_pages;
   decltype(&dsa_reserve_pages_workspace_size) reserve_pages_workspace_size;
@@ -209,9 +210,9 @@ PyObject* dequantize_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (q, cache, table, seq, idx, start, attn_sink, scale, out, lse, stream)
+// (q, cache, table, seq, idx, start, attn_sink, scale, out, lse, workspace, stream)
 PyObject* sparse_attn_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded("sparse_attn_kv4", n, 11, [&] {
+  return guarded("sparse_attn_kv4", n, 12, [&] {
     const at::Tensor& q = arg(a[0], "q", at::kBFloat16, 3);
     const int64_t T = q.size(0), H = q.size(1), D = q.size(2);
     const Pool c(a[1], a[2], D);
@@ -225,13 +226,21 @@ PyObject* sparse_attn_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (scale == -1.0 && PyErr_Occurred()) throw Refusal{nullptr, ""};
     at::Tensor out = out_arg(a[8], "out", at::kBFloat16, {T, H, D});
     const at::Tensor lse = out_arg(a[9], "lse", at::kFloat, {T, H});
-    const Where w(a[10], {&q, &c.cache, &c.table, &seq, &idx, start.defined() ? &start : nullptr, sink.defined() ? &sink : nullptr,
-                          out.defined() ? &out : nullptr, lse.defined() ? &lse : nullptr});
+    at::Tensor ws;
+    if (a[10] != Py_None) ws = arg(a[10], "workspace", at::kByte, 1);
+    const Where w(a[11], {&q, &c.cache, &c.table, &seq, &idx, start.defined() ? &start : nullptr, sink.defined() ? &sink : nullptr,
+                          out.defined() ? &out : nullptr, lse.defined() ? &lse : nullptr, ws.defined() ? &ws : nullptr});
     if (!out.defined()) out = w.make({T, H, D}, at::kBFloat16);
+    if (!ws.defined()) {
+      const size_t need = g_abi.sparse_attn_kv4_workspace_size(as_int(T, "q"), as_int(H, "q"), static_cast<int>(D),
+                                                               as_int(idx.size(1), "idx"));
+      if (need > 0) ws = w.make({static_cast<int64_t>(need)}, at::kByte);
+    }
     check(g_abi.sparse_attn_kv4(bf16(q), ptr<const uint8_t>(c.cache), c.P, c.rows, i32(c.table), c.R, c.M, i32(seq),
                                 start.defined() ? i32(start) : nullptr, sink.defined() ? ptr<const float>(sink) : nullptr, i32(idx),
                                 as_int(T, "q"), as_int(H, "q"), static_cast<int>(D), as_int(idx.size(1), "idx"),
-                                static_cast<float>(scale), ptr<uint16_t>(out), lse.defined() ? ptr<float>(lse) : nullptr, w.stream),
+                                static_cast<float>(scale), ptr<uint16_t>(out), lse.defined() ? ptr<float>(lse) : nullptr, ws.defined() ? ws.data_ptr() : nullptr,
+                                ws.defined() ? static_cast<size_t>(ws.numel()) : 0, w.stream),
           "dsa_sparse_attn_kv4");
     return a[8] != Py_None ? keep(a[8]) : THPVariable_Wrap(out);
   });

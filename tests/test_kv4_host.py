@@ -60,7 +60,7 @@ def lib():
     p, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     lib.dsa_quantize_kv4.argtypes = [p, p, p, i, i, p, i, i, p, i, i, p]
     lib.dsa_dequantize_kv4.argtypes = [p, i, i, p, i, i, p, p, i, i, p, p]
-    lib.dsa_sparse_attn_kv4.argtypes = [p, p, i, i, p, i, i, p, p, p, p, i, i, i, i, ctypes.c_float, p, p, p]
+    lib.dsa_sparse_attn_kv4.argtypes = [p, p, i, i, p, i, i, p, p, p, p, i, i, i, i, ctypes.c_float, p, p, p, sz, p]
     lib.dsa_fork_pages.argtypes = [p, p, i, i, i, p, p, p]
     lib.dsa_reserve_pages.argtypes = [p, p, p, p, i, i, i, i, p, p, p, p, sz, p]
     lib.dsa_reserve_pages_workspace_size.restype = lib.dsa_compact_pages_workspace_size.restype = sz
@@ -106,7 +106,7 @@ def test_attention_refusals(lib, mem):
 
     def f(q=a, cache=a, P=2, rows=64, table=a, R=1, M=2, seq=a, start=None, sink=None, idx=a, T=2, H=4, D=128, K=3, out=a,
           lse=None):
-        return lib.dsa_sparse_attn_kv4(q, cache, P, rows, table, R, M, seq, start, sink, idx, T, H, D, K, 1.0, out, lse, None)
+        return lib.dsa_sparse_attn_kv4(q, cache, P, rows, table, R, M, seq, start, sink, idx, T, H, D, K, 1.0, out, lse, None, 0, None)
 
     assert f(D=96) == f(rows=24) == f(M=1 << 26) == f(T=1 << 30, H=256) == UNSUPPORTED
     assert f(T=-1) == f(H=0) == f(K=-1) == f(P=-1) == f(R=-3) == INVALID
