@@ -178,6 +178,13 @@ __device__ __forceinline__ float softmax_factor(float m, float l, const float* s
   return l > 0.f ? f / l : 0.f;
 }
 
+// The larger magnitudes of two pairs of bf16 values (their signs mean nothing).
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Two bf16 values to fp16, times f.
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float f) {
   const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     float f = 1.0f;
     const uint16_t* q = p.q + (static_cast<int64_t>(t) * H + h0) * D;
     constexpr int kPieces = kTcAttnHeads * (D / 8) / kKv4ConvThreads;  // 16-byte pieces of a thread
-    constexpr int kMost = kSingle ? 8 : 4;  // in flight at a time
+    constexpr int kMost = kSingle || D == 512 ? 4 : 2;  // in flight at a time (more spilled registers)
     constexpr int kBatch = kPieces < kMost ? kPieces : kMost;
     for (int pass = 0; pass < 2; ++pass) {
       uint32_t top = 0u;
@@ -308,14 +315,19 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
           const int at = tid + (i0 + i) * kKv4ConvThreads;
           const int h = at / (D / 8), pc = at % (D / 8);
           const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint4* dst = reinterpret_cast<uint4*>(q_s + (pc / 8) * L::kQChunkBytes + swz128(h, (pc % 8) * 16));
+          if (pass == 0) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) top = max(top, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
-          *reinterpret_cast<uint4*>(q_s + (pc / 8) * L::kQChunkBytes + swz128(h, (pc % 8) * 16)) = make_uint4(
-              bf16x2_to_f16x2(x[0], f), bf16x2_to_f16x2(x[1], f), bf16x2_to_f16x2(x[2], f), bf16x2_to_f16x2(x[3], f));
+            for (int j = 0; j < 4; ++j) top = max_abs_bf16x2(top, x[j]);
+            *dst = make_uint4(bf16x2_to_f16x2(x[0], 1.0f), bf16x2_to_f16x2(x[1], 1.0f), bf16x2_to_f16x2(x[2], 1.0f),
+                              bf16x2_to_f16x2(x[3], 1.0f));
+          } else {
+            *dst = make_uint4(bf16x2_to_f16x2(x[0], f), bf16x2_to_f16x2(x[1], f), bf16x2_to_f16x2(x[2], f), bf16x2_to_f16x2(x[3], f));
+          }
         }
       }
       if (pass == 1) break;
-      top = __reduce_max_sync(0xffffffffu, top);
+      top = __reduce_max_sync(0xffffffffu, max(top & 0x7FFFu, (top >> 16) & 0x7FFFu));
       if (lane == 0) misc[8 + (tid >> 5)] = static_cast<int>(top);
       named_bar_sync(kTcGatherBar, kKv4ConvThreads);
       int all = 0;
@@ -406,21 +418,17 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
             const int row = row0 + kRowStep * k;
             const uint32_t s2 = e4m3x2_to_f16x2(grp[i][k]);
             const uint32_t w[4] = {raw[i][k].x, raw[i][k].y, raw[i][k].z, raw[i][k].w};
-            uint4 o[4];
+            if (k == 0 && gb >= kSt) mbar_wait(&kv_empty[st * kTi + m], (gb / kSt - 1) & 1u, abort_flag, err, 0x42);
+            if (!has_part) continue;
 #pragma unroll
             for (int j0 = 0; j0 < 4; ++j0) {
               // the two chunks' threads take their pieces in different order: no bank conflicts
-              const uint32_t wj = (part & 2) ? w[j0 ^ 2] : w[j0];
-              const uint32_t s = ((part & 2) ? (j0 ^ 2) : j0) & 2 ? __byte_perm(s2, s2, 0x3232) : __byte_perm(s2, s2, 0x1010);
+              const int j = (part & 2) ? (j0 ^ 2) : j0;
+              const uint32_t s = (j & 2) ? __byte_perm(s2, s2, 0x3232) : __byte_perm(s2, s2, 0x1010);
               uint32_t v[4];
-              e2m1x8_to_f16x2(wj, v);
-              o[j0] = make_uint4(hmul2(v[0], s), hmul2(v[1], s), hmul2(v[2], s), hmul2(v[3], s));
-            }
-            if (k == 0 && gb >= kSt) mbar_wait(&kv_empty[st * kTi + m], (gb / kSt - 1) & 1u, abort_flag, err, 0x42);
-            if (has_part) {
-#pragma unroll
-              for (int j0 = 0; j0 < 4; ++j0)
-                *reinterpret_cast<uint4*>(chunk + swz128(row, (part & 1) * 64 + ((part & 2) ? (j0 ^ 2) : j0) * 16)) = o[j0];
+              e2m1x8_to_f16x2((part & 2) ? w[j0 ^ 2] : w[j0], v);
+              *reinterpret_cast<uint4*>(chunk + swz128(row, (part & 1) * 64 + j * 16)) =
+                  make_uint4(hmul2(v[0], s), hmul2(v[1], s), hmul2(v[2], s), hmul2(v[3], s));
             }
           }
           fence_proxy_async_shared();
