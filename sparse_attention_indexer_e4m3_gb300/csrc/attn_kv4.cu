@@ -39,8 +39,8 @@ int clusters_d(int shares) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   c.attrs = &attr;
   c.numAttrs = 1;
-  int clusters = 0;
-  if (cudaOccupancyMaxActiveClusters(&clusters, sparse_attn_kv4_kernel<D, true>, &c) != cudaSuccess) {
+  int clusters = shares == 1 ? 1 : 0;
+  if (shares > 1 && cudaOccupancyMaxActiveClusters(&clusters, sparse_attn_kv4_kernel<D, true>, &c) != cudaSuccess) {
     (void)cudaGetLastError();
     clusters = 0;
   }

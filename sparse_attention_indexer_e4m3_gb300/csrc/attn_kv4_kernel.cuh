@@ -849,10 +849,11 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     __syncthreads();
     // this CTA's share of the group's [64][D] outputs, four dims at a time.  The partial outputs pass through
     // L2: read from the other CTAs' shared memory instead, 128 KB arrive at 13 bytes a clock (10,000 cycles at D = 512).
-    const int per = kTcAttnHeads * D / 4 / shares;
+    constexpr int kAll = kTcAttnHeads * D / 4;
+    const int per = (kAll + shares - 1) / shares;
     const float4* part = reinterpret_cast<const float4*>(p.partial) + static_cast<int64_t>(unit0) * shares * kTcAttnHeads * (D / 4);
     uint16_t* out = p.out + (static_cast<int64_t>(t) * H + h0) * D;
-    for (int i = share * per + threadIdx.x; i < (share + 1) * per; i += kKv4Threads) {
+    for (int i = share * per + threadIdx.x; i < min(kAll, (share + 1) * per); i += kKv4Threads) {
       const int h = i / (D / 4);
       if (h >= nh) break;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -37,13 +37,19 @@ dsa_status check_tables(int R, int M, int P) {
   return DSA_OK;
 }
 
-// CTAs that share a unit's list: the largest power of two for which the device runs all units' clusters at once and every
-// share keeps a block of the list.
+// CTAs that share a unit's list: as few blocks per share as the device has clusters for, all units at once.  Joining the shares
+// takes as long as two to three blocks do, so a list is shared where at least that many of its blocks go to other CTAs
+// (one token, 64 heads, shared against not: D = 128, 3 blocks 10.5 to 10.3 us, 4 blocks 10.5 to 11.4, 16 blocks
+// 10.9 to 24.2; D = 512, 2 blocks 16.2 to 15.2 us, 4 blocks 15.6 to 21.1, 16 blocks 15.4 to 55.0).
 int list_shares(int64_t units, int D, int K) {
   const int blocks = (K + kKv4Block - 1) / kKv4Block;
-  int shares = 1;
-  while (shares < kKv4MaxShares && shares * 2 <= blocks && units <= sparse_attn_kv4_clusters(D, shares * 2)) shares *= 2;
-  return shares;
+  const int worth = D == 512 ? 2 : 3;
+  if (blocks <= worth || units > sparse_attn_kv4_clusters(D, 2)) return 1;
+  for (int each = (blocks + kKv4MaxShares - 1) / kKv4MaxShares; blocks - each >= worth; ++each) {
+    const int shares = (blocks + each - 1) / each;
+    if (units <= sparse_attn_kv4_clusters(D, shares)) return shares;
+  }
+  return 1;
 }
 
 size_t partial_bytes(int64_t units, int shares, int D) {

@@ -205,6 +205,33 @@ def test_attention_shared_lists(dsa, D):
         c.check(*c.run(dsa))
 
 
+@pytest.mark.parametrize("D", [128, 512])
+@pytest.mark.parametrize("K", [300, 385, 600, 900, 1100, 1500, 1900, 5000])
+def test_attention_share_counts(dsa, D, K):
+    """Lists of 3 to 40 blocks for one token: 3, 4, 5, 8, 9, 12, 15 and 14 shares of one to three blocks (as far as the device
+    has such clusters), ragged lists whose last shares hold nothing, an empty one."""
+    c = Case(D + K, 4, 20, D, K, 64, length=500, sink=True)
+    for t in range(c.T):
+        c.idx[t, [K, K // 2, 130, 0][t]:] = -1
+    c.check(*c.run(dsa))
+
+
+def test_attention_workspace(dsa):
+    import torch
+
+    c = Case(21, 2, 64, 512, 700, 64, length=500)
+    need = dsa.sparse_attn_kv4_workspace_size(c.T, c.H, c.D, c.K)
+    assert need > 0 and dsa.sparse_attn_kv4_workspace_size(4096, 64, 512, 2048) == 0
+    want = c.run(dsa)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = c.run(dsa, workspace=ws)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+    for bad in (ws[:need - 16], ws[8:]):
+        with pytest.raises(dsa.DsaError) as e:
+            c.run(dsa, workspace=bad)
+        assert e.value.status == 3
+
+
 @pytest.mark.parametrize("D,H,T", [(64, 64, 400), (128, 20, 400), (256, 130, 170), (512, 64, 330)])
 def test_attention_many_tokens(dsa, D, H, T):
     """More units than SMs, ragged lists with holes, entries out of range, rows without a key at the first and last
