@@ -74,13 +74,6 @@ __device__ __forceinline__ int kv4_page(const Kv4Pool& c, int seq, int pos) {
   return static_cast<unsigned>(page) < static_cast<unsigned>(c.P) ? page : -1;
 }
 
-// Two e2m1 codes (one byte, low half first) to two fp16 values.
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(byte));
-  return r;
-}
-
 // The eight e2m1 codes of a word to four fp16 pairs.
 __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&v)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
@@ -97,10 +90,15 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
   return r;
 }
 
-// Two floats to two e2m1 codes (nearest, ties to even, saturating); lo lands in the low half.
-__device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
+// Eight floats to the eight e2m1 codes of a word (nearest, ties to even, saturating; the first in the low bits).
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 a;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.u32.u8 %0, a;\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
 

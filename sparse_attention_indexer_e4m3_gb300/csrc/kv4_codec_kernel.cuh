@@ -76,8 +76,12 @@ __global__ void __launch_bounds__(kKv4CodecThreads) kv4_write_kernel(const uint1
   for (int j = 0; j < 8; ++j) both = max_bf16x2(both, w[j] & 0x7FFF7FFFu);
   const uint32_t g = max(both & 0xFFFFu, both >> 16);
   uint32_t top = g;
+  if constexpr (kLanes == 32) {
+    top = __reduce_max_sync(0xffffffffu, top);
+  } else {
 #pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  }
   if (page < 0) return;
   // 2688 = 1.3125 * 2^11: the exponent of r from the exponent and the 7 mantissa bits of max|x|
   int e = static_cast<int>(top >> 7) - 127 - ((top & 0x7Fu) <= 40u ? 11 : 10);
@@ -90,13 +94,14 @@ __global__ void __launch_bounds__(kKv4CodecThreads) kv4_write_kernel(const uint1
   uint32_t codes[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    uint32_t c2[4];
+    float v[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float lo = __uint_as_float(w[4 * i + j] << 16), hi = __uint_as_float(w[4 * i + j] & 0xFFFF0000u);
-      c2[j] = cvt_e2m1x2(copysignf(fmaf(fabsf(lo), f, 6144.0f) - 6144.0f, lo), copysignf(fmaf(fabsf(hi), f, 6144.0f) - 6144.0f, hi));
+      v[2 * j] = copysignf(fmaf(fabsf(lo), f, 6144.0f) - 6144.0f, lo);
+      v[2 * j + 1] = copysignf(fmaf(fabsf(hi), f, 6144.0f) - 6144.0f, hi);
     }
-    codes[i] = __byte_perm(__byte_perm(c2[0], c2[1], 0x0040), __byte_perm(c2[2], c2[3], 0x0040), 0x5410);
+    codes[i] = cvt_e2m1x8(v);
   }
   uint8_t* base = c.cache + static_cast<int64_t>(page) * rows * kv4_row_bytes(D);
   *reinterpret_cast<uint2*>(base + at * (D / 2) + sub * 8) = make_uint2(codes[0], codes[1]);
