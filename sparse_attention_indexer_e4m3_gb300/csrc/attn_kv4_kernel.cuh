@@ -619,28 +619,19 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
           }
           continue;
         }
-        // through P's place, as [head pair][dim] words: then 16-byte stores of 8 dims of a head
-        uint32_t* tile = reinterpret_cast<uint32_t*>(p_s);
+        // Neighbouring lanes (dims) trade halves of a pair of heads, so that each stores two dims of one head: 64
+        // contiguous bytes per head and warp, without shared memory or barriers.
+        const bool odd = (lane & 1) != 0;
+        uint16_t* dst = out + static_cast<int64_t>(hb + (odd ? 1 : 0)) * D + 128 * m + (r & ~1);
 #pragma unroll
         for (int j = 0; j < kKv4SoftHeads; j += 2) {
           const float2 f = *reinterpret_cast<const float2*>(alpha_s + hb + j);
-          const __nv_bfloat162 w = __floats2bfloat162_rn(o[j] * f.x, o[j + 1] * f.y);
-          tile[(hb + j) / 2 * 128 + r] = *reinterpret_cast<const uint32_t*>(&w);
+          const __nv_bfloat162 two = __floats2bfloat162_rn(o[j] * f.x, o[j + 1] * f.y);
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(&two);
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 1);
+          const uint32_t mine = odd ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
+          if (row && hb + j + (odd ? 1 : 0) < nh) *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(j) * D) = mine;
         }
-        named_bar_sync(kTcEpiBar, kKv4SoftThreads);
-        {
-          const int pair = etid / 16, d8 = (etid & 15) * 8;
-          const uint4 lo = *reinterpret_cast<const uint4*>(tile + pair * 128 + d8);
-          const uint4 hi = *reinterpret_cast<const uint4*>(tile + pair * 128 + d8 + 4);
-          uint16_t* dst = out + static_cast<int64_t>(2 * pair) * D + 128 * m + d8;
-          if (2 * pair < nh && d8 < D)
-            *reinterpret_cast<uint4*>(dst) = make_uint4(__byte_perm(lo.x, lo.y, 0x5410), __byte_perm(lo.z, lo.w, 0x5410),
-                                                        __byte_perm(hi.x, hi.y, 0x5410), __byte_perm(hi.z, hi.w, 0x5410));
-          if (2 * pair + 1 < nh && d8 < D)
-            *reinterpret_cast<uint4*>(dst + D) = make_uint4(__byte_perm(lo.x, lo.y, 0x7632), __byte_perm(lo.z, lo.w, 0x7632),
-                                                            __byte_perm(hi.x, hi.y, 0x7632), __byte_perm(hi.z, hi.w, 0x7632));
-        }
-        named_bar_sync(kTcEpiBar, kKv4SoftThreads);  // the next tile, or the next unit's P, takes the place
       }
       tc_fence_before_sync();
       __syncwarp();
