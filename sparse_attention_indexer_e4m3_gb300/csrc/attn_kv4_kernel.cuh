@@ -22,8 +22,17 @@
 //                          bound m moves only when exceeded by more than 2^8;
 //   weighted (warp 0)      O^T += V^T . P^T: M = 128 output dims (D / 128 tiles), N = 64, K = 128 keys.
 // A tile of 128 dims is converted anew as soon as the weighted sum has read it; the global loads of the next
-// block are in flight while its tiles are waited for.  Up to D = 256 two blocks fit, and the score product of
-// the next block is issued before the weighted sum of the last, so the softmax runs beside it.
+// block are in flight while its tiles are waited for.  Up to D = 256 two or four blocks fit, and the score product
+// of the next block is issued before the weighted sum of the last, so the softmax runs beside it.
+//
+// What bounds it (D = 512, 64 heads, lists of 2048; 4096 tokens in 1.20 ms, 916 TFLOP/s, 48% of the measured
+// bf16 rate; the attention over bf16 rows reaches 595 TFLOP/s): a tensor-core instruction of these shapes takes 52 to 63
+// cycles whatever its 64 heads need (at 128 columns it does twice the work in 64), so a block's 64 instructions take
+// 3,650 cycles of its 4,700; the softmax (1,500) stands between the two products, because one block and
+// the 64 KB of q fill shared memory, and overlaps them in part.  At D = 256 and below a block takes 2,100 to
+// 2,300 cycles, the softmax's latency.  A unit costs 5,000 to 12,000 cycles beside its blocks (its q, its first
+// block's way in, its output).  Tried without gain: 8 softmax warps of 32 heads (registers), the next q brought
+// by the softmax warps or by asynchronous copies, two buffers of P, register shares moved between the roles.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -638,8 +647,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       if (lane == 0) mbar_arrive(o_empty);
       named_bar_sync(kTcEpiBar, kKv4SoftThreads);  // alpha_s and max_s are rewritten by the next unit
     }
-  } else {
-    if (warp >= 1) {
+  } else if (warp >= 1) {
     // ------------------------------------------------------------------ scout
     uint32_t gb = 0;
     int n = 0;
@@ -707,7 +715,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
         mbar_arrive(&scl_full[slot]);
       }
     }
-    } else {
+  } else {
     // ------------------------------------------------------------------ MMA issuer (the whole warp, one thread elected)
     const uint32_t on = elect_one();
     const auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
@@ -799,7 +807,6 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     mma_commit_if(on, drain);
     mbar_wait_drain(drain, 0);
     __syncwarp();
-    }
   }
 
   if (kSingle && shares > 1) {

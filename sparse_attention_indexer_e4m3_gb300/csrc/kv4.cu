@@ -55,10 +55,16 @@ cudaError_t launch_pages_reserve(const ReserveArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_pages_compact(const CompactArgs& a, int32_t* table, int64_t entries, cudaStream_t stream) {
+cudaError_t launch_pages_compact(CompactArgs a, int32_t* table, int64_t entries, cudaStream_t stream) {
+  // A small table in the same launch, a large one over all SMs in a second (16384 pages: 450 entries 7.6 to 7.9 us, 16384
+  // entries 8.0 to 8.0, 65536 9.3 to 8.5, 1 M 24.7 to 11.6; the second launch also costs the host 2 us).
+  constexpr int64_t kSmallTable = 1 << 14;
+  const bool small = entries <= kSmallTable;
+  a.table = small ? table : nullptr;
+  a.entries = small ? static_cast<int>(entries) : 0;
   pages_compact_kernel<<<kPagesCluster, kPagesThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || entries == 0) return e;
+  if (e != cudaSuccess || small) return e;
   const int grid = static_cast<int>(std::min<int64_t>((entries + 255) / 256, 1 << 16));
   pages_relabel_kernel<<<grid, 256, 0, stream>>>(table, entries, a.P, a.remap);
   return cudaGetLastError();

@@ -65,6 +65,8 @@ struct CompactArgs {
   int32_t* dst;    // [P / 2]
   int32_t* n_live; // [1]
   int32_t* remap;  // workspace [P]: new id of each page, -1 for a free one
+  int32_t* table;  // [entries], relabelled by the same kernel where it is small, else null
+  int entries;
 };
 
 // Page of row `pos` of sequence `seq`, or -1 where there is none.

@@ -45,8 +45,10 @@ int list_shares(int64_t units, int D, int K) {
   const int blocks = (K + kKv4Block - 1) / kKv4Block;
   const int worth = D == 512 ? 2 : 3;
   if (blocks <= worth || units > sparse_attn_kv4_clusters(D, 2)) return 1;
-  for (int each = (blocks + kKv4MaxShares - 1) / kKv4MaxShares; blocks - each >= worth; ++each) {
-    const int shares = (blocks + each - 1) / each;
+  for (int most = std::min(blocks, kKv4MaxShares); most > 1; --most) {
+    const int each = (blocks + most - 1) / most;
+    if (blocks - each < worth) break;
+    const int shares = (blocks + each - 1) / each;  // no more than it takes for `each` blocks per share
     if (units <= sparse_attn_kv4_clusters(D, shares)) return shares;
   }
   return 1;
@@ -175,7 +177,7 @@ dsa_status dsa_compact_pages(int32_t* table, int32_t* ref, int R, int M, int P, 
   if (P > 1 && (!src || !aligned(src, 4) || !dst || !aligned(dst, 4))) return DSA_ERR_INVALID_ARG;
   if (P > 0 && (!workspace || !aligned(workspace, 4) || workspace_bytes < dsa_compact_pages_workspace_size(P)))
     return DSA_ERR_WORKSPACE;
-  const CompactArgs a{ref, P, src, dst, n_live, static_cast<int32_t*>(workspace)};
+  const CompactArgs a{ref, P, src, dst, n_live, static_cast<int32_t*>(workspace), nullptr, 0};
   return done(launch_pages_compact(a, table, entries, static_cast<cudaStream_t>(stream)));
 }
 

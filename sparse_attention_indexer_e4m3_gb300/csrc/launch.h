@@ -66,7 +66,7 @@ cudaError_t launch_kv4_read(int D, uint16_t* out, int N, const int32_t* seq, con
 cudaError_t launch_pages_fork(const int32_t* table, const int32_t* parent, int R, int M, int P, int32_t* ref,
                               int32_t* out, cudaStream_t stream);
 cudaError_t launch_pages_reserve(const ReserveArgs& a, cudaStream_t stream);
-cudaError_t launch_pages_compact(const CompactArgs& a, int32_t* table, int64_t entries, cudaStream_t stream);
+cudaError_t launch_pages_compact(CompactArgs a, int32_t* table, int64_t entries, cudaStream_t stream);
 cudaError_t launch_pages_copy(uint8_t* pages, int64_t page_bytes, int P, const int32_t* src, const int32_t* dst, int n,
                               int sms, cudaStream_t stream);
 // Sparse attention over the 4-bit paged cache (D in {64, 128, 256, 512}); `shares` CTAs of a cluster

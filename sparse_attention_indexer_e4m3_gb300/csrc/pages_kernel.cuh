@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kPagesThreads) __cluster_dims__(kPagesCluster,
 
 // With L live pages, the k-th live page at or above L moves to the k-th free page below L.  (1) count the
 // live pages of each share; (2) the free pages below L and the live ones from L on; (3) their lists and
-// the map of the pages that stay; (4) the map of those that move, and the counts.
+// the map of the pages that stay; (4) the map of those that move, and the counts; (5) a small table.
 __global__ void __launch_bounds__(kPagesThreads) __cluster_dims__(kPagesCluster, 1, 1)
     pages_compact_kernel(const CompactArgs a) {
   __shared__ WarpCounts s;
@@ -277,9 +277,15 @@ __global__ void __launch_bounds__(kPagesThreads) __cluster_dims__(kPagesCluster,
     a.ref[to] = a.ref[from];
     a.ref[from] = 0;
   }
+  if (a.table == nullptr) return;
+  cluster_sync_all();
+  for (int i = gtid; i < a.entries; i += kPagesCluster * kPagesThreads) {
+    const int p = a.table[i];
+    a.table[i] = static_cast<unsigned>(p) < static_cast<unsigned>(a.P) ? a.remap[p] : -1;
+  }
 }
 
-// table[i] = remap[table[i]] (no page where it names none).
+// table[i] = remap[table[i]] (no page where it names none): a large table, over all SMs.
 __global__ void __launch_bounds__(256) pages_relabel_kernel(int32_t* __restrict__ table, int64_t n, int P,
                                                             const int32_t* __restrict__ remap) {
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {

@@ -35,7 +35,7 @@ def random_state(rng, R, M, P, fill=0.6, share=0.4, junk=True):
     return table, ref.astype(np.int32)
 
 
-SIZES = [(1, 1, 1), (1, 5, 3), (7, 9, 40), (33, 65, 900), (300, 31, 9000), (5, 700, 3000), (600, 3, 65537)]
+SIZES = [(1, 1, 1), (1, 5, 3), (7, 9, 40), (33, 65, 900), (300, 31, 9000), (5, 700, 3000), (600, 3, 65537), (700, 190, 20000)]
 
 
 @pytest.mark.parametrize("R,M,P", SIZES)
