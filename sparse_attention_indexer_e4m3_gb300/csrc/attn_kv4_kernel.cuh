@@ -25,7 +25,7 @@
 // block are in flight while its tiles are waited for.  Up to D = 256 two or four blocks fit, and the score product
 // of the next block is issued before the weighted sum of the last, so the softmax runs beside it.
 //
-// What bounds it (D = 512, 64 heads, lists of 2048; 4096 tokens in 1.20 ms, 916 TFLOP/s, 48% of the measured
+// What bounds it (D = 512, 64 heads, lists of 2048; 4096 tokens in 1.19 ms, 925 TFLOP/s, 48% of the measured
 // bf16 rate; the attention over bf16 rows reaches 595 TFLOP/s): a tensor-core instruction of these shapes takes 52 to 63
 // cycles whatever its 64 heads need (at 128 columns it does twice the work in 64), so a block's 64 instructions take
 // 3,650 cycles of its 4,700; the softmax (1,500) stands between the two products, because one block and
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
         const bool valid = rs > 0.f;
         const float a = to_log2 * rs;                    // score to log2 units
         const float lr = valid ? log2f(rs) : -INFINITY;  // a masked key's weight is 0
-        const float inv = valid ? 1.0f / rs : 0.f;
+        const float inv = valid ? rcp_approx(rs) : 0.f;  // (2^-23 off; a division took 1% of a long prompt)
         const uint64_t a2 = pack_f32x2(a, a), lr2 = pack_f32x2(lr, lr), inv2 = pack_f32x2(inv, inv);
         const uint32_t s_at = s_tmem + 64 * (gb % kSc) + lane_off + hb;
         mbar_wait(&s_full[gb % kSc], (gb / kSc) & 1u, abort_flag, err, 0x61);

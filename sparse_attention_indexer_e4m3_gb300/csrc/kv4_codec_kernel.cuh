@@ -47,12 +47,6 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
 }
 // Rounded to 12 significant bits (finite, not at the top of the range).
 __device__ __forceinline__ float round_12bits(float x) { return __uint_as_float((__float_as_uint(x) + 0x800u) & 0xFFFFF000u); }
-__device__ __forceinline__ float rcp_approx(float x) {  // off by at most 2^-23 of the reciprocal
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kKv4CodecThreads) kv4_write_kernel(const uint16_t* __restrict__ x, int N,
                                                                      const int32_t* __restrict__ seq,
