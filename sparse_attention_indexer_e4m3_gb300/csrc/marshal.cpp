@@ -263,6 +263,14 @@ PyObject* fork_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// n elements of a one-dimensional tensor from `at` on, sharing its memory.
+at::Tensor part_of(const at::Tensor& all, int64_t at, int64_t n) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(all.storage()), all.key_set(), all.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(n);
+  return t;
+}
+
 // The outputs src [n], dst [n] and one [1] and the workspace of a page call: the caller's where given.
 struct Lists {
   at::Tensor src, dst, one, ws;
@@ -280,10 +288,9 @@ struct Lists {
     // one allocation for what is left out, the workspace last
     const int64_t scratch = ws.defined() ? 0 : static_cast<int64_t>((need + 3) / 4);
     const at::Tensor all = w.make({2 * n + 1 + scratch}, at::kInt);
-    const at::AutoDispatchBelowADInplaceOrView below;
-    if (!src.defined()) src = all.as_strided({n}, {1}, 0);
-    if (!dst.defined()) dst = all.as_strided({n}, {1}, n);
-    if (!one.defined()) one = all.as_strided({1}, {1}, 2 * n);
+    if (!src.defined()) src = part_of(all, 0, n);
+    if (!dst.defined()) dst = part_of(all, n, n);
+    if (!one.defined()) one = part_of(all, 2 * n, 1);
     workspace = ws.defined() ? ws.data_ptr() : (need > 0 ? ptr<int32_t>(all) + 2 * n + 1 : nullptr);
     workspace_bytes = ws.defined() ? static_cast<size_t>(ws.numel()) : static_cast<size_t>(scratch) * 4;
   }
