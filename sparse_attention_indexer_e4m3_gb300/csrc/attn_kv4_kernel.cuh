@@ -77,8 +77,7 @@ struct AttnKv4Layout {
   static constexpr int kRed = kScl + kKv4Slots * kTcAttnKeys * 4;  // float [4][64] cross-warp scratch
   static constexpr int kMax = kRed + 4 * kTcAttnHeads * 4;      // float [64] running bound (log2 units)
   static constexpr int kAlpha = kMax + kTcAttnHeads * 4;        // float [64] rescale / output factors
-  static constexpr int kSum = kAlpha + kTcAttnHeads * 4;        // float [64] denominators (of this share)
-  static constexpr int kJoin = kSum + kTcAttnHeads * 4;         // float [shares][64] factors of the shares
+  static constexpr int kJoin = kAlpha + kTcAttnHeads * 4;       // float [shares][64] factors of the shares
   static constexpr int kMisc = kJoin + kKv4Shares * kTcAttnHeads * 4;  // int [32]
   static constexpr int kBar = kMisc + 128;
   static constexpr int kNumBars = 15 + 3 * kKv4Slots + 2 * kStages * kTiles;
@@ -219,7 +218,6 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   float* red_s = reinterpret_cast<float*>(smem + L::kRed);
   float* max_s = reinterpret_cast<float*>(smem + L::kMax);
   float* alpha_s = reinterpret_cast<float*>(smem + L::kAlpha);
-  float* sum_s = reinterpret_cast<float*>(smem + L::kSum);
   float* join_s = reinterpret_cast<float*>(smem + L::kJoin);
   // [0, 1] blocks of the units in flight, [2, 3] the bits of their q factors, [8..15] the convert warps' maxima,
   // [16..18] by block modulo 3: a bound has to be raised
@@ -598,7 +596,9 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       if (etid < kTcAttnHeads) {
         const float l = (red_s[etid] + red_s[kTcAttnHeads + etid]) + (red_s[2 * kTcAttnHeads + etid] + red_s[3 * kTcAttnHeads + etid]);
         if (kSingle && shares > 1) {
-          sum_s[etid] = l;
+          float* stats = p.partial_stats + (static_cast<int64_t>(u) * shares + share) * 2 * kTcAttnHeads;
+          __stcg(stats + etid, max_s[etid]);
+          __stcg(stats + kTcAttnHeads + etid, l);
         } else if (etid < nh) {
           alpha_s[etid] = softmax_factor(max_s[etid], l, p.sink, h0 + etid,
                                          p.lse != nullptr ? p.lse + static_cast<int64_t>(t) * H + h0 + etid : nullptr);
@@ -816,68 +816,68 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     const int t = unit0 / p.groups;
     const int h0 = (unit0 % p.groups) * kTcAttnHeads;
     const int nh = min(kTcAttnHeads, H - h0);
-    if (threadIdx.x < kTcAttnHeads) {
-      const int h = threadIdx.x;
-      float m[kKv4Shares], l[kKv4Shares];
-      float top = kKv4NoBound;
+    // This CTA's share of the group's [64][D] outputs, four dims at a time.  Partial outputs, bounds and sums pass
+    // through L2: read from the other CTAs' shared memory instead, 128 KB arrive at 13 bytes a clock (10,000 cycles at
+    // D = 512).  The first loads are in flight while the shares' factors are formed.
+    constexpr int kAll = kTcAttnHeads * D / 4;
+    constexpr int kPart = 8;  // partial outputs in flight per thread
+    const int per = (kAll + shares - 1) / shares;
+    const int end = min(min(kAll, (share + 1) * per), nh * (D / 4));
+    const float4* part = reinterpret_cast<const float4*>(p.partial) + static_cast<int64_t>(unit0) * shares * kAll;
+    const float* stats = p.partial_stats + static_cast<int64_t>(unit0) * shares * 2 * kTcAttnHeads;
+    uint16_t* out = p.out + (static_cast<int64_t>(t) * H + h0) * D;
+    int i = share * per + threadIdx.x;
+    float4 v[kPart];
+    const auto fetch = [&](int k0) {
 #pragma unroll
-      for (int i = 0; i < kKv4Shares; ++i) {
-        m[i] = kKv4NoBound;
-        l[i] = 0.f;
-        if (i < shares) {
-          m[i] = ld_cluster_f32(smem_addr(max_s + h), i);
-          l[i] = ld_cluster_f32(smem_addr(sum_s + h), i);
-        }
+      for (int k = 0; k < kPart; ++k) {
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < end && k0 + k < shares) v[k] = __ldcg(part + static_cast<int64_t>(k0 + k) * kAll + i);
       }
-#pragma unroll
-      for (int i = 0; i < kKv4Shares; ++i) top = fmaxf(top, m[i]);
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < kKv4Shares; ++i) {
-        m[i] = m[i] == kKv4NoBound ? 0.f : exp2f(m[i] - top);
-        sum = fmaf(l[i], m[i], sum);
-      }
-      float f = 0.f;
-      if (h < nh)
-        f = softmax_factor(top, sum, p.sink, h0 + h,
-                           p.lse != nullptr && share == 0 ? p.lse + static_cast<int64_t>(t) * H + h0 + h : nullptr);
-#pragma unroll
-      for (int i = 0; i < kKv4Shares; ++i) join_s[i * kTcAttnHeads + h] = m[i] * f;
+    };
+    fetch(0);
+    float* sum_s = reinterpret_cast<float*>(p_s);  // [shares][64] sums (P's place: every product is done)
+    for (int j = threadIdx.x; j < shares * kTcAttnHeads; j += kKv4Threads) {
+      const float* at = stats + (j / kTcAttnHeads) * 2 * kTcAttnHeads + j % kTcAttnHeads;
+      join_s[j] = __ldcg(at);
+      sum_s[j] = __ldcg(at + kTcAttnHeads);
     }
     __syncthreads();
-    // this CTA's share of the group's [64][D] outputs, four dims at a time.  The partial outputs pass through
-    // L2: read from the other CTAs' shared memory instead, 128 KB arrive at 13 bytes a clock (10,000 cycles at D = 512).
-    constexpr int kAll = kTcAttnHeads * D / 4;
-    const int per = (kAll + shares - 1) / shares;
-    const float4* part = reinterpret_cast<const float4*>(p.partial) + static_cast<int64_t>(unit0) * shares * kTcAttnHeads * (D / 4);
-    uint16_t* out = p.out + (static_cast<int64_t>(t) * H + h0) * D;
-    for (int i = share * per + threadIdx.x; i < min(kAll, (share + 1) * per); i += kKv4Threads) {
+    if (threadIdx.x < nh) {
+      const int h = threadIdx.x;
+      float top = kKv4NoBound, sum = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < shares; ++k) top = fmaxf(top, join_s[k * kTcAttnHeads + h]);
+#pragma unroll 4
+      for (int k = 0; k < shares; ++k) {
+        const float m = join_s[k * kTcAttnHeads + h];
+        const float w = m == kKv4NoBound ? 0.f : exp2f(m - top);
+        sum = fmaf(sum_s[k * kTcAttnHeads + h], w, sum);
+        join_s[k * kTcAttnHeads + h] = w;
+      }
+      alpha_s[h] = softmax_factor(top, sum, p.sink, h0 + h,
+                                  p.lse != nullptr && share == 0 ? p.lse + static_cast<int64_t>(t) * H + h0 + h : nullptr);
+    }
+    __syncthreads();
+    for (; i < end; i += kKv4Threads) {
       const int h = i / (D / 4);
-      if (h >= nh) break;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k0 = 0; k0 < shares; k0 += kPart) {
+        if (k0 > 0 || i >= share * per + kKv4Threads) fetch(k0);
 #pragma unroll
-      for (int k0 = 0; k0 < kKv4Shares; k0 += 8) {
-        if (k0 >= shares) break;
-        float4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (k0 + k < shares) v[k] = __ldcg(part + static_cast<int64_t>(k0 + k) * kTcAttnHeads * (D / 4) + i);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float f = k0 + k < shares ? join_s[(k0 + k) * kTcAttnHeads + h] : 0.f;
-          acc.x = fmaf(v[k].x, f, acc.x);
-          acc.y = fmaf(v[k].y, f, acc.y);
-          acc.z = fmaf(v[k].z, f, acc.z);
-          acc.w = fmaf(v[k].w, f, acc.w);
+        for (int k = 0; k < kPart; ++k) {
+          const float w = k0 + k < shares ? join_s[(k0 + k) * kTcAttnHeads + h] : 0.f;
+          acc.x = fmaf(v[k].x, w, acc.x);
+          acc.y = fmaf(v[k].y, w, acc.y);
+          acc.z = fmaf(v[k].z, w, acc.z);
+          acc.w = fmaf(v[k].w, w, acc.w);
         }
       }
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+      const float f = alpha_s[h];
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f), hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
       *reinterpret_cast<uint2*>(out + static_cast<int64_t>(i) * 4) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
-    cluster_sync_all();  // no CTA leaves while another reads its bounds and sums
   }
 
   tc_fence_before_sync();

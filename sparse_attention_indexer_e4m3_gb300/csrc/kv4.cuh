@@ -40,6 +40,7 @@ struct AttnKv4Params {
   uint16_t* out;          // [T][H][D] bf16
   float* lse;             // [T][H] or null
   float* partial;         // [unit][share][64][D] partial outputs where a list is shared
+  float* partial_stats;   // [unit][share][2][64] their bounds and sums
   int T, H, K;
   int groups;             // ceil(H / 64)
   float scale;

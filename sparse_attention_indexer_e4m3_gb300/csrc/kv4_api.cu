@@ -55,7 +55,7 @@ int list_shares(int64_t units, int D, int K) {
 }
 
 size_t partial_bytes(int64_t units, int shares, int D) {
-  return shares > 1 ? static_cast<size_t>(units) * shares * kTcMaxHeads * D * sizeof(float) : 0;
+  return shares > 1 ? static_cast<size_t>(units) * shares * kTcMaxHeads * (D + 2) * sizeof(float) : 0;
 }
 
 dsa_status done(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
@@ -122,8 +122,9 @@ dsa_status dsa_sparse_attn_kv4(const uint16_t* q, const uint8_t* cache, int P, i
   if (shares > 1 && (!workspace || !aligned(workspace, 16) || workspace_bytes < partial_bytes(units, shares, D)))
     return DSA_ERR_WORKSPACE;
   const int grid = shares > 1 ? static_cast<int>(units) * shares : static_cast<int>(std::min<int64_t>(units, dev.sms));
-  const AttnKv4Params p{q,   c,   seq, start, attn_sink, idx,    out, lse, shares > 1 ? static_cast<float*>(workspace) : nullptr,
-                        T,   H,   K,   groups, scale};
+  float* partial = shares > 1 ? static_cast<float*>(workspace) : nullptr;
+  float* stats = shares > 1 ? partial + units * shares * kTcMaxHeads * D : nullptr;
+  const AttnKv4Params p{q, c, seq, start, attn_sink, idx, out, lse, partial, stats, T, H, K, groups, scale};
   return done(launch_sparse_attn_kv4(D, grid, shares, p, dev.err, static_cast<cudaStream_t>(stream)));
 }
 

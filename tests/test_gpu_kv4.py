@@ -256,6 +256,29 @@ def test_attention_many_tokens(dsa, D, H, T):
         assert np.all(out[t] == 0.0) and np.allclose(lse[t], c.sink, rtol=2.0 ** -22)
 
 
+@pytest.mark.parametrize("D,H", [(64, 16), (128, 64), (256, 65), (512, 64)])
+def test_attention_mostly_empty_lists(dsa, D, H):
+    """Long runs of tokens without entries between tokens with one to three blocks."""
+    c = Case(31 + D, 1300, H, D, 300, 32, R=3, length=200, sink=True)
+    rng = c.rng
+    keep = rng.random(c.T) < 0.3
+    keep[400:800] = False
+    keep[1299] = True
+    c.idx[~keep] = -1
+    for t in np.flatnonzero(keep):
+        c.idx[t, rng.integers(1, 301):] = -1
+    out, lse = c.run(dsa)
+    assert np.all(out[~keep] == 0.0) and np.allclose(lse[~keep], c.sink, rtol=2.0 ** -22)
+    c.check(out, lse, rows=np.flatnonzero(keep)[::17])
+
+
+def test_attention_very_long_list(dsa):
+    """70,000 entries over 500 rows: every row counts about 140 times."""
+    c = Case(41, 2, 5, 128, 70000, 64, length=500)
+    c.idx[1, 65000:] = -1
+    c.check(*c.run(dsa))
+
+
 def test_attention_no_keys_at_all(dsa):
     c = Case(1, 3, 5, 128, 4, 16)
     c.idx[:] = -1
