@@ -60,13 +60,15 @@ cudaError_t launch_d(int grid, int shares, const AttnKv4Params& p, unsigned* err
   c.blockDim = dim3(kKv4Threads);
   c.dynamicSmemBytes = AttnKv4Layout<D>::kSmem;
   c.stream = stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(shares);
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  c.attrs = &attr;
-  c.numAttrs = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(shares);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (the kernel waits for the stream itself)
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = attr;
+  c.numAttrs = 2;
   return cudaLaunchKernelEx(&c, kernel, p, shares, err);
 }
 

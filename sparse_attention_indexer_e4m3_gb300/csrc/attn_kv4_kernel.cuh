@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  wait_stream();  // (the set-up above overlaps the end of the kernel before)
   const uint32_t tbase = *tmem_slot;
   const uint32_t s_tmem = tbase;
   const uint32_t o_tmem = tbase + 64 * L::kScores;

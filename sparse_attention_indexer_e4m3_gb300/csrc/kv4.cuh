@@ -19,6 +19,10 @@ namespace dsa {
 constexpr int kKv4Group = 16;      // values per e4m3 scale
 constexpr int kKv4MinExp = -100;   // smallest exponent of a row scale that the quantiser writes
 
+// Waits until the work before this kernel in its stream is complete and visible; nothing in global memory is
+// touched before it.
+__device__ __forceinline__ void wait_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Bytes of a held row of D values: codes, group scales, row scale.
 __host__ __device__ constexpr int kv4_row_bytes(int D) { return D / 2 + D / kKv4Group + 4; }
 

@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(kKv4CodecThreads) kv4_write_kernel(const uint1
   const int rows = 1 << c.log_rows;
   uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
   int page = -1, at = 0;
+  wait_stream();
   if (row < N) {
     at = __ldg(pos + row);
     page = __ldg(seq + row);
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(kKv4CodecThreads) kv4_read_kernel(uint16_t* __
   constexpr int kLanes = D / kKv4Group;
   const int64_t row = (static_cast<int64_t>(blockIdx.x) * kKv4CodecThreads + threadIdx.x) / kLanes;
   const int sub = threadIdx.x % kLanes;
+  wait_stream();
   if (row >= N) return;
   const int rows = 1 << c.log_rows;
   int at = __ldg(pos + row);

@@ -91,6 +91,7 @@ static_assert(kPagesThreads / 32 == 32 && kPagesWarps <= kPagesThreads, "one war
 __global__ void __launch_bounds__(256) pages_fork_kernel(const int32_t* __restrict__ table,
                                                          const int32_t* __restrict__ parent, int R, int M, int P,
                                                          int32_t* __restrict__ ref, int32_t* __restrict__ out) {
+  wait_stream();
   for (int r = blockIdx.y; r < R; r += gridDim.y) {
     const int p = __ldg(parent + r);
     const int32_t* now = table + static_cast<int64_t>(r) * M;
@@ -135,6 +136,7 @@ __device__ __forceinline__ int reserve_need(const ReserveArgs& a, int p) {
 __global__ void __launch_bounds__(kPagesThreads) __cluster_dims__(kPagesCluster, 1, 1)
     pages_reserve_kernel(const ReserveArgs a) {
   __shared__ WarpCounts s;
+  wait_stream();
   const uint32_t rank = cluster_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = static_cast<int>(rank) * (kPagesThreads / 32) + warp;
@@ -228,6 +230,7 @@ __global__ void __launch_bounds__(kPagesThreads) __cluster_dims__(kPagesCluster,
 __global__ void __launch_bounds__(kPagesThreads) __cluster_dims__(kPagesCluster, 1, 1)
     pages_compact_kernel(const CompactArgs a) {
   __shared__ WarpCounts s;
+  wait_stream();
   const uint32_t rank = cluster_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = static_cast<int>(rank) * (kPagesThreads / 32) + warp;
@@ -288,6 +291,7 @@ __global__ void __launch_bounds__(kPagesThreads) __cluster_dims__(kPagesCluster,
 // table[i] = remap[table[i]] (no page where it names none): a large table, over all SMs.
 __global__ void __launch_bounds__(256) pages_relabel_kernel(int32_t* __restrict__ table, int64_t n, int P,
                                                             const int32_t* __restrict__ remap) {
+  wait_stream();
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
     const int p = table[i];
     table[i] = static_cast<unsigned>(p) < static_cast<unsigned>(P) ? remap[p] : -1;
@@ -305,6 +309,7 @@ constexpr int kCopyPiece = kCopyThreads * kCopyUnroll * 16;
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(uint8_t* __restrict__ pages, int64_t page_bytes, int P,
                                                                   const int32_t* __restrict__ src,
                                                                   const int32_t* __restrict__ dst, int n, int pieces) {
+  wait_stream();
   for (int64_t w = blockIdx.x; w < static_cast<int64_t>(n) * pieces; w += gridDim.x) {
     const int i = static_cast<int>(w / pieces);
     const int64_t at = (w % pieces) * static_cast<int64_t>(kCopyPiece) + threadIdx.x * 16;
