@@ -173,7 +173,7 @@ __device__ __forceinline__ float softmax_factor(float m, float l, const float* s
   float f = keys ? 1.f : 0.f, unit = m;
   if (!keys) l = 0.f;
   if (sink != nullptr) {
-    const float s2 = __ldg(sink + h) * 1.4426950408889634f;
+    const float s2 = ld_after_wait(sink + h) * 1.4426950408889634f;
     if (keys && s2 - m <= 64.f) {
       l += exp2f(s2 - m);
     } else if (s2 != -INFINITY) {
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
           const int at = tid + (i0 + i) * kKv4ConvThreads;
           const int h = at / (D / 8), pc = at % (D / 8);
           v[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (h < nh) v[i] = __ldg(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * D) + pc);
+          if (h < nh) v[i] = ld_after_wait(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * D) + pc);
         }
         if (pass == 0 && i0 == 0) free();
 #pragma unroll
@@ -391,8 +391,8 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
           raw[i][k] = make_uint4(0u, 0u, 0u, 0u);
           grp[i][k] = 0u;
           if (ent.x >= 0 && has_part) {
-            raw[i][k] = __ldg(reinterpret_cast<const uint4*>(codes + i * 128));
-            grp[i][k] = __ldg(reinterpret_cast<const uint16_t*>(scales + i * 16));
+            raw[i][k] = ld_after_wait(reinterpret_cast<const uint4*>(codes + i * 128));
+            grp[i][k] = ld_after_wait(reinterpret_cast<const uint16_t*>(scales + i * 16));
           }
         }
       }
@@ -655,14 +655,14 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     for (int u = unit0; u < (kSingle ? unit0 + 1 : units); u += unit_step, ++n) {
       const int t = u / p.groups;
       const int32_t* list = p.idx + static_cast<int64_t>(t) * p.K;
-      const int seq = __ldg(p.seq + t);
-      const int start = p.start != nullptr ? __ldg(p.start + t) : 0;
+      const int seq = ld_after_wait(p.seq + t);
+      const int start = p.start != nullptr ? ld_after_wait(p.start + t) : 0;
       // blocks to walk: up to the last entry that names a row, looked for from the end
       int last = -1;
       for (int j0 = (p.K - 1) / 256 * 256; j0 >= 0 && last < 0; j0 -= 256) {
         int v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = j0 + 32 * i + lane < p.K ? __ldg(list + j0 + 32 * i + lane) : -1;
+        for (int i = 0; i < 8; ++i) v[i] = j0 + 32 * i + lane < p.K ? ld_after_wait(list + j0 + 32 * i + lane) : -1;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (v[i] >= 0) last = j0 + 32 * i + lane;
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int j = (blk0 + b) * kTcAttnKeys + 32 * i + lane;
-          ent[i].x = j < p.K ? __ldg(list + j) : -1;
+          ent[i].x = j < p.K ? ld_after_wait(list + j) : -1;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
         for (int i = 0; i < 4; ++i) {
           r[i] = 0.0f;
           if (ent[i].x >= 0)
-            r[i] = __ldg(reinterpret_cast<const float*>(p.pool.cache + ent[i].x * page_bytes +
+            r[i] = ld_after_wait(reinterpret_cast<const float*>(p.pool.cache + ent[i].x * page_bytes +
                                                         rows * (D / 2 + D / kKv4Group)) + ent[i].y);
         }
         if (gb >= kKv4Slots) mbar_wait(&ent_empty[slot], (gb / kKv4Slots - 1) & 1u, abort_flag, err, 0x45);

@@ -23,6 +23,14 @@ constexpr int kKv4MinExp = -100;   // smallest exponent of a row scale that the 
 // touched before it.
 __device__ __forceinline__ void wait_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// An ordinary load.  Not __ldg, and no const __restrict__ parameters: those promise memory that does not change while
+// the kernel runs, and a kernel that starts before the work it waits for is done may not promise that (the
+// compiler could move such a load ahead of wait_stream()).
+template <class T>
+__device__ __forceinline__ T ld_after_wait(const T* p) {
+  return *p;
+}
+
 // Bytes of a held row of D values: codes, group scales, row scale.
 __host__ __device__ constexpr int kv4_row_bytes(int D) { return D / 2 + D / kKv4Group + 4; }
 
@@ -77,7 +85,7 @@ struct CompactArgs {
 // Page of row `pos` of sequence `seq`, or -1 where there is none.
 __device__ __forceinline__ int kv4_page(const Kv4Pool& c, int seq, int pos) {
   if (static_cast<unsigned>(seq) >= static_cast<unsigned>(c.R) || pos < 0 || (pos >> c.log_rows) >= c.M) return -1;
-  const int page = __ldg(c.table + static_cast<int64_t>(seq) * c.M + (pos >> c.log_rows));
+  const int page = ld_after_wait(c.table + static_cast<int64_t>(seq) * c.M + (pos >> c.log_rows));
   return static_cast<unsigned>(page) < static_cast<unsigned>(c.P) ? page : -1;
 }
 

@@ -37,12 +37,14 @@ dsa_status check_tables(int R, int M, int P) {
   return DSA_OK;
 }
 
+int head_groups(int H) { return H / kTcMaxHeads + (H % kTcMaxHeads != 0 ? 1 : 0); }
+
 // CTAs that share a unit's list: as few blocks per share as the device has clusters for, all units at once.  Joining the shares
 // takes as long as two to three blocks do, so a list is shared where at least that many of its blocks go to other CTAs
 // (one token, 64 heads, shared against not: D = 128, 3 blocks 10.5 to 10.3 us, 4 blocks 10.5 to 11.4, 16 blocks
 // 10.9 to 24.2; D = 512, 2 blocks 16.2 to 15.2 us, 4 blocks 15.6 to 21.1, 16 blocks 15.4 to 55.0).
 int list_shares(int64_t units, int D, int K) {
-  const int blocks = (K + kKv4Block - 1) / kKv4Block;
+  const int blocks = K / kKv4Block + (K % kKv4Block != 0 ? 1 : 0);
   const int worth = D == 512 ? 2 : 3;
   if (blocks <= worth || units > sparse_attn_kv4_clusters(D, 2)) return 1;
   for (int most = std::min(blocks, kKv4MaxShares); most > 1; --most) {
@@ -95,7 +97,7 @@ dsa_status dsa_dequantize_kv4(const uint8_t* cache, int P, int page_rows, const 
 
 size_t dsa_sparse_attn_kv4_workspace_size(int T, int H, int D, int K) {
   if (T <= 0 || H < 1 || K <= 0 || !kv4_d(D)) return 0;
-  const int64_t units = static_cast<int64_t>(T) * ((H + kTcMaxHeads - 1) / kTcMaxHeads);
+  const int64_t units = static_cast<int64_t>(T) * head_groups(H);
   return partial_bytes(units, list_shares(units, D, K), D);
 }
 
@@ -112,7 +114,7 @@ dsa_status dsa_sparse_attn_kv4(const uint16_t* q, const uint8_t* cache, int P, i
   if (K > 0 && (!idx || !aligned(idx, 4))) return DSA_ERR_INVALID_ARG;
   if ((start && !aligned(start, 4)) || (attn_sink && !aligned(attn_sink, 4)) || (lse && !aligned(lse, 4)))
     return DSA_ERR_INVALID_ARG;
-  const int groups = (H + kTcMaxHeads - 1) / kTcMaxHeads;
+  const int groups = head_groups(H);
   const int64_t units = static_cast<int64_t>(T) * groups;
   if (units > INT_MAX / 2 || K > INT_MAX / 2) return DSA_ERR_UNSUPPORTED;
   DeviceFacts dev;

@@ -29,9 +29,10 @@ constexpr int kKv4CodecThreads = 256;
 
 // 32 contiguous bytes (32-byte aligned) in one access, not kept in L1.
 __device__ __forceinline__ void ld_32(const void* p, uint32_t (&v)[8]) {
-  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "l"(p));
+               : "l"(p)
+               : "memory");
 }
 __device__ __forceinline__ void st_32(void* p, const uint32_t (&v)[8]) {
   asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
@@ -48,9 +49,9 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
 // Rounded to 12 significant bits (finite, not at the top of the range).
 __device__ __forceinline__ float round_12bits(float x) { return __uint_as_float((__float_as_uint(x) + 0x800u) & 0xFFFFF000u); }
 template <int D>
-__global__ void __launch_bounds__(kKv4CodecThreads) kv4_write_kernel(const uint16_t* __restrict__ x, int N,
-                                                                     const int32_t* __restrict__ seq,
-                                                                     const int32_t* __restrict__ pos, Kv4Pool c) {
+__global__ void __launch_bounds__(kKv4CodecThreads) kv4_write_kernel(const uint16_t* x, int N,
+                                                                     const int32_t* seq,
+                                                                     const int32_t* pos, Kv4Pool c) {
   constexpr int kLanes = D / kKv4Group;  // lanes per row
   const int64_t row = (static_cast<int64_t>(blockIdx.x) * kKv4CodecThreads + threadIdx.x) / kLanes;
   const int sub = threadIdx.x % kLanes;
@@ -59,8 +60,8 @@ __global__ void __launch_bounds__(kKv4CodecThreads) kv4_write_kernel(const uint1
   int page = -1, at = 0;
   wait_stream();
   if (row < N) {
-    at = __ldg(pos + row);
-    page = __ldg(seq + row);
+    at = ld_after_wait(pos + row);
+    page = ld_after_wait(seq + row);
     ld_32(x + row * D + sub * kKv4Group, w);
     page = kv4_page(c, page, at);
     at &= rows - 1;
@@ -106,17 +107,17 @@ __global__ void __launch_bounds__(kKv4CodecThreads) kv4_write_kernel(const uint1
 }
 
 template <int D>
-__global__ void __launch_bounds__(kKv4CodecThreads) kv4_read_kernel(uint16_t* __restrict__ out, int N,
-                                                                    const int32_t* __restrict__ seq,
-                                                                    const int32_t* __restrict__ pos, Kv4Pool c) {
+__global__ void __launch_bounds__(kKv4CodecThreads) kv4_read_kernel(uint16_t* out, int N,
+                                                                    const int32_t* seq,
+                                                                    const int32_t* pos, Kv4Pool c) {
   constexpr int kLanes = D / kKv4Group;
   const int64_t row = (static_cast<int64_t>(blockIdx.x) * kKv4CodecThreads + threadIdx.x) / kLanes;
   const int sub = threadIdx.x % kLanes;
   wait_stream();
   if (row >= N) return;
   const int rows = 1 << c.log_rows;
-  int at = __ldg(pos + row);
-  const int page = kv4_page(c, __ldg(seq + row), at);
+  int at = ld_after_wait(pos + row);
+  const int page = kv4_page(c, ld_after_wait(seq + row), at);
   at &= rows - 1;
   uint2 raw = make_uint2(0u, 0u);
   uint32_t s8 = 0u;

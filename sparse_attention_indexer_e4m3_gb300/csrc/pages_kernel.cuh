@@ -88,18 +88,18 @@ static_assert(kPagesThreads / 32 == 32 && kPagesWarps <= kPagesThreads, "one war
 
 // out[r] = table[parent[r]] (no pages where parent[r] is outside [0, R)); ref follows the entries that
 // change.  One thread per entry: the bytes of the two tables and of the counts bound it.
-__global__ void __launch_bounds__(256) pages_fork_kernel(const int32_t* __restrict__ table,
-                                                         const int32_t* __restrict__ parent, int R, int M, int P,
-                                                         int32_t* __restrict__ ref, int32_t* __restrict__ out) {
+__global__ void __launch_bounds__(256) pages_fork_kernel(const int32_t* table,
+                                                         const int32_t* parent, int R, int M, int P,
+                                                         int32_t* ref, int32_t* out) {
   wait_stream();
   for (int r = blockIdx.y; r < R; r += gridDim.y) {
-    const int p = __ldg(parent + r);
+    const int p = ld_after_wait(parent + r);
     const int32_t* now = table + static_cast<int64_t>(r) * M;
     const bool some = static_cast<unsigned>(p) < static_cast<unsigned>(R);
     const int32_t* from = table + static_cast<int64_t>(some ? p : 0) * M;
     for (int64_t j = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; j < M; j += static_cast<int64_t>(gridDim.x) * 256) {
-      const int a = __ldg(now + j);
-      const int b = some ? __ldg(from + j) : -1;
+      const int a = ld_after_wait(now + j);
+      const int b = some ? ld_after_wait(from + j) : -1;
       out[static_cast<int64_t>(r) * M + j] = b;
       if (a != b) {
         if (static_cast<unsigned>(b) < static_cast<unsigned>(P)) atomicAdd(ref + b, 1);
@@ -113,8 +113,8 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(const int32_t* __restri
 
 // Page span [first, last] that rows [begin, end) of sequence r cover (last < first: none).
 __device__ __forceinline__ void reserve_span(const ReserveArgs& a, int r, int64_t& b, int64_t& e, int& first, int& last) {
-  b = max(0, __ldg(a.begin + r));
-  e = min(static_cast<int64_t>(__ldg(a.end + r)), static_cast<int64_t>(a.M) << a.log_rows);
+  b = max(0, ld_after_wait(a.begin + r));
+  e = min(static_cast<int64_t>(ld_after_wait(a.end + r)), static_cast<int64_t>(a.M) << a.log_rows);
   first = 0;
   last = -1;
   if (e > b) {
@@ -289,8 +289,8 @@ __global__ void __launch_bounds__(kPagesThreads) __cluster_dims__(kPagesCluster,
 }
 
 // table[i] = remap[table[i]] (no page where it names none): a large table, over all SMs.
-__global__ void __launch_bounds__(256) pages_relabel_kernel(int32_t* __restrict__ table, int64_t n, int P,
-                                                            const int32_t* __restrict__ remap) {
+__global__ void __launch_bounds__(256) pages_relabel_kernel(int32_t* table, int64_t n, int P,
+                                                            const int32_t* remap) {
   wait_stream();
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
     const int p = table[i];
@@ -306,14 +306,14 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 4;
 constexpr int kCopyPiece = kCopyThreads * kCopyUnroll * 16;
 
-__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(uint8_t* __restrict__ pages, int64_t page_bytes, int P,
-                                                                  const int32_t* __restrict__ src,
-                                                                  const int32_t* __restrict__ dst, int n, int pieces) {
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(uint8_t* pages, int64_t page_bytes, int P,
+                                                                  const int32_t* src,
+                                                                  const int32_t* dst, int n, int pieces) {
   wait_stream();
   for (int64_t w = blockIdx.x; w < static_cast<int64_t>(n) * pieces; w += gridDim.x) {
     const int i = static_cast<int>(w / pieces);
     const int64_t at = (w % pieces) * static_cast<int64_t>(kCopyPiece) + threadIdx.x * 16;
-    const int from = __ldg(src + i), to = __ldg(dst + i);
+    const int from = ld_after_wait(src + i), to = ld_after_wait(dst + i);
     if (static_cast<unsigned>(from) >= static_cast<unsigned>(P) || static_cast<unsigned>(to) >= static_cast<unsigned>(P) ||
         from == to)
       continue;
