@@ -61,6 +61,7 @@ def lib():
     lib.dsa_quantize_kv4.argtypes = [p, p, p, i, i, p, i, i, p, i, i, p]
     lib.dsa_dequantize_kv4.argtypes = [p, i, i, p, i, i, p, p, i, i, p, p]
     lib.dsa_sparse_attn_kv4.argtypes = [p, p, i, i, p, i, i, p, p, p, p, i, i, i, i, ctypes.c_float, p, p, p, sz, p]
+    lib.dsa_sparse_attn_kv4_workspace_size.argtypes, lib.dsa_sparse_attn_kv4_workspace_size.restype = [i] * 4, sz
     lib.dsa_fork_pages.argtypes = [p, p, i, i, i, p, p, p]
     lib.dsa_reserve_pages.argtypes = [p, p, p, p, i, i, i, i, p, p, p, p, sz, p]
     lib.dsa_reserve_pages_workspace_size.restype = lib.dsa_compact_pages_workspace_size.restype = sz
@@ -113,6 +114,15 @@ def test_attention_refusals(lib, mem):
     assert f(q=None) == f(out=None) == f(seq=None) == f(idx=None) == f(cache=None) == f(table=None) == INVALID
     assert f(q=a + 8) == f(cache=a + 4) == f(out=a + 1) == f(start=a + 1) == f(sink=a + 2) == f(lse=a + 1) == f(idx=a + 2) == INVALID
     assert f(T=0, q=None, out=None, seq=None, idx=None) == OK
+
+
+def test_attention_workspace_of_extreme_counts(lib):
+    """Head and block counts near the largest int neither wrap nor ask for memory: so many units share no list."""
+    top = 2 ** 31 - 1
+    for T, H, K in [(1, top, 2048), (1, top - 63, top), (top, top, top), (3, top - 1, 1)]:
+        for D in (64, 128, 256, 512):
+            assert lib.dsa_sparse_attn_kv4_workspace_size(T, H, D, K) == 0
+    assert lib.dsa_sparse_attn_kv4_workspace_size(0, 64, 128, 64) == lib.dsa_sparse_attn_kv4_workspace_size(1, 64, 96, 64) == 0
 
 
 def test_page_call_refusals(lib, mem):
