@@ -7,8 +7,14 @@
 // exactly (times a power of two of the token where its largest value is not in [1, 2^15), values more than
 // 2^29 below the largest rounded); the weights enter the second product as w_j = r_j * 2^(y_j - m), y = x log2 e,
 // rounded to fp16 (half a step, 2^-11), with m a bound on y_j + log2 r_j so that w_j <= 2^8 whatever the
-// row scales are.  The denominator sums w_j / r_j in fp32.  fp16 weights rather than bf16 ones because
-// their rounding would otherwise be as large as the output's own.
+// row scales are.  fp16 weights rather than bf16 ones because their rounding would otherwise be as large as the
+// output's own.
+// The denominator is the sum of 2^(y_j - m) in fp32.  Its terms are w_j / r_j, without a second exponential, as long
+// as none is lost where w_j underflows: m is at most (the largest y) + log2 of (the largest row scale so far), so with row
+// scales within 2^100 of one another a row whose w_j is below 2^-126 has a weight below 2^-26 of the largest.  A
+// block with row scales further below the largest so far (rows of zeros, held with r = 2^-100, beside rows of 2^11
+// or more) forms its terms by an exponential of their own, which may be subnormal: y_j - m lies between -125 (at least for
+// the largest y: m is at most 117 and the 2^8 above it) and 108, so they keep 24 bits below the largest and do not overflow.
 //
 // A unit is (token, group of up to 64 heads, share of the token's list); a cluster of S CTAs shares
 // one list and joins its S partial results, so a call with few tokens still uses most SMs and needs no second
@@ -58,6 +64,7 @@ constexpr int kKv4Scouts = 3;             // scout warps; one of them looks up e
 constexpr int kKv4Slots = 2 * kKv4Scouts; // blocks whose entries are looked up ahead (a slot is always one scout's)
 constexpr int kKv4Shares = kKv4MaxShares; // most CTAs that share a list
 constexpr float kKv4NoBound = -1e30f;     // bound of a head without keys so far
+constexpr float kKv4Spread = 1.2676506002282294e30f;  // 2^100: row scales within it share the weights' exponentials
 
 template <int D>
 struct AttnKv4Layout {
@@ -79,7 +86,8 @@ struct AttnKv4Layout {
   static constexpr int kAlpha = kMax + kTcAttnHeads * 4;        // float [64] rescale / output factors
   static constexpr int kJoin = kAlpha + kTcAttnHeads * 4;       // float [shares][64] factors of the shares
   static constexpr int kMisc = kJoin + kKv4Shares * kTcAttnHeads * 4;  // int [32]
-  static constexpr int kBar = kMisc + 128;
+  static constexpr int kLargest = kMisc + 128;                  // float [softmax warps]
+  static constexpr int kBar = kLargest + kKv4SoftWarps * 4;
   static constexpr int kNumBars = 15 + 3 * kKv4Slots + 2 * kStages * kTiles;
   static constexpr int kSmem = kBar + kNumBars * 8 + 1024;      // + alignment slack
   // tensor memory: S^T (kScores of them) from column 0, O^T tile m from column 64 (kScores + m)
@@ -165,6 +173,13 @@ __device__ __forceinline__ void xpose_reduce16(float (&v)[16], int lane, Op op) 
   v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
+// 2^x, subnormal results included.
+__device__ __forceinline__ float exp2_gradual(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Output factor of a head whose weights' bound is m (log2 units) and whose denominator, in units of
 // 2^m, is l without the sink; writes the natural log of the whole denominator where lse is given.  0 for
 // a head without keys (m = kKv4NoBound) and sink.  The larger of bound and sink is the unit, so neither overflows.
@@ -220,8 +235,11 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   float* alpha_s = reinterpret_cast<float*>(smem + L::kAlpha);
   float* join_s = reinterpret_cast<float*>(smem + L::kJoin);
   // [0, 1] blocks of the units in flight, [2, 3] the bits of their q factors, [8..15] the convert warps' maxima,
-  // [16..18] by block modulo 3: a bound has to be raised
+  // [16..18] by block modulo 3: a bound has to be raised, [20..31] by slot: its smallest and largest row scale
   volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMisc);
+  float2* span_s = reinterpret_cast<float2*>(smem + L::kMisc + 80);
+  float* largest_s = reinterpret_cast<float*>(smem + L::kLargest);
+  static_assert(kKv4Slots <= 6, "spans of the slots lie behind the flags");
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   // (a barrier that its waiters may lag behind by more than a phase is a pair, or one per stage)
   uint64_t* q_full = bars + 0;  // [2]
@@ -474,17 +492,24 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       for (int h = 0; h < kKv4SoftHeads / 2; ++h) lsum[h] = 0ull;
       named_bar_sync(kTcEpiBar, kKv4SoftThreads);
       if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
+      volatile float* largest = largest_s + (warp - 4);  // row scale of the unit so far (this warp's, all lanes alike)
+      *largest = 0.f;
       for (int b = 0; b < nb; ++b, ++gb) {
         const uint32_t slot = gb % kKv4Slots;
         mbar_wait(&scl_full[slot], (gb / kKv4Slots) & 1u, abort_flag, err, 0x65);
         const float rs = scl_s[slot * kTcAttnKeys + r];
+        const float2 span = span_s[slot];
+        const float most = fmaxf(*largest, span.y);
+        *largest = most;
+        const bool apart = most > span.x * kKv4Spread;  // some row's weight may underflow
         __syncwarp();
         if (lane == 0) mbar_arrive(&ent_empty[slot]);
         const bool valid = rs > 0.f;
         const float a = to_log2 * rs;                    // score to log2 units
         const float lr = valid ? log2f(rs) : -INFINITY;  // a masked key's weight is 0
-        const float inv = valid ? rcp_approx(rs) : 0.f;  // (2^-23 off; a division took 1% of a long prompt)
-        const uint64_t a2 = pack_f32x2(a, a), lr2 = pack_f32x2(lr, lr), inv2 = pack_f32x2(inv, inv);
+        // what makes a weight a term of the denominator (2^-23 off; a division took 1% of a long prompt), or -1
+        float inv = apart ? -1.f : (valid ? rcp_approx(rs) : 0.f);
+        const uint64_t a2 = pack_f32x2(a, a), lr2 = pack_f32x2(lr, lr);
         const uint32_t s_at = s_tmem + 64 * (gb % kSc) + lane_off + hb;
         mbar_wait(&s_full[gb % kSc], (gb / kSc) & 1u, abort_flag, err, 0x61);
         tc_fence_after_sync();
@@ -519,8 +544,9 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
         };
         // A unit's first block sets the bounds.  After that the weights are formed with the bounds as they are,
         // while the warps tell one another whether an exponent exceeds its bound by more than 2^8; if one
-        // does, which is rare, the bounds are raised and the weights formed again.
-        bool raise = b == 0;
+        // does, which is rare, the bounds are raised and the weights formed again.  (A block with row scales far apart, which is
+        // rare too, goes the same way: one branch less for all others.)
+        bool raise = b == 0 || apart;
         if (!raise) {
           exponents();
           float over = x[0];
@@ -552,36 +578,46 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
                                    fmaxf(red_s[2 * kTcAttnHeads + etid], red_s[3 * kTcAttnHeads + etid]));
             const float mo = max_s[etid];
             const float mn = (bm > mo + kTcLazyLog2) ? bm : mo;
-            alpha_s[etid] = (mo == kKv4NoBound || mn == mo) ? 1.f : exp2f(mo - mn);
+            // (the root of the factor: a sum may be as large as 2^100 times the bound's unit and is not to be lost)
+            alpha_s[etid] = (mo == kKv4NoBound || mn == mo) ? 1.f : exp2f(0.5f * (mo - mn));
             max_s[etid] = mn;
           }
           named_bar_sync(kTcEpiBar, kKv4SoftThreads);
+          // the previous weighted sum has read P and written O (known already where the bounds were checked)
+          if (gb > 0) mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x62);
           if (b > 0) {
             // sums and output accumulators of earlier blocks follow the new bound (this thread: its dim row r
             // of every tile, its 16 head columns)
 #pragma unroll
-            for (int h = 0; h < kKv4SoftHeads; h += 2)
-              lsum[h / 2] = fma_f32x2(lsum[h / 2], pack_f32x2(alpha_s[hb + h], alpha_s[hb + h + 1]), 0ull);
+            for (int h = 0; h < kKv4SoftHeads; h += 2) {
+              const uint64_t root = pack_f32x2(alpha_s[hb + h], alpha_s[hb + h + 1]);
+              lsum[h / 2] = fma_f32x2(fma_f32x2(lsum[h / 2], root, 0ull), root, 0ull);
+            }
             tc_fence_after_sync();
 #pragma unroll 1
             for (int m = 0; m < kTi; ++m) {
               tmem_ld_x16(o_tmem + lane_off + 64 * m + hb, x);
               tmem_wait_ld_regs16(x);
 #pragma unroll
-              for (int j = 0; j < kKv4SoftHeads; ++j) x[j] *= alpha_s[hb + j];
+              for (int j = 0; j < kKv4SoftHeads; ++j) x[j] = x[j] * alpha_s[hb + j] * alpha_s[hb + j];
               tmem_st_x16(o_tmem + lane_off + 64 * m + hb, x);
             }
             tmem_wait_st();
-          } else if (gb > 0) {
-            mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x62);
           }
           exponents();
           weights();
+          if (inv < 0.f) {  // the denominator's terms by themselves, from the same exponents (the scores are still there)
+            exponents();
+#pragma unroll
+            for (int h = 0; h < kKv4SoftHeads; ++h) x[h] = lr > -INFINITY ? exp2_gradual(x[h] - lr) : 0.f;
+            inv = 1.f;
+          }
         }
         fence_proxy_async_shared();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
+        const uint64_t inv2 = pack_f32x2(inv, inv);
 #pragma unroll
         for (int h = 0; h < kKv4SoftHeads; h += 2) lsum[h / 2] = fma_f32x2(pack_f32x2(x[h], x[h + 1]), inv2, lsum[h / 2]);
       }
@@ -711,8 +747,18 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
 #pragma unroll
         for (int i = 0; i < 4; ++i) ent_s[slot * kTcAttnKeys + 32 * i + lane] = ent[i];
         mbar_arrive(&ent_full[slot]);
+        uint32_t lo = 0x7F7FFFFFu, hi = 0u;  // the block's row scales (as bits: they are positive)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) scl_s[slot * kTcAttnKeys + 32 * i + lane] = fmaxf(r[i], ent[i].x >= 0 ? kKv4MinScale : 0.0f);
+        for (int i = 0; i < 4; ++i) {
+          r[i] = ent[i].x >= 0 ? fmaxf(r[i], kKv4MinScale) : 0.0f;
+          if (ent[i].x >= 0) lo = min(lo, __float_as_uint(r[i]));
+          hi = max(hi, __float_as_uint(r[i]));
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) scl_s[slot * kTcAttnKeys + 32 * i + lane] = r[i];
+        if (lane == 0) span_s[slot] = make_float2(__uint_as_float(lo), __uint_as_float(hi));
         mbar_arrive(&scl_full[slot]);
       }
     }
@@ -852,9 +898,9 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
 #pragma unroll 4
       for (int k = 0; k < shares; ++k) {
         const float m = join_s[k * kTcAttnHeads + h];
-        const float w = m == kKv4NoBound ? 0.f : exp2f(m - top);
-        sum = fmaf(sum_s[k * kTcAttnHeads + h], w, sum);
-        join_s[k * kTcAttnHeads + h] = w;
+        const float root = m == kKv4NoBound ? 0.f : exp2f(0.5f * (m - top));  // (as where a bound is raised)
+        sum = fmaf(sum_s[k * kTcAttnHeads + h] * root, root, sum);
+        join_s[k * kTcAttnHeads + h] = root * root;
       }
       alpha_s[h] = softmax_factor(top, sum, p.sink, h0 + h,
                                   p.lse != nullptr && share == 0 ? p.lse + static_cast<int64_t>(t) * H + h0 + h : nullptr);
