@@ -63,7 +63,7 @@ constexpr int kKv4Threads = 32 * (kKv4FirstConv + kKv4ConvWarps);
 constexpr int kKv4Scouts = 3;             // scout warps; one of them looks up every third block
 constexpr int kKv4Slots = 2 * kKv4Scouts; // blocks whose entries are looked up ahead (a slot is always one scout's)
 constexpr int kKv4Shares = kKv4MaxShares; // most CTAs that share a list
-constexpr float kKv4NoBound = -1e30f;     // bound of a head without keys so far
+constexpr float kKv4NoBound = -3e38f;     // bound of a head without keys so far (finite: a masked key is minus infinity)
 constexpr float kKv4Spread = 1.2676506002282294e30f;  // 2^100: row scales within it share the weights' exponentials
 
 template <int D>

@@ -79,3 +79,21 @@ def test_attention_sequence_of_growing_rows(dsa):  # noqa: F811
         c.idx[:] = np.sort(c.rng.integers(0, c.length, c.idx.shape), axis=1)
         c.scale *= 2.0 ** -119
         c.check(*c.run(dsa), rows=range(0, T, 23))
+
+
+# ------------------------------------------------------------------------------------ scores
+
+
+@pytest.mark.parametrize("T,K", [(2, 1), (2, 900), (170, 1)])
+def test_attention_very_negative_scores(dsa, T, K):  # noqa: F811
+    """A key whose score is -1e33 or so (q 2^60, kv -2^55, scale 0.05) is a key: alone in its list it has all the weight."""
+    c = Case(T + K, T, 10, 128, K, 32, start=False)
+    for s in range(c.R):
+        hold(c, s, -np.abs(c.rng.standard_normal((c.length, c.D))) * 2.0 ** 55)
+    c.q_t, c.q = bf16(np.abs(c.q) * 2.0 ** 60)
+    c.idx[:, 1:] = -1
+    if K > 1:
+        c.idx[1] = np.roll(c.idx[1], K - 1)  # the only entry is the last
+    out, lse = c.run(dsa)
+    assert np.all(lse < -1e31)
+    c.check(out, lse, rows=range(0, T, 13))
