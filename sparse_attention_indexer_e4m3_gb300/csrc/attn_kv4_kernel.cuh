@@ -3,9 +3,9 @@
 // exact fp16 values s * c of kv4.cuh):
 //     x_j = scale * q[t,h,:] . kv_j
 //     out[t,h,:] = sum_j e^{x_j} kv_j / ( sum_j e^{x_j} + e^{sink[h]} )
-// Both products run on fp16 operands with fp32 accumulators.  v_j is exact; q is bf16 and becomes fp16
-// exactly (times a power of two of the token where its largest value is not in [1, 2^15), values more than
-// 2^29 below the largest rounded); the weights enter the second product as w_j = r_j * 2^(y_j - m), y = x log2 e,
+// Both products run on fp16 operands with fp32 accumulators.  v_j is exact; q is bf16 and becomes fp16 times a
+// power of two of its head, each value off by at most 2^-29 of the head's largest (those down to 2^-21 of it not at all);
+// the weights enter the second product as w_j = r_j * 2^(y_j - m), y = x log2 e,
 // rounded to fp16 (half a step, 2^-11), with m a bound on y_j + log2 r_j so that w_j <= 2^8 whatever the
 // row scales are.  fp16 weights rather than bf16 ones because their rounding would otherwise be as large as the
 // output's own.
@@ -64,6 +64,9 @@ constexpr int kKv4Scouts = 3;             // scout warps; one of them looks up e
 constexpr int kKv4Slots = 2 * kKv4Scouts; // blocks whose entries are looked up ahead (a slot is always one scout's)
 constexpr int kKv4Shares = kKv4MaxShares; // most CTAs that share a list
 constexpr float kKv4NoBound = -3e38f;     // bound of a head without keys so far (finite: a masked key is minus infinity)
+// q enters as 2^kKv4QExp of itself where the largest value of its head has an exponent in [kKv4QLow, kKv4QHigh] (ordinary q;
+// every value is then off by at most 2^-25 / 2^8, 2^-29 of the head's largest), else by the head's own power of two.
+constexpr int kKv4QExp = 8, kKv4QLow = -4, kKv4QHigh = 7;
 constexpr float kKv4Spread = 1.2676506002282294e30f;  // 2^100: row scales within it share the weights' exponentials
 
 template <int D>
@@ -87,7 +90,8 @@ struct AttnKv4Layout {
   static constexpr int kJoin = kAlpha + kTcAttnHeads * 4;       // float [shares][64] factors of the shares
   static constexpr int kMisc = kJoin + kKv4Shares * kTcAttnHeads * 4;  // int [32]
   static constexpr int kLargest = kMisc + 128;                  // float [softmax warps]
-  static constexpr int kBar = kLargest + kKv4SoftWarps * 4;
+  static constexpr int kQFac = kLargest + kKv4SoftWarps * 4;    // float [2][64] by unit: what undoes the heads' q factors
+  static constexpr int kBar = kQFac + 2 * kTcAttnHeads * 4;
   static constexpr int kNumBars = 15 + 3 * kKv4Slots + 2 * kStages * kTiles;
   static constexpr int kSmem = kBar + kNumBars * 8 + 1024;      // + alignment slack
   // tensor memory: S^T (kScores of them) from column 0, O^T tile m from column 64 (kScores + m)
@@ -234,9 +238,9 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   float* max_s = reinterpret_cast<float*>(smem + L::kMax);
   float* alpha_s = reinterpret_cast<float*>(smem + L::kAlpha);
   float* join_s = reinterpret_cast<float*>(smem + L::kJoin);
-  // [0, 1] blocks of the units in flight, [2, 3] the bits of their q factors, [8..15] the convert warps' maxima,
-  // [16..18] by block modulo 3: a bound has to be raised, [20..31] by slot: its smallest and largest row scale
+  // [0, 1] blocks of the units in flight, [16..18] by block modulo 3: a bound has to be raised, [20..31] by slot: its smallest and largest row scale
   volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMisc);
+  float* qfac_s = reinterpret_cast<float*>(smem + L::kQFac);
   float2* span_s = reinterpret_cast<float2*>(smem + L::kMisc + 80);
   float* largest_s = reinterpret_cast<float*>(smem + L::kLargest);
   static_assert(kKv4Slots <= 6, "spans of the slots lie behind the flags");
@@ -316,56 +320,55 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   const int rows = 1 << p.pool.log_rows;
   const int64_t page_bytes = static_cast<int64_t>(rows) * kv4_row_bytes(D);
 
-  // q of unit n (token t, heads [h0, h0 + nh)) as fp16, by 256 threads; the place is written after free() returns.
-  const auto bring_q = [&](int tid, int n, int t, int h0, int nh, auto free) {
-    float f = 1.0f;
+  // q of unit n (token t, heads [h0, h0 + nh)) as fp16 times a power of two of each head, by eight warps (w of them); the
+  // place is written after free() returns.  A warp takes whole heads, so the largest value of a head is known from
+  // its own loads.
+  const auto bring_q = [&](int w, int n, int t, int h0, int nh, auto free) {
     const uint16_t* q = p.q + (static_cast<int64_t>(t) * H + h0) * D;
-    constexpr int kPieces = kTcAttnHeads * (D / 8) / kKv4ConvThreads;  // 16-byte pieces of a thread
-    constexpr int kMost = kSingle || D == 512 ? 4 : 2;  // in flight at a time (more spilled registers)
-    constexpr int kBatch = kPieces < kMost ? kPieces : kMost;
-    for (int pass = 0; pass < 2; ++pass) {
-      uint32_t top = 0u;
+    constexpr int kAcross = D / 8 < 32 ? D / 8 : 32;  // lanes of a head
+    constexpr int kEach = D / 8 / kAcross;            // 16-byte pieces of a lane
+    constexpr int kHeads = 32 / kAcross;              // heads at a time
+    constexpr int kSteps = kTcAttnHeads / (kKv4ConvWarps * kHeads);
+    constexpr int kMost = (kSingle || D == 512 ? 4 : 2) / kEach;  // in flight at a time (more spilled registers)
+    constexpr int kBatch = kSteps < kMost ? kSteps : kMost;
+    const int head = w * kHeads + lane / kAcross, piece = lane % kAcross;
 #pragma unroll 1
-      for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
-        uint4 v[kBatch];
+    for (int s0 = 0; s0 < kSteps; s0 += kBatch) {
+      uint4 v[kBatch][kEach];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int at = tid + (i0 + i) * kKv4ConvThreads;
-          const int h = at / (D / 8), pc = at % (D / 8);
-          v[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (h < nh) v[i] = ld_after_wait(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * D) + pc);
-        }
-        if (pass == 0 && i0 == 0) free();
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = (s0 + i) * kKv4ConvWarps * kHeads + head;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int at = tid + (i0 + i) * kKv4ConvThreads;
-          const int h = at / (D / 8), pc = at % (D / 8);
-          const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-          uint4* dst = reinterpret_cast<uint4*>(q_s + (pc / 8) * L::kQChunkBytes + swz128(h, (pc % 8) * 16));
-          if (pass == 0) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) top = max_abs_bf16x2(top, x[j]);
-            *dst = make_uint4(bf16x2_to_f16x2(x[0], 1.0f), bf16x2_to_f16x2(x[1], 1.0f), bf16x2_to_f16x2(x[2], 1.0f),
-                              bf16x2_to_f16x2(x[3], 1.0f));
-          } else {
-            *dst = make_uint4(bf16x2_to_f16x2(x[0], f), bf16x2_to_f16x2(x[1], f), bf16x2_to_f16x2(x[2], f), bf16x2_to_f16x2(x[3], f));
-          }
+        for (int k = 0; k < kEach; ++k) {
+          v[i][k] = make_uint4(0u, 0u, 0u, 0u);
+          if (h < nh) v[i][k] = ld_after_wait(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * D) + piece + kAcross * k);
         }
       }
-      if (pass == 1) break;
-      top = __reduce_max_sync(0xffffffffu, max(top & 0x7FFFu, (top >> 16) & 0x7FFFu));
-      if (lane == 0) misc[8 + (tid >> 5)] = static_cast<int>(top);
-      named_bar_sync(kTcGatherBar, kKv4ConvThreads);
-      int all = 0;
+      if (s0 == 0) free();
 #pragma unroll
-      for (int i = 0; i < kKv4ConvWarps; ++i) all = max(all, misc[8 + i]);
-      named_bar_sync(kTcGatherBar, kKv4ConvThreads);
-      const int e = (all >> 7) - 127;  // exponent of the largest
-      if (e >= 0 && e < 15) break;
-      if (e < -126 || e > 127) break;  // zeros (or less than the least normal number), or not finite
-      f = __int_as_float((127 + min(13 - e, 126)) << 23);  // the largest lands in [2^13, 2^14)
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = (s0 + i) * kKv4ConvWarps * kHeads + head;
+        uint32_t top = 0u;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+          top = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(top, v[i][k].x), v[i][k].y), v[i][k].z), v[i][k].w);
+        top = max(top & 0x7FFFu, (top >> 16) & 0x7FFFu);
+#pragma unroll
+        for (int o = kAcross / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int e = static_cast<int>(top >> 7) - 127;  // exponent of the largest
+        int up = kKv4QExp;
+        if (top != 0u && e < 128 && (e < kKv4QLow || e > kKv4QHigh)) up = min(13 - e, 126);  // it lands in [2^13, 2^14)
+        const float f = __int_as_float((127 + up) << 23);
+        if (piece == 0) qfac_s[(n & 1) * kTcAttnHeads + h] = __int_as_float((127 - up) << 23);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          const int pc = piece + kAcross * k;
+          *reinterpret_cast<uint4*>(q_s + (pc / 8) * L::kQChunkBytes + swz128(h, (pc % 8) * 16)) =
+              make_uint4(bf16x2_to_f16x2(v[i][k].x, f), bf16x2_to_f16x2(v[i][k].y, f), bf16x2_to_f16x2(v[i][k].z, f),
+                         bf16x2_to_f16x2(v[i][k].w, f));
+        }
+      }
     }
-    if (tid == 0) misc[2 + (n & 1)] = __float_as_int(f);
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) mbar_arrive(&q_full[n & 1]);
@@ -426,7 +429,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       } else {
         const int t = u / p.groups;
         const int h0 = (u % p.groups) * kTcAttnHeads;
-        bring_q(ctid, n, t, h0, min(kTcAttnHeads, H - h0), [&]() {
+        bring_q(warp - kKv4FirstConv, n, t, h0, min(kTcAttnHeads, H - h0), [&]() {
           nb = take_unit(n);
           // q's place is free once the previous unit's score products are done
           if (n > 0) mbar_wait(q_empty, static_cast<uint32_t>(n - 1) & 1u, abort_flag, err, 0x41);
@@ -477,7 +480,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     uint64_t lsum[kKv4SoftHeads / 2];
     if (kSingle && etid < kKv4ConvThreads) {
       const int h0 = (unit0 % p.groups) * kTcAttnHeads;
-      bring_q(etid, 0, unit0 / p.groups, h0, min(kTcAttnHeads, H - h0), []() {});
+      bring_q(warp - 4, 0, unit0 / p.groups, h0, min(kTcAttnHeads, H - h0), []() {});
     }
     for (int u = unit0; u < (kSingle ? unit0 + 1 : units); u += unit_step, ++n) {
       const int t = u / p.groups;
@@ -486,37 +489,39 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       mbar_wait(&unit_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x60);
       const int nb = misc[n & 1];
       mbar_wait(&q_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x66);  // the q factor
-      const float to_log2 = p.scale * 1.4426950408889634f / __int_as_float(misc[2 + (n & 1)]);
+      const float to_log2 = p.scale * 1.4426950408889634f;
+      const float* qfac = qfac_s + (n & 1) * kTcAttnHeads;
+      constexpr float kQFac = 1.0f / (1 << kKv4QExp);
       if (etid < kTcAttnHeads) max_s[etid] = kKv4NoBound;
 #pragma unroll
       for (int h = 0; h < kKv4SoftHeads / 2; ++h) lsum[h] = 0ull;
       named_bar_sync(kTcEpiBar, kKv4SoftThreads);
       if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
-      volatile float* largest = largest_s + (warp - 4);  // row scale of the unit so far (this warp's, all lanes alike)
-      *largest = 0.f;
+      // largest row scale of the unit so far (this warp's, all lanes alike); infinite where heads have q factors of their own,
+      // which makes every block of the unit take the general path
+      volatile float* largest = largest_s + (warp - 4);
+      *largest = __any_sync(0xffffffffu, qfac[lane] != kQFac || qfac[32 + lane] != kQFac) ? INFINITY : 0.f;
       for (int b = 0; b < nb; ++b, ++gb) {
         const uint32_t slot = gb % kKv4Slots;
         mbar_wait(&scl_full[slot], (gb / kKv4Slots) & 1u, abort_flag, err, 0x65);
-        const float rs = scl_s[slot * kTcAttnKeys + r];
+        float rs = scl_s[slot * kTcAttnKeys + r];
         const float2 span = span_s[slot];
         const float most = fmaxf(*largest, span.y);
         *largest = most;
-        const bool apart = most > span.x * kKv4Spread;  // some row's weight may underflow
+        const bool apart = most > span.x * kKv4Spread;  // (or a unit with q factors)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ent_empty[slot]);
         const bool valid = rs > 0.f;
-        const float a = to_log2 * rs;                    // score to log2 units
+        float a = to_log2 * (rs * kQFac);                // score to log2 units
         const float lr = valid ? log2f(rs) : -INFINITY;  // a masked key's weight is 0
-        // what makes a weight a term of the denominator (2^-23 off; a division took 1% of a long prompt), or -1
-        float inv = apart ? -1.f : (valid ? rcp_approx(rs) : 0.f);
-        const uint64_t a2 = pack_f32x2(a, a), lr2 = pack_f32x2(lr, lr);
+        const uint64_t lr2 = pack_f32x2(lr, lr);
         const uint32_t s_at = s_tmem + 64 * (gb % kSc) + lane_off + hb;
         mbar_wait(&s_full[gb % kSc], (gb / kSc) & 1u, abort_flag, err, 0x61);
         tc_fence_after_sync();
         float x[kKv4SoftHeads];
         // exponents relative to the running bounds
         const auto exponents = [&]() {
-          const uint64_t minus = pack_f32x2(-1.f, -1.f);
+          const uint64_t minus = pack_f32x2(-1.f, -1.f), a2 = pack_f32x2(a, a);
           tmem_ld_x16(s_at, x);
           tmem_wait_ld_regs16(x);
 #pragma unroll
@@ -544,8 +549,8 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
         };
         // A unit's first block sets the bounds.  After that the weights are formed with the bounds as they are,
         // while the warps tell one another whether an exponent exceeds its bound by more than 2^8; if one
-        // does, which is rare, the bounds are raised and the weights formed again.  (A block with row scales far apart, which is
-        // rare too, goes the same way: one branch less for all others.)
+        // does, which is rare, the bounds are raised and the weights formed again.  (What else is rare goes that way too: no
+        // branches for all other blocks.)
         bool raise = b == 0 || apart;
         if (!raise) {
           exponents();
@@ -565,6 +570,18 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
           if (etid == 0) misc[16 + (checks + 1) % 3] = 0;
         }
         if (raise) {
+          if (*largest == INFINITY) {  // the scores with the heads' own q factors, once and for all that follows
+            tmem_ld_x16(s_at, x);
+            tmem_wait_ld_regs16(x);
+#pragma unroll
+            for (int h = 0; h < kKv4SoftHeads; ++h) {
+              const float f = qfac_s[(n & 1) * kTcAttnHeads + hb + h];
+              x[h] *= f > 1.f ? (to_log2 * f) * rs : to_log2 * (f * rs);  // (neither overflows nor vanishes before its time)
+            }
+            tmem_st_x16(s_at, x);
+            tmem_wait_st();
+            a = 1.f;
+          }
           // the largest exponents per head across the 128 keys (the reduction consumes x)
           tmem_ld_x16(s_at, x);
           tmem_wait_ld_regs16(x);
@@ -606,17 +623,19 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
           }
           exponents();
           weights();
-          if (inv < 0.f) {  // the denominator's terms by themselves, from the same exponents (the scores are still there)
+          if (apart) {  // the denominator's terms by themselves, from the same exponents (the scores are still there)
             exponents();
 #pragma unroll
             for (int h = 0; h < kKv4SoftHeads; ++h) x[h] = lr > -INFINITY ? exp2_gradual(x[h] - lr) : 0.f;
-            inv = 1.f;
+            rs = -1.f;
           }
         }
         fence_proxy_async_shared();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
+        // what makes a weight a term of the denominator (2^-23 off; a division took 1% of a long prompt), or x is the term
+        const float inv = rs > 0.f ? rcp_approx(rs) : (rs < 0.f ? 1.f : 0.f);
         const uint64_t inv2 = pack_f32x2(inv, inv);
 #pragma unroll
         for (int h = 0; h < kKv4SoftHeads; h += 2) lsum[h / 2] = fma_f32x2(pack_f32x2(x[h], x[h + 1]), inv2, lsum[h / 2]);

@@ -97,3 +97,66 @@ def test_attention_very_negative_scores(dsa, T, K):  # noqa: F811
     out, lse = c.run(dsa)
     assert np.all(lse < -1e31)
     c.check(out, lse, rows=range(0, T, 13))
+
+
+# ------------------------------------------------------------------------------------ q
+#
+# A head's q enters as fp16 times a power of two of the head: each value is off by at most 2^-29 of the head's largest.  Beside
+# attend_tolerance's 4 D 2^-24 of sum |q| |kv| that is nothing where the head's values are of one size, and where they
+# are not, the tests below hold values that are exact all the same (8 significant bits, 2^20 below the largest).
+
+
+@pytest.mark.parametrize("D,H,T", [(64, 7, 2), (128, 64, 3), (256, 20, 160), (512, 70, 2), (512, 64, 160)])
+@pytest.mark.parametrize("low", [-20, -40, -100])
+def test_attention_heads_of_different_size(dsa, D, H, T, low):  # noqa: F811
+    """Heads whose q is 2^low of the others', with a scale at which their scores count: a head is as exact as alone."""
+    c = Case(D + H + T, T, H, D, 200, 32, sink=True, spread=0)
+    size = np.where(np.arange(H) % 3 == 1, 2.0 ** low, 1.0)
+    c.q_t, c.q = bf16(c.q * size[None, :, None])
+    c.scale *= 2.0 ** -low
+    for t in range(0, T, 13):  # (the other heads' scores are beyond what fp32 tells apart, those of the small ones are not)
+        out, lse = c.run(dsa) if t == 0 else (out, lse)
+        kv, r = c.listed(t)
+        small = np.flatnonzero(size < 1.0)
+        q, sink = c.q[t][small], c.sink[small]
+        o, l, p, x = K4.attend(q, kv, sink, c.scale)
+        to, tl = K4.attend_tolerance(q, kv, r, p, x, o, l, c.scale)
+        assert np.all(np.abs(out[t][small] - o) <= to) and np.all(np.abs(lse[t][small] - l) <= tl)
+    assert np.all(np.isfinite(out))
+
+
+@pytest.mark.parametrize("top", [0.0625, 1.0, 2.0, 200.0, 40000.0])
+@pytest.mark.parametrize("T", [2, 160])
+def test_attention_small_values_beside_a_large_one(dsa, T, top):  # noqa: F811
+    """One value of each head's q far above the others, where the rows are zero: the others alone make the scores, and
+    their lowest bits count."""
+    c = Case(T, T, 12, 128, 200, 32, sink=True, spread=0)
+    for s in range(c.R):
+        x = c.rng.standard_normal((c.length, c.D))
+        x[:, :16] = 0.0
+        hold(c, s, x)
+    tiny = top * 2.0 ** -19 * (1.0 + c.rng.integers(0, 128, c.q.shape) / 128.0) * c.rng.choice([-1.0, 1.0], c.q.shape)
+    tiny[:, :, :16] = 0.0
+    tiny[:, :, 3] = top
+    c.q_t, c.q = bf16(tiny)
+    c.scale = 2.0 / (np.sqrt(c.D) * top * 2.0 ** -19)
+    c.check(*c.run(dsa), rows=range(0, T, 13))
+
+
+def test_attention_heads_of_extreme_size(dsa):  # noqa: F811
+    """Heads of zeros, of the least and of the largest bf16 values in one token."""
+    for T in (2, 160):
+        c = Case(T, T, 9, 64, 100, 16, sink=True, spread=0)
+        size = 2.0 ** np.array([0, -133, -126, -30, 30, 100, 126, 0, 0], np.float64)
+        q = np.clip(c.q, -2.0, 2.0) * 0.9 * size[None, :, None]
+        q[:, 7] = 0.0
+        c.q_t, c.q = bf16(q)
+        for e, heads in ((0, [0, 7, 8, 3]), (100, [1, 2]), (-30, [4]), (-100, [5]), (-120, [6])):
+            c.scale = 0.3 * 2.0 ** e
+            out, lse = c.run(dsa)
+            for t in range(0, T, 13):
+                kv, r = c.listed(t)
+                q, sink = c.q[t][heads], c.sink[heads]
+                o, l, p, x = K4.attend(q, kv, sink, c.scale)
+                to, tl = K4.attend_tolerance(q, kv, r, p, x, o, l, c.scale)
+                assert np.all(np.abs(out[t][heads] - o) <= to) and np.all(np.abs(lse[t][heads] - l) <= tl), (T, e)
