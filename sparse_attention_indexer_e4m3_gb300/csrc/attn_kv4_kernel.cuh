@@ -91,8 +91,9 @@ struct AttnKv4Layout {
   static constexpr int kMisc = kJoin + kKv4Shares * kTcAttnHeads * 4;  // int [32]
   static constexpr int kLargest = kMisc + 128;                  // float [softmax warps]
   static constexpr int kQFac = kLargest + kKv4SoftWarps * 4;    // float [2][64] by unit: what undoes the heads' q factors
-  static constexpr int kBar = kQFac + 2 * kTcAttnHeads * 4;
-  static constexpr int kNumBars = 15 + 3 * kKv4Slots + 2 * kStages * kTiles;
+  static constexpr int kPhase = kQFac + 2 * kTcAttnHeads * 4;   // int [softmax warps]
+  static constexpr int kBar = kPhase + kKv4SoftWarps * 4;
+  static constexpr int kNumBars = 16 + 3 * kKv4Slots + 2 * kStages * kTiles;
   static constexpr int kSmem = kBar + kNumBars * 8 + 1024;      // + alignment slack
   // tensor memory: S^T (kScores of them) from column 0, O^T tile m from column 64 (kScores + m)
   static constexpr int kTmemCols = kScores + kTiles <= 4 ? 256 : 512;
@@ -263,6 +264,8 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   uint64_t* ent_empty = scl_full + kKv4Slots;
   uint64_t* kv_full = ent_empty + kKv4Slots;  // [stage][tile]
   uint64_t* kv_empty = kv_full + kSt * kTi;
+  uint64_t* soft_all = kv_empty + kSt * kTi;  // all softmax warps
+  volatile uint32_t* phase_s = reinterpret_cast<volatile uint32_t*>(smem + L::kPhase);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -277,10 +280,13 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       for (int i = threadIdx.x; i < L::kChunkBytes / 16; i += kKv4Threads)
         reinterpret_cast<uint4*>(kv_s + s * L::kStageBytes + L::kChunkBytes)[i] = make_uint4(0u, 0u, 0u, 0u);
   }
+  if (threadIdx.x < 32) misc[threadIdx.x] = 0;
+  if (threadIdx.x < kKv4SoftWarps) phase_s[threadIdx.x] = 0u;
+  for (int i = threadIdx.x; i < kKv4Slots * kTcAttnKeys; i += kKv4Threads) ent_s[i] = make_int2(-1, 0);
   if (threadIdx.x == 0) {
     mbar_init(q_empty, 1);
     mbar_init(checked, kKv4SoftWarps);
-    misc[16] = misc[17] = misc[18] = 0;
+    mbar_init(soft_all, kKv4SoftWarps);
     mbar_init(p_full, kKv4SoftWarps);
     mbar_init(pv_done, 1);
     mbar_init(o_empty, kKv4SoftWarps);
@@ -320,10 +326,20 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   const int rows = 1 << p.pool.log_rows;
   const int64_t page_bytes = static_cast<int64_t>(rows) * kv4_row_bytes(D);
 
+  // A wait that expires, in any role, sets the abort flag, and later waits return at once; what happens then is bounded too:
+  //   - a block count is used by a warp whose lanes all waited for it with success (gone() is the same for the whole
+  //     warp, and true wherever a wait of one of its lanes failed), by the softmax warps if all of them did;
+  //   - a page id is one that was found mapped, or -1 as from the start, whether the wait for it succeeded or not;
+  //   - the softmax warps pass the same hardware barriers (whose wait has no limit): those of a unit and its first block, which
+  //     they enter together or not at all.  Where they may differ on whether a bound has to be raised they meet at an
+  //     mbarrier, in a bounded wait, and a warp may leave the blocks after the first at any time.
+  const auto gone = [&]() -> bool { return __any_sync(0xffffffffu, *abort_flag != 0) != 0; };
+  constexpr int kLook = 16;  // blocks between two looks at the abort flag
+
   // q of unit n (token t, heads [h0, h0 + nh)) as fp16 times a power of two of each head, by eight warps (w of them); the
-  // place is written after free() returns.  A warp takes whole heads, so the largest value of a head is known from
+  // place is written after free() returns true.  A warp takes whole heads, so the largest value of a head is known from
   // its own loads.
-  const auto bring_q = [&](int w, int n, int t, int h0, int nh, auto free) {
+  const auto bring_q = [&](int w, int n, int t, int h0, int nh, auto free) -> bool {
     const uint16_t* q = p.q + (static_cast<int64_t>(t) * H + h0) * D;
     constexpr int kAcross = D / 8 < 32 ? D / 8 : 32;  // lanes of a head
     constexpr int kEach = D / 8 / kAcross;            // 16-byte pieces of a lane
@@ -344,7 +360,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
           if (h < nh) v[i][k] = ld_after_wait(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * D) + piece + kAcross * k);
         }
       }
-      if (s0 == 0) free();
+      if (s0 == 0 && !free()) return false;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int h = (s0 + i) * kKv4ConvWarps * kHeads + head;
@@ -372,13 +388,15 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) mbar_arrive(&q_full[n & 1]);
+    return true;
   };
 
   if (warp >= kKv4FirstConv) {
     // ------------------------------------------------------------------ convert
-    // blocks of unit n, once the scouts know
-    const auto take_unit = [&](int n) {
+    // blocks of unit n, once the scouts know; -1 where they are not to be known
+    const auto take_unit = [&](int n) -> int {
       mbar_wait(&unit_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x44);
+      if (gone()) return -1;
       const int nb = misc[n & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
@@ -429,14 +447,17 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       } else {
         const int t = u / p.groups;
         const int h0 = (u % p.groups) * kTcAttnHeads;
-        bring_q(warp - kKv4FirstConv, n, t, h0, min(kTcAttnHeads, H - h0), [&]() {
+        bring_q(warp - kKv4FirstConv, n, t, h0, min(kTcAttnHeads, H - h0), [&]() -> bool {
           nb = take_unit(n);
           // q's place is free once the previous unit's score products are done
-          if (n > 0) mbar_wait(q_empty, static_cast<uint32_t>(n - 1) & 1u, abort_flag, err, 0x41);
+          if (n > 0 && nb >= 0) mbar_wait(q_empty, static_cast<uint32_t>(n - 1) & 1u, abort_flag, err, 0x41);
+          return nb >= 0;
         });
       }
+      if (nb < 0) break;
       if (nb > 0) load(gb);
       for (int b = 0; b < nb; ++b, ++gb) {
+        if (b % kLook == kLook - 1 && gone()) break;
         const int st = static_cast<int>(gb % kSt);
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
@@ -469,6 +490,20 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ softmax and output
+    // The softmax warps meet: in a unit's first block, which all of them enter, at a hardware barrier, later with a limit.
+    const auto meet = [&](bool first) {
+      if (first) {
+        named_bar_sync(kTcEpiBar, kKv4SoftThreads);
+        return;
+      }
+      const uint32_t phase = phase_s[warp - 4];
+      __syncwarp();
+      if (lane == 0) {
+        phase_s[warp - 4] = phase ^ 1u;
+        mbar_arrive(soft_all);
+      }
+      mbar_wait(soft_all, phase, abort_flag, err, 0x68);
+    };
     const int etid = threadIdx.x - 128;
     const int quarter = warp & 3;                     // tensor-memory lane quarter
     const int hb = ((warp - 4) >> 2) * kKv4SoftHeads;  // this thread's heads [hb, hb + 16)
@@ -480,7 +515,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     uint64_t lsum[kKv4SoftHeads / 2];
     if (kSingle && etid < kKv4ConvThreads) {
       const int h0 = (unit0 % p.groups) * kTcAttnHeads;
-      bring_q(warp - 4, 0, unit0 / p.groups, h0, min(kTcAttnHeads, H - h0), []() {});
+      bring_q(warp - 4, 0, unit0 / p.groups, h0, min(kTcAttnHeads, H - h0), []() { return true; });
     }
     for (int u = unit0; u < (kSingle ? unit0 + 1 : units); u += unit_step, ++n) {
       const int t = u / p.groups;
@@ -495,13 +530,14 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       if (etid < kTcAttnHeads) max_s[etid] = kKv4NoBound;
 #pragma unroll
       for (int h = 0; h < kKv4SoftHeads / 2; ++h) lsum[h] = 0ull;
-      named_bar_sync(kTcEpiBar, kKv4SoftThreads);
+      if (bar_or(kTcEpiBar, kKv4SoftThreads, *abort_flag != 0)) break;
       if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
       // largest row scale of the unit so far (this warp's, all lanes alike); infinite where heads have q factors of their own,
       // which makes every block of the unit take the general path
       volatile float* largest = largest_s + (warp - 4);
       *largest = __any_sync(0xffffffffu, qfac[lane] != kQFac || qfac[32 + lane] != kQFac) ? INFINITY : 0.f;
       for (int b = 0; b < nb; ++b, ++gb) {
+        if (b % kLook == kLook - 1 && gone()) break;
         const uint32_t slot = gb % kKv4Slots;
         mbar_wait(&scl_full[slot], (gb / kKv4Slots) & 1u, abort_flag, err, 0x65);
         float rs = scl_s[slot * kTcAttnKeys + r];
@@ -549,28 +585,30 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
         };
         // A unit's first block sets the bounds.  After that the weights are formed with the bounds as they are,
         // while the warps tell one another whether an exponent exceeds its bound by more than 2^8; if one
-        // does, which is rare, the bounds are raised and the weights formed again.  (What else is rare goes that way too: no
-        // branches for all other blocks.)
-        bool raise = b == 0 || apart;
+        // does, which is rare, the bounds are raised and the weights formed again.  (What else is rare goes that way too, as if a
+        // bound were exceeded: no branches for all other blocks.)
+        bool raise = b == 0;
         if (!raise) {
           exponents();
           float over = x[0];
 #pragma unroll
           for (int h = 1; h + 1 < kKv4SoftHeads; h += 2) over = max3(over, x[h], x[h + 1]);
           over = fmaxf(over, x[kKv4SoftHeads - 1]);
-          if (__any_sync(0xffffffffu, over > kTcLazyLog2) && lane == 0) misc[16 + checks % 3] = 1;
+          if (__any_sync(0xffffffffu, over > kTcLazyLog2 || apart) && lane == 0) misc[16 + checks % 3] = 1;
           __syncwarp();
           if (lane == 0) mbar_arrive(checked);
           mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x63);  // the previous weighted sum has read P
           weights();
           mbar_wait(checked, checks & 1u, abort_flag, err, 0x67);
-          raise = misc[16 + checks % 3] != 0;
+          raise = __any_sync(0xffffffffu, misc[16 + checks % 3] != 0) != 0;
           ++checks;
           // this flag's next use but one: every warp has read it (two blocks ago), none sets it before the next check
           if (etid == 0) misc[16 + (checks + 1) % 3] = 0;
         }
         if (raise) {
-          if (*largest == INFINITY) {  // the scores with the heads' own q factors, once and for all that follows
+          if (b > 0 && gone()) break;
+          const bool far = __any_sync(0xffffffffu, apart) != 0;
+          if (__any_sync(0xffffffffu, *largest == INFINITY)) {  // the scores with the heads' own q factors, once and for all that follows
             tmem_ld_x16(s_at, x);
             tmem_wait_ld_regs16(x);
 #pragma unroll
@@ -589,7 +627,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
           for (int h = 0; h < kKv4SoftHeads; ++h) x[h] = fmaf(x[h], a, lr);
           xpose_reduce16(x, lane, [](float v, float w) { return fmaxf(v, w); });
           if ((lane & 1) == 0) red_s[quarter * kTcAttnHeads + hb + (lane >> 1)] = x[0];
-          named_bar_sync(kTcEpiBar, kKv4SoftThreads);
+          meet(b == 0);
           if (etid < kTcAttnHeads) {
             const float bm = fmaxf(fmaxf(red_s[etid], red_s[kTcAttnHeads + etid]),
                                    fmaxf(red_s[2 * kTcAttnHeads + etid], red_s[3 * kTcAttnHeads + etid]));
@@ -599,9 +637,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
             alpha_s[etid] = (mo == kKv4NoBound || mn == mo) ? 1.f : exp2f(0.5f * (mo - mn));
             max_s[etid] = mn;
           }
-          named_bar_sync(kTcEpiBar, kKv4SoftThreads);
-          // the previous weighted sum has read P and written O (known already where the bounds were checked)
-          if (gb > 0) mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x62);
+          meet(b == 0);
           if (b > 0) {
             // sums and output accumulators of earlier blocks follow the new bound (this thread: its dim row r
             // of every tile, its 16 head columns)
@@ -620,10 +656,12 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
               tmem_st_x16(o_tmem + lane_off + 64 * m + hb, x);
             }
             tmem_wait_st();
+          } else if (gb > 0) {
+            mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x62);
           }
           exponents();
           weights();
-          if (apart) {  // the denominator's terms by themselves, from the same exponents (the scores are still there)
+          if (far) {  // the denominator's terms by themselves, from the same exponents (the scores are still there)
             exponents();
 #pragma unroll
             for (int h = 0; h < kKv4SoftHeads; ++h) x[h] = lr > -INFINITY ? exp2_gradual(x[h] - lr) : 0.f;
@@ -708,6 +746,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     uint32_t gb = 0;
     int n = 0;
     for (int u = unit0; u < (kSingle ? unit0 + 1 : units); u += unit_step, ++n) {
+      if (gone()) break;
       const int t = u / p.groups;
       const int32_t* list = p.idx + static_cast<int64_t>(t) * p.K;
       const int seq = ld_after_wait(p.seq + t);
@@ -734,6 +773,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       const int nb = first_block(all, share + 1) - blk0;
       if (warp == 1) {
         if (n > 1) mbar_wait(&unit_empty[n & 1], static_cast<uint32_t>((n >> 1) - 1) & 1u, abort_flag, err, 0x40);
+        if (gone()) break;
         if (lane == 0) {
           misc[n & 1] = nb;
           mbar_arrive(&unit_full[n & 1]);
@@ -763,6 +803,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
                                                         rows * (D / 2 + D / kKv4Group)) + ent[i].y);
         }
         if (gb >= kKv4Slots) mbar_wait(&ent_empty[slot], (gb / kKv4Slots - 1) & 1u, abort_flag, err, 0x45);
+        if (gone()) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) ent_s[slot * kTcAttnKeys + 32 * i + lane] = ent[i];
         mbar_arrive(&ent_full[slot]);
