@@ -309,15 +309,17 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     *abort_flag = 0;
     fence_mbar_init();
   }
+  fence_proxy_async_shared();
+  // The set-up above overlaps the end of the kernel before.  Tensor memory is taken only after it: a kernel that lets its
+  // dependents start early may still have to allocate its own, on an SM where this one would hold all of it and wait.
+  wait_stream();
   if (warp == 0) {
     tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
   }
-  fence_proxy_async_shared();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  wait_stream();  // (the set-up above overlaps the end of the kernel before)
   const uint32_t tbase = *tmem_slot;
   const uint32_t s_tmem = tbase;
   const uint32_t o_tmem = tbase + 64 * L::kScores;

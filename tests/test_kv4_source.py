@@ -79,3 +79,9 @@ def test_start_values(code):
     """Counts, flags and page ids are defined before any role reads them."""
     setup = code[:code.index("__syncthreads()")]
     assert "misc[threadIdx.x] = 0" in setup and "ent_s[i] = make_int2(-1, 0)" in setup
+
+
+def test_tensor_memory_is_taken_behind_the_stream(code):
+    """A kernel that lets its dependents start early may allocate tensor memory after that: one of them that holds all of an
+    SM's and waits for that kernel would never be done."""
+    assert code.index("wait_stream();") < code.index("tmem_alloc(")
