@@ -326,6 +326,17 @@ DSA_API dsa_status dsa_quantize_kv4(const uint16_t* kv, const int32_t* seq, cons
                                     void* stream);
 
 /*
+ * dsa_quantize_kv4_reserved -- dsa_quantize_kv4 of rows that dsa_reserve_pages was called for: nothing is written
+ * where it fell short of pages, as the table may then still lead to pages that other sequences share.  What it
+ * wrote to `lacking` is read on the device, so a captured step needs no look at it from the host.
+ *
+ *   lacking    int32 [1], dsa_reserve_pages' output (0: the rows are written), or NULL (as dsa_quantize_kv4)
+ */
+DSA_API dsa_status dsa_quantize_kv4_reserved(const uint16_t* kv, const int32_t* seq, const int32_t* pos, int N, int D,
+                                             uint8_t* cache, int P, int page_rows, const int32_t* table, int R, int M,
+                                             const int32_t* lacking, void* stream);
+
+/*
  * dsa_dequantize_kv4 -- row pos[i] of sequence seq[i] as bf16: r s c, exact for rows that
  * dsa_quantize_kv4 wrote (otherwise rounded to the nearest bf16; next to the largest bf16 a scale that was
  * rounded up can take values past it, which come back as infinities).  A place that is not mapped gives zeros.
@@ -385,7 +396,8 @@ DSA_API dsa_status dsa_fork_pages(const int32_t* table, const int32_t* parent, i
  *   src, dst   int32 [2 R]  OUTPUT: entries 2 r and 2 r + 1 are the first and the last page of r's span
  *              where they are replaced and not wholly covered, else -1
  *   lacking    int32 [1]    OUTPUT: 0, or by how many pages the free ones fall short; then nothing
- *              else changes and the lists are all -1
+ *              else changes and the lists are all -1: the rows must not be written, which
+ *              dsa_quantize_kv4_reserved sees to
  *   workspace  dsa_reserve_pages_workspace_size(P) bytes, 4-byte aligned (DSA_ERR_WORKSPACE); its contents on
  *              entry do not matter; two calls running at the same time must not share it
  */
@@ -409,7 +421,8 @@ DSA_API dsa_status dsa_compact_pages(int32_t* table, int32_t* ref, int R, int M,
 /*
  * dsa_copy_pages -- pages[dst[i]] = pages[src[i]] for the n entries whose two ids lie in [0, P); others
  * are skipped.  `pages` is any array of P pages of page_bytes bytes (a multiple of 16, else
- * DSA_ERR_UNSUPPORTED; 16-byte aligned): a 4-bit cache, or index keys and their scales kept in the same pages.
+ * DSA_ERR_UNSUPPORTED; 16-byte aligned): a 4-bit cache, or index keys and their scales that a program keeps in pages
+ * of the same table (dsa_index_topk itself reads contiguous keys).
  * The copies have no order: a page must not be both a source and a destination, nor twice a destination.
  */
 DSA_API dsa_status dsa_copy_pages(void* pages, size_t page_bytes, int P, const int32_t* src, const int32_t* dst, int n,

@@ -445,18 +445,19 @@ def _native():
         m = importlib.import_module(__name__ + "._marshal")
         if m.torch_version != torch.__version__.split("+")[0]:
             raise RuntimeError(f"_marshal.so was built for torch {m.torch_version}, not {torch.__version__}: build it again")
-        names = ("quantize_kv4", "dequantize_kv4", "sparse_attn_kv4", "sparse_attn_kv4_workspace_size", "fork_pages", "reserve_pages",
+        names = ("quantize_kv4_reserved", "dequantize_kv4", "sparse_attn_kv4", "sparse_attn_kv4_workspace_size", "fork_pages", "reserve_pages",
                  "reserve_pages_workspace_size", "compact_pages", "compact_pages_workspace_size", "copy_pages")
         m.bind(tuple(ctypes.cast(getattr(lib, "dsa_" + n), ctypes.c_void_p).value for n in names), DsaError)
         _calls = m
     return _calls
 
 
-def quantize_kv4(kv, cache, table, seq, pos, stream=None):
+def quantize_kv4(kv, cache, table, seq, pos, stream=None, lacking=None):
     """Write bf16 rows kv [N, D] in 4 bits into the paged cache (uint8 [P, kv4_page_bytes]): row i as
     row pos[i] of sequence seq[i], whose pages are table[seq[i]] (int32 [R, M], -1 = none); rows
-    whose place is not mapped are left out.  Returns cache."""
-    return (_calls or _native()).quantize_kv4(kv, cache, table, seq, pos, stream)
+    whose place is not mapped are left out.  With lacking (int32 [1], from reserve_pages for these rows) nothing
+    is written where it is not 0: the rows' pages may then still be shared.  Returns cache."""
+    return (_calls or _native()).quantize_kv4(kv, cache, table, seq, pos, stream, lacking)
 
 
 def dequantize_kv4(cache, table, seq, pos, D: int, out=None, stream=None):
@@ -493,7 +494,8 @@ def reserve_pages(table, ref, begin, end, page_rows: int, src=None, dst=None, la
     """Before rows [begin[r], end[r]) of each sequence are written: maps every page they cover and gives
     the sequence a page of its own where one is shared (table and ref in place).  Returns (src, dst, lacking):
     copy_pages(cache, src, dst) brings along what the replaced pages hold (int32 [2 R], -1 = none), and
-    lacking (int32 [1]) is 0 or by how many pages the pool falls short (then nothing changed)."""
+    lacking (int32 [1]) is 0 or by how many pages the pool falls short (then nothing changed, and the rows
+    must not be written: pass it on to quantize_kv4)."""
     return (_calls or _native()).reserve_pages(table, ref, begin, end, page_rows, src, dst, lacking, workspace, stream)
 
 

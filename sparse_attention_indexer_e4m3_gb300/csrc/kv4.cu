@@ -43,9 +43,9 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, unsigned block,
     default: return cudaErrorInvalidValue; \
   }
 
-cudaError_t launch_kv4_write(int D, const uint16_t* x, int N, const int32_t* seq, const int32_t* pos, const Kv4Pool& c,
-                             cudaStream_t stream) {
-#define DSA_CALL(DD) return launch_dependent(kv4_write_kernel<DD>, dim3(codec_grid<DD>(N)), kKv4CodecThreads, stream, x, N, seq, pos, c)
+cudaError_t launch_kv4_write(int D, const uint16_t* x, int N, const int32_t* seq, const int32_t* pos, const int32_t* lacking,
+                             const Kv4Pool& c, cudaStream_t stream) {
+#define DSA_CALL(DD) return launch_dependent(kv4_write_kernel<DD>, dim3(codec_grid<DD>(N)), kKv4CodecThreads, stream, x, N, seq, pos, lacking, c)
   DSA_KV4_BY_D(D, DSA_CALL)
 #undef DSA_CALL
 }

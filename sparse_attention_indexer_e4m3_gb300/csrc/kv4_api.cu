@@ -75,13 +75,20 @@ size_t dsa_kv4_page_bytes(int page_rows, int D) {
 
 dsa_status dsa_quantize_kv4(const uint16_t* kv, const int32_t* seq, const int32_t* pos, int N, int D, uint8_t* cache,
                             int P, int page_rows, const int32_t* table, int R, int M, void* stream) {
+  return dsa_quantize_kv4_reserved(kv, seq, pos, N, D, cache, P, page_rows, table, R, M, nullptr, stream);
+}
+
+dsa_status dsa_quantize_kv4_reserved(const uint16_t* kv, const int32_t* seq, const int32_t* pos, int N, int D,
+                                     uint8_t* cache, int P, int page_rows, const int32_t* table, int R, int M,
+                                     const int32_t* lacking, void* stream) {
   Kv4Pool c;
   const dsa_status st = check_pool(&c, cache, P, page_rows, table, R, M, D);
   if (st != DSA_OK) return st;
   if (N < 0) return DSA_ERR_INVALID_ARG;
   if (N == 0) return DSA_OK;
   if (!kv || !aligned(kv, 32) || !seq || !aligned(seq, 4) || !pos || !aligned(pos, 4)) return DSA_ERR_INVALID_ARG;
-  return done(launch_kv4_write(D, kv, N, seq, pos, c, static_cast<cudaStream_t>(stream)));
+  if (lacking && !aligned(lacking, 4)) return DSA_ERR_INVALID_ARG;
+  return done(launch_kv4_write(D, kv, N, seq, pos, lacking, c, static_cast<cudaStream_t>(stream)));
 }
 
 dsa_status dsa_dequantize_kv4(const uint8_t* cache, int P, int page_rows, const int32_t* table, int R, int M,

@@ -50,8 +50,8 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float round_12bits(float x) { return __uint_as_float((__float_as_uint(x) + 0x800u) & 0xFFFFF000u); }
 template <int D>
 __global__ void __launch_bounds__(kKv4CodecThreads) kv4_write_kernel(const uint16_t* x, int N,
-                                                                     const int32_t* seq,
-                                                                     const int32_t* pos, Kv4Pool c) {
+                                                                     const int32_t* seq, const int32_t* pos,
+                                                                     const int32_t* lacking, Kv4Pool c) {
   constexpr int kLanes = D / kKv4Group;  // lanes per row
   const int64_t row = (static_cast<int64_t>(blockIdx.x) * kKv4CodecThreads + threadIdx.x) / kLanes;
   const int sub = threadIdx.x % kLanes;
@@ -60,11 +60,13 @@ __global__ void __launch_bounds__(kKv4CodecThreads) kv4_write_kernel(const uint1
   int page = -1, at = 0;
   wait_stream();
   if (row < N) {
+    const int short_of = lacking != nullptr ? ld_after_wait(lacking) : 0;
     at = ld_after_wait(pos + row);
     page = ld_after_wait(seq + row);
     ld_32(x + row * D + sub * kKv4Group, w);
     page = kv4_page(c, page, at);
     at &= rows - 1;
+    if (short_of != 0) page = -1;
   }
   // largest magnitudes, as bf16 bits
   uint32_t both = 0u;

@@ -58,8 +58,9 @@ cudaError_t launch_sparse_attn_bwd_tc(int D, int grid, const AttnBwdParams& p, u
 int sparse_attn_bwd_tc_smem(int D);
 
 // 4-bit paged cache: N rows of D (64, 128, 256 or 512) bf16 values into their pages and back.
-cudaError_t launch_kv4_write(int D, const uint16_t* x, int N, const int32_t* seq, const int32_t* pos, const Kv4Pool& c,
-                             cudaStream_t stream);
+// (into: nothing is written where *lacking is given and not 0).
+cudaError_t launch_kv4_write(int D, const uint16_t* x, int N, const int32_t* seq, const int32_t* pos, const int32_t* lacking,
+                             const Kv4Pool& c, cudaStream_t stream);
 cudaError_t launch_kv4_read(int D, uint16_t* out, int N, const int32_t* seq, const int32_t* pos, const Kv4Pool& c,
                             cudaStream_t stream);
 // Page tables: rows from their parents, pages for rows about to be written, live pages to the front, copies.

@@ -22,7 +22,7 @@
 namespace {
 
 struct Entry {
-  decltype(&dsa_quantize_kv4) quantize_kv4;
+  decltype(&dsa_quantize_kv4_reserved) quantize_kv4_reserved;
   decltype(&dsa_dequantize_kv4) dequantize_kv4;
   decltype(&dsa_sparse_attn_kv4) sparse_attn_kv4;
   decltype(&dsa_sparse_attn_kv4_workspace_size) sparse_attn_kv4_workspace_size;
@@ -174,19 +174,21 @@ int64_t long_of(PyObject* o, const char* name) {
   return v;
 }
 
-// (kv, cache, table, seq, pos, stream)
+// (kv, cache, table, seq, pos, stream, lacking)
 PyObject* quantize_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded("quantize_kv4", n, 6, [&] {
+  return guarded("quantize_kv4", n, 7, [&] {
     const at::Tensor& kv = arg(a[0], "kv", at::kBFloat16, 2);
     const Pool c(a[1], a[2], kv.size(1));
     const at::Tensor& seq = arg(a[3], "seq", at::kInt, 1);
     const at::Tensor& pos = arg(a[4], "pos", at::kInt, 1);
     shape(seq, "seq", {kv.size(0)});
     shape(pos, "pos", {kv.size(0)});
-    const Where w(a[5], {&kv, &c.cache, &c.table, &seq, &pos});
-    check(g_abi.quantize_kv4(bf16(kv), i32(seq), i32(pos), as_int(kv.size(0), "kv"), static_cast<int>(kv.size(1)),
-                             ptr<uint8_t>(c.cache), c.P, c.rows, i32(c.table), c.R, c.M, w.stream),
-          "dsa_quantize_kv4");
+    const at::Tensor lacking = out_arg(a[6], "lacking", at::kInt, {1});
+    const Where w(a[5], {&kv, &c.cache, &c.table, &seq, &pos, lacking.defined() ? &lacking : nullptr});
+    check(g_abi.quantize_kv4_reserved(bf16(kv), i32(seq), i32(pos), as_int(kv.size(0), "kv"), static_cast<int>(kv.size(1)),
+                                      ptr<uint8_t>(c.cache), c.P, c.rows, i32(c.table), c.R, c.M,
+                                      lacking.defined() ? i32(lacking) : nullptr, w.stream),
+          "dsa_quantize_kv4_reserved");
     return keep(a[1]);
   });
 }

@@ -1,0 +1,34 @@
+"""The 4-bit cache's calls without a GPU, beyond test_kv4_host.py: refusals of the C ABI and of the binding."""
+import ctypes
+
+import pytest
+import torch
+
+import kv4_ref as K4
+import sparse_attention_indexer_e4m3_gb300 as dsa
+from test_kv4_host import CACHE, D, INVALID, M, OK, P, R, T, UNSUPPORTED, bf16, lib, mem, z  # noqa: F401  (lib, mem: fixtures)
+
+
+def test_reserved_write_refusals(lib, mem):  # noqa: F811
+    _, a = mem
+    p, i = ctypes.c_void_p, ctypes.c_int
+    f = lib.dsa_quantize_kv4_reserved
+    f.argtypes = [p, p, p, i, i, p, i, i, p, i, i, p, p]
+
+    def w(kv=a, seq=a, pos=a, N=4, D=128, cache=a, P=2, rows=64, table=a, R=1, M=2, lacking=a):
+        return f(kv, seq, pos, N, D, cache, P, rows, table, R, M, lacking, None)
+
+    assert w(lacking=a + 2) == w(kv=None) == w(cache=a + 8) == INVALID and w(D=96) == UNSUPPORTED
+    assert w(N=0, kv=None, seq=None, pos=None, lacking=None) == OK
+
+
+@pytest.mark.parametrize("lacking", [z(2), z(1, 1), z(1, t=torch.int64), 0])
+def test_binding_refuses_lacking(lib, lacking):  # noqa: F811
+    with pytest.raises((ValueError, TypeError)) as e:
+        dsa.quantize_kv4(z(T, D, t=bf16), CACHE(), z(R, M), z(T), z(T), lacking=lacking)
+    assert "CUDA" not in str(e.value)
+
+
+def test_binding_wants_lacking_on_the_device(lib):  # noqa: F811
+    with pytest.raises(ValueError, match="CUDA"):
+        dsa.quantize_kv4(z(T, D, t=bf16), CACHE(), z(R, M), z(T), z(T), lacking=z(1))
