@@ -6,6 +6,7 @@
 
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
@@ -70,8 +71,8 @@ int as_int(int64_t n, const char* name) {
 // The current device and the stream of the call.  Every tensor has to lie on that device.
 struct Where {
   c10::DeviceIndex device = -1;
-  cudaStream_t stream = nullptr;
-  bool given = false;  // another stream than the current one may be meant
+  cudaStream_t stream = nullptr;   // of the call
+  cudaStream_t current = nullptr;  // the caller's
 
   Where(PyObject* stream_object, std::initializer_list<const at::Tensor*> tensors) {
     for (const at::Tensor* t : tensors)
@@ -79,10 +80,10 @@ struct Where {
     device = c10::cuda::current_device();
     for (const at::Tensor* t : tensors)
       if (t != nullptr && t->get_device() != device) bad_value("tensors must be on the current CUDA device");
+    current = c10::cuda::getCurrentCUDAStream(device).stream();
     if (stream_object == Py_None) {
-      stream = c10::cuda::getCurrentCUDAStream(device).stream();
+      stream = current;
     } else {
-      given = true;
       PyObject* h = PyObject_GetAttrString(stream_object, "cuda_stream");
       if (h == nullptr) throw Refusal{nullptr, ""};
       stream = static_cast<cudaStream_t>(PyLong_AsVoidPtr(h));
@@ -91,11 +92,19 @@ struct Where {
     }
   }
 
-  // A new tensor, kept for the stream where that is not the one it is allocated for.
+  // A new tensor.  It is allocated for the stream that writes it: memory of the current stream's pool may still be in use
+  // there by what held it last.  The caller gets it on the current stream, so it is not used anew before that
+  // stream is done with it either.
   at::Tensor make(at::IntArrayRef sizes, at::ScalarType type) const {
     const at::AutoDispatchBelowADInplaceOrView below;  // nothing here is differentiated
-    at::Tensor t = at::empty(sizes, at::TensorOptions().dtype(type).device(c10::Device(c10::DeviceType::CUDA, device)));
-    if (given) t.record_stream(c10::cuda::getStreamFromExternal(stream, device).unwrap());
+    const at::TensorOptions options = at::TensorOptions().dtype(type).device(c10::Device(c10::DeviceType::CUDA, device));
+    if (stream == current) return at::empty(sizes, options);
+    at::Tensor t;
+    {
+      const c10::cuda::CUDAStreamGuard there(c10::cuda::getStreamFromExternal(stream, device));
+      t = at::empty(sizes, options);
+    }
+    t.record_stream(c10::cuda::getCurrentCUDAStream(device).unwrap());
     return t;
   }
 };

@@ -1,0 +1,89 @@
+"""Calls with stream=: what they allocate belongs to that stream, so that work still running on the current one, on memory that
+was freed there, and the call do not meet in one buffer."""
+import numpy as np
+import pytest
+
+import kv4_ref as K4
+from test_gpu_kv4 import dev, dsa, rows_of, bf16  # noqa: F401  (dsa: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+T, H, D, K, N, B, R = 2, 64, 512, 700, 640, 64, 1
+
+
+@pytest.fixture(scope="module")
+def world():
+    import torch
+
+    rng = np.random.default_rng(1)
+    P = N // B + 2
+    kv, _ = bf16(rows_of(rng, N, D, 2))
+    q, _ = bf16(rng.standard_normal((T, H, D)))
+    return dict(kv=kv, q=q, cache=torch.zeros(P, K4.page_bytes(B, D), dtype=torch.uint8, device="cuda"),
+                table=dev(np.arange(N // B)[None, :], np.int32), seq=dev(np.zeros(N), np.int32), pos=dev(np.arange(N), np.int32),
+                tok=dev(np.zeros(T), np.int32), idx=dev(rng.integers(0, N, (T, K)), np.int32),
+                ref=dev(K4.counts(np.arange(N // B, dtype=np.int32)[None, :], P)), parent=dev([0], np.int32),
+                begin=dev([5], np.int32), end=dev([70], np.int32))
+
+
+def calls(m, w):
+    """(call, shapes and type of what it allocates to return) of every call of the 4-bit cache that allocates."""
+    i32, P = "int32", w["ref"].numel()
+    return {
+        "dequantize_kv4": (lambda s: m.dequantize_kv4(w["cache"], w["table"], w["seq"], w["pos"], D, stream=s), (N, D), "bfloat16"),
+        "sparse_attn_kv4": (lambda s: m.sparse_attn_kv4(w["q"], w["cache"], w["table"], w["tok"], w["idx"], stream=s), (T, H, D), "bfloat16"),
+        "fork_pages": (lambda s: m.fork_pages(w["table"], w["parent"], w["ref"], stream=s), (R, N // B), i32),
+        "reserve_pages": (lambda s: m.reserve_pages(w["table"], w["ref"], w["begin"], w["end"], B, stream=s)[0], (4 * R + 1 + 2 * P,), i32),
+        "compact_pages": (lambda s: m.compact_pages(w["table"], w["ref"], stream=s)[0], (2 * (P // 2) + 1 + P,), i32),
+    }
+
+
+NAMES = ["dequantize_kv4", "sparse_attn_kv4", "fork_pages", "reserve_pages", "compact_pages"]
+
+
+def check(f, shape, t):
+    """What the current stream freed is not what the call on another stream is given; and the other way round."""
+    import torch
+
+    side = torch.cuda.Stream()
+    want = f(None).clone()
+    f(side)
+    torch.cuda.synchronize()
+    freed = torch.empty(shape, dtype=getattr(torch, t), device="cuda")
+    here = freed.untyped_storage().data_ptr()
+    del freed
+    got = f(side)
+    torch.cuda.synchronize()
+    assert got.untyped_storage().data_ptr() != here
+    assert torch.equal(got, want)
+    there = got.untyped_storage().data_ptr()
+    del got
+    again = torch.empty(shape, dtype=getattr(torch, t), device="cuda")
+    assert again.untyped_storage().data_ptr() != there
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_allocations_of_the_4_bit_cache_s_calls(dsa, world, name):  # noqa: F811
+    dsa.quantize_kv4(world["kv"], world["cache"], world["table"], world["seq"], world["pos"])
+    check(*calls(dsa, world)[name])
+
+
+def test_captured_call_on_a_side_stream(dsa, world):  # noqa: F811
+    """stream= naming a stream that takes part in a capture: the allocation is the graph's."""
+    import torch
+
+    dsa.quantize_kv4(world["kv"], world["cache"], world["table"], world["seq"], world["pos"])
+    want = dsa.sparse_attn_kv4(world["q"], world["cache"], world["table"], world["tok"], world["idx"])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        out = dsa.sparse_attn_kv4(world["q"], world["cache"], world["table"], world["tok"], world["idx"], stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    out.zero_()
+    for _ in range(2):
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert dsa.get_device_error() == 0
