@@ -153,6 +153,19 @@ def _shape(t, name, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on `stream`, allocated for that stream: memory of the current stream's pool may still be in
+    use there by what held it last.  It is not used anew before the current stream is done with it either."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
 def _check(status: int, where: str):
     if status != DSA_OK:
         raise DsaError(status, where)
@@ -190,7 +203,7 @@ def index_score(q, w, k, k_scale, ks, ke, logits=None, stream=None):
     torch = _torch()
     q, w, k, k_scale, ks, ke, T, N, H, D = _inputs(q, w, k, k_scale, ks, ke)
     if logits is None:
-        logits = torch.empty((T, N), dtype=torch.float32, device=q.device)
+        logits = _empty((T, N), torch.float32, q.device, stream)
     logits = _dev(logits, "logits", (torch.float32,))
     if tuple(logits.shape) != (T, N):
         raise ValueError("logits must be [T, N]")
@@ -210,11 +223,12 @@ def index_score_kres(q, w, k, k_scale, ks, ke, logits=None, workspace=None, stre
     torch = _torch()
     q, w, k, k_scale, ks, ke, T, N, H, D = _inputs(q, w, k, k_scale, ks, ke)
     if logits is None:
-        logits = torch.empty((T, N), dtype=torch.float32, device=q.device)
+        logits = _empty((T, N), torch.float32, q.device, stream)
     logits = _dev(logits, "logits", (torch.float32,))
     if tuple(logits.shape) != (T, N):
         raise ValueError("logits must be [T, N]")
-    ws, nbytes = _workspace(index_score_kres_workspace_size(T, N, H, D), workspace, q.device)
+    need = index_score_kres_workspace_size(T, N, H, D)
+    ws, nbytes = _workspace(need, _scratch(need, workspace, q.device, stream), q.device)
     st = load().dsa_index_score_kres(q.data_ptr(), w.data_ptr(), k.data_ptr(), k_scale.data_ptr(), ks.data_ptr(),
                                      ke.data_ptr(), T, N, H, D, logits.data_ptr(),
                                      ws.data_ptr() if ws is not None else None, nbytes, _stream_ptr(stream))
@@ -228,6 +242,13 @@ def topk_workspace_size(T: int, N: int, k: int) -> int:
 
 def index_topk_workspace_size(T: int, N: int, H: int, D: int, k: int) -> int:
     return int(load().dsa_index_topk_workspace_size(T, N, H, D, k))
+
+
+def _scratch(nbytes, workspace, device, stream):
+    """The caller's workspace, or one for a call on another stream (none here for the current one: _workspace's)."""
+    if workspace is not None or stream is None or nbytes == 0:
+        return workspace
+    return _empty(nbytes, _torch().uint8, device, stream)
 
 
 def _workspace(nbytes, workspace, device):
@@ -252,10 +273,11 @@ def topk(logits, ks, ke, k: int, idx=None, workspace=None, stream=None):
     _shape(ks, "ks", (T,))
     _shape(ke, "ke", (T,))
     if idx is None:
-        idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+        idx = _empty((T, k), torch.int32, logits.device, stream)
     idx = _dev(idx, "idx", (torch.int32,))
     _shape(idx, "idx", (T, k))
-    ws, wsb = _workspace(topk_workspace_size(T, N, k), workspace, logits.device)
+    need = topk_workspace_size(T, N, k)
+    ws, wsb = _workspace(need, _scratch(need, workspace, logits.device, stream), logits.device)
     st = load().dsa_topk(logits.data_ptr(), ks.data_ptr(), ke.data_ptr(), T, N, k, idx.data_ptr(),
                          None if ws is None else ws.data_ptr(), wsb, _stream_ptr(stream))
     _check(st, "dsa_topk")
@@ -267,11 +289,11 @@ def index_topk(q, w, k, k_scale, ks, ke, topk_k: int, idx=None, workspace=None, 
     torch = _torch()
     q, w, k, k_scale, ks, ke, T, N, H, D = _inputs(q, w, k, k_scale, ks, ke)
     if idx is None:
-        idx = torch.empty((T, topk_k), dtype=torch.int32, device=q.device)
+        idx = _empty((T, topk_k), torch.int32, q.device, stream)
     idx = _dev(idx, "idx", (torch.int32,))
     _shape(idx, "idx", (T, topk_k))
     need = index_topk_workspace_size(T, N, H, D, topk_k)
-    ws, wsb = _workspace(need, workspace, q.device)
+    ws, wsb = _workspace(need, _scratch(need, workspace, q.device, stream), q.device)
     st = load().dsa_index_topk(q.data_ptr(), w.data_ptr(), k.data_ptr(), k_scale.data_ptr(), ks.data_ptr(),
                                ke.data_ptr(), T, N, H, D, topk_k, idx.data_ptr(),
                                None if ws is None else ws.data_ptr(), wsb, _stream_ptr(stream))
@@ -289,7 +311,7 @@ def index_topk_plan(ks, ke, N: int, H: int, D: int, topk_k: int, workspace=None,
     T = ks.shape[0]
     _shape(ke, "ke", (T,))
     need = index_topk_workspace_size(T, N, H, D, topk_k)
-    ws, wsb = _workspace(need, workspace, ks.device)
+    ws, wsb = _workspace(need, _scratch(need, workspace, ks.device, stream), ks.device)
     st = load().dsa_index_topk_plan(ks.data_ptr(), ke.data_ptr(), T, N, H, D, topk_k,
                                     None if ws is None else ws.data_ptr(), wsb, _stream_ptr(stream))
     _check(st, "dsa_index_topk_plan")
@@ -301,7 +323,7 @@ def index_topk_run(q, w, k, k_scale, ks, ke, topk_k: int, workspace, idx=None, s
     torch = _torch()
     q, w, k, k_scale, ks, ke, T, N, H, D = _inputs(q, w, k, k_scale, ks, ke)
     if idx is None:
-        idx = torch.empty((T, topk_k), dtype=torch.int32, device=q.device)
+        idx = _empty((T, topk_k), torch.int32, q.device, stream)
     idx = _dev(idx, "idx", (torch.int32,))
     _shape(idx, "idx", (T, topk_k))
     ws = None if workspace is None else _dev(workspace, "workspace", (torch.uint8,))
@@ -326,9 +348,9 @@ def quantize_k(k, codes=None, scale=None, stream=None):
         raise ValueError("k must be [N, D]")
     N, D = k.shape
     if codes is None:
-        codes = torch.empty((N, D), dtype=torch.uint8, device=k.device)
+        codes = _empty((N, D), torch.uint8, k.device, stream)
     if scale is None:
-        scale = torch.empty(N, dtype=torch.float32, device=k.device)
+        scale = _empty(N, torch.float32, k.device, stream)
     codes = _dev(codes, "codes", (torch.uint8,))
     scale = _dev(scale, "scale", (torch.float32,))
     _shape(codes, "codes", (N, D))
@@ -360,7 +382,7 @@ def sparse_attn(q, kv, idx, attn_sink=None, scale=None, out=None, lse=None, stre
             raise ValueError("attn_sink must be [H]")
         sink_ptr = attn_sink.data_ptr()
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty((T, H, D), torch.bfloat16, q.device, stream)
     out = _dev(out, "out", (torch.bfloat16,))
     _shape(out, "out", (T, H, D))
     lse_ptr = None
@@ -402,11 +424,11 @@ def sparse_attn_bwd(q, kv, idx, out, lse, dout, attn_sink=None, scale=None, dq=N
             raise ValueError("attn_sink must be [H]")
         sink_ptr = attn_sink.data_ptr()
         if dsink is None:
-            dsink = torch.empty(H, dtype=torch.float32, device=q.device)
+            dsink = _empty(H, torch.float32, q.device, stream)
     if dq is None:
-        dq = torch.empty((T, H, D), dtype=torch.float32, device=q.device)
+        dq = _empty((T, H, D), torch.float32, q.device, stream)
     if dkv is None:
-        dkv = torch.empty((N, D), dtype=torch.float32, device=q.device)
+        dkv = _empty((N, D), torch.float32, q.device, stream)
     dq = _dev(dq, "dq", (torch.float32,))
     _shape(dq, "dq", (T, H, D))
     dkv = _dev(dkv, "dkv", (torch.float32,))

@@ -87,3 +87,48 @@ def test_captured_call_on_a_side_stream(dsa, world):  # noqa: F811
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     assert dsa.get_device_error() == 0
+
+
+# ------------------------------------------------------------------------------------ the other calls
+
+
+def small(m):
+    """Calls of the indexer and the bf16 attention that allocate, as in `calls`; the outputs are compared where the call
+    writes all of them."""
+    import torch
+
+    rng = np.random.default_rng(2)
+    t, h, d, n, k = 40, 8, 64, 512, 32
+    q = torch.from_numpy(rng.standard_normal((t, h, d)).astype(np.float32)).cuda().to(torch.float8_e4m3fn)
+    key = torch.from_numpy(rng.standard_normal((n, d)).astype(np.float32)).cuda().to(torch.bfloat16)
+    codes, scale = m.quantize_k(key)
+    w = torch.ones(t, h, device="cuda")
+    ks, ke = dev(np.zeros(t), np.int32), dev(np.full(t, n), np.int32)
+    logits = m.index_score(q, w, codes, scale, ks, ke)
+    idx = m.index_topk(q, w, codes, scale, ks, ke, k)
+    qb, _ = bf16(rng.standard_normal((t, h, 128)))
+    kb, _ = bf16(rng.standard_normal((n, 128)))
+    lse = torch.empty(t, h, device="cuda")
+    out = m.sparse_attn(qb, kb, idx, lse=lse)
+
+    def run(s):
+        plan = m.index_topk_plan(ks, ke, n, h, d, k, stream=s)
+        return m.index_topk_run(q, w, codes, scale, ks, ke, k, plan, stream=s)
+
+    return {
+        "index_score": (lambda s: m.index_score(q, w, codes, scale, ks, ke, stream=s), (t, n), "float32"),
+        "index_score_kres": (lambda s: m.index_score_kres(q, w, codes, scale, ks, ke, stream=s), (t, n), "float32"),
+        "topk": (lambda s: m.topk(logits, ks, ke, k, stream=s), (t, k), "int32"),
+        "index_topk": (lambda s: m.index_topk(q, w, codes, scale, ks, ke, k, stream=s), (t, k), "int32"),
+        "index_topk_plan, _run": (run, (t, k), "int32"),
+        "quantize_k": (lambda s: m.quantize_k(key, stream=s)[0], (n, d), "uint8"),
+        "sparse_attn": (lambda s: m.sparse_attn(qb, kb, idx, stream=s), (t, h, 128), "bfloat16"),
+        "sparse_attn_bwd": (lambda s: m.sparse_attn_bwd(qb, kb, idx, out, lse, out, stream=s)[0], (t, h, 128), "float32"),
+    }
+
+
+@pytest.mark.parametrize("name", ["index_score", "index_score_kres", "topk", "index_topk", "index_topk_plan, _run", "quantize_k",
+                                  "sparse_attn", "sparse_attn_bwd"])
+def test_allocations_of_the_other_calls(dsa, name):  # noqa: F811
+    check(*small(dsa)[name])
+    assert dsa.get_device_error() == 0
