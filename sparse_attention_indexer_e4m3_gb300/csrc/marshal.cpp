@@ -298,12 +298,25 @@ struct Lists {
   void fill(const Where& w, int64_t n, size_t need) {
     // one allocation for what is left out, the workspace last
     const int64_t scratch = ws.defined() ? 0 : static_cast<int64_t>((need + 3) / 4);
-    const at::Tensor all = w.make({2 * n + 1 + scratch}, at::kInt);
-    if (!src.defined()) src = part_of(all, 0, n);
-    if (!dst.defined()) dst = part_of(all, n, n);
-    if (!one.defined()) one = part_of(all, 2 * n, 1);
-    workspace = ws.defined() ? ws.data_ptr() : (need > 0 ? ptr<int32_t>(all) + 2 * n + 1 : nullptr);
-    workspace_bytes = ws.defined() ? static_cast<size_t>(ws.numel()) : static_cast<size_t>(scratch) * 4;
+    const int64_t total = (src.defined() ? 0 : n) + (dst.defined() ? 0 : n) + (one.defined() ? 0 : 1) + scratch;
+    const bool given = src.defined() && dst.defined() && one.defined() && scratch == 0;
+    const at::Tensor all = given ? at::Tensor() : w.make({total}, at::kInt);
+    int64_t at = 0;
+    const auto take = [&](at::Tensor& t, int64_t count) {
+      if (t.defined()) return;
+      t = part_of(all, at, count);
+      at += count;
+    };
+    take(src, n);
+    take(dst, n);
+    take(one, 1);
+    if (ws.defined()) {
+      workspace = ws.data_ptr();
+      workspace_bytes = static_cast<size_t>(ws.numel());
+    } else if (scratch > 0) {
+      workspace = ptr<int32_t>(all) + at;
+      workspace_bytes = static_cast<size_t>(scratch) * 4;
+    }
   }
   PyObject* result(PyObject* const* a) const {
     PyObject* r = PyTuple_New(3);

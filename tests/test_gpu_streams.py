@@ -132,3 +132,30 @@ def small(m):
 def test_allocations_of_the_other_calls(dsa, name):  # noqa: F811
     check(*small(dsa)[name])
     assert dsa.get_device_error() == 0
+
+
+def test_nothing_is_allocated_when_the_caller_brings_everything(dsa, world):  # noqa: F811
+    import torch
+
+    w, P = world, world["ref"].numel()
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    u8 = lambda n: torch.zeros(n, dtype=torch.uint8, device="cuda")  # noqa: E731
+    src, dst, one, ws = i32(2 * R), i32(2 * R), i32(1), u8(dsa.reserve_pages_workspace_size(P))
+    s2, d2, n2, ws2 = i32(P // 2), i32(P // 2), i32(1), u8(dsa.compact_pages_workspace_size(P))
+    none = i32(0)
+    empty, e_begin = torch.zeros(0, 3, dtype=torch.int32, device="cuda"), i32(0)
+    count = lambda: torch.cuda.memory_stats()["allocation.all.allocated"]  # noqa: E731
+    before = count()
+    got = dsa.reserve_pages(w["table"], w["ref"], w["begin"], w["end"], B, src=src, dst=dst, lacking=one, workspace=ws)
+    assert got[0] is src and got[1] is dst and got[2] is one
+    got = dsa.compact_pages(w["table"], w["ref"], src=s2, dst=d2, n_live=n2, workspace=ws2)
+    assert got[0] is s2 and got[1] is d2 and got[2] is n2
+    assert count() == before
+    # some of them, and lists of no entries
+    for kw in ({}, dict(src=src), dict(dst=dst, workspace=ws), dict(lacking=one, workspace=ws), dict(src=src, dst=dst, workspace=ws),
+               dict(src=src, dst=dst, lacking=one)):
+        got = dsa.reserve_pages(w["table"], w["ref"], w["begin"], w["end"], B, **kw)
+        assert [t.numel() for t in got] == [2 * R, 2 * R, 1] and got[2].item() == 0 and bool((got[0] == -1).all())
+    for kw in (dict(lacking=one, workspace=ws), dict(src=none, lacking=one, workspace=ws), {}):
+        got = dsa.reserve_pages(empty, w["ref"], e_begin, e_begin, B, **kw)
+        assert [t.numel() for t in got] == [0, 0, 1] and got[2].item() == 0
