@@ -1,5 +1,6 @@
 """Builds the CUDA library libdsa_gb300.so in-tree for sm_103a (GB300), and the native argument
-marshalling _marshal.so of the 4-bit cache's calls against the installed torch (g++).
+marshalling _marshal.so of the 4-bit cache's calls against the installed torch (g++).  The library needs nvcc only:
+without torch the marshalling is left out, which nothing but the Python calls on the 4-bit cache use.
 
 Plain nvcc, no CMake: each translation unit under csrc/ compiles in parallel to an object,
 then one shared library is linked.  The CUDA runtime is linked statically, so the library
@@ -44,16 +45,35 @@ def _deps() -> list[str]:
     return files
 
 
+def _newer(path: str, deps: list[str]) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in deps)
+
+
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec is not None else None
+
+
+def lib_up_to_date() -> bool:
+    return _newer(LIB_PATH, [f for f in _deps() if os.path.basename(f) != "marshal.cpp"])
+
+
+def marshal_up_to_date() -> bool:
+    """_marshal.so is newer than its sources (or torch, which it is built against, is not there)."""
+    if _torch_dir() is None:
+        return True
+    return _newer(MARSHAL_PATH, [os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "dsa.h"), os.path.abspath(__file__)])
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(MARSHAL_PATH)):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(MARSHAL_PATH))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    return lib_up_to_date() and marshal_up_to_date()
 
 
 def _compile_marshal(cc: str) -> None:
-    """g++ of marshal.cpp against the installed torch's headers and libraries."""
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    """g++ of marshal.cpp against the installed torch's headers and libraries; nothing without torch."""
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        return
     inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")
     tmp = MARSHAL_PATH + f".tmp{os.getpid()}"
@@ -69,7 +89,9 @@ def _compile_marshal(cc: str) -> None:
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     """Compile (if stale) and return the path of libdsa_gb300.so."""
-    if not force and not extra_flags and up_to_date():
+    make_lib = force or bool(extra_flags) or not lib_up_to_date()
+    make_marshal = force or not marshal_up_to_date()
+    if not (make_lib or make_marshal):
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
@@ -88,15 +110,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        marshal = ex.submit(_compile_marshal, cc)
-        objs = list(ex.map(compile_one, SOURCES))
-        marshal.result()
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
+        marshal = ex.submit(_compile_marshal, cc) if make_marshal else None
+        objs = list(ex.map(compile_one, SOURCES)) if make_lib else []
+        if make_lib:
+            tmp = LIB_PATH + f".tmp{os.getpid()}"
+            cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, LIB_PATH)
+        if marshal is not None:
+            marshal.result()
     return LIB_PATH
 
 
