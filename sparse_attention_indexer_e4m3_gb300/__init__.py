@@ -462,11 +462,15 @@ def _native():
     if _calls is None:
         lib, torch = load(), _torch()
         path = os.path.join(_HERE, "_marshal.so")
+        how = "build it with `python -m sparse_attention_indexer_e4m3_gb300.build`"
         if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with `python -m sparse_attention_indexer_e4m3_gb300.build`")
-        m = importlib.import_module(__name__ + "._marshal")
+            raise RuntimeError(f"{path} is missing: {how}")
+        try:
+            m = importlib.import_module(__name__ + "._marshal")
+        except ImportError as e:
+            raise RuntimeError(f"{path} does not load, as if built for another torch or Python ({e}): {how}") from e
         if m.torch_version != torch.__version__.split("+")[0]:
-            raise RuntimeError(f"_marshal.so was built for torch {m.torch_version}, not {torch.__version__}: build it again")
+            raise RuntimeError(f"{path} was built for torch {m.torch_version}, not {torch.__version__}: {how}")
         names = ("quantize_kv4_reserved", "dequantize_kv4", "sparse_attn_kv4", "sparse_attn_kv4_workspace_size", "fork_pages", "reserve_pages",
                  "reserve_pages_workspace_size", "compact_pages", "compact_pages_workspace_size", "copy_pages")
         m.bind(tuple(ctypes.cast(getattr(lib, "dsa_" + n), ctypes.c_void_p).value for n in names), DsaError)

@@ -23,6 +23,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libdsa_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 MARSHAL_PATH = os.path.join(HERE, "_marshal.so")
+MARSHAL_STAMP = os.path.join(BUILD_DIR, "_marshal.txt")  # what _marshal.so was built against
 
 SOURCES = ["dsa_api.cu", "index_d128.cu", "index_d64.cu", "kres_d128.cu", "kres_d64.cu", "select_kernels.cu", "attn.cu", "attn_bwd.cu", "attn_kv4.cu", "kv4.cu",
            "kv4_api.cu"]
@@ -58,10 +59,23 @@ def lib_up_to_date() -> bool:
     return _newer(LIB_PATH, [f for f in _deps() if os.path.basename(f) != "marshal.cpp"])
 
 
+def _marshal_stamp(torch_dir: str) -> str:
+    """The torch and Python whose C++ interfaces _marshal.so uses."""
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        version = f.read()
+    return f"{sysconfig.get_config_var('SOABI')}\n{torch_dir}\n{version}"
+
+
 def marshal_up_to_date() -> bool:
-    """_marshal.so is newer than its sources (or torch, which it is built against, is not there)."""
-    if _torch_dir() is None:
+    """_marshal.so is newer than its sources and built against this torch and Python (or torch is not there)."""
+    torch_dir = _torch_dir()
+    if torch_dir is None:
         return True
+    if not os.path.exists(MARSHAL_STAMP):
+        return False
+    with open(MARSHAL_STAMP) as f:
+        if f.read() != _marshal_stamp(torch_dir):
+            return False
     return _newer(MARSHAL_PATH, [os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "dsa.h"), os.path.abspath(__file__)])
 
 
@@ -85,6 +99,8 @@ def _compile_marshal(cc: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, MARSHAL_PATH)
+    with open(MARSHAL_STAMP, "w") as f:
+        f.write(_marshal_stamp(torch_dir))
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:

@@ -62,3 +62,31 @@ def test_each_part_for_itself(place):
     os.remove(build.LIB_PATH)
     build.build()
     assert sorted(place) == sorted(build.SOURCES + ["link"])
+
+
+def test_marshalling_is_built_again_for_another_torch(place):
+    build.build()
+    place.clear()
+    with open(build.MARSHAL_STAMP) as f:
+        ours = f.read()
+    with open(build.MARSHAL_STAMP, "w") as f:
+        f.write(ours.replace("__version__ = '", "__version__ = '1"))
+    assert not build.up_to_date()
+    build.build()
+    assert place == ["marshal.cpp"] and build.up_to_date()
+    with open(build.MARSHAL_STAMP) as f:
+        assert f.read() == ours
+
+
+def test_a_marshalling_that_does_not_load_says_how_to_build_it(monkeypatch):
+    import sparse_attention_indexer_e4m3_gb300 as dsa
+
+    build.build()
+    monkeypatch.setattr(dsa, "_calls", None)
+
+    def load(name, *a):
+        raise ImportError("undefined symbol: _ZN3c10")
+
+    monkeypatch.setattr(dsa.importlib, "import_module", load)
+    with pytest.raises(RuntimeError, match=r"python -m sparse_attention_indexer_e4m3_gb300\.build"):
+        dsa.fork_pages(None, None, None)
