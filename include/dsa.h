@@ -400,6 +400,7 @@ DSA_API dsa_status dsa_fork_pages(const int32_t* table, const int32_t* parent, i
  *              dsa_quantize_kv4_reserved sees to
  *   workspace  dsa_reserve_pages_workspace_size(P) bytes, 4-byte aligned (DSA_ERR_WORKSPACE); its contents on
  *              entry do not matter; two calls running at the same time must not share it
+ * page_rows as above, M * page_rows and R * M < 2^31 (DSA_ERR_UNSUPPORTED otherwise).
  */
 DSA_API size_t dsa_reserve_pages_workspace_size(int P);
 DSA_API dsa_status dsa_reserve_pages(int32_t* table, int32_t* ref, const int32_t* begin, const int32_t* end, int R,

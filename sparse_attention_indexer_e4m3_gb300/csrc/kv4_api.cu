@@ -161,6 +161,7 @@ dsa_status dsa_reserve_pages(int32_t* table, int32_t* ref, const int32_t* begin,
   const dsa_status st = check_tables(R, M, P);
   if (st != DSA_OK) return st;
   if (!kv4_rows(page_rows) || static_cast<int64_t>(M) * page_rows > INT_MAX || R > INT_MAX / 2) return DSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(R) * M > INT_MAX) return DSA_ERR_UNSUPPORTED;  // as many needs at most, which are counted in ints
   if (!lacking || !aligned(lacking, 4)) return DSA_ERR_INVALID_ARG;
   if (R > 0 && (!begin || !aligned(begin, 4) || !end || !aligned(end, 4) || !src || !aligned(src, 4) || !dst ||
                 !aligned(dst, 4)))

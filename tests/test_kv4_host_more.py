@@ -32,3 +32,10 @@ def test_binding_refuses_lacking(lib, lacking):  # noqa: F811
 def test_binding_wants_lacking_on_the_device(lib):  # noqa: F811
     with pytest.raises(ValueError, match="CUDA"):
         dsa.quantize_kv4(z(T, D, t=bf16), CACHE(), z(R, M), z(T), z(T), lacking=z(1))
+
+
+def test_reserve_refuses_more_entries_than_it_can_count(lib, mem):  # noqa: F811
+    """All entries of a table may need pages, and that number has to fit an int: past it the count wrapped."""
+    _, a = mem
+    f = lambda R, M: lib.dsa_reserve_pages(a, a, a, a, R, M, 3, 16, a, a, a, a, 1 << 10, None)  # noqa: E731
+    assert f(1 << 16, 1 << 15) == f(1 << 24, 1 << 24) == f((1 << 30) - 1, 3) == UNSUPPORTED
