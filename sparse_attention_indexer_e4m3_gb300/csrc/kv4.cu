@@ -59,7 +59,8 @@ cudaError_t launch_kv4_read(int D, uint16_t* out, int N, const int32_t* seq, con
 
 cudaError_t launch_pages_fork(const int32_t* table, const int32_t* parent, int R, int M, int P, int32_t* ref,
                               int32_t* out, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(std::min((M + 255) / 256, 1 << 16)), static_cast<unsigned>(std::min(R, 65535)));
+  const dim3 grid(static_cast<unsigned>(std::min((static_cast<int64_t>(M) + 255) / 256, static_cast<int64_t>(1) << 16)),
+                  static_cast<unsigned>(std::min(R, 65535)));
   return launch_dependent(pages_fork_kernel, grid, 256u, stream, table, parent, R, M, P, ref, out);
 }
 
