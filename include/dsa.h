@@ -364,7 +364,7 @@ DSA_API dsa_status dsa_dequantize_kv4(const uint8_t* cache, int P, int page_rows
  *   workspace  dsa_sparse_attn_kv4_workspace_size(T, H, D, K) bytes, 16-byte aligned (may be NULL when that is 0:
  *              with as many tokens and head groups of 64 as SMs); its contents on entry do not matter; two calls
  *              running at the same time must not share it.  DSA_ERR_WORKSPACE if it is missing, short or misaligned
- * H >= 1.  Deterministic.
+ * H >= 1, K <= 2^26 (DSA_ERR_UNSUPPORTED).  Deterministic.
  */
 DSA_API size_t dsa_sparse_attn_kv4_workspace_size(int T, int H, int D, int K);
 DSA_API dsa_status dsa_sparse_attn_kv4(const uint16_t* q, const uint8_t* cache, int P, int page_rows,

@@ -37,6 +37,10 @@ dsa_status check_tables(int R, int M, int P) {
   return DSA_OK;
 }
 
+// Longest list.  A list's last entry is looked for from its end, 256 entries at a time, while the other roles of the
+// kernel wait for it: with nothing but -1 behind its first entry that takes 0.2 s at this length (a wait expires after 1 s).
+constexpr int kKv4MaxList = 1 << 26;
+
 int head_groups(int H) { return H / kTcMaxHeads + (H % kTcMaxHeads != 0 ? 1 : 0); }
 
 // CTAs that share a unit's list: as few blocks per share as the device has clusters for, all units at once.  Joining the shares
@@ -123,7 +127,7 @@ dsa_status dsa_sparse_attn_kv4(const uint16_t* q, const uint8_t* cache, int P, i
     return DSA_ERR_INVALID_ARG;
   const int groups = head_groups(H);
   const int64_t units = static_cast<int64_t>(T) * groups;
-  if (units > INT_MAX / 2 || K > INT_MAX / 2) return DSA_ERR_UNSUPPORTED;
+  if (units > INT_MAX / 2 || K > kKv4MaxList) return DSA_ERR_UNSUPPORTED;
   DeviceFacts dev;
   if (!device_facts(&dev)) return DSA_ERR_CUDA;
   if (sparse_attn_kv4_smem(D) > dev.max_smem) return DSA_ERR_UNSUPPORTED;

@@ -160,3 +160,26 @@ def test_attention_heads_of_extreme_size(dsa):  # noqa: F811
                 o, l, p, x = K4.attend(q, kv, sink, c.scale)
                 to, tl = K4.attend_tolerance(q, kv, r, p, x, o, l, c.scale)
                 assert np.all(np.abs(out[t][heads] - o) <= to) and np.all(np.abs(lse[t][heads] - l) <= tl), (T, e)
+
+
+# ------------------------------------------------------------------------------------ list lengths
+
+
+@pytest.mark.parametrize("at", [0, 2 ** 25 + 7])
+def test_attention_longest_list(dsa, at):  # noqa: F811
+    """2^26 entries, of which one names a row."""
+    import torch
+
+    c = Case(5, 1, 3, 64, 1, 16, start=False, R=1)
+    want = c.run(dsa)
+    long = torch.full((1, 2 ** 26), -1, dtype=torch.int32, device="cuda")
+    long[0, at] = int(c.idx[0, 0])
+    table, cache = torch.from_numpy(c.table).cuda(), torch.from_numpy(c.cache).cuda()
+    seq, lse = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, 3, device="cuda")
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    out = dsa.sparse_attn_kv4(c.q_t, cache, table, seq, long, scale=c.scale, lse=lse)
+    b.record()
+    assert dsa.get_device_error() == 0
+    print(f"{a.elapsed_time(b):.1f} ms")
+    assert np.array_equal(out.double().cpu().numpy(), want[0]) and np.allclose(lse.double().cpu().numpy(), want[1], rtol=2.0 ** -20)

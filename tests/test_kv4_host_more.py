@@ -39,3 +39,9 @@ def test_reserve_refuses_more_entries_than_it_can_count(lib, mem):  # noqa: F811
     _, a = mem
     f = lambda R, M: lib.dsa_reserve_pages(a, a, a, a, R, M, 3, 16, a, a, a, a, 1 << 10, None)  # noqa: E731
     assert f(1 << 16, 1 << 15) == f(1 << 24, 1 << 24) == f((1 << 30) - 1, 3) == UNSUPPORTED
+
+
+def test_attention_refuses_longer_lists_than_it_can_scan_in_time(lib, mem):  # noqa: F811
+    _, a = mem
+    f = lambda K: lib.dsa_sparse_attn_kv4(a, a, 2, 64, a, 1, 2, a, None, None, a, 2, 4, 128, K, 1.0, a, None, None, 0, None)  # noqa: E731
+    assert f((1 << 26) + 1) == f(2 ** 31 - 1) == UNSUPPORTED
