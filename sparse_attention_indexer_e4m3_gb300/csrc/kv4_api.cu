@@ -45,8 +45,8 @@ int head_groups(int H) { return H / kTcMaxHeads + (H % kTcMaxHeads != 0 ? 1 : 0)
 
 // CTAs that share a unit's list: as few blocks per share as the device has clusters for, all units at once.  Joining the shares
 // takes as long as two to three blocks do, so a list is shared where at least that many of its blocks go to other CTAs
-// (one token, 64 heads, shared against not: D = 128, 3 blocks 10.5 to 10.3 us, 4 blocks 10.5 to 11.4, 16 blocks
-// 10.9 to 24.2; D = 512, 2 blocks 16.2 to 15.2 us, 4 blocks 15.6 to 21.1, 16 blocks 15.4 to 55.0).
+// (one token, 64 heads, in a graph, shared against not: 4 blocks, D = 64 9.4 to 10.8 us, 128 9.6 to 10.8, 256 11.6 to 13.2,
+// 512 14.9 to 19.5; 16 blocks 10.6 to 23.8, 10.8 to 24.0, 12.1 to 32.2, 15.2 to 54.1; 3 blocks at D = 512 15.8 to 16.6).
 int list_shares(int64_t units, int D, int K) {
   const int blocks = K / kKv4Block + (K % kKv4Block != 0 ? 1 : 0);
   const int worth = D == 512 ? 2 : 3;

@@ -133,6 +133,8 @@ __device__ __forceinline__ int reserve_need(const ReserveArgs& a, int p) {
 // by the table and counts as they were at the call: (1) count the needs of each row and the free
 // pages of each share of the counts; (2) the k-th lowest free page, for each k below the number of
 // needs, into the workspace; (3) the k-th need, in the order of (r, page of r), takes the k-th page; (4) counts.
+// A warp takes its rows one after another, so past a few hundred sequences the time grows with them (one row of each
+// written, 64 pages a sequence: 64 sequences 8.5 us, 256 9.8, 1024 13.9, 4096 33, 16384 105).
 __global__ void __launch_bounds__(kPagesThreads) __cluster_dims__(kPagesCluster, 1, 1)
     pages_reserve_kernel(const ReserveArgs a) {
   __shared__ WarpCounts s;

@@ -183,3 +183,23 @@ def test_attention_longest_list(dsa, at):  # noqa: F811
     assert dsa.get_device_error() == 0
     print(f"{a.elapsed_time(b):.1f} ms")
     assert np.array_equal(out.double().cpu().numpy(), want[0]) and np.allclose(lse.double().cpu().numpy(), want[1], rtol=2.0 ** -20)
+
+
+# ------------------------------------------------------------------------------------ workspaces
+
+
+def test_attention_workspace_alignment_and_size(dsa):  # noqa: F811
+    """Of the right size but 8 bytes off, 16 bytes short, and 16 bytes into a larger buffer."""
+    import torch
+
+    c = Case(21, 2, 64, 512, 700, 64, length=500)
+    need = dsa.sparse_attn_kv4_workspace_size(c.T, c.H, c.D, c.K)
+    big = torch.full((need + 32,), 0xFF, dtype=torch.uint8, device="cuda")
+    assert need > 0 and big.data_ptr() % 16 == 0
+    for bad in (big[8:8 + need], big[4:], big[:need - 16], big[:need - 1]):
+        with pytest.raises(dsa.DsaError) as e:
+            c.run(dsa, workspace=bad)
+        assert e.value.status == 3
+    want, got = c.run(dsa), c.run(dsa, workspace=big[16:16 + need])
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+    assert bool((big[:16] == 0xFF).all()) and bool((big[16 + need:] == 0xFF).all())
