@@ -353,8 +353,8 @@ DSA_API dsa_status dsa_dequantize_kv4(const uint8_t* cache, int P, int page_rows
  * An entry that is negative, lies before start[t] or behind the sequence's table row, or whose page is not
  * mapped is skipped (its memory is not read); a token without entries gets zeros and an lse of its sink (-inf
  * without one).  With dsa_index_topk, start[t] = ks[t] when the keys of seq[t] are packed from ks[t] on.
- * Weights enter the weighted sum as fp16, q as fp16 times a power of two of each head (a value is off by at most 2^-29
- * of the largest of its token and head, and not at all down to 2^-21 of it); products accumulate in fp32.
+ * Weights enter the weighted sum as fp16, q as fp16 times a power of two of each head (a value is off by at most 2^-23
+ * of the largest of its token and head, and not at all down to 2^-15 of it); products accumulate in fp32.
  *
  *   q          bf16 [T][H][D], 16-byte aligned
  *   seq        int32 [T];  start  int32 [T] or NULL (0)

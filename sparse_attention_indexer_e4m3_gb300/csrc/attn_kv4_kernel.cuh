@@ -4,7 +4,7 @@
 //     x_j = scale * q[t,h,:] . kv_j
 //     out[t,h,:] = sum_j e^{x_j} kv_j / ( sum_j e^{x_j} + e^{sink[h]} )
 // Both products run on fp16 operands with fp32 accumulators.  v_j is exact; q is bf16 and becomes fp16 times a
-// power of two of its head, each value off by at most 2^-29 of the head's largest (those down to 2^-21 of it not at all);
+// power of two of its head, each value off by at most 2^-23 of the head's largest (those down to 2^-15 of it not at all);
 // the weights enter the second product as w_j = r_j * 2^(y_j - m), y = x log2 e,
 // rounded to fp16 (half a step, 2^-11), with m a bound on y_j + log2 r_j so that w_j <= 2^8 whatever the
 // row scales are.  fp16 weights rather than bf16 ones because their rounding would otherwise be as large as the
@@ -13,8 +13,9 @@
 // as none is lost where w_j underflows: m is at most (the largest y) + log2 of (the largest row scale so far), so with row
 // scales within 2^100 of one another a row whose w_j is below 2^-126 has a weight below 2^-26 of the largest.  A
 // block with row scales further below the largest so far (rows of zeros, held with r = 2^-100, beside rows of 2^11
-// or more) forms its terms by an exponential of their own, which may be subnormal: y_j - m lies between -125 (at least for
-// the largest y: m is at most 117 and the 2^8 above it) and 108, so they keep 24 bits below the largest and do not overflow.
+// or more) forms its terms by an exponential of their own, which may be subnormal: y_j - m lies between -117 (for the largest
+// y, as m is at most 117 above it) and 108 (rows of the least scale, 2^8 above the bound), so the largest keep 24 bits and
+// more, and sums of up to 2^19 rows, 2^26 with scores that do not grow, do not overflow.
 //
 // A unit is (token, group of up to 64 heads, share of the token's list); a cluster of S CTAs shares
 // one list and joins its S partial results, so a call with few tokens still uses most SMs and needs no second
@@ -43,6 +44,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "attn_tc_kernel.cuh"
 #include "cluster.cuh"
 #include "kv4.cuh"
@@ -64,9 +67,11 @@ constexpr int kKv4Scouts = 3;             // scout warps; one of them looks up e
 constexpr int kKv4Slots = 2 * kKv4Scouts; // blocks whose entries are looked up ahead (a slot is always one scout's)
 constexpr int kKv4Shares = kKv4MaxShares; // most CTAs that share a list
 constexpr float kKv4NoBound = -3e38f;     // bound of a head without keys so far (finite: a masked key is minus infinity)
-// q enters as 2^kKv4QExp of itself where the largest value of its head has an exponent in [kKv4QLow, kKv4QHigh] (ordinary q;
-// every value is then off by at most 2^-25 / 2^8, 2^-29 of the head's largest), else by the head's own power of two.
-constexpr int kKv4QExp = 8, kKv4QLow = -4, kKv4QHigh = 7;
+// q enters times 2^kKv4QExp where the largest value of its head has an exponent in [kKv4QLow, kKv4QHigh] (ordinary q), else
+// times a power of two of the head, which brings that to [2^13, 2^14); the softmax then takes the unit's scores to one
+// scale first (7% of a 4096-token prompt, 17% at D = 128).  In fp16 a value of 2^-17 or more is exact and others are
+// off by at most 2^-25: here 2^-15 and 2^-23 of the head's largest.
+constexpr int kKv4QExp = 7, kKv4QLow = -9, kKv4QHigh = 8;
 constexpr float kKv4Spread = 1.2676506002282294e30f;  // 2^100: row scales within it share the weights' exponentials
 
 template <int D>
@@ -89,8 +94,7 @@ struct AttnKv4Layout {
   static constexpr int kAlpha = kMax + kTcAttnHeads * 4;        // float [64] rescale / output factors
   static constexpr int kJoin = kAlpha + kTcAttnHeads * 4;       // float [shares][64] factors of the shares
   static constexpr int kMisc = kJoin + kKv4Shares * kTcAttnHeads * 4;  // int [32]
-  static constexpr int kLargest = kMisc + 128;                  // float [softmax warps]
-  static constexpr int kQFac = kLargest + kKv4SoftWarps * 4;    // float [2][64] by unit: what undoes the heads' q factors
+  static constexpr int kQFac = kMisc + 128;                     // float [2][64] by unit: what undoes the heads' q factors
   static constexpr int kPhase = kQFac + 2 * kTcAttnHeads * 4;   // int [softmax warps]
   static constexpr int kBar = kPhase + kKv4SoftWarps * 4;
   static constexpr int kNumBars = 16 + 3 * kKv4Slots + 2 * kStages * kTiles;
@@ -239,11 +243,11 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
   float* max_s = reinterpret_cast<float*>(smem + L::kMax);
   float* alpha_s = reinterpret_cast<float*>(smem + L::kAlpha);
   float* join_s = reinterpret_cast<float*>(smem + L::kJoin);
-  // [0, 1] blocks of the units in flight, [16..18] by block modulo 3: a bound has to be raised, [20..31] by slot: its smallest and largest row scale
+  // [0, 1] blocks of the units in flight, [16..18] by block modulo 3: a bound has to be raised, [20..31] by slot: its
+  // smallest and largest row scale
   volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMisc);
   float* qfac_s = reinterpret_cast<float*>(smem + L::kQFac);
   float2* span_s = reinterpret_cast<float2*>(smem + L::kMisc + 80);
-  float* largest_s = reinterpret_cast<float*>(smem + L::kLargest);
   static_assert(kKv4Slots <= 6, "spans of the slots lie behind the flags");
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   // (a barrier that its waiters may lag behind by more than a phase is a pair, or one per stage)
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
     constexpr int kEach = D / 8 / kAcross;            // 16-byte pieces of a lane
     constexpr int kHeads = 32 / kAcross;              // heads at a time
     constexpr int kSteps = kTcAttnHeads / (kKv4ConvWarps * kHeads);
-    constexpr int kMost = (kSingle || D == 512 ? 4 : 2) / kEach;  // in flight at a time (more spilled registers)
+    constexpr int kMost = (D == 512 ? 8 : 4) / kEach;  // in flight at a time
     constexpr int kBatch = kSteps < kMost ? kSteps : kMost;
     const int head = w * kHeads + lane / kAcross, piece = lane % kAcross;
 #pragma unroll 1
@@ -534,83 +538,28 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
       for (int h = 0; h < kKv4SoftHeads / 2; ++h) lsum[h] = 0ull;
       if (bar_or(kTcEpiBar, kKv4SoftThreads, *abort_flag != 0)) break;
       if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
-      // largest row scale of the unit so far (this warp's, all lanes alike); infinite where heads have q factors of their own,
-      // which makes every block of the unit take the general path
-      volatile float* largest = largest_s + (warp - 4);
-      *largest = __any_sync(0xffffffffu, qfac[lane] != kQFac || qfac[32 + lane] != kQFac) ? INFINITY : 0.f;
-      for (int b = 0; b < nb; ++b, ++gb) {
-        if (b % kLook == kLook - 1 && gone()) break;
-        const uint32_t slot = gb % kKv4Slots;
-        mbar_wait(&scl_full[slot], (gb / kKv4Slots) & 1u, abort_flag, err, 0x65);
-        float rs = scl_s[slot * kTcAttnKeys + r];
-        const float2 span = span_s[slot];
-        const float most = fmaxf(*largest, span.y);
-        *largest = most;
-        const bool apart = most > span.x * kKv4Spread;  // (or a unit with q factors)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ent_empty[slot]);
-        const bool valid = rs > 0.f;
-        float a = to_log2 * (rs * kQFac);                // score to log2 units
-        const float lr = valid ? log2f(rs) : -INFINITY;  // a masked key's weight is 0
-        const uint64_t lr2 = pack_f32x2(lr, lr);
-        const uint32_t s_at = s_tmem + 64 * (gb % kSc) + lane_off + hb;
-        mbar_wait(&s_full[gb % kSc], (gb / kSc) & 1u, abort_flag, err, 0x61);
-        tc_fence_after_sync();
-        float x[kKv4SoftHeads];
-        // exponents relative to the running bounds
-        const auto exponents = [&]() {
-          const uint64_t minus = pack_f32x2(-1.f, -1.f), a2 = pack_f32x2(a, a);
-          tmem_ld_x16(s_at, x);
-          tmem_wait_ld_regs16(x);
-#pragma unroll
-          for (int h = 0; h < kKv4SoftHeads; h += 4) {
-            const float4 mv = *reinterpret_cast<const float4*>(max_s + hb + h);
-            unpack_f32x2(fma_f32x2(pack_f32x2(mv.x, mv.y), minus, fma_f32x2(pack_f32x2(x[h], x[h + 1]), a2, lr2)), x[h], x[h + 1]);
-            unpack_f32x2(fma_f32x2(pack_f32x2(mv.z, mv.w), minus, fma_f32x2(pack_f32x2(x[h + 2], x[h + 3]), a2, lr2)), x[h + 2],
-                         x[h + 3]);
-          }
-        };
-        // weights, written into the fp16 row P[key r]; x keeps them
-        const auto weights = [&]() {
-#pragma unroll
-          for (int hh = 0; hh < kKv4SoftHeads; hh += 8) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[hh + 2 * i] = exp2_approx(x[hh + 2 * i]);
-              x[hh + 2 * i + 1] = exp2_approx(x[hh + 2 * i + 1]);
-              const __half2 w = __floats2half2_rn(x[hh + 2 * i], x[hh + 2 * i + 1]);
-              pk[i] = *reinterpret_cast<const uint32_t*>(&w);
-            }
-            *reinterpret_cast<uint4*>(p_s + swz128(r, 2 * (hb + hh))) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          }
-        };
-        // A unit's first block sets the bounds.  After that the weights are formed with the bounds as they are,
-        // while the warps tell one another whether an exponent exceeds its bound by more than 2^8; if one
-        // does, which is rare, the bounds are raised and the weights formed again.  (What else is rare goes that way too, as if a
-        // bound were exceeded: no branches for all other blocks.)
-        bool raise = b == 0;
-        if (!raise) {
-          exponents();
-          float over = x[0];
-#pragma unroll
-          for (int h = 1; h + 1 < kKv4SoftHeads; h += 2) over = max3(over, x[h], x[h + 1]);
-          over = fmaxf(over, x[kKv4SoftHeads - 1]);
-          if (__any_sync(0xffffffffu, over > kTcLazyLog2 || apart) && lane == 0) misc[16 + checks % 3] = 1;
+      float largest = 0.f;  // row scale of the unit so far
+      // the unit's blocks, of q with or without factors of the heads' own (one loop that looks in each block took 3% longer)
+      const auto walk = [&](auto with_own) {
+        for (int b = 0; b < nb; ++b, ++gb) {
+          if (b % kLook == kLook - 1 && gone()) break;
+          const uint32_t slot = gb % kKv4Slots;
+          mbar_wait(&scl_full[slot], (gb / kKv4Slots) & 1u, abort_flag, err, 0x65);
+          float rs = scl_s[slot * kTcAttnKeys + r];
+          const float2 span = span_s[slot];
+          largest = fmaxf(largest, span.y);
+          const bool apart = largest > span.x * kKv4Spread;  // some row's weight may underflow
           __syncwarp();
-          if (lane == 0) mbar_arrive(checked);
-          mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x63);  // the previous weighted sum has read P
-          weights();
-          mbar_wait(checked, checks & 1u, abort_flag, err, 0x67);
-          raise = __any_sync(0xffffffffu, misc[16 + checks % 3] != 0) != 0;
-          ++checks;
-          // this flag's next use but one: every warp has read it (two blocks ago), none sets it before the next check
-          if (etid == 0) misc[16 + (checks + 1) % 3] = 0;
-        }
-        if (raise) {
-          if (b > 0 && gone()) break;
-          const bool far = __any_sync(0xffffffffu, apart) != 0;
-          if (__any_sync(0xffffffffu, *largest == INFINITY)) {  // the scores with the heads' own q factors, once and for all that follows
+          if (lane == 0) mbar_arrive(&ent_empty[slot]);
+          const bool valid = rs > 0.f;
+          float a = to_log2 * (rs * kQFac);                // score to log2 units
+          const float lr = valid ? log2f(rs) : -INFINITY;  // a masked key's weight is 0
+          const uint64_t lr2 = pack_f32x2(lr, lr);
+          const uint32_t s_at = s_tmem + 64 * (gb % kSc) + lane_off + hb;
+          mbar_wait(&s_full[gb % kSc], (gb / kSc) & 1u, abort_flag, err, 0x61);
+          tc_fence_after_sync();
+          float x[kKv4SoftHeads];
+          if constexpr (decltype(with_own)::value) {  // the scores with the heads' own q factors, once and for all that follows
             tmem_ld_x16(s_at, x);
             tmem_wait_ld_regs16(x);
 #pragma unroll
@@ -622,64 +571,122 @@ __global__ void __launch_bounds__(kKv4Threads, 1) sparse_attn_kv4_kernel(const A
             tmem_wait_st();
             a = 1.f;
           }
-          // the largest exponents per head across the 128 keys (the reduction consumes x)
-          tmem_ld_x16(s_at, x);
-          tmem_wait_ld_regs16(x);
+          // exponents relative to the running bounds
+          const auto exponents = [&]() {
+            const uint64_t minus = pack_f32x2(-1.f, -1.f), a2 = pack_f32x2(a, a);
+            tmem_ld_x16(s_at, x);
+            tmem_wait_ld_regs16(x);
 #pragma unroll
-          for (int h = 0; h < kKv4SoftHeads; ++h) x[h] = fmaf(x[h], a, lr);
-          xpose_reduce16(x, lane, [](float v, float w) { return fmaxf(v, w); });
-          if ((lane & 1) == 0) red_s[quarter * kTcAttnHeads + hb + (lane >> 1)] = x[0];
-          meet(b == 0);
-          if (etid < kTcAttnHeads) {
-            const float bm = fmaxf(fmaxf(red_s[etid], red_s[kTcAttnHeads + etid]),
-                                   fmaxf(red_s[2 * kTcAttnHeads + etid], red_s[3 * kTcAttnHeads + etid]));
-            const float mo = max_s[etid];
-            const float mn = (bm > mo + kTcLazyLog2) ? bm : mo;
-            // (the root of the factor: a sum may be as large as 2^100 times the bound's unit and is not to be lost)
-            alpha_s[etid] = (mo == kKv4NoBound || mn == mo) ? 1.f : exp2f(0.5f * (mo - mn));
-            max_s[etid] = mn;
-          }
-          meet(b == 0);
-          if (b > 0) {
-            // sums and output accumulators of earlier blocks follow the new bound (this thread: its dim row r
-            // of every tile, its 16 head columns)
-#pragma unroll
-            for (int h = 0; h < kKv4SoftHeads; h += 2) {
-              const uint64_t root = pack_f32x2(alpha_s[hb + h], alpha_s[hb + h + 1]);
-              lsum[h / 2] = fma_f32x2(fma_f32x2(lsum[h / 2], root, 0ull), root, 0ull);
+            for (int h = 0; h < kKv4SoftHeads; h += 4) {
+              const float4 mv = *reinterpret_cast<const float4*>(max_s + hb + h);
+              unpack_f32x2(fma_f32x2(pack_f32x2(mv.x, mv.y), minus, fma_f32x2(pack_f32x2(x[h], x[h + 1]), a2, lr2)), x[h], x[h + 1]);
+              unpack_f32x2(fma_f32x2(pack_f32x2(mv.z, mv.w), minus, fma_f32x2(pack_f32x2(x[h + 2], x[h + 3]), a2, lr2)), x[h + 2],
+                           x[h + 3]);
             }
-            tc_fence_after_sync();
-#pragma unroll 1
-            for (int m = 0; m < kTi; ++m) {
-              tmem_ld_x16(o_tmem + lane_off + 64 * m + hb, x);
-              tmem_wait_ld_regs16(x);
+          };
+          // weights, written into the fp16 row P[key r]; x keeps them
+          const auto weights = [&]() {
 #pragma unroll
-              for (int j = 0; j < kKv4SoftHeads; ++j) x[j] = x[j] * alpha_s[hb + j] * alpha_s[hb + j];
-              tmem_st_x16(o_tmem + lane_off + 64 * m + hb, x);
+            for (int hh = 0; hh < kKv4SoftHeads; hh += 8) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                x[hh + 2 * i] = exp2_approx(x[hh + 2 * i]);
+                x[hh + 2 * i + 1] = exp2_approx(x[hh + 2 * i + 1]);
+                const __half2 w = __floats2half2_rn(x[hh + 2 * i], x[hh + 2 * i + 1]);
+                pk[i] = *reinterpret_cast<const uint32_t*>(&w);
+              }
+              *reinterpret_cast<uint4*>(p_s + swz128(r, 2 * (hb + hh))) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
-            tmem_wait_st();
-          } else if (gb > 0) {
-            mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x62);
-          }
-          exponents();
-          weights();
-          if (far) {  // the denominator's terms by themselves, from the same exponents (the scores are still there)
+          };
+          // A unit's first block sets the bounds.  After that the weights are formed with the bounds as they are,
+          // while the warps tell one another whether an exponent exceeds its bound by more than 2^8; if one
+          // does, which is rare, the bounds are raised and the weights formed again.  (What else is rare goes that way too, as if a
+          // bound were exceeded: no branches for all other blocks.)
+          bool raise = b == 0;
+          if (!raise) {
             exponents();
+            float over = x[0];
 #pragma unroll
-            for (int h = 0; h < kKv4SoftHeads; ++h) x[h] = lr > -INFINITY ? exp2_gradual(x[h] - lr) : 0.f;
-            rs = -1.f;
+            for (int h = 1; h + 1 < kKv4SoftHeads; h += 2) over = max3(over, x[h], x[h + 1]);
+            over = fmaxf(over, x[kKv4SoftHeads - 1]);
+            if (__any_sync(0xffffffffu, over > kTcLazyLog2 || apart) && lane == 0) misc[16 + checks % 3] = 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(checked);
+            mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x63);  // the previous weighted sum has read P
+            weights();
+            mbar_wait(checked, checks & 1u, abort_flag, err, 0x67);
+            raise = __any_sync(0xffffffffu, misc[16 + checks % 3] != 0) != 0;
+            ++checks;
+            // this flag's next use but one: every warp has read it (two blocks ago), none sets it before the next check
+            if (etid == 0) misc[16 + (checks + 1) % 3] = 0;
           }
-        }
-        fence_proxy_async_shared();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
-        // what makes a weight a term of the denominator (2^-23 off; a division took 1% of a long prompt), or x is the term
-        const float inv = rs > 0.f ? rcp_approx(rs) : (rs < 0.f ? 1.f : 0.f);
-        const uint64_t inv2 = pack_f32x2(inv, inv);
+          if (raise) {
+            if (b > 0 && gone()) break;
+            const bool far = __any_sync(0xffffffffu, apart) != 0;
+            // the largest exponents per head across the 128 keys (the reduction consumes x)
+            tmem_ld_x16(s_at, x);
+            tmem_wait_ld_regs16(x);
 #pragma unroll
-        for (int h = 0; h < kKv4SoftHeads; h += 2) lsum[h / 2] = fma_f32x2(pack_f32x2(x[h], x[h + 1]), inv2, lsum[h / 2]);
-      }
+            for (int h = 0; h < kKv4SoftHeads; ++h) x[h] = fmaf(x[h], a, lr);
+            xpose_reduce16(x, lane, [](float v, float w) { return fmaxf(v, w); });
+            if ((lane & 1) == 0) red_s[quarter * kTcAttnHeads + hb + (lane >> 1)] = x[0];
+            meet(b == 0);
+            if (etid < kTcAttnHeads) {
+              const float bm = fmaxf(fmaxf(red_s[etid], red_s[kTcAttnHeads + etid]),
+                                     fmaxf(red_s[2 * kTcAttnHeads + etid], red_s[3 * kTcAttnHeads + etid]));
+              const float mo = max_s[etid];
+              const float mn = (bm > mo + kTcLazyLog2) ? bm : mo;
+              // (the root of the factor: a sum may be as large as 2^100 times the bound's unit and is not to be lost)
+              alpha_s[etid] = (mo == kKv4NoBound || mn == mo) ? 1.f : exp2f(0.5f * (mo - mn));
+              max_s[etid] = mn;
+            }
+            meet(b == 0);
+            if (b > 0) {
+              // sums and output accumulators of earlier blocks follow the new bound (this thread: its dim row r
+              // of every tile, its 16 head columns)
+#pragma unroll
+              for (int h = 0; h < kKv4SoftHeads; h += 2) {
+                const uint64_t root = pack_f32x2(alpha_s[hb + h], alpha_s[hb + h + 1]);
+                lsum[h / 2] = fma_f32x2(fma_f32x2(lsum[h / 2], root, 0ull), root, 0ull);
+              }
+              tc_fence_after_sync();
+#pragma unroll 1
+              for (int m = 0; m < kTi; ++m) {
+                tmem_ld_x16(o_tmem + lane_off + 64 * m + hb, x);
+                tmem_wait_ld_regs16(x);
+#pragma unroll
+                for (int j = 0; j < kKv4SoftHeads; ++j) x[j] = x[j] * alpha_s[hb + j] * alpha_s[hb + j];
+                tmem_st_x16(o_tmem + lane_off + 64 * m + hb, x);
+              }
+              tmem_wait_st();
+            } else if (gb > 0) {
+              mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0x62);
+            }
+            exponents();
+            weights();
+            if (far) {  // the denominator's terms by themselves, from the same exponents (the scores are still there)
+              exponents();
+#pragma unroll
+              for (int h = 0; h < kKv4SoftHeads; ++h) x[h] = lr > -INFINITY ? exp2_gradual(x[h] - lr) : 0.f;
+              rs = -1.f;
+            }
+          }
+          fence_proxy_async_shared();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full);
+          // what makes a weight a term of the denominator (2^-23 off; a division took 1% of a long prompt), or x is the term
+          const float inv = rs > 0.f ? rcp_approx(rs) : (rs < 0.f ? 1.f : 0.f);
+          const uint64_t inv2 = pack_f32x2(inv, inv);
+#pragma unroll
+          for (int h = 0; h < kKv4SoftHeads; h += 2) lsum[h / 2] = fma_f32x2(pack_f32x2(x[h], x[h + 1]), inv2, lsum[h / 2]);
+        }
+      };
+      if (__any_sync(0xffffffffu, qfac[lane] != kQFac || qfac[32 + lane] != kQFac))
+        walk(std::true_type());
+      else
+        walk(std::false_type());
       // end of the unit: denominators (partial sums across the 128 keys)
       {
         float l[kKv4SoftHeads];

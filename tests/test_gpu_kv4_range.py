@@ -101,9 +101,10 @@ def test_attention_very_negative_scores(dsa, T, K):  # noqa: F811
 
 # ------------------------------------------------------------------------------------ q
 #
-# A head's q enters as fp16 times a power of two of the head: each value is off by at most 2^-29 of the head's largest.  Beside
-# attend_tolerance's 4 D 2^-24 of sum |q| |kv| that is nothing where the head's values are of one size, and where they
-# are not, the tests below hold values that are exact all the same (8 significant bits, 2^20 below the largest).
+# A head's q enters as fp16 times a power of two: each value is off by at most 2^-23 of the head's largest.  Beside
+# attend_tolerance's 4 D 2^-24 of sum |q| |kv| that is little where the head's values are of one size (the largest of D normal
+# values is below 6 times their mean), and where they are not, the tests below hold values that are exact all the same
+# (8 significant bits, 2^19 below a largest value of 2^-4 or more).
 
 
 @pytest.mark.parametrize("D,H,T", [(64, 7, 2), (128, 64, 3), (256, 20, 160), (512, 70, 2), (512, 64, 160)])
@@ -123,6 +124,25 @@ def test_attention_heads_of_different_size(dsa, D, H, T, low):  # noqa: F811
         to, tl = K4.attend_tolerance(q, kv, r, p, x, o, l, c.scale)
         assert np.all(np.abs(out[t][small] - o) <= to) and np.all(np.abs(lse[t][small] - l) <= tl)
     assert np.all(np.isfinite(out))
+
+
+@pytest.mark.parametrize("base", [0, -20, 30])
+@pytest.mark.parametrize("T", [2, 160])
+def test_attention_heads_about_the_widest_common_factor(dsa, T, base):  # noqa: F811
+    """Heads 2^9 and 2^10, 2^14 to 2^16 and 2^19 below the largest: where one factor serves all of them and where not."""
+    for spread in (0, 9, 10, 14, 15, 16, 19):
+        c = Case(T + spread, T, 66, 128, 150, 32, sink=True, spread=0)
+        size = 2.0 ** (base - spread * (np.arange(66) % 2))
+        c.q_t, c.q = bf16(c.q * size[None, :, None])
+        for part in (0, 1):
+            c.scale = 0.6 / np.sqrt(c.D) * 2.0 ** (spread * part - base)
+            out, lse = c.run(dsa)
+            for t in range(0, T, 31):
+                kv, r = c.listed(t)
+                q, sink = c.q[t][part::2], c.sink[part::2]
+                o, l, p, x = K4.attend(q, kv, sink, c.scale)
+                to, tl = K4.attend_tolerance(q, kv, r, p, x, o, l, c.scale)
+                assert np.all(np.abs(out[t][part::2] - o) <= to) and np.all(np.abs(lse[t][part::2] - l) <= tl), (spread, part)
 
 
 @pytest.mark.parametrize("top", [0.0625, 1.0, 2.0, 200.0, 40000.0])

@@ -51,7 +51,7 @@ def test_decisions_are_the_warp_s(roles):
     """What a warp's lanes read after a wait that may have failed for some of them and decide by, they vote on."""
     text = roles["softmax"]
     for name in ("raise = __any_sync(0xffffffffu, misc[16 + checks % 3] != 0)", "far = __any_sync(0xffffffffu, apart)",
-                 "if (__any_sync(0xffffffffu, *largest == INFINITY))"):
+                 "if (__any_sync(0xffffffffu, qfac[lane] != kQFac || qfac[32 + lane] != kQFac))"):
         assert name in text, name
     for use in re.finditer(r"if \(apart\)|if \(valid\)|if \(rs", text):
         raise AssertionError(use.group())
