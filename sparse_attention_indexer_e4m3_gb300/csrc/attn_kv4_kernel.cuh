@@ -32,13 +32,14 @@
 // block are in flight while its tiles are waited for.  Up to D = 256 two or four blocks fit, and the score product
 // of the next block is issued before the weighted sum of the last, so the softmax runs beside it.
 //
-// What bounds it (D = 512, 64 heads, lists of 2048; 4096 tokens in 1.19 ms, 925 TFLOP/s, 48% of the measured
+// What bounds it (D = 512, 64 heads, lists of 2048; 4096 tokens in 1.22 ms, 901 TFLOP/s, 47% of the measured
 // bf16 rate; the attention over bf16 rows reaches 595 TFLOP/s): a tensor-core instruction of these shapes takes 52 to 63
 // cycles whatever its 64 heads need (at 128 columns it does twice the work in 64), so a block's 64 instructions take
-// 3,650 cycles of its 4,700; the softmax (1,500) stands between the two products, because one block and
-// the 64 KB of q fill shared memory, and overlaps them in part.  At D = 256 and below a block takes 2,100 to
-// 2,300 cycles, the softmax's latency.  A unit costs 5,000 to 12,000 cycles beside its blocks (its q, its first
-// block's way in, its output).  Tried without gain: 8 softmax warps of 32 heads (registers), the next q brought
+// 3,650 cycles of its 4,800; the softmax (1,500) stands between the two products, because one block and
+// the 64 KB of q fill shared memory, and overlaps them in part.  At D = 256 and below a block takes 1.04 us (D = 64 and
+// 128) to 1.34 us (256), the softmax's latency, against 2.6 at 512.  A unit costs 5,000 to 12,000 cycles beside its
+// blocks (its q, its first block's way in, its output).  72 registers a thread are all that 896 threads have: the roles
+// spill up to 28 bytes, and a change in one of them moves the others' time by a few percent.  Tried without gain: 8 softmax warps of 32 heads (registers), the next q brought
 // by the softmax warps or by asynchronous copies, two buffers of P, register shares moved between the roles.
 #pragma once
 
