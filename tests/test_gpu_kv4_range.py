@@ -223,3 +223,26 @@ def test_attention_workspace_alignment_and_size(dsa):  # noqa: F811
     want, got = c.run(dsa), c.run(dsa, workspace=big[16:16 + need])
     assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
     assert bool((big[:16] == 0xFF).all()) and bool((big[16 + need:] == 0xFF).all())
+
+
+@pytest.mark.parametrize("size", ["small", "mixed"])
+@pytest.mark.parametrize("T,K", [(2, 900), (160, 300)])
+def test_attention_own_factors_beside_rows_far_apart(dsa, T, K, size):  # noqa: F811
+    """Heads that need powers of two of their own, over lists of rows whose scales lie far apart."""
+    c = Case(T + K, T, 20, 128, K, 32, spread=0, sink=True)
+    for s in range(c.R):
+        x = c.rng.standard_normal((c.length, c.D))
+        x[:100] *= 2.0 ** 50
+        x[100:200] = 0.0
+        hold(c, s, x)
+    head = 2.0 ** -30 * np.ones(20) if size == "small" else np.where(np.arange(20) % 2, 2.0 ** -25, 1.0)
+    c.q_t, c.q = bf16(c.q * head[None, :, None])
+    c.scale *= 2.0 ** -50 / head.min()
+    heads = np.flatnonzero(head == head.min())
+    out, lse = c.run(dsa)
+    for t in range(0, T, 13):
+        kv, r = c.listed(t)
+        q, sink = c.q[t][heads], c.sink[heads]
+        o, l, p, x = K4.attend(q, kv, sink, c.scale)
+        to, tl = K4.attend_tolerance(q, kv, r, p, x, o, l, c.scale)
+        assert np.all(np.abs(out[t][heads] - o) <= to) and np.all(np.abs(lse[t][heads] - l) <= tl)
