@@ -159,8 +159,10 @@ def _empty(shape, dtype, device, stream):
     torch = _torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    here = torch.cuda.current_stream(device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)):
+    here, handle = torch.cuda.current_stream(device), int(stream.cuda_stream)
+    # (an ExternalStream of handle 0 would be some other stream, not the default one)
+    there = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(there):
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(here)
     return t

@@ -159,3 +159,34 @@ def test_nothing_is_allocated_when_the_caller_brings_everything(dsa, world):  # 
     for kw in (dict(lacking=one, workspace=ws), dict(src=none, lacking=one, workspace=ws), {}):
         got = dsa.reserve_pages(empty, w["ref"], e_begin, e_begin, B, **kw)
         assert [t.numel() for t in got] == [0, 0, 1] and got[2].item() == 0
+
+
+def pool_of(t):
+    """The stream whose pool the tensor's memory belongs to."""
+    import torch
+
+    p = t.untyped_storage().data_ptr()
+    found = [s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= p < s["address"] + s["total_size"]]
+    assert len(found) == 1
+    return found[0]
+
+
+@pytest.mark.parametrize("name", NAMES + ["index_score", "topk", "quantize_k", "sparse_attn", "sparse_attn_bwd"])
+def test_allocations_from_the_right_pool(dsa, world, name):  # noqa: F811
+    """For another stream, for the default stream (whose handle is 0) beside another current one, and without stream=."""
+    import torch
+
+    f = (calls(dsa, world) if name in NAMES else small(dsa))[name][0]
+    side, third = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    assert pool_of(f(side)) == side.cuda_stream
+    assert pool_of(f(torch.cuda.ExternalStream(side.cuda_stream))) == side.cuda_stream
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        assert pool_of(f(torch.cuda.default_stream())) == 0
+        assert pool_of(f(third)) == third.cuda_stream
+        assert pool_of(f(None)) == side.cuda_stream
+        assert pool_of(f(side)) == side.cuda_stream
+    torch.cuda.synchronize()
+    assert pool_of(f(torch.cuda.current_stream())) == 0 and pool_of(f(None)) == 0
+    torch.cuda.synchronize()
