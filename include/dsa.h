@@ -430,6 +430,82 @@ DSA_API dsa_status dsa_copy_pages(void* pages, size_t page_bytes, int P, const i
                                   void* stream);
 
 /*
+ * The bf16 paged cache: pages uint16 (bf16 bits) [P][page_rows][D], 16-byte aligned, each row both key and value,
+ * under the same tables as the 4-bit cache (page_rows a power of two in [16, 256], M * page_rows < 2^31, D in
+ * {64, 128, 256, 512}; DSA_ERR_UNSUPPORTED otherwise).  The page calls above serve it as they are.
+ *
+ * dsa_step_maps -- the tokens of a step from the sequences' lengths.  Sequence r holds held[r] rows and gets added[r]
+ * more (below 0: 0); the added tokens lie one sequence after the other.  With A = the sum of added and K the sum of
+ * held + added over the sequences before r, token t of A <= t < A + added[r] gets
+ *     seq[t] = r,  pos[t] = held[r] + t - A,  ks[t] = K,  ke[t] = K + pos[t] + 1
+ * (the last two: its window among index keys packed sequence by sequence), a token behind the last -1, -1, 0, 0, which
+ * every call on a cache leaves out.  Tokens from T on are dropped; a value past the largest int becomes it.
+ *   held, added   int32 [R];  seq, pos, ks, ke  int32 [T]  OUTPUT
+ */
+DSA_API dsa_status dsa_step_maps(const int32_t* held, const int32_t* added, int R, int T, int32_t* seq, int32_t* pos,
+                                 int32_t* ks, int32_t* ke, void* stream);
+
+/*
+ * dsa_page_slots -- rows of a sequence as rows of the pages: entry v = idx[t][k] >= 0 names row j = v - start[t] of sequence
+ * seq[t], slots[t][k] = table[seq[t]][j / page_rows] * page_rows + j % page_rows, -1 for a negative entry or one without a page.
+ * With the pages as kv [P * page_rows][D], dsa_sparse_attn and dsa_sparse_attn_bwd take the slots of dsa_index_topk's
+ * lists (start[t] = ks[t] where the keys of seq[t] are packed from ks[t] on) and so read a paged cache.
+ *   seq int32 [T];  start int32 [T] or NULL (0);  idx int32 [T][K];  slots int32 [T][K]  OUTPUT (may be idx)
+ * P * page_rows < 2^31 (DSA_ERR_UNSUPPORTED).
+ */
+DSA_API dsa_status dsa_page_slots(const int32_t* table, int R, int M, int P, int page_rows, const int32_t* seq,
+                                  const int32_t* start, const int32_t* idx, int T, int K, int32_t* slots, void* stream);
+
+/*
+ * dsa_store_kv -- writes row i of kv as row pos[i] of sequence seq[i].  A row whose place is not mapped is left out, and
+ * all are where *lacking (dsa_reserve_pages' output, or NULL) is not 0.
+ *   kv         bf16 (uint16 bits), row i at kv + i * stride (in values, a multiple of 8, at least D); 16-byte aligned
+ *   seq, pos   int32 [N]; the same place at most once (else the rows may end up mixed)
+ */
+DSA_API dsa_status dsa_store_kv(const uint16_t* kv, int64_t stride, const int32_t* seq, const int32_t* pos, int N, int D,
+                                uint16_t* pages, int P, int page_rows, const int32_t* table, int R, int M,
+                                const int32_t* lacking, void* stream);
+
+/*
+ * dsa_paged_attn -- attention over a sequence's rows: token t, at position p = pos[t] of sequence seq[t], sees the rows
+ * j <= p, with window > 0 only those with j > p - window or j < first.  For head h
+ *     x_j = scale * sum_d q[t,h,d] kv[j,d],   out[t,h,:] = sum_j e^{x_j} kv[j,:] / ( sum_j e^{x_j} + e^{sink[h]} )
+ * Rows without a page are skipped; a token that sees none (seq outside [0, R), a negative position) gets zeros and an lse of its
+ * sink (-inf without one).  What rows hold that a token does not see does not matter to it, no numbers included; a row that it
+ * sees and that holds one makes its outputs no numbers.  Tokens may come in any order; those that share a sequence
+ * are best neighbours.  Weights enter the weighted sum as bf16; products accumulate in fp32.  Deterministic.
+ *
+ *   q          bf16 [T][H][D], 16-byte aligned;  seq, pos  int32 [T]
+ *   attn_sink  float [H] or NULL;  window  0 (none) or more;  first  0 or more;  scale  softmax scale
+ *   out        bf16 [T][H][D], 16-byte aligned   OUTPUT;  lse  float [T][H] or NULL  OUTPUT, as dsa_sparse_attn's
+ *   workspace  dsa_paged_attn_workspace_size(T, H, D) bytes, 16-byte aligned; its contents on entry do not matter; two
+ *              calls running at the same time must not share it.  DSA_ERR_WORKSPACE if it is missing, short or misaligned
+ * T * H < 2^30, P * page_rows < 2^31 (DSA_ERR_UNSUPPORTED).
+ */
+DSA_API size_t dsa_paged_attn_workspace_size(int T, int H, int D);
+DSA_API dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* pages, int P, int page_rows, const int32_t* table,
+                                  int R, int M, const int32_t* seq, const int32_t* pos, const float* attn_sink, int T,
+                                  int H, int D, int window, int first, float scale, uint16_t* out, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dsa_verify_drafts -- drafted tokens against the target's probabilities, by rejection sampling with given random numbers.
+ * Sequence r drafted n = min(count[r], G) tokens d_i from probabilities draft[r][i]; token i is accepted while
+ *     u[r][i] * draft[r][i][d_i] < target[r][i][d_i]       (compared exactly; d_i outside [0, V) is refused)
+ * accepted[r] = a, the number before the first refusal, and token[r] = the lowest v with
+ *     w[0] + ... + w[v] > u[r][G] * (w[0] + ... + w[V - 1]),
+ * w = max(target[r][a] - draft[r][a], 0) where a < n (target[r][a] where that is all zero), else target[r][a].
+ * The sums are of whole multiples of 2^-56, to which each probability is rounded (above 1: 1; no number: 0), and so
+ * exact.  token[r] = -1 where w is all zero; count[r] < 0 (a place without a sequence): 0 and -1.
+ * The step's sequences then grow by accepted + 1 tokens: held + added of the next dsa_step_maps, without the host.
+ *   target  float [R][G + 1][V];  draft  float [R][G][V];  tokens  int32 [R][G];  count  int32 [R]
+ *   u       float [R][G + 1] in [0, 1);  accepted, token  int32 [R]   OUTPUT
+ * R < 2^28 (DSA_ERR_UNSUPPORTED); V >= 1, rows whose probabilities sum to less than 256.
+ */
+DSA_API dsa_status dsa_verify_drafts(const float* target, const float* draft, const int32_t* tokens, const int32_t* count,
+                                     const float* u, int R, int G, int V, int32_t* accepted, int32_t* token, void* stream);
+
+/*
  * dsa_check_bounded_wait -- failure-detection self-check (no counterpart in the method's
  * description: it tests the library's own guarantee that no device-side wait is unbounded).
  * Runs one CTA on `stream` in which one warp waits, through the same bounded wait as every

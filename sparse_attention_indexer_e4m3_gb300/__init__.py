@@ -22,6 +22,7 @@ __all__ = [
     "index_topk_workspace_size", "get_device_error", "status_string", "version", "MAX_TOPK", "SUPPORTED_H",
     "SUPPORTED_D", "kv4_page_bytes", "quantize_kv4", "dequantize_kv4", "sparse_attn_kv4", "sparse_attn_kv4_workspace_size", "fork_pages", "reserve_pages",
     "reserve_pages_workspace_size", "compact_pages", "compact_pages_workspace_size", "copy_pages", "SUPPORTED_KV4_D",
+    "step_maps", "page_slots", "store_kv", "paged_attn", "paged_attn_workspace_size", "verify_drafts",
 ]
 
 MAX_TOPK = 2048
@@ -98,6 +99,8 @@ def load():
             lib.dsa_reserve_pages_workspace_size.restype = sz
             lib.dsa_compact_pages_workspace_size.argtypes = [i]
             lib.dsa_compact_pages_workspace_size.restype = sz
+            lib.dsa_paged_attn_workspace_size.argtypes = [i, i, i]
+            lib.dsa_paged_attn_workspace_size.restype = sz
             lib.dsa_check_bounded_wait.argtypes = [p, p]
             lib.dsa_check_bounded_wait.restype = i
             lib.dsa_status_string.argtypes = [i]
@@ -474,7 +477,8 @@ def _native():
         if m.torch_version != torch.__version__.split("+")[0]:
             raise RuntimeError(f"{path} was built for torch {m.torch_version}, not {torch.__version__}: {how}")
         names = ("quantize_kv4_reserved", "dequantize_kv4", "sparse_attn_kv4", "sparse_attn_kv4_workspace_size", "fork_pages", "reserve_pages",
-                 "reserve_pages_workspace_size", "compact_pages", "compact_pages_workspace_size", "copy_pages")
+                 "reserve_pages_workspace_size", "compact_pages", "compact_pages_workspace_size", "copy_pages",
+                 "step_maps", "page_slots", "store_kv", "paged_attn", "paged_attn_workspace_size", "verify_drafts")
         m.bind(tuple(ctypes.cast(getattr(lib, "dsa_" + n), ctypes.c_void_p).value for n in names), DsaError)
         _calls = m
     return _calls
@@ -541,6 +545,54 @@ def copy_pages(pages, src, dst, stream=None):
     """pages[dst[i]] = pages[src[i]] in place for the entries whose two ids name pages (src, dst int32 [n]);
     pages is any contiguous tensor [P, ...] whose pages take a multiple of 16 bytes.  Returns pages."""
     return (_calls or _native()).copy_pages(pages, src, dst, stream)
+
+
+# ------------------------------------------------------------------ the bf16 paged kv cache
+
+
+def step_maps(held, added, T: int, seq=None, pos=None, ks=None, ke=None, stream=None):
+    """The tokens of a step from the sequences' lengths: sequence r holds held[r] rows and gets added[r] more (int32 [R];
+    below 0: 0), one sequence's tokens after the other's.  Returns (seq, pos, ks, ke), int32 [T]: a token's sequence,
+    its position, and its window among index keys packed sequence by sequence; -1, -1, 0, 0 behind the last
+    token, which the calls on a cache leave out."""
+    return (_calls or _native()).step_maps(held, added, T, seq, pos, ks, ke, stream)
+
+
+def page_slots(pages, table, seq, idx, start=None, out=None, stream=None):
+    """Rows of the sequences as rows of the pages: entry v of idx (int32 [T, K] or [T]) names row v - start[t] of sequence
+    seq[t]; the result, of idx's shape, its row in pages.flatten(0, 1), or -1 (negative entries, no page).  Of pages
+    ([P, page_rows, ...], any type) only the shape is used.  So sparse_attn(q, pages.flatten(0, 1), page_slots(...)) and
+    sparse_attn_bwd take index_topk's lists over a paged cache (start = ks).  out may be idx."""
+    return (_calls or _native()).page_slots(pages, table, seq, idx, start, out, stream)
+
+
+def store_kv(kv, pages, table, seq, pos, lacking=None, stream=None):
+    """Write bf16 rows kv [N, D] (contiguous rows, a multiple of 8 values apart) into the paged cache (bf16 [P, page_rows,
+    D]): row i as row pos[i] of sequence seq[i]; rows whose place is not mapped are left out, all where lacking (int32 [1],
+    from reserve_pages for these rows) is not 0.  Returns pages."""
+    return (_calls or _native()).store_kv(kv, pages, table, seq, pos, lacking, stream)
+
+
+def paged_attn_workspace_size(T: int, H: int, D: int) -> int:
+    return int(load().dsa_paged_attn_workspace_size(T, H, D))
+
+
+def paged_attn(q, pages, table, seq, pos, window=None, first=0, attn_sink=None, scale=None, out=None, lse=None, workspace=None,
+               stream=None):
+    """Attention over the sequences' rows in the paged cache (bf16 [P, page_rows, D], keys = values): q bf16 [T, H, D]; token
+    t, at position pos[t] of sequence seq[t], sees the rows up to its own, with a window only the last `window` of them and
+    the `first` first ones.  attn_sink fp32 [H] or None, scale default 1 / sqrt(D).  Returns bf16 [T, H, D] (zeros for
+    a token that sees nothing); with lse (fp32 [T, H]) given, also writes the natural log of each softmax denominator."""
+    return (_calls or _native()).paged_attn(q, pages, table, seq, pos, window, first, attn_sink, scale, out, lse, workspace,
+                                            stream)
+
+
+def verify_drafts(target, draft, tokens, count, u, accepted=None, token=None, stream=None):
+    """Drafted tokens (int32 [R, G], of which count[r] were drafted) against the target's probabilities target [R, G + 1, V],
+    drawn from draft [R, G, V], with random numbers u [R, G + 1] in [0, 1) (all fp32): accepted while
+    u * draft < target.  Returns (accepted, token), int32 [R]: how many, and the token that follows them, drawn with the
+    last random number from what the target leaves over the draft, or from the target where all were accepted."""
+    return (_calls or _native()).verify_drafts(target, draft, tokens, count, u, accepted, token, stream)
 
 
 def check_bounded_wait(stream=None):

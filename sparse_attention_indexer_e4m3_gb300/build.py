@@ -26,7 +26,7 @@ MARSHAL_PATH = os.path.join(HERE, "_marshal.so")
 MARSHAL_STAMP = os.path.join(BUILD_DIR, "_marshal.txt")  # what _marshal.so was built against
 
 SOURCES = ["dsa_api.cu", "index_d128.cu", "index_d64.cu", "kres_d128.cu", "kres_d64.cu", "select_kernels.cu", "attn.cu", "attn_bwd.cu", "attn_kv4.cu", "kv4.cu",
-           "kv4_api.cu"]
+           "kv4_api.cu", "paged_attn.cu", "step.cu", "paged_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xcompiler", "-fvisibility=hidden"]

@@ -5,6 +5,7 @@
 
 #include "kv4_codec_kernel.cuh"
 #include "launch.h"
+#include "launch_dependent.cuh"
 #include "pages_kernel.cuh"
 
 namespace dsa {
@@ -14,22 +15,6 @@ namespace {
 template <int D>
 unsigned codec_grid(int N) {
   return static_cast<unsigned>((static_cast<int64_t>(N) * (D / kKv4Group) + kKv4CodecThreads - 1) / kKv4CodecThreads);
-}
-
-// Launch of a kernel that waits for the stream's earlier work itself (griddepcontrol.wait): its own way onto the SMs
-// then overlaps the end of the kernel before it, which a decoding step's small calls are mostly made of.
-template <class... Args>
-cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, unsigned block, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t c = {};
-  c.gridDim = grid;
-  c.blockDim = dim3(block);
-  c.stream = stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = &attr;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
 }  // namespace

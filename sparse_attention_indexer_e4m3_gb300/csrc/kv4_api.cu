@@ -6,25 +6,17 @@
 #include <cstdint>
 
 #include "../../include/dsa.h"
+#include "api_checks.h"
 #include "kv4.cuh"
 #include "launch.h"
 
 namespace dsa {
 namespace {
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-bool kv4_d(int D) { return D == 64 || D == 128 || D == 256 || D == 512; }
-bool kv4_rows(int rows) { return rows >= 16 && rows <= 256 && (rows & (rows - 1)) == 0; }
-int log2_of(int rows) {
-  int l = 0;
-  while ((1 << l) < rows) ++l;
-  return l;
-}
-
 // The checks that the calls on a pool share; fills `c`.
 dsa_status check_pool(Kv4Pool* c, const uint8_t* cache, int P, int page_rows, const int32_t* table, int R, int M, int D) {
   if (P < 0 || R < 0 || M < 0) return DSA_ERR_INVALID_ARG;
-  if (!kv4_d(D) || !kv4_rows(page_rows)) return DSA_ERR_UNSUPPORTED;
+  if (!paged_d(D) || !paged_rows(page_rows)) return DSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(M) * page_rows > INT_MAX) return DSA_ERR_UNSUPPORTED;  // a row's position is an int
   if (P > 0 && (!cache || !aligned(cache, 16))) return DSA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(R) * M > 0 && (!table || !aligned(table, 4))) return DSA_ERR_INVALID_ARG;
@@ -64,8 +56,6 @@ size_t partial_bytes(int64_t units, int shares, int D) {
   return shares > 1 ? static_cast<size_t>(units) * shares * kTcMaxHeads * (D + 2) * sizeof(float) : 0;
 }
 
-dsa_status done(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
-
 }  // namespace
 }  // namespace dsa
 
@@ -74,7 +64,7 @@ using namespace dsa;
 extern "C" {
 
 size_t dsa_kv4_page_bytes(int page_rows, int D) {
-  return kv4_d(D) && kv4_rows(page_rows) ? static_cast<size_t>(page_rows) * kv4_row_bytes(D) : 0;
+  return paged_d(D) && paged_rows(page_rows) ? static_cast<size_t>(page_rows) * kv4_row_bytes(D) : 0;
 }
 
 dsa_status dsa_quantize_kv4(const uint16_t* kv, const int32_t* seq, const int32_t* pos, int N, int D, uint8_t* cache,
@@ -107,7 +97,7 @@ dsa_status dsa_dequantize_kv4(const uint8_t* cache, int P, int page_rows, const 
 }
 
 size_t dsa_sparse_attn_kv4_workspace_size(int T, int H, int D, int K) {
-  if (T <= 0 || H < 1 || K <= 0 || !kv4_d(D)) return 0;
+  if (T <= 0 || H < 1 || K <= 0 || !paged_d(D)) return 0;
   const int64_t units = static_cast<int64_t>(T) * head_groups(H);
   return partial_bytes(units, list_shares(units, D, K), D);
 }
@@ -164,7 +154,7 @@ dsa_status dsa_reserve_pages(int32_t* table, int32_t* ref, const int32_t* begin,
                              size_t workspace_bytes, void* stream) {
   const dsa_status st = check_tables(R, M, P);
   if (st != DSA_OK) return st;
-  if (!kv4_rows(page_rows) || static_cast<int64_t>(M) * page_rows > INT_MAX || R > INT_MAX / 2) return DSA_ERR_UNSUPPORTED;
+  if (!paged_rows(page_rows) || static_cast<int64_t>(M) * page_rows > INT_MAX || R > INT_MAX / 2) return DSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(R) * M > INT_MAX) return DSA_ERR_UNSUPPORTED;  // as many needs at most, which are counted in ints
   if (!lacking || !aligned(lacking, 4)) return DSA_ERR_INVALID_ARG;
   if (R > 0 && (!begin || !aligned(begin, 4) || !end || !aligned(end, 4) || !src || !aligned(src, 4) || !dst ||

@@ -20,6 +20,10 @@ struct AttnKv4Params;
 struct Kv4Pool;
 struct ReserveArgs;
 struct CompactArgs;
+struct PageTable;
+struct StepMapArgs;
+struct PagedAttnParams;
+struct VerifyArgs;
 
 // Index kernel for head dimension 128 / 64; `fused` selects the fused index + top-k mode.
 cudaError_t launch_index_d128(int H, bool fused, int grid, size_t smem, cudaStream_t stream, const CUtensorMap& kmap,
@@ -79,6 +83,24 @@ cudaError_t launch_sparse_attn_kv4(int D, int grid, int shares, const AttnKv4Par
 int sparse_attn_kv4_smem(int D);
 // How many clusters of `shares` of its CTAs this device runs at a time (0: none of that size; < 0: a CUDA error).
 int sparse_attn_kv4_clusters(int D, int shares);
+
+// bf16 paged cache: attention (D in {64, 128, 256, 512}) by `grid` CTAs and the join of the units that they share;
+// its maps' boxes are [64 dims][a page's rows, 128 at most] and [64 dims][paged_attn_cols(D)].
+cudaError_t launch_paged_attn(int D, int grid, const CUtensorMap& kvmap, const CUtensorMap& qmap, const PagedAttnParams& p,
+                              unsigned* err, cudaStream_t stream);
+int paged_attn_smem(int D);
+int paged_attn_cols(int D);  // columns (token, head) of a unit
+constexpr int kPagedMaxTokens = 32;  // most tokens of a unit
+// A step's tokens from the sequences' lengths; packed keys to rows of the pages; bf16 rows into their pages.
+cudaError_t launch_step_maps(const StepMapArgs& a, cudaStream_t stream);
+cudaError_t launch_page_slots(const PageTable& c, const int32_t* seq, const int32_t* start, const int32_t* idx, int T, int K,
+                              int32_t* slots, cudaStream_t stream);
+cudaError_t launch_store_kv(int D, const uint16_t* kv, int64_t stride, int N, const int32_t* seq, const int32_t* pos,
+                            const int32_t* lacking, uint16_t* pages, const PageTable& c, cudaStream_t stream);
+// Drafted tokens against the target's probabilities, by clusters of CTAs.
+cudaError_t launch_verify_drafts(const VerifyArgs& a, int sms, cudaStream_t stream);
+// 2-D map over a row-major bf16 matrix [rows, D], box [64 dims][box_rows], 128-byte swizzle; false where it cannot be made.
+bool make_bf16_map(CUtensorMap* map, const void* base, int64_t rows, int D, int box_rows);
 
 // Facts of the current device that the entry points need; false on a CUDA error.
 struct DeviceFacts {

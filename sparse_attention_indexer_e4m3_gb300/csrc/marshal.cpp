@@ -1,4 +1,4 @@
-// Argument marshalling of the 4-bit cache's calls for Python: checks torch tensors, allocates the outputs
+// Argument marshalling of the paged caches' calls for Python: checks torch tensors, allocates the outputs
 // and workspaces that the caller leaves out, and passes device pointers and the stream to the C ABI (whose
 // addresses Python hands over once).  The calls themselves take a few microseconds on the GPU in a decoding step; checked
 // in Python, tensor by tensor, each took 10 to 20 us on the host, here 3 to 6.
@@ -17,6 +17,7 @@
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
+#include <utility>
 
 #include "dsa.h"
 
@@ -33,6 +34,12 @@ struct Entry {
   decltype(&dsa_compact_pages) compact_pages;
   decltype(&dsa_compact_pages_workspace_size) compact_pages_workspace_size;
   decltype(&dsa_copy_pages) copy_pages;
+  decltype(&dsa_step_maps) step_maps;
+  decltype(&dsa_page_slots) page_slots;
+  decltype(&dsa_store_kv) store_kv;
+  decltype(&dsa_paged_attn) paged_attn;
+  decltype(&dsa_paged_attn_workspace_size) paged_attn_workspace_size;
+  decltype(&dsa_verify_drafts) verify_drafts;
 } g_abi;
 PyObject* g_error = nullptr;  // DsaError
 
@@ -387,6 +394,187 @@ PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------------------------ the bf16 paged cache
+
+// Pages [P, page_rows, ...] of any type and the table of their sequences.
+struct Pages {
+  const at::Tensor& pages;
+  const at::Tensor& table;
+  int P, rows, R, M;
+
+  Pages(PyObject* pages_object, PyObject* table_object) : pages(tensor(pages_object)), table(arg(table_object, "table", at::kInt, 2)) {
+    if (pages.dim() < 2) bad_value("pages must be [P, page_rows, ...]");
+    if (!pages.is_contiguous()) bad_value("pages must be contiguous");
+    const int64_t n = pages.size(1);
+    if (n < 16 || n > 256 || (n & (n - 1)) != 0) bad_value("pages must hold a power of two in [16, 256] of rows");
+    P = as_int(pages.size(0), "pages");
+    rows = static_cast<int>(n);
+    R = as_int(table.size(0), "table");
+    M = as_int(table.size(1), "table");
+  }
+  // The bf16 cache of rows of D values.
+  void hold(int64_t D) const {
+    if (pages.scalar_type() != at::kBFloat16) bad_type(std::string("pages: dtype ") + type_name(pages.scalar_type()) + " is not BFloat16");
+    if (D != 64 && D != 128 && D != 256 && D != 512) bad_value("D must be 64, 128, 256 or 512");
+    shape(pages, "pages", {pages.size(0), pages.size(1), D});
+  }
+
+ private:
+  static const at::Tensor& tensor(PyObject* o) {
+    if (!THPVariable_Check(o)) bad_type("pages must be a torch.Tensor");
+    return THPVariable_Unpack(o);
+  }
+};
+
+const at::Tensor* given(const at::Tensor& t) { return t.defined() ? &t : nullptr; }
+
+// A tuple of the given objects, where the caller passed them, or of the tensors.
+PyObject* tuple_of(std::initializer_list<std::pair<PyObject*, const at::Tensor*>> parts) {
+  PyObject* r = PyTuple_New(static_cast<Py_ssize_t>(parts.size()));
+  if (r == nullptr) throw Refusal{nullptr, ""};
+  Py_ssize_t i = 0;
+  for (const auto& p : parts) PyTuple_SET_ITEM(r, i++, p.first != Py_None ? keep(p.first) : THPVariable_Wrap(*p.second));
+  return r;
+}
+
+// (held, added, T, seq, pos, ks, ke, stream)
+PyObject* step_maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("step_maps", n, 8, [&] {
+    const at::Tensor& held = arg(a[0], "held", at::kInt, 1);
+    const at::Tensor& added = arg(a[1], "added", at::kInt, 1);
+    shape(added, "added", held.sizes());
+    const int T = as_int(long_of(a[2], "T"), "T");
+    static const char* const names[4] = {"seq", "pos", "ks", "ke"};
+    at::Tensor out[4];
+    int left = 0;
+    for (int i = 0; i < 4; ++i) {
+      out[i] = out_arg(a[3 + i], names[i], at::kInt, {T});
+      left += out[i].defined() ? 0 : 1;
+    }
+    const Where w(a[7], {&held, &added, given(out[0]), given(out[1]), given(out[2]), given(out[3])});
+    if (left > 0) {  // one allocation for what is left out
+      const at::Tensor all = w.make({static_cast<int64_t>(left) * T}, at::kInt);
+      for (int i = 3; i >= 0; --i)
+        if (!out[i].defined()) out[i] = part_of(all, static_cast<int64_t>(--left) * T, T);
+    }
+    check(g_abi.step_maps(i32(held), i32(added), as_int(held.size(0), "held"), T, ptr<int32_t>(out[0]), ptr<int32_t>(out[1]),
+                          ptr<int32_t>(out[2]), ptr<int32_t>(out[3]), w.stream),
+          "dsa_step_maps");
+    return tuple_of({{a[3], &out[0]}, {a[4], &out[1]}, {a[5], &out[2]}, {a[6], &out[3]}});
+  });
+}
+
+// (pages, table, seq, idx, start, out, stream)
+PyObject* page_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("page_slots", n, 7, [&] {
+    const Pages c(a[0], a[1]);
+    const at::Tensor& seq = arg(a[2], "seq", at::kInt, 1);
+    const bool one = THPVariable_Check(a[3]) && THPVariable_Unpack(a[3]).dim() == 1;  // a row of each token
+    const at::Tensor& idx = arg(a[3], "idx", at::kInt, one ? 1 : 2);
+    const int64_t T = seq.size(0);
+    if (idx.size(0) != T) bad_value("idx must be [T] or [T, K]");
+    const at::Tensor start = out_arg(a[4], "start", at::kInt, {T});
+    at::Tensor out = out_arg(a[5], "out", at::kInt, idx.sizes());
+    const Where w(a[6], {&c.pages, &c.table, &seq, &idx, given(start), given(out)});
+    if (!out.defined()) out = w.make(idx.sizes(), at::kInt);
+    check(g_abi.page_slots(i32(c.table), c.R, c.M, c.P, c.rows, i32(seq), start.defined() ? i32(start) : nullptr, i32(idx),
+                           as_int(T, "seq"), one ? 1 : as_int(idx.size(1), "idx"), ptr<int32_t>(out), w.stream),
+          "dsa_page_slots");
+    return a[5] != Py_None ? keep(a[5]) : THPVariable_Wrap(out);
+  });
+}
+
+// (kv, pages, table, seq, pos, lacking, stream)
+PyObject* store_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("store_kv", n, 7, [&] {
+    if (!THPVariable_Check(a[0])) bad_type("kv must be a torch.Tensor");
+    const at::Tensor& kv = THPVariable_Unpack(a[0]);
+    if (kv.scalar_type() != at::kBFloat16) bad_type(std::string("kv: dtype ") + type_name(kv.scalar_type()) + " is not BFloat16");
+    if (kv.dim() != 2) bad_value("kv must have 2 dimensions");
+    const int64_t N = kv.size(0), D = kv.size(1);
+    const int64_t stride = N > 1 ? kv.stride(0) : D;  // (rows may be parts of longer ones)
+    if ((D > 1 && kv.stride(1) != 1) || stride < D || stride % 8 != 0)
+      bad_value("rows of kv must be contiguous and start a multiple of 8 values apart");
+    const Pages c(a[1], a[2]);
+    c.hold(D);
+    const at::Tensor& seq = arg(a[3], "seq", at::kInt, 1);
+    const at::Tensor& pos = arg(a[4], "pos", at::kInt, 1);
+    shape(seq, "seq", {N});
+    shape(pos, "pos", {N});
+    const at::Tensor lacking = out_arg(a[5], "lacking", at::kInt, {1});
+    const Where w(a[6], {&kv, &c.pages, &c.table, &seq, &pos, given(lacking)});
+    check(g_abi.store_kv(bf16(kv), stride, i32(seq), i32(pos), as_int(N, "kv"), static_cast<int>(D), ptr<uint16_t>(c.pages), c.P,
+                         c.rows, i32(c.table), c.R, c.M, lacking.defined() ? i32(lacking) : nullptr, w.stream),
+          "dsa_store_kv");
+    return keep(a[1]);
+  });
+}
+
+// (q, pages, table, seq, pos, window, first, attn_sink, scale, out, lse, workspace, stream)
+PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("paged_attn", n, 13, [&] {
+    const at::Tensor& q = arg(a[0], "q", at::kBFloat16, 3);
+    const int64_t T = q.size(0), H = q.size(1), D = q.size(2);
+    const Pages c(a[1], a[2]);
+    c.hold(D);
+    const at::Tensor& seq = arg(a[3], "seq", at::kInt, 1);
+    const at::Tensor& pos = arg(a[4], "pos", at::kInt, 1);
+    shape(seq, "seq", {T});
+    shape(pos, "pos", {T});
+    int window = 0;
+    if (a[5] != Py_None) {
+      window = as_int(long_of(a[5], "window"), "window");
+      if (window == 0) bad_value("window must be positive (None: no window)");
+    }
+    const int first = as_int(long_of(a[6], "first"), "first");
+    const at::Tensor sink = out_arg(a[7], "attn_sink", at::kFloat, {H});
+    const double scale = a[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(D)) : PyFloat_AsDouble(a[8]);
+    if (scale == -1.0 && PyErr_Occurred()) throw Refusal{nullptr, ""};
+    at::Tensor out = out_arg(a[9], "out", at::kBFloat16, {T, H, D});
+    const at::Tensor lse = out_arg(a[10], "lse", at::kFloat, {T, H});
+    at::Tensor ws;
+    if (a[11] != Py_None) ws = arg(a[11], "workspace", at::kByte, 1);
+    const Where w(a[12], {&q, &c.pages, &c.table, &seq, &pos, given(sink), given(out), given(lse), given(ws)});
+    if (!out.defined()) out = w.make({T, H, D}, at::kBFloat16);
+    if (!ws.defined()) {
+      const size_t need = g_abi.paged_attn_workspace_size(as_int(T, "q"), as_int(H, "q"), static_cast<int>(D));
+      if (need > 0) ws = w.make({static_cast<int64_t>(need)}, at::kByte);
+    }
+    check(g_abi.paged_attn(bf16(q), ptr<const uint16_t>(c.pages), c.P, c.rows, i32(c.table), c.R, c.M, i32(seq), i32(pos),
+                           sink.defined() ? ptr<const float>(sink) : nullptr, as_int(T, "q"), as_int(H, "q"), static_cast<int>(D),
+                           window, first, static_cast<float>(scale), ptr<uint16_t>(out), lse.defined() ? ptr<float>(lse) : nullptr,
+                           ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? static_cast<size_t>(ws.numel()) : 0, w.stream),
+          "dsa_paged_attn");
+    return a[9] != Py_None ? keep(a[9]) : THPVariable_Wrap(out);
+  });
+}
+
+// (target, draft, tokens, count, u, accepted, token, stream)
+PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("verify_drafts", n, 8, [&] {
+    const at::Tensor& target = arg(a[0], "target", at::kFloat, 3);
+    const at::Tensor& draft = arg(a[1], "draft", at::kFloat, 3);
+    const at::Tensor& tokens = arg(a[2], "tokens", at::kInt, 2);
+    const at::Tensor& count = arg(a[3], "count", at::kInt, 1);
+    const at::Tensor& u = arg(a[4], "u", at::kFloat, 2);
+    const int64_t R = tokens.size(0), G = tokens.size(1), V = target.size(2);
+    if (V < 1) bad_value("target must be [R, G + 1, V] with V of 1 or more");
+    shape(target, "target", {R, G + 1, V});
+    shape(draft, "draft", {R, G, V});
+    shape(count, "count", {R});
+    shape(u, "u", {R, G + 1});
+    at::Tensor accepted = out_arg(a[5], "accepted", at::kInt, {R}), token = out_arg(a[6], "token", at::kInt, {R});
+    const Where w(a[7], {&target, &draft, &tokens, &count, &u, given(accepted), given(token)});
+    if (!accepted.defined()) accepted = w.make({R}, at::kInt);
+    if (!token.defined()) token = w.make({R}, at::kInt);
+    check(g_abi.verify_drafts(ptr<const float>(target), ptr<const float>(draft), i32(tokens), i32(count), ptr<const float>(u),
+                              as_int(R, "tokens"), as_int(G, "tokens"), as_int(V, "target"), ptr<int32_t>(accepted),
+                              ptr<int32_t>(token), w.stream),
+          "dsa_verify_drafts");
+    return tuple_of({{a[5], &accepted}, {a[6], &token}});
+  });
+}
+
 // (addresses of the C ABI in Entry's order, DsaError)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("bind", n, 2, [&]() -> PyObject* {
@@ -405,7 +593,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define DSA_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {DSA_METHOD(bind),          DSA_METHOD(quantize_kv4), DSA_METHOD(dequantize_kv4),
                            DSA_METHOD(sparse_attn_kv4), DSA_METHOD(fork_pages),   DSA_METHOD(reserve_pages),
-                           DSA_METHOD(compact_pages), DSA_METHOD(copy_pages),   {nullptr, nullptr, 0, nullptr}};
+                           DSA_METHOD(compact_pages), DSA_METHOD(copy_pages),   DSA_METHOD(step_maps),
+                           DSA_METHOD(page_slots),    DSA_METHOD(store_kv),     DSA_METHOD(paged_attn),
+                           DSA_METHOD(verify_drafts), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,61 @@
+// The bf16 paged kv cache: parameters of its kernels.  Row pos of sequence r is row pos % page_rows of page
+// table[r][pos / page_rows]; a page is page_rows rows of D bf16 values, each both key and value.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace dsa {
+
+// The table that gives each sequence its pages.
+struct PageTable {
+  const int32_t* table;  // [R][M] page ids; anything outside [0, P) is no page
+  int P, R, M;
+  int log_rows;          // log2 of the page's rows
+};
+
+struct StepMapArgs {
+  const int32_t* held;   // [R]
+  const int32_t* added;  // [R]
+  int R, T;
+  int32_t* seq;          // [T] each
+  int32_t* pos;
+  int32_t* ks;
+  int32_t* ke;
+};
+
+struct PagedAttnParams {
+  PageTable pages;
+  const int32_t* seq;   // [T]
+  const int32_t* pos;   // [T]
+  const float* sink;    // [H] or null
+  uint16_t* out;        // [T][H][D] bf16
+  float* lse;           // [T][H] or null
+  float* partial;       // [2 CTAs][N][D] partial outputs of units that several CTAs share
+  float* stats;         // [2 CTAs][2][N] their bounds and sums
+  int4* shared;         // [min(units, CTAs)] the shared units: unit, first CTA, CTAs (0: none)
+  int T, H;
+  int tokens;           // tokens of a unit
+  int groups;           // units of a token, where its heads take several
+  int units;
+  int window;           // rows that a token sees up to its own
+  int first;            // first rows that stay visible
+  int box_rows;         // rows of one copy: those of a page, at most a block's
+  float scale;
+};
+
+// 32-bit words are read after wait_stream() by ordinary loads (kv4.cuh, ld_after_wait).
+
+struct VerifyArgs {
+  const float* target;    // [R][G + 1][V]
+  const float* draft;     // [R][G][V]
+  const int32_t* tokens;  // [R][G]
+  const int32_t* count;   // [R]
+  const float* u;         // [R][G + 1]
+  int R, G, V;
+  int32_t* accepted;      // [R]
+  int32_t* token;         // [R]
+};
+
+}  // namespace dsa

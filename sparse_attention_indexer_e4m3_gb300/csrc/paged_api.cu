@@ -1,0 +1,153 @@
+// The C ABI of the bf16 paged cache and of the drafts' check (declared in include/dsa.h): argument checks and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "../../include/dsa.h"
+#include "api_checks.h"
+#include "launch.h"
+#include "paged.cuh"
+
+namespace dsa {
+namespace {
+
+dsa_status check_table(PageTable* c, const int32_t* table, int R, int M, int P, int page_rows) {
+  if (P < 0 || R < 0 || M < 0) return DSA_ERR_INVALID_ARG;
+  if (!paged_rows(page_rows)) return DSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(M) * page_rows > INT_MAX) return DSA_ERR_UNSUPPORTED;  // a row's position is an int
+  if (static_cast<int64_t>(R) * M > 0 && (!table || !aligned(table, 4))) return DSA_ERR_INVALID_ARG;
+  *c = PageTable{table, P, R, M, log2_of(page_rows)};
+  return DSA_OK;
+}
+
+// How the (token, head) rows of a call are cut into units of at most N columns.
+struct Units {
+  int tokens, groups;
+  int64_t units;
+};
+Units units_of(int T, int H, int D) {
+  const int N = paged_attn_cols(D);
+  Units u;
+  u.tokens = H >= N ? 1 : std::min(kPagedMaxTokens, N / H);
+  u.groups = H > N ? H / N + (H % N != 0 ? 1 : 0) : 1;
+  u.units = u.groups > 1 ? static_cast<int64_t>(T) * u.groups : (static_cast<int64_t>(T) + u.tokens - 1) / u.tokens;
+  return u;
+}
+
+struct Workspace {
+  size_t partial, stats, bytes;  // offsets of the parts behind the shared units' entries
+};
+Workspace workspace_of(int D, int ctas) {
+  const size_t n = paged_attn_cols(D);
+  Workspace w;
+  w.partial = static_cast<size_t>(ctas) * sizeof(int4);
+  w.stats = w.partial + 2 * static_cast<size_t>(ctas) * n * D * sizeof(float);
+  w.bytes = w.stats + 2 * static_cast<size_t>(ctas) * 2 * n * sizeof(float);
+  return w;
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" {
+
+dsa_status dsa_step_maps(const int32_t* held, const int32_t* added, int R, int T, int32_t* seq, int32_t* pos, int32_t* ks,
+                         int32_t* ke, void* stream) {
+  if (R < 0 || T < 0) return DSA_ERR_INVALID_ARG;
+  if (T == 0) return DSA_OK;
+  if (R > 0 && (!held || !aligned(held, 4) || !added || !aligned(added, 4))) return DSA_ERR_INVALID_ARG;
+  if (!seq || !aligned(seq, 4) || !pos || !aligned(pos, 4) || !ks || !aligned(ks, 4) || !ke || !aligned(ke, 4))
+    return DSA_ERR_INVALID_ARG;
+  return done(launch_step_maps(StepMapArgs{held, added, R, T, seq, pos, ks, ke}, static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_page_slots(const int32_t* table, int R, int M, int P, int page_rows, const int32_t* seq, const int32_t* start,
+                          const int32_t* idx, int T, int K, int32_t* slots, void* stream) {
+  PageTable c;
+  const dsa_status st = check_table(&c, table, R, M, P, page_rows);
+  if (st != DSA_OK) return st;
+  if (T < 0 || K < 0) return DSA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(P) * page_rows > INT_MAX) return DSA_ERR_UNSUPPORTED;  // a row of the pages is an int
+  if (T == 0 || K == 0) return DSA_OK;
+  if (!seq || !aligned(seq, 4) || !idx || !aligned(idx, 4) || !slots || !aligned(slots, 4) || (start && !aligned(start, 4)))
+    return DSA_ERR_INVALID_ARG;
+  return done(launch_page_slots(c, seq, start, idx, T, K, slots, static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_store_kv(const uint16_t* kv, int64_t stride, const int32_t* seq, const int32_t* pos, int N, int D, uint16_t* pages,
+                        int P, int page_rows, const int32_t* table, int R, int M, const int32_t* lacking, void* stream) {
+  PageTable c;
+  const dsa_status st = check_table(&c, table, R, M, P, page_rows);
+  if (st != DSA_OK) return st;
+  if (!paged_d(D)) return DSA_ERR_UNSUPPORTED;
+  if (P > 0 && (!pages || !aligned(pages, 16))) return DSA_ERR_INVALID_ARG;
+  if (N < 0 || (N > 1 && stride < D) || stride % 8 != 0) return DSA_ERR_INVALID_ARG;
+  if (N == 0) return DSA_OK;
+  if (!kv || !aligned(kv, 16) || !seq || !aligned(seq, 4) || !pos || !aligned(pos, 4) || (lacking && !aligned(lacking, 4)))
+    return DSA_ERR_INVALID_ARG;
+  return done(launch_store_kv(D, kv, stride, N, seq, pos, lacking, pages, c, static_cast<cudaStream_t>(stream)));
+}
+
+size_t dsa_paged_attn_workspace_size(int T, int H, int D) {
+  DeviceFacts dev;
+  if (T <= 0 || H < 1 || !paged_d(D) || !device_facts(&dev)) return 0;
+  return workspace_of(D, dev.sms).bytes;
+}
+
+dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* pages, int P, int page_rows, const int32_t* table, int R, int M,
+                          const int32_t* seq, const int32_t* pos, const float* attn_sink, int T, int H, int D, int window,
+                          int first, float scale, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  PageTable c;
+  const dsa_status st = check_table(&c, table, R, M, P, page_rows);
+  if (st != DSA_OK) return st;
+  if (!paged_d(D)) return DSA_ERR_UNSUPPORTED;
+  if (T < 0 || H < 1 || window < 0 || first < 0) return DSA_ERR_INVALID_ARG;
+  if (P > 0 && (!pages || !aligned(pages, 16))) return DSA_ERR_INVALID_ARG;
+  if (T == 0) return DSA_OK;
+  if (!q || !aligned(q, 16) || !out || !aligned(out, 16) || !seq || !aligned(seq, 4) || !pos || !aligned(pos, 4))
+    return DSA_ERR_INVALID_ARG;
+  if ((attn_sink && !aligned(attn_sink, 4)) || (lse && !aligned(lse, 4))) return DSA_ERR_INVALID_ARG;
+  const Units un = units_of(T, H, D);
+  // rows of q and of the pages are coordinates of the copies, which are ints
+  if (static_cast<int64_t>(T) * H > INT_MAX / 2 || un.units > INT_MAX / 2 || static_cast<int64_t>(P) * page_rows > INT_MAX)
+    return DSA_ERR_UNSUPPORTED;
+  DeviceFacts dev;
+  if (!device_facts(&dev)) return DSA_ERR_CUDA;
+  if (paged_attn_smem(D) > dev.max_smem) return DSA_ERR_UNSUPPORTED;
+  const Workspace w = workspace_of(D, dev.sms);
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < w.bytes) return DSA_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int box = std::min(page_rows, 128);
+  CUtensorMap kvmap, qmap;
+  // (without pages the map is over q, of which no row of a page is read)
+  if (!make_bf16_map(&kvmap, P > 0 ? pages : q, P > 0 ? static_cast<int64_t>(P) * page_rows : 1, D, box) ||
+      !make_bf16_map(&qmap, q, static_cast<int64_t>(T) * H, D, paged_attn_cols(D)))
+    return DSA_ERR_CUDA;
+  const PagedAttnParams p{c, seq, pos, attn_sink, out, lse, reinterpret_cast<float*>(ws + w.partial),
+                          reinterpret_cast<float*>(ws + w.stats), reinterpret_cast<int4*>(ws), T, H, un.tokens, un.groups,
+                          static_cast<int>(un.units), window == 0 ? INT_MAX : window, first, box, scale};
+  return done(launch_paged_attn(D, dev.sms, kvmap, qmap, p, dev.err, static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_verify_drafts(const float* target, const float* draft, const int32_t* tokens, const int32_t* count,
+                             const float* u, int R, int G, int V, int32_t* accepted, int32_t* token, void* stream) {
+  if (R < 0 || G < 0 || V < 1) return DSA_ERR_INVALID_ARG;
+  if (R > INT_MAX / 8 || G == INT_MAX) return DSA_ERR_UNSUPPORTED;  // CTAs of a launch; G + 1
+  if (R == 0) return DSA_OK;
+  if (!target || !aligned(target, 4) || !count || !aligned(count, 4) || !u || !aligned(u, 4) || !accepted || !aligned(accepted, 4) ||
+      !token || !aligned(token, 4))
+    return DSA_ERR_INVALID_ARG;
+  if (G > 0 && (!draft || !aligned(draft, 4) || !tokens || !aligned(tokens, 4))) return DSA_ERR_INVALID_ARG;
+  DeviceFacts dev;
+  if (!device_facts(&dev)) return DSA_ERR_CUDA;
+  return done(launch_verify_drafts(VerifyArgs{target, draft, tokens, count, u, R, G, V, accepted, token}, dev.sms,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
