@@ -85,11 +85,12 @@ int sparse_attn_kv4_smem(int D);
 int sparse_attn_kv4_clusters(int D, int shares);
 
 // bf16 paged cache: attention (D in {64, 128, 256, 512}) by `grid` CTAs and the join of the units that they share;
-// its maps' boxes are [64 dims][a page's rows, 128 at most] and [64 dims][paged_attn_cols(D)].
+// its maps' boxes are [64 dims][a page's rows, paged_attn_block(D) at most] and [64 dims][paged_attn_cols(D)].
 cudaError_t launch_paged_attn(int D, int grid, const CUtensorMap& kvmap, const CUtensorMap& qmap, const PagedAttnParams& p,
                               unsigned* err, cudaStream_t stream);
 int paged_attn_smem(int D);
-int paged_attn_cols(int D);  // columns (token, head) of a unit
+int paged_attn_cols(int D);   // most columns (token, head) of a unit
+int paged_attn_block(int D);  // rows of a block
 constexpr int kPagedMaxTokens = 32;  // most tokens of a unit
 // A step's tokens from the sequences' lengths; packed keys to rows of the pages; bf16 rows into their pages.
 cudaError_t launch_step_maps(const StepMapArgs& a, cudaStream_t stream);

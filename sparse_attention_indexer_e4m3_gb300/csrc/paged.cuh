@@ -36,16 +36,14 @@ struct PagedAttnParams {
   float* stats;         // [2 CTAs][2][N] their bounds and sums
   int4* shared;         // [min(units, CTAs)] the shared units: unit, first CTA, CTAs (0: none)
   int T, H;
-  int tokens;           // tokens of a unit
-  int groups;           // units of a token, where its heads take several
+  int rows;             // (token, head) rows of a unit
+  int groups;           // units of a token, where a token's heads take several of their own; else 1
   int units;
   int window;           // rows that a token sees up to its own
   int first;            // first rows that stay visible
   int box_rows;         // rows of one copy: those of a page, at most a block's
   float scale;
 };
-
-// 32-bit words are read after wait_stream() by ordinary loads (kv4.cuh, ld_after_wait).
 
 struct VerifyArgs {
   const float* target;    // [R][G + 1][V]

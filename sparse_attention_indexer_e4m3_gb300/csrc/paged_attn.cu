@@ -30,7 +30,7 @@ cudaError_t launch_d(int grid, const CUtensorMap& kvmap, const CUtensorMap& qmap
   }
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(static_cast<unsigned>(grid));
-  c.blockDim = dim3(kPgThreads);
+  c.blockDim = dim3(PagedLayout<D>::kThreads);
   c.dynamicSmemBytes = PagedLayout<D>::kSmem;
   c.stream = stream;
   cudaLaunchAttribute attr = {};
@@ -38,12 +38,11 @@ cudaError_t launch_d(int grid, const CUtensorMap& kvmap, const CUtensorMap& qmap
   attr.val.programmaticStreamSerializationAllowed = 1;
   c.attrs = &attr;
   c.numAttrs = 1;
-  e = cudaLaunchKernelEx(&c, paged_attn_kernel<D>, kvmap, qmap, p, kPgMinBlocks, err);
+  e = cudaLaunchKernelEx(&c, paged_attn_kernel<D>, kvmap, qmap, p, err);
   if (e != cudaSuccess || grid == 1) return e;  // (one CTA shares nothing)
   // the shared units: an entry each, over enough blocks for all SMs where they are few
-  const int entries = std::min(p.units, grid);
-  const int cols = p.groups > 1 ? paged_cols(D) : std::min(paged_cols(D), p.tokens * p.H);
-  c.gridDim = dim3(static_cast<unsigned>(entries), static_cast<unsigned>(std::min(cols, std::max(1, 4 * grid / entries))));
+  const int entries = std::min(p.units, grid), items = p.rows * std::max(1, D / 128);
+  c.gridDim = dim3(static_cast<unsigned>(entries), static_cast<unsigned>(std::min(items, std::max(1, 8 * grid / entries))));
   c.blockDim = dim3(kPgJoinThreads);
   c.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&c, paged_join_kernel<D>, p);
@@ -52,6 +51,7 @@ cudaError_t launch_d(int grid, const CUtensorMap& kvmap, const CUtensorMap& qmap
 }  // namespace
 
 int paged_attn_cols(int D) { return paged_cols(D); }
+int paged_attn_block(int D) { return paged_block(D); }
 
 int paged_attn_smem(int D) {
   switch (D) {

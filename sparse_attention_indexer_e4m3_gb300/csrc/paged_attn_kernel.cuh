@@ -4,26 +4,29 @@
 // (a kv row is both key and value).  Products run on bf16 operands with fp32 accumulators; the weights enter the second
 // one as bf16 (off by half a step, 2^-8 of each, at most), the denominator sums them in fp32.
 //
-// Rows of q are (token, head) pairs, which lie one after the other; a unit is up to N of them: some consecutive
-// tokens with all their heads, or N heads of one token.  The tokens of a unit need not share a sequence: the unit's
-// blocks are those of its runs of tokens of one sequence, one run after the other, and a run's blocks are masked for
-// the other tokens.  (A product of N = 128 columns takes 64 cycles and one of 64 takes 52 to 63, so the idle columns
-// of such a block cost nothing that a unit of its own would not.)
+// Rows of q are (token, head) pairs, which lie one after the other; a unit is up to N of them.  Its tokens need not
+// share a sequence: the unit's blocks are those of its runs of tokens of one sequence, one run after the other, and
+// a run's blocks are masked for the other tokens.  (An instruction of N = 128 columns takes 64 cycles, one of 64 takes
+// 48: idle columns cost little.)
 //
 // All blocks of all units, and for each unit a constant for its q and output, lie on one line that is cut into as
 // many equal pieces as there are CTAs; each CTA finds its piece by a scan over the units.  So one long sequence
 // uses all SMs, a batch of uneven ones keeps them equally busy, and a prompt's units go out whole but for one at
 // each cut.  The parts of a unit that several CTAs share go to the workspace and are joined by a second kernel.
 //
-// One CTA per SM, 640 threads, per block of 128 rows:
+// One CTA per SM; per block of B rows (128; 64 at D = 512):
 //   scout    (warp 2)      the unit's runs and blocks; the pages of the next blocks, four blocks at a time;
-//   load     (warp 1)      the rows by TMA, as D / 64 chunks of [128 rows x 128 bytes], 128-byte swizzled, page by
-//                          page (a page without a row that some token sees becomes zeros: its memory is not read);
-//   score    (warp 0)      S^T = KV . Q^T: M = 128 rows, N columns, K = D (tcgen05.mma kind::f16, bf16);
-//   softmax  (warps 4-19)  thread = (row, N / 4 columns): weights as bf16 rows P[row][column]; the running bound of a
-//                          column moves only when exceeded by more than 2^8;
-//   weighted (warp 0)      O^T += KV^T . P^T: M = 128 dims (D / 128 tiles), N columns, K = 128 rows.
-// Where two blocks fit (D <= 256) the score product of the next block is issued before the weighted sum of the last.
+//   load     (warp 1)      the rows by TMA into a ring of tiles of 128 dims, as chunks of [B rows x 128 bytes], 128-byte
+//                          swizzled, page by page (a page without a row that some token sees becomes zeros: its
+//                          memory is not read);
+//   score    (warp 0)      S^T = KV . Q^T: M = B rows, N columns, K = D (tcgen05.mma kind::f16, bf16);
+//   softmax  (warps 3 on)  thread = (row, 32 columns; 16 of them at B = 64): weights as bf16 rows P[row][column]; the
+//                          running bound of a column moves only when exceeded by more than 2^8;
+//   weighted (warp 0)      O^T += KV^T . P^T: M = 128 dims (D / 128 tiles), N columns, K = B rows.
+// The score product of the next block, of the next unit as well, is issued before the weighted sum of the last, so
+// the softmax runs beside both.  At D = 512 the accumulators of 64 columns take half of tensor memory and q and two
+// blocks of 64 rows all shared memory; an instruction reads its operands from there at 128 bytes a clock, which takes
+// (M + N) / 4 cycles: 48 for M = 128, N = 64, 34 for M = 64 (N = 128, M = 128: 64, the rate of the tensor core itself).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -33,28 +36,31 @@
 
 namespace dsa {
 
-constexpr int kPgKeys = 128;              // rows of a block
-constexpr int kPgSoftWarps = 16;
-constexpr int kPgSoftThreads = 32 * kPgSoftWarps;
-constexpr int kPgThreads = 128 + kPgSoftThreads;
+constexpr int kPgFirstSoft = 3;           // first softmax warp: the three before issue, load and scout
+constexpr int kPgSoftWarps = 8;
+constexpr int kPgSoft = 32 * kPgSoftWarps;
 constexpr int kPgSlots = 8;               // blocks whose pages are looked up ahead
 constexpr int kPgBatch = 4;               // blocks looked up at a time
 constexpr int kPgMaxTokens = 32;          // tokens of a unit: a lane of the scout each
-constexpr int kPgUnitCost = 2;            // what a unit costs beside its blocks, in blocks
-constexpr int kPgMinBlocks = 2;           // least piece of the line (in blocks): joining a part takes about as long
 constexpr float kPgNoBound = -3e38f;      // bound of a column without rows so far
 
-// Columns of a unit at head dimension D: with 128 the output accumulators of D = 512 would take all tensor memory.
+// Columns of a unit at head dimension D (with 128 the output accumulators of D = 512 would take all tensor memory), and
+// rows of a block.
 __host__ __device__ constexpr int paged_cols(int D) { return D == 512 ? 64 : 128; }
+__host__ __device__ constexpr int paged_block(int D) { return D == 512 ? 64 : 128; }
+// What a unit costs beside its blocks, and the least piece of the line of a CTA (joining a part takes about as long), in blocks.
+__host__ __device__ constexpr int paged_unit_cost(int D) { return D == 512 ? 3 : 2; }
+__host__ __device__ constexpr int paged_min_piece(int D) { return D == 512 ? 4 : 2; }
 
 // What the load and softmax warps know of a block.
 struct PagedBlock {
   int row;         // its first row in the sequence
-  int c0, c1;      // columns that it is for
+  int i0, i1;      // tokens of the unit that it is for
   int full;        // every column sees every row
+  int starts;      // the first block of its tokens here
   uint32_t pages;  // bit i: page i of the block is there
   int id[8];       // pages of the block
-  int pad[3];
+  int pad[2];
 };
 
 // What the CTA does of a unit.
@@ -68,52 +74,74 @@ constexpr int kPgWhole = 0, kPgHead = 1, kPgTail = 2;
 
 template <int D>
 struct PagedLayout {
+  static constexpr bool kByRow = D <= 256;                           // a softmax thread has a row of q (else a row of the block)
   static constexpr int kCols = paged_cols(D);
-  static constexpr int kStages = D <= 128 ? 4 : (D <= 256 ? 2 : 1);  // blocks held
-  static constexpr int kScores = kStages < 2 ? 1 : 2;                // score accumulators
+  static constexpr int kKeys = paged_block(D);
+  static constexpr int kThreads = 32 * (kPgFirstSoft + kPgSoftWarps);
   static constexpr int kChunks = D / 64;
-  static constexpr int kTiles = D >= 128 ? D / 128 : 1;              // output tiles (D = 64: half of one is zero)
-  static constexpr int kChunkBytes = kPgKeys * 128;
-  static constexpr int kStageBytes = 2 * kTiles * kChunkBytes;
-  static constexpr int kTileBytes = (D >= 128 ? 2 : 1) * kChunkBytes;  // of a tile that are loaded
+  static constexpr int kTiles = D >= 128 ? D / 128 : 1;              // tiles of a block
+  static constexpr int kTileChunks = kChunks / kTiles;
+  static constexpr int kChunkBytes = kKeys * 128;
+  static constexpr int kTileBytes = kTileChunks * kChunkBytes;
+  static constexpr int kRing = D == 512 ? 9 : (D == 64 ? 8 : 5);     // tiles held
+  static constexpr int kQBufs = D <= 128 ? 2 : 1;
   static constexpr int kQChunkBytes = kCols * 128;
+  static constexpr int kQBytes = kChunks * kQChunkBytes;
   static constexpr int kKv = 0;
-  static constexpr int kQ = kKv + kStages * kStageBytes;
-  static constexpr int kP = kQ + kChunks * kQChunkBytes;          // bf16, kCols / 64 chunks of [128 rows][64 columns]
-  static constexpr int kMax = kP + kPgKeys * kCols * 2;           // float [cols] running bounds (log2 units)
-  static constexpr int kAlpha = kMax + kCols * 4;                 // float [cols] rescale / output factors, or reduced bounds
-  static constexpr int kEnd = kAlpha + kCols * 4;                 // int [2][cols] by unit: rows below this are seen
-  static constexpr int kBlocks = kEnd + 2 * kCols * 4;            // PagedBlock [slots]
+  static constexpr int kQ = kKv + kRing * kTileBytes;
+  static constexpr int kP = kQ + kQBufs * kQBytes;                // not by row: bf16 [rows][64 columns]
+  static constexpr int kNeg = kP + (kByRow ? 0 : kKeys * kCols * 2);  // float [cols] the running bounds (log2 units); not by row: negated
+  static constexpr int kAlpha = kNeg + kCols * 4;                 // float [cols] rescale / output factors; by row: [2][cols] sums
+  static constexpr int kTop = kAlpha + (kByRow ? 2 : 1) * kCols * 4;  // not by row: int [cols] largest scores, being reduced
+  static constexpr int kEnd = kTop + (kByRow ? 0 : 1) * kCols * 4;    // int [2][tokens] by unit: rows below this are seen
+  static constexpr int kBlocks = kEnd + 2 * kPgMaxTokens * 4;     // PagedBlock [slots]
   static constexpr int kParts = kBlocks + kPgSlots * static_cast<int>(sizeof(PagedBlock));  // PagedPart [2]
-  static constexpr int kPlan = kParts + 2 * static_cast<int>(sizeof(PagedPart));            // int [12]
-  static constexpr int kBar = kPlan + 48;
-  static constexpr int kNumBars = 14 + 2 * kPgSlots + 2 * kStages * kTiles;
+  static constexpr int kPlan = kParts + 2 * static_cast<int>(sizeof(PagedPart));            // int [8]
+  static constexpr int kScan = kPlan + 32;                        // int64 [warps]
+  static constexpr int kBar = kScan + 96;
+  static constexpr int kNumBars = 22 + 2 * kPgSlots + 2 * kRing;
   static constexpr int kSmem = kBar + kNumBars * 8;
-  // tensor memory: S^T (kScores of them) from column 0, O^T tile m from column kCols (kScores + m)
+  // softmax warps that read a block, or fill a P
+  static constexpr int kReaders = kByRow ? kPgSoftWarps / 2 : kPgSoftWarps;
+  // tensor memory: two S (or S^T) from column 0, O (or O^T) tile m behind them
+  static constexpr int kSCols = kByRow ? kKeys : kCols;
+  static constexpr int kOTile = kByRow ? (D < 128 ? D : 128) : kCols;
+  static_assert(2 * kSCols + kTiles * kOTile <= 512, "tensor memory");
+  static_assert(kRing >= 2 * kTiles, "the next block's score product goes before the last one's weighted sum");
+  static_assert(kSmem <= 232448, "shared memory");
 };
 static_assert(sizeof(PagedBlock) == 64 && sizeof(PagedPart) == 16, "layout");
+
+// mbar_wait with its loop out of line: written out at each of the kernel's waits it made 90 KB of code, and instructions were
+// waited for.
+__device__ __noinline__ bool paged_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err, int site) {
+  return mbar_wait(bar, parity, abort, err, site);
+}
+__device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err, int site) {
+  return mbar_try_wait(bar, parity) || paged_wait_long(bar, parity, abort, err, site);
+}
 
 // ------------------------------------------------------------------------------------ units and runs
 
 struct PagedUnit {
-  int t0, n;    // tokens
-  int h0;       // first head
-  int cols;     // columns in use
+  int row0, cols;  // its (token, head) rows
+  int t0, n;       // tokens that they lie in
+  int skip;        // rows of the first token before them
 };
 
-__device__ __forceinline__ PagedUnit paged_unit(const PagedAttnParams& p, int u, int N) {
+__device__ __forceinline__ PagedUnit paged_unit(const PagedAttnParams& p, int u) {
   PagedUnit r;
   if (p.groups > 1) {
-    r.t0 = u / p.groups;
-    r.n = 1;
-    r.h0 = (u % p.groups) * N;
-    r.cols = min(N, p.H - r.h0);
+    const int t = u / p.groups, h = (u % p.groups) * p.rows;
+    r.row0 = t * p.H + h;
+    r.cols = min(p.rows, p.H - h);
   } else {
-    r.t0 = u * p.tokens;
-    r.n = min(p.tokens, p.T - r.t0);
-    r.h0 = 0;
-    r.cols = r.n * p.H;
+    r.row0 = u * p.rows;
+    r.cols = min(p.rows, p.T * p.H - r.row0);
   }
+  r.t0 = r.row0 / p.H;
+  r.n = (r.row0 + r.cols - 1) / p.H - r.t0 + 1;
+  r.skip = r.row0 - r.t0 * p.H;
   return r;
 }
 
@@ -128,41 +156,37 @@ __device__ __forceinline__ void paged_token(const PagedAttnParams& p, int t, int
 
 // A run of tokens of one sequence, from what its tokens see: [0, some) and [low, high).
 struct PagedRun {
-  int low, high, some;  // union
-  int all_low, all_end;  // what every token sees: [all_low, all_end)
+  int low, high, some;
   __device__ __forceinline__ void start() {
     low = INT32_MAX;
-    high = some = all_low = 0;
-    all_end = INT32_MAX;
+    high = some = 0;
   }
   __device__ __forceinline__ void add(const PagedAttnParams& p, int end) {
-    const int lo = max(0, end - p.window);
-    low = min(low, lo);
-    all_low = max(all_low, lo);
+    low = min(low, max(0, end - p.window));
     high = max(high, end);
-    all_end = min(all_end, end);
     some = max(some, min(p.first, end));
   }
   // blocks [0, a) and [b, b + the rest); the number of them
-  __device__ __forceinline__ int blocks(const PagedAttnParams& p, int& a, int& b) const {
+  __device__ __forceinline__ int blocks(const PagedAttnParams& p, int size, int& a, int& b) const {
     const int rows = min(high, p.pages.M << p.pages.log_rows);
-    const auto up_to = [](int n) { return n > 0 ? (n - 1) / kPgKeys + 1 : 0; };
-    b = low / kPgKeys;
+    const auto up_to = [&](int n) { return n > 0 ? (n - 1) / size + 1 : 0; };
+    b = low / size;
     a = min(up_to(min(some, rows)), b);
     return a + max(0, up_to(rows) - b);
   }
 };
 
-// Blocks of a unit.
-__device__ __forceinline__ int paged_blocks(const PagedAttnParams& p, const PagedUnit& u) {
+// Blocks of a unit, by one thread.
+__device__ __forceinline__ int paged_blocks(const PagedAttnParams& p, const PagedUnit& u, int size) {
   int n = 0, seq = -1, a, b;
   PagedRun run;
   run.start();
+#pragma unroll 1
   for (int i = 0; i <= u.n; ++i) {
     int s = -1, end = 0;
     if (i < u.n) paged_token(p, u.t0 + i, s, end);
     if (s != seq || i == u.n) {
-      if (seq >= 0) n += run.blocks(p, a, b);
+      if (seq >= 0) n += run.blocks(p, size, a, b);
       run.start();
       seq = s;
     }
@@ -172,7 +196,7 @@ __device__ __forceinline__ int paged_blocks(const PagedAttnParams& p, const Page
 }
 
 // Factor of a column's outputs whose weights' bound is m (log2 units) and whose denominator is l, in units of 2^m,
-// without the sink; writes the natural log of the whole denominator where lse is given (a NaN stays one).
+// without the sink; writes the natural log of the whole denominator where lse is given (what is no number stays so).
 __device__ __forceinline__ float paged_factor(float m, float l, const float* sink, int h, float* lse) {
   if (l != l) {
     if (lse != nullptr) *lse = l;
@@ -181,51 +205,112 @@ __device__ __forceinline__ float paged_factor(float m, float l, const float* sin
   return softmax_factor(m, l, sink, h, lse);
 }
 
-// An fp32 value as an int of the same order (no NaN).
+// An fp32 value as an int of the same order.
 __device__ __forceinline__ int ordered(float x) {
   const int b = __float_as_int(x);
   return b ^ ((b >> 31) & 0x7FFFFFFF);
 }
 __device__ __forceinline__ float from_ordered(int b) { return __int_as_float(b ^ ((b >> 31) & 0x7FFFFFFF)); }
 
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The low n bits (n in [0, 32]).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+
+// Tensor-memory load of the 16 lanes that hold a quarter of an M = 64 accumulator: thread i has lane i % 16 and 16 columns, the
+// upper half of the threads those 16 further on.
+__device__ __forceinline__ void tmem_ld_half_x16(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16], 16;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// Reduces n values a lane (one of each of n columns) across n lanes, by recursive halving: afterwards v[0] holds
+// column lane % n.
+template <int kN, class Op>
+__device__ __forceinline__ void xpose_reduce(float (&v)[kN], int lane, Op op) {
+#pragma unroll
+  for (int half = kN / 2; half >= 1; half >>= 1) {
+    const bool up = (lane & half) != 0;
+#pragma unroll
+    for (int i = 0; i < kN / 2; ++i) {
+      if (i < half) {
+        const float send = up ? v[i] : v[i + half];
+        const float keep = up ? v[i + half] : v[i];
+        v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, half));
+      }
+    }
+  }
+}
+
+// tcgen05.mma kind::f16 with the A operand in tensor memory, issued where `on` is set.
+__device__ __forceinline__ void mma_f16_ts_if(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(on), "r"(acc)
+      : "memory");
+}
+
+// Tensor-memory store of 16 columns of words.
+__device__ __forceinline__ void tmem_st_words_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 template <int D>
-__global__ void __launch_bounds__(kPgThreads, 1)
+__global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
-                      const PagedAttnParams p, int min_blocks, unsigned* err) {
+                      const PagedAttnParams p, unsigned* err) {
   using L = PagedLayout<D>;
   constexpr int N = L::kCols;
+  constexpr int kKeys = L::kKeys;
   constexpr int kCh = L::kChunks;
   constexpr int kTi = L::kTiles;
-  constexpr int kSt = L::kStages;
-  constexpr int kSc = L::kScores;
-  constexpr int kC = N / 4;  // columns of a softmax thread
+  constexpr int kRing = L::kRing;
+  constexpr int kQb = L::kQBufs;
+  constexpr int kThreads = L::kThreads;
   extern __shared__ __align__(1024) uint8_t paged_smem[];
   uint8_t* smem = paged_smem;
   uint8_t* kv_s = smem + L::kKv;
   uint8_t* q_s = smem + L::kQ;
   uint8_t* p_s = smem + L::kP;
-  float* max_s = reinterpret_cast<float*>(smem + L::kMax);
+  float* neg_s = reinterpret_cast<float*>(smem + L::kNeg);
   float* alpha_s = reinterpret_cast<float*>(smem + L::kAlpha);
+  int* top_s = reinterpret_cast<int*>(smem + L::kTop);
   int* end_s = reinterpret_cast<int*>(smem + L::kEnd);
   PagedBlock* block_s = reinterpret_cast<PagedBlock*>(smem + L::kBlocks);
   PagedPart* part_s = reinterpret_cast<PagedPart*>(smem + L::kParts);
   volatile int* plan_s = reinterpret_cast<volatile int*>(smem + L::kPlan);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  uint64_t* q_full = bars + 0;
-  uint64_t* q_empty = bars + 1;
-  uint64_t* p_full = bars + 2;
-  uint64_t* pv_done = bars + 3;
-  uint64_t* o_empty = bars + 4;
-  uint64_t* drain = bars + 5;
-  uint64_t* part_full = bars + 6;   // [2]
-  uint64_t* part_empty = bars + 8;  // [2]
-  uint64_t* s_full = bars + 10;     // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 12);
+  uint64_t* q_full = bars + 0;      // [2]
+  uint64_t* q_empty = bars + 2;     // [2]
+  uint64_t* pv_done = bars + 5;
+  uint64_t* o_empty = bars + 6;
+  uint64_t* drain = bars + 7;
+  uint64_t* part_full = bars + 8;   // [2]
+  uint64_t* part_empty = bars + 10; // [2]
+  uint64_t* s_full = bars + 12;     // [2]
+  uint64_t* p_full = bars + 16;     // [2]; not by row: [1]
+  uint64_t* decided = bars + 18;    // [4] by row: bounds of a quarter's rows
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint64_t* blk_full = bars + 14;   // [slots]
+  uint64_t* blk_full = bars + 22;   // [slots]
   uint64_t* blk_empty = blk_full + kPgSlots;
-  uint64_t* kv_full = blk_empty + kPgSlots;  // [stage][tile]
-  uint64_t* kv_empty = kv_full + kSt * kTi;
+  uint64_t* kv_full = blk_empty + kPgSlots;  // [ring]
+  uint64_t* kv_empty = kv_full + kRing;
 
   if ((smem_addr(smem) & 1023u) != 0u) {  // (the swizzle goes by addresses; nothing else lies before this memory)
     if (threadIdx.x == 0) record_error(err, kErrPlan);
@@ -234,30 +319,27 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  if constexpr (D == 64) {  // the upper half of a 64-dim row's tile stays zero
-    for (int s = 0; s < kSt; ++s)
-      for (int i = threadIdx.x; i < L::kChunkBytes / 16; i += kPgThreads)
-        reinterpret_cast<uint4*>(kv_s + s * L::kStageBytes + L::kChunkBytes)[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
   if (threadIdx.x < kPgSlots * sizeof(PagedBlock) / 4) reinterpret_cast<int*>(block_s)[threadIdx.x] = 0;
   if (threadIdx.x < 2 * sizeof(PagedPart) / 4) reinterpret_cast<int*>(part_s)[threadIdx.x] = 0;
+  if (!L::kByRow && threadIdx.x < N) top_s[threadIdx.x] = ordered(-INFINITY);
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    mbar_init(p_full, kPgSoftWarps);
     mbar_init(pv_done, 1);
     mbar_init(o_empty, kPgSoftWarps);
     mbar_init(drain, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
       mbar_init(&part_full[i], 1);
       mbar_init(&part_empty[i], 2 + kPgSoftWarps);
+      mbar_init(&p_full[i], L::kReaders);
       mbar_init(&s_full[i], 1);
     }
     for (int i = 0; i < kPgSlots; ++i) {
       mbar_init(&blk_full[i], 1);
-      mbar_init(&blk_empty[i], 1 + kPgSoftWarps);
+      mbar_init(&blk_empty[i], 1 + L::kReaders);
     }
-    for (int i = 0; i < kSt * kTi; ++i) {
+    for (int i = 0; i < 4; ++i) mbar_init(&decided[i], 1);
+    for (int i = 0; i < kRing; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
     }
@@ -274,52 +356,49 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   }
 
   // ------------------------------------------------------------------ the CTA's piece of the line
-  // Cost of a unit: its blocks and kPgUnitCost.  [from, to) of the line is this CTA's.  A unit belongs to the CTA on
-  // whose piece it starts (that one has at least one of its blocks) and to those whose pieces its blocks reach into.
-  int64_t* scan = reinterpret_cast<int64_t*>(p_s);  // [threads + 1] (P's place; 640 * 8 bytes)
-  const int u_first = static_cast<int>(static_cast<int64_t>(p.units) * threadIdx.x / kPgThreads);
-  const int u_last = static_cast<int>(static_cast<int64_t>(p.units) * (threadIdx.x + 1) / kPgThreads);
+  // Cost of a unit: its blocks and a constant.  [from, to) of the line is this CTA's.  A unit starts on one CTA's piece (which
+  // has at least one of its blocks) and belongs to those, too, whose pieces its blocks reach into.
+  constexpr int kUnitCost = paged_unit_cost(D);
+  int64_t* warp_scan = reinterpret_cast<int64_t*>(smem + L::kScan);  // [warps]
+  const int u_first = static_cast<int>(static_cast<int64_t>(p.units) * threadIdx.x / kThreads);
+  const int u_last = static_cast<int>(static_cast<int64_t>(p.units) * (threadIdx.x + 1) / kThreads);
   int64_t mine = 0;
-  for (int u = u_first; u < u_last; ++u) mine += paged_blocks(p, paged_unit(p, u, N)) + kPgUnitCost;
-  scan[threadIdx.x] = mine;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t base = 0;
-    for (int i = 0; i < kPgThreads; i += 32) {
-      const int64_t v = scan[i + lane];
-      int64_t s = v;
+#pragma unroll 1
+  for (int u = u_first; u < u_last; ++u) mine += paged_blocks(p, paged_unit(p, u), kKeys) + kUnitCost;
+  int64_t upto = mine;  // the line up to the end of this thread's units
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t other = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += other;
-      }
-      scan[i + lane] = base + s - v;  // before thread i + lane's units
-      base += __shfl_sync(0xffffffffu, s, 31);
-    }
-    if (lane == 0) scan[kPgThreads] = base;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t other = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += other;
   }
+  if (lane == 31) warp_scan[warp] = upto;
   __syncthreads();
-  const int64_t line = scan[kPgThreads];
-  const int64_t ctas = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), line / min_blocks));
+  int64_t line = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int64_t v = warp_scan[w];
+    if (w < warp) upto += v;
+    line += v;
+  }
+  const int64_t ctas = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), line / paged_min_piece(D)));
   const int cta = static_cast<int>(blockIdx.x);
   const int64_t from = cta < ctas ? line * cta / ctas : line, to = cta < ctas ? line * (cta + 1) / ctas : line;
-  if (u_first < u_last) {
-    int64_t at = scan[threadIdx.x];
-    const int64_t end = at + mine;
-    // the thread whose units the piece starts (ends) on walks over them again
-    const bool has_from = from < to && at <= from && from < end, has_to = from < to && at < to && to <= end;
-    if (has_from || has_to) {
+  if (from < to && mine > 0 && upto > from && upto - mine < to) {
+    // the threads whose units the piece starts or ends on walk over them again
+    int64_t at = upto - mine;
+    if (at <= from || upto >= to) {
+#pragma unroll 1
       for (int u = u_first; u < u_last; ++u) {
-        const int nb = paged_blocks(p, paged_unit(p, u, N));
-        const int64_t next = at + nb + kPgUnitCost;
+        const int nb = paged_blocks(p, paged_unit(p, u), kKeys);
+        const int64_t next = at + nb + kUnitCost;
         if (at <= from && from < next) {
           plan_s[0] = u;
           plan_s[1] = static_cast<int>(min(from - at, static_cast<int64_t>(nb)));  // its first block here
-          plan_s[4] = from == at;                                                    // it starts here
+          plan_s[2] = from == at;                                                    // it starts here
         }
         if (at < to && to <= next) {
-          plan_s[2] = u;
-          plan_s[3] = static_cast<int>(min(to - at, static_cast<int64_t>(nb)));  // the end of its blocks here
+          plan_s[3] = u;
+          plan_s[4] = static_cast<int>(min(to - at, static_cast<int64_t>(nb)));  // the end of its blocks here
           // the last CTA that has one of its blocks: the one on whose piece the last of them lies
           plan_s[5] = static_cast<int>(((at + max(nb, 1)) * ctas - 1) / line);
           plan_s[6] = nb;
@@ -333,53 +412,72 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   tc_fence_after_sync();
   const uint32_t tbase = *tmem_slot;
   const uint32_t s_tmem = tbase;
-  const uint32_t o_tmem = tbase + N * kSc;
+  const uint32_t o_tmem = tbase + 2 * L::kSCols;
   const bool idle = from >= to;
-  const int unit0 = idle ? 0 : plan_s[0], unit1 = idle ? -1 : plan_s[2];
-  const int from_block = plan_s[1], to_block = plan_s[3];
-  const bool starts = plan_s[4] != 0;
-  const int last_cta = plan_s[5], last_blocks = plan_s[6];
-  // [units <= CTAs] by unit (written by the CTA that it starts on), else by CTA
-  const bool by_unit = p.units <= static_cast<int>(gridDim.x);
+  const int unit0 = idle ? 0 : plan_s[0], unit1 = idle ? -1 : plan_s[3];
+  const int from_block = plan_s[1], to_block = plan_s[4];
+  const bool starts = plan_s[2] != 0;
   if (threadIdx.x == 0) {
-    if (!by_unit) {
-      const bool shared = !idle && to_block < last_blocks && (unit1 > unit0 || starts);
-      p.shared[cta] = shared ? make_int4(unit1, cta, last_cta - cta + 1, 0) : make_int4(0, 0, 0, 0);
-    } else if (!idle) {
-      for (int u = starts ? unit0 : unit0 + 1; u <= unit1; ++u)
-        p.shared[u] = u == unit1 && to_block < last_blocks ? make_int4(u, cta, last_cta - cta + 1, 0) : make_int4(0, 0, 0, 0);
+    // entries of the shared units: by unit, written by the CTA that it starts on, where there are no more than CTAs, else by CTA
+    const bool shared = !idle && to_block < plan_s[6] && (unit1 > unit0 || starts);
+    const int4 entry = shared ? make_int4(unit1, cta, plan_s[5] - cta + 1, 0) : make_int4(0, 0, 0, 0);
+    if (p.units > static_cast<int>(gridDim.x)) {
+      p.shared[cta] = entry;
+    } else {
+      for (int u = starts ? unit0 : unit0 + 1; u <= unit1; ++u) p.shared[u] = u == unit1 ? entry : make_int4(0, 0, 0, 0);
     }
   }
-  // the unit's first block here, the end of its blocks here and what this CTA does of it (nb: all its blocks)
-  const auto part_of = [&](int u, int nb, int& b0, int& b1) -> int {
-    b0 = u == unit0 ? from_block : 0;
-    b1 = u == unit1 ? to_block : nb;
-    if (u == unit0 && !starts) return kPgTail;
-    return b1 < nb ? kPgHead : kPgWhole;
-  };
   const auto gone = [&]() -> bool { return __any_sync(0xffffffffu, *abort_flag != 0) != 0; };
 
   if (warp == 2) {
     // ------------------------------------------------------------------ scout
     uint32_t gb = 0;  // blocks of this CTA so far
     int n = 0;        // parts of this CTA so far
-    for (int u = unit0; u <= unit1; ++u) {
-      if (gone()) break;
-      const PagedUnit un = paged_unit(p, u, N);
-      int seq = -1, end = 0;
+    constexpr int kPages = kKeys / 16;  // most pages of a block
+    static_assert(kPages * kPgBatch <= 32, "a lane for each page of a batch");
+    int seq = -1, end = 0;  // of the unit's token `lane`, read a unit ahead
+    if (unit0 <= unit1) {
+      const PagedUnit un = paged_unit(p, unit0);
       if (lane < un.n) paged_token(p, un.t0 + lane, seq, end);
-      const int nb = paged_blocks(p, un);
-      int b0, b1;
-      const int way = part_of(u, nb, b0, b1);
-      if (way == kPgTail && b0 >= b1) continue;  // (its blocks end before this CTA's piece)
-      if (n > 1) mbar_wait(&part_empty[n & 1], static_cast<uint32_t>((n >> 1) - 1) & 1u, abort_flag, err, 0x80);
-      if (gone()) break;
-      for (int i = 0; i < un.n; ++i) {
-        const int e = __shfl_sync(0xffffffffu, end, i);
-        const int c_end = p.groups > 1 ? un.cols : (i + 1) * p.H;
-        for (int c = (p.groups > 1 ? 0 : i * p.H) + lane; c < c_end; c += 32) end_s[(n & 1) * N + c] = e;
+    }
+    bool ok = true;
+    for (int u = unit0; ok && u <= unit1; ++u) {
+      const PagedUnit un = paged_unit(p, u);
+      const int my_seq = seq, my_end = end;
+      seq = -1;
+      end = 0;
+      if (u < unit1) {
+        const PagedUnit next = paged_unit(p, u + 1);
+        if (lane < next.n) paged_token(p, next.t0 + lane, seq, end);
       }
-      for (int c = un.cols + lane; c < N; c += 32) end_s[(n & 1) * N + c] = 0;
+      // tokens that begin a run, and the runs' spans: reduced over their lanes
+      const int before_seq = __shfl_up_sync(0xffffffffu, my_seq, 1);
+      const uint32_t begins = __ballot_sync(0xffffffffu, lane < un.n && (lane == 0 || my_seq != before_seq));
+      const auto run_of = [&](int i0, int i1) {
+        const bool in = lane >= i0 && lane < i1;
+        PagedRun run;
+        run.low = __reduce_min_sync(0xffffffffu, in ? max(0, my_end - p.window) : INT32_MAX);
+        run.high = __reduce_max_sync(0xffffffffu, in ? my_end : 0);
+        run.some = __reduce_max_sync(0xffffffffu, in ? min(p.first, my_end) : 0);
+        return run;
+      };
+      const auto run_end = [&](int i0) {
+        const uint32_t after = i0 < 31 ? begins & ~low_bits(i0 + 1) : 0u;
+        return after != 0u ? __ffs(after) - 1 : un.n;
+      };
+      int nb = 0;
+      for (int i = 0; i < un.n;) {
+        const int i1 = run_end(i);
+        int a, b;
+        if (__shfl_sync(0xffffffffu, my_seq, i) >= 0) nb += run_of(i, i1).blocks(p, kKeys, a, b);
+        i = i1;
+      }
+      const int b0 = u == unit0 ? from_block : 0, b1 = u == unit1 ? to_block : nb;
+      const int way = u == unit0 && !starts ? kPgTail : (b1 < nb ? kPgHead : kPgWhole);
+      if (way == kPgTail && b0 >= b1) continue;  // (its blocks end before this CTA's piece)
+      if (n > 1) paged_wait(&part_empty[n & 1], static_cast<uint32_t>((n >> 1) - 1) & 1u, abort_flag, err, 0x80);
+      if (gone()) break;
+      end_s[(n & 1) * kPgMaxTokens + lane] = my_end;
       if (lane == 0) {
         part_s[n & 1].unit = u;
         part_s[n & 1].blocks = b1 - b0;
@@ -388,53 +486,61 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&part_full[n & 1]);
       ++n;
-      // the runs, one after the other
       int before = 0;  // blocks of the runs before
-      bool ok = true;
-      for (int i = 0; ok && i < un.n && before < b1;) {
-        const int s = __shfl_sync(0xffffffffu, seq, i);
-        const int first_token = i;
-        PagedRun run;
-        run.start();
-        for (; i < un.n && __shfl_sync(0xffffffffu, seq, i) == s; ++i) run.add(p, __shfl_sync(0xffffffffu, end, i));
+      for (int i0 = 0; ok && i0 < un.n && before < b1;) {
+        const int i1 = run_end(i0), s = __shfl_sync(0xffffffffu, my_seq, i0);
+        const int first_token = i0;
+        i0 = i1;
         if (s < 0) continue;
+        const PagedRun run = run_of(first_token, i1);
         int ra, rb;
-        const int count = run.blocks(p, ra, rb);
-        const bool whole = first_token == 0 && i == un.n;
-        const int c0 = p.groups > 1 ? 0 : first_token * p.H, c1 = p.groups > 1 ? un.cols : i * p.H;
+        const int count = run.blocks(p, kKeys, ra, rb);
+        const bool in = lane >= first_token && lane < i1;
+        const int all_low = __reduce_max_sync(0xffffffffu, in ? max(0, my_end - p.window) : 0);
+        const int all_end = __reduce_min_sync(0xffffffffu, in ? my_end : INT32_MAX);
+        const bool whole = first_token == 0 && i1 == un.n;
         const int32_t* table = p.pages.table + static_cast<int64_t>(s) * p.pages.M;
-        const int k_end = min(count, b1 - before);
-        for (int k0 = max(0, b0 - before); ok && k0 < k_end; k0 += kPgBatch) {
-          // lane = (block of the batch, page of the block)
+        const int k_first = max(0, b0 - before), k_end = min(count, b1 - before);
+        // lane = (block of the batch, page of the block)
+        const int sub = lane & 7, off = sub << p.pages.log_rows;
+        const bool is_page = sub < kPages && off < kKeys;
+        const uint32_t want = __ballot_sync(0xffffffffu, is_page) & 0xFFu;
+        const auto first_row = [&](int k0) {
           const int k = min(k0 + (lane >> 3), k_end - 1);
-          const int row = (k < ra ? k : rb + k - ra) * kPgKeys;
-          const int at = row + ((lane & 7) << p.pages.log_rows);  // its first row (a page of more than 128: the block's)
-          bool there = ((lane & 7) << p.pages.log_rows) < kPgKeys;
-          // rows [at, at + box) that some token of the run sees
-          there = there && (at < run.some || (at < run.high && at - run.low > -p.box_rows));
-          const int index = at >> p.pages.log_rows;
+          return (k < ra ? k : rb + k - ra) * kKeys;
+        };
+        const auto look_up = [&](int k0) -> int {  // -1: no page, or none of whose rows [at, at + box) some token of the run sees
+          if (k0 >= k_end) return -1;
+          const int at = first_row(k0) + off, index = at >> p.pages.log_rows;
+          const bool there = is_page && (at < run.some || (at < run.high && at - run.low > -p.box_rows));
           int page = -1;
           if (there && index < p.pages.M) page = ld_after_wait(table + index);
+          return page;
+        };
+        int next_page = k_first < k_end ? look_up(k_first) : -1;
+        for (int k0 = k_first; ok && k0 < k_end; k0 += kPgBatch) {
+          int page = next_page;
+          next_page = look_up(k0 + kPgBatch);  // (in flight while this batch is handed out)
+          const int row = first_row(k0);
           if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages.P)) page = -1;
           const uint32_t mapped = __ballot_sync(0xffffffffu, page >= 0);
-          const uint32_t wanted = __ballot_sync(0xffffffffu, ((lane & 7) << p.pages.log_rows) < kPgKeys);
           for (int j = 0; j < kPgBatch && k0 + j < k_end; ++j, ++gb) {
             const uint32_t slot = gb % kPgSlots;
-            if (gb >= kPgSlots) mbar_wait(&blk_empty[slot], (gb / kPgSlots - 1) & 1u, abort_flag, err, 0x81);
+            if (gb >= kPgSlots) paged_wait(&blk_empty[slot], (gb / kPgSlots - 1) & 1u, abort_flag, err, 0x81);
             if (gone()) {
               ok = false;
               break;
             }
             PagedBlock& blk = block_s[slot];
-            if ((lane >> 3) == j) blk.id[lane & 7] = page;
+            if ((lane >> 3) == j) blk.id[sub] = page;
             if (lane == 8 * j) {
-              const uint32_t have = (mapped >> (8 * j)) & 0xFFu, want = (wanted >> (8 * j)) & 0xFFu;
+              const uint32_t have = (mapped >> (8 * j)) & 0xFFu;
               blk.row = row;
-              blk.c0 = c0;
-              blk.c1 = c1;
+              blk.i0 = first_token;
+              blk.i1 = i1;
               blk.pages = have;
-              blk.full = whole && have == want && row <= run.all_end - kPgKeys &&
-                         (row >= run.all_low || row <= p.first - kPgKeys);
+              blk.starts = k0 + j == k_first;
+              blk.full = whole && have == want && row <= all_end - kKeys && (row >= all_low || row <= p.first - kKeys);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&blk_full[slot]);
@@ -442,11 +548,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         }
         before += count;
       }
-      if (!ok) break;
     }
     // the end: a part without a unit
     if (!gone()) {
-      if (n > 1) mbar_wait(&part_empty[n & 1], static_cast<uint32_t>((n >> 1) - 1) & 1u, abort_flag, err, 0x82);
+      if (n > 1) paged_wait(&part_empty[n & 1], static_cast<uint32_t>((n >> 1) - 1) & 1u, abort_flag, err, 0x82);
       if (!gone() && lane == 0) {
         part_s[n & 1].unit = -1;
         part_s[n & 1].blocks = 0;
@@ -455,14 +560,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ load
-    uint32_t gb = 0, nq = 0;   // blocks and q's of this CTA so far
-    uint32_t tiles = 0;        // tiles whose copies were issued
-    int pages = kPgKeys >> p.pages.log_rows;
-    if (pages == 0) pages = 1;
-    const int rows = 1 << p.pages.log_rows;
+    uint32_t gb = 0, nq = 0;  // blocks and q's of this CTA so far
+    uint32_t tile = 0;        // tiles whose copies were issued
+    const int page_rows = 1 << p.pages.log_rows;
+    const int pages = kKeys >> p.pages.log_rows > 0 ? kKeys >> p.pages.log_rows : 1;
     const int none = max(1, p.pages.P << p.pages.log_rows);  // a row behind the last page: the copy fills in zeros
-    for (int n = 0;; ++n) {
-      mbar_wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x83);
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      paged_wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x83);
       if (gone()) break;
       const int u = part_s[n & 1].unit;
       const int nb = part_s[n & 1].blocks;
@@ -470,22 +575,20 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       if (lane == 0) mbar_arrive(&part_empty[n & 1]);
       if (u < 0) break;
       if (nb == 0) continue;
-      const PagedUnit un = paged_unit(p, u, N);
-      // q's place is free once the score products of the part before are done
-      if (nq > 0) mbar_wait(q_empty, (nq - 1) & 1u, abort_flag, err, 0x84);
+      // a place for q is free once the score products of the part that had it are done
+      const uint32_t qb = nq % kQb;
+      if (nq >= kQb) paged_wait(&q_empty[qb], (nq / kQb - 1) & 1u, abort_flag, err, 0x84);
       if (gone()) break;
       ++nq;
       if (lane == 0) {
-        mbar_arrive_expect_tx(q_full, kCh * L::kQChunkBytes);
-        const int y = un.t0 * p.H + un.h0;
-        for (int c = 0; c < kCh; ++c) tma_load_2d(q_s + c * L::kQChunkBytes, &qmap, q_full, 64 * c, y);
+        mbar_arrive_expect_tx(&q_full[qb], L::kQBytes);
+        const int y = paged_unit(p, u).row0;
+        for (int c = 0; c < kCh; ++c) tma_load_2d(q_s + qb * L::kQBytes + c * L::kQChunkBytes, &qmap, &q_full[qb], 64 * c, y);
       }
       __syncwarp();
-      bool ok = true;
-      for (int b = 0; b < nb; ++b, ++gb) {
+      for (int b = 0; ok && b < nb; ++b, ++gb) {
         const uint32_t slot = gb % kPgSlots;
-        const int st = static_cast<int>(gb % kSt);
-        mbar_wait(&blk_full[slot], (gb / kPgSlots) & 1u, abort_flag, err, 0x85);
+        paged_wait(&blk_full[slot], (gb / kPgSlots) & 1u, abort_flag, err, 0x85);
         if (gone()) {
           ok = false;
           break;
@@ -493,395 +596,661 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const PagedBlock& blk = block_s[slot];
         const int i = lane >> 1;  // page of the block
         int y = none;
-        if (i < pages && blk.id[i & 7] >= 0) y = (blk.id[i & 7] << p.pages.log_rows) + (blk.row & (rows - 1));
+        if (i < pages && blk.id[i & 7] >= 0) y = (blk.id[i & 7] << p.pages.log_rows) + (blk.row & (page_rows - 1));
         __syncwarp();
         if (lane == 0) mbar_arrive(&blk_empty[slot]);
-#pragma unroll
+#pragma unroll 1
         for (int m = 0; m < kTi; ++m) {
-          if (gb >= kSt) mbar_wait(&kv_empty[st * kTi + m], (gb / kSt - 1) & 1u, abort_flag, err, 0x86);
+          const uint32_t at = tile % kRing;
+          if (tile >= kRing) paged_wait(&kv_empty[at], (tile / kRing - 1) & 1u, abort_flag, err, 0x86);
           if (gone()) {
             ok = false;
             break;
           }
-          ++tiles;
-          if (lane == 0) mbar_arrive_expect_tx(&kv_full[st * kTi + m], L::kTileBytes);
+          ++tile;
+          if (lane == 0) mbar_arrive_expect_tx(&kv_full[at], L::kTileBytes);
           __syncwarp();
           const int c = 2 * m + (lane & 1);
-          if (i < pages && c < kCh)
-            tma_load_2d(kv_s + st * L::kStageBytes + c * L::kChunkBytes + i * p.box_rows * 128, &kvmap, &kv_full[st * kTi + m], 64 * c, y);
+          if (i < pages && (lane & 1) < L::kTileChunks)
+            tma_load_2d(kv_s + at * L::kTileBytes + (lane & 1) * L::kChunkBytes + i * p.box_rows * 128, &kvmap, &kv_full[at], 64 * c, y);
         }
-        if (!ok) break;
       }
-      if (!ok) break;
     }
     if (gone()) {  // copies in flight land before the CTA ends
-      if (nq > 0) mbar_wait_drain(q_full, (nq - 1) & 1u);
-      for (uint32_t i = tiles > kSt * kTi ? tiles - kSt * kTi : 0; i < tiles; ++i)
-        mbar_wait_drain(&kv_full[(i / kTi) % kSt * kTi + i % kTi], (i / (kSt * kTi)) & 1u);
+      for (uint32_t i = nq > kQb ? nq - kQb : 0; i < nq; ++i) mbar_wait_drain(&q_full[i % kQb], (i / kQb) & 1u);
+      for (uint32_t i = tile > kRing ? tile - kRing : 0; i < tile; ++i) mbar_wait_drain(&kv_full[i % kRing], (i / kRing) & 1u);
     }
   } else if (warp == 0) {
     // ------------------------------------------------------------------ MMA issuer (the whole warp, one thread elected)
     const uint32_t on = elect_one();
     const auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, site)) != 0;
+      return __all_sync(0xffffffffu, paged_wait(bar, parity, abort_flag, err, site)) != 0;
     };
-    constexpr uint32_t id_qk = idesc_bf16(kPgKeys, N, false, false);
-    constexpr uint32_t id_pv = idesc_bf16(128, N, true, true);
+    // by row: S = Q . KV^T and O += P . KV with P in tensor memory; else S^T = KV . Q^T and O^T += KV^T . P^T
+    constexpr uint32_t id_qk = L::kByRow ? idesc_bf16(N, kKeys, false, false) : idesc_bf16(kKeys, N, false, false);
+    constexpr uint32_t id_pv = L::kByRow ? idesc_bf16(N, L::kOTile, false, true) : idesc_bf16(128, N, true, true);
     const uint64_t kv_k = desc_sw128(smem_addr(kv_s), 16, 1024);                // K-major: rows x dims
     const uint64_t q_k = desc_sw128(smem_addr(q_s), 16, 1024);                  // K-major: columns x dims
     const uint64_t kv_mn = desc_sw128(smem_addr(kv_s), L::kChunkBytes, 1024);   // MN-major: dims x rows
-    const uint64_t p_mn = desc_sw128(smem_addr(p_s), kPgKeys * 128, 1024);      // MN-major: columns x rows
-    const auto score = [&](uint32_t gb) -> bool {
-      const uint32_t st = gb % kSt;
-      const uint64_t a = kv_k + st * (L::kStageBytes >> 4);
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) {
-        if ((c & 1) == 0) {
-          if (!wait(&kv_full[st * kTi + c / 2], (gb / kSt) & 1u, 0x90)) return false;
-          tc_fence_after_sync();
+    const uint64_t p_mn = desc_sw128(smem_addr(p_s), kKeys * 128, 1024);        // MN-major: columns x rows
+    // the score products go one block ahead of the weighted sums, across parts
+    int n = 0, left = 0;             // parts taken; blocks of the last one whose scores are still to come
+    uint32_t gs = 0, nq = 0;         // blocks scored, q's used
+    uint32_t q_at = 0;
+    bool ended = false, failed = false;
+    int part_no = 0;                 // units so far
+    // Scores the next block; false where there is none, or where the look ahead met a part without blocks: what comes
+    // after that is made known only when the part before it is done, which takes the weighted sum still to be issued.
+    const auto score = [&](int& opens, bool ahead) -> bool {  // opens: the part's number where the block is its first, else 0
+      opens = 0;
+      while (left == 0) {
+        if (ended) return false;
+        if (!wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, 0x90)) {
+          failed = true;
+          return false;
         }
+        const int u = __shfl_sync(0xffffffffu, part_s[n & 1].unit, 0);
+        left = __shfl_sync(0xffffffffu, part_s[n & 1].blocks, 0);
+        if (lane == 0) mbar_arrive(&part_empty[n & 1]);
+        __syncwarp();
+        ++n;
+        if (u < 0) {
+          ended = true;
+          return false;
+        }
+        ++part_no;
+        if (left == 0) {
+          if (ahead) return false;
+          continue;
+        }
+        q_at = nq % kQb;
+        if (!wait(&q_full[q_at], (nq / kQb) & 1u, 0x91)) {
+          failed = true;
+          return false;
+        }
+        ++nq;
+        opens = part_no;
+      }
+      const uint32_t to = s_tmem + L::kSCols * (gs & 1u);
+      const uint64_t q = q_k + q_at * (L::kQBytes >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t ad = a + ((c * L::kChunkBytes + kk * 32) >> 4), bd = q_k + ((c * L::kQChunkBytes + kk * 32) >> 4);
-          if (c == 0 && kk == 0)
-            mma_f16_if<false>(on, s_tmem + N * (gb % kSc), ad, bd, id_qk, 0u);
+      for (int m = 0; m < kTi; ++m) {
+        const uint32_t tile = gs * kTi + m, at = tile % kRing;
+        if (!wait(&kv_full[at], (tile / kRing) & 1u, 0x92)) {
+          failed = true;
+          return false;
+        }
+        tc_fence_after_sync();
+        const uint64_t a = kv_k + at * (L::kTileBytes >> 4);
+#pragma unroll
+        for (int k = 0; k < (D == 64 ? 4 : 8); ++k) {
+          const uint64_t kv = a + (((k / 4) * L::kChunkBytes + (k % 4) * 32) >> 4);
+          const uint64_t qd = q + (((2 * m + k / 4) * L::kQChunkBytes + (k % 4) * 32) >> 4);
+          if (m == 0 && k == 0)
+            mma_f16_if<false>(on, to, L::kByRow ? qd : kv, L::kByRow ? kv : qd, id_qk, 0u);
           else
-            mma_f16_if<true>(on, s_tmem + N * (gb % kSc), ad, bd, id_qk);
+            mma_f16_if<true>(on, to, L::kByRow ? qd : kv, L::kByRow ? kv : qd, id_qk);
         }
       }
-      mma_commit_if(on, &s_full[gb % kSc]);
+      mma_commit_if(on, &s_full[gs & 1u]);
+      ++gs;
+      if (--left == 0) mma_commit_if(on, &q_empty[q_at]);
       return true;
     };
     uint32_t gb = 0;
-    uint32_t nq = 0, no = 0;  // parts with blocks so far, parts so far
-    bool ok = true;
-    for (int n = 0; ok; ++n) {
-      if (!wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, 0x91)) break;
-      const int u = __shfl_sync(0xffffffffu, part_s[n & 1].unit, 0);
-      const int nb = __shfl_sync(0xffffffffu, part_s[n & 1].blocks, 0);
-      if (lane == 0) mbar_arrive(&part_empty[n & 1]);
-      __syncwarp();
-      if (u < 0) break;
-      ++no;
-      if (nb == 0) continue;
-      if (!wait(q_full, nq & 1u, 0x92)) break;
-      ++nq;
-      if (!score(gb)) break;
-      if (nb == 1) mma_commit_if(on, q_empty);  // (after the part's last score product)
-      for (int b = 0; b < nb; ++b, ++gb) {
-        if (kSt > 1 && b + 1 < nb) {
-          if (!score(gb + 1)) {
-            ok = false;
-            break;
-          }
-          if (b + 2 == nb) mma_commit_if(on, q_empty);
-        }
-        if (!wait(p_full, gb & 1u, 0x93)) {
-          ok = false;
-          break;
-        }
-        // the part's first weighted sum overwrites O: the previous part's output must be read
-        if (b == 0 && no > 1 && !wait(o_empty, (no - 2) & 1u, 0x94)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        const uint32_t st = gb % kSt;
-        const uint64_t a = kv_mn + st * (L::kStageBytes >> 4);
-        const uint32_t more = b > 0 ? 1u : 0u;
+    int opens, next_opens;
+    bool more = score(opens, false);
+    while (more) {
+      more = score(next_opens, true);
+      if (failed) break;
+      if (!(L::kByRow ? wait(&p_full[gb & 1u], (gb >> 1) & 1u, 0x93) : wait(p_full, gb & 1u, 0x93))) break;
+      // a part's first weighted sum overwrites O: the output of the part before must be read
+      if (opens > 1 && !wait(o_empty, static_cast<uint32_t>(opens) & 1u, 0x94)) break;
+      tc_fence_after_sync();
+      const uint32_t add = opens != 0 ? 0u : 1u;
 #pragma unroll
-        for (int m = 0; m < kTi; ++m) {
+      for (int m = 0; m < kTi; ++m) {
+        const uint32_t at = (gb * kTi + m) % kRing;
+        const uint64_t a = kv_mn + at * (L::kTileBytes >> 4);
 #pragma unroll
-          for (int ks = 0; ks < kPgKeys / 16; ++ks) {
-            const uint64_t ad = a + ((2 * m * L::kChunkBytes + ks * 16 * 128) >> 4), bd = p_mn + ((ks * 16 * 128) >> 4);
-            if (ks == 0)
-              mma_f16_if<false>(on, o_tmem + N * m, ad, bd, id_pv, more);
-            else
-              mma_f16_if<true>(on, o_tmem + N * m, ad, bd, id_pv);
-          }
-          mma_commit_if(on, &kv_empty[st * kTi + m]);
+        for (int ks = 0; ks < kKeys / 16; ++ks) {
+          const uint64_t kv = a + ((ks * 16 * 128) >> 4);
+          if constexpr (L::kByRow)
+            mma_f16_ts_if(on, o_tmem + L::kOTile * m, s_tmem + L::kSCols * (gb & 1u) + 8 * ks, kv, id_pv, ks == 0 ? add : 1u);
+          else if (ks == 0)
+            mma_f16_if<false>(on, o_tmem + L::kOTile * m, kv, p_mn + ((ks * 16 * 128) >> 4), id_pv, add);
+          else
+            mma_f16_if<true>(on, o_tmem + L::kOTile * m, kv, p_mn + ((ks * 16 * 128) >> 4), id_pv);
         }
-        mma_commit_if(on, pv_done);
-        if (kSt == 1 && b + 1 < nb) {
-          if (!score(gb + 1)) {
-            ok = false;
-            break;
-          }
-          if (b + 2 == nb) mma_commit_if(on, q_empty);
-        }
+        mma_commit_if(on, &kv_empty[at]);
       }
+      mma_commit_if(on, pv_done);
+      ++gb;
+      if (!more && !ended) more = score(next_opens, false);
+      if (failed) break;
+      opens = next_opens;
     }
     // every MMA issued by this thread has completed once `drain` flips
     mma_commit_if(on, drain);
     mbar_wait_drain(drain, 0);
     __syncwarp();
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------------ softmax and output
+  } else if constexpr (L::kByRow) {
+    // ------------------------------------------------------------------ softmax and output, a thread with a row of q
+    // Warps 3-6 take the even blocks, 7-10 the odd ones; a row's two threads (of the same quarter of the two groups) take
+    // turns in deciding on its bound, so a block's exponentials run beside the next one's.  The hardware barriers, whose wait
+    // has no limit, are those of a unit, which all pass or none: a block has none.
+    const int group = (warp - kPgFirstSoft) >> 2;
+    const int quarter = warp & 3;               // tensor-memory lane quarter
+    const int r = quarter * 32 + lane;          // the unit's row
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_at = s_tmem + L::kSCols * group + lane_off;
+    const float to_log2 = p.scale * 1.4426950408889634f;
+    const uint64_t to_log2_2 = pack_f32x2(to_log2, to_log2);
+    volatile float* bound_s = neg_s;                                  // [N]
+    float* sum_s = alpha_s;                                           // [2][N]
+    uint32_t gb0 = 0;                                                 // blocks of the parts before
+    float x[32];
+    for (int n = 0;; ++n) {
+      paged_wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0xA0);
+      const int nb = part_s[n & 1].blocks;
+      if (bar_or(kTcEpiBar, kPgSoft, *abort_flag != 0)) break;
+      if (part_s[n & 1].unit < 0) break;
+      const PagedUnit un = paged_unit(p, part_s[n & 1].unit);
+      const bool used = quarter * 32 < un.cols;             // (of a quarter without rows nothing is read, written or kept)
+      const int token = r < un.cols ? (un.skip + r) / p.H : kPgMaxTokens;
+      const int end = token < kPgMaxTokens ? end_s[(n & 1) * kPgMaxTokens + token] : 0;
+      const int low = max(0, end - p.window);
+      float l0 = 0.f, l1 = 0.f, l_bound = kPgNoBound;       // this thread's sums, in units of 2^l_bound
+      for (int b = static_cast<int>((gb0 ^ group) & 1u); b < nb; b += 2) {
+        const uint32_t gb = gb0 + b, slot = gb % kPgSlots;
+        paged_wait(&blk_full[slot], (gb / kPgSlots) & 1u, abort_flag, err, 0xA1);
+        const PagedBlock& blk = block_s[slot];
+        const int row = blk.row;
+        const bool full = __any_sync(0xffffffffu, blk.full != 0) != 0;
+        const bool mine = token >= blk.i0 && token < blk.i1;
+        const uint32_t there = blk.pages;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&blk_empty[slot]);
+        // The block's rows [32 i, 32 i + 32) that this row sees.
+        const auto mask_of = [&](int i) -> uint32_t {
+          if (!mine) return 0u;
+          const auto upto = [&](int e) { return low_bits(min(max(e - row - 32 * i, 0), 32)); };
+          uint32_t m = upto(end) & (~upto(low) | upto(p.first));
+          if (p.pages.log_rows == 4) {  // two pages
+            if (((there >> (2 * i)) & 1u) == 0u) m &= 0xFFFF0000u;
+            if (((there >> (2 * i + 1)) & 1u) == 0u) m &= 0x0000FFFFu;
+          } else if (((there >> ((32 * i) >> p.pages.log_rows)) & 1u) == 0u) {
+            m = 0u;
+          }
+          return m;
+        };
+        paged_wait(&s_full[group], (gb >> 1) & 1u, abort_flag, err, 0xA2);
+        tc_fence_after_sync();
+        // the largest score
+        float top = -INFINITY;
+        bool odd = false;  // a score that is no number in a block that not every row of q sees all of
+        if (used) {
+#pragma unroll 1
+          for (int i = 0; i < kKeys / 32; ++i) {
+            tmem_ld_x32_sync(s_at + 32 * i, x);
+            if (!full) {
+              uint64_t none = 0ull;  // is a number where every score is
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) none = fma_f32x2(pack_f32x2(x[c], x[c + 1]), 0ull, none);
+              float n0, n1;
+              unpack_f32x2(none, n0, n1);
+              odd |= n0 != n0 || n1 != n1;
+              const uint32_t mask = mask_of(i);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if ((mask & (1u << c)) == 0u) x[c] = to_log2 < 0.f ? INFINITY : -INFINITY;
+            }
+            if (to_log2 < 0.f) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) x[c] = -x[c];
+            }
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) top = max3(top, x[c], x[c + 1]);
+          }
+          if (__any_sync(0xffffffffu, odd)) {
+            // Weights of 0 times values that are no numbers would still be none.  So the kv rows that hold such are zeroed (by each
+            // warp that finds them: all four of the group do), and rows of q that see such a score get a sum that is none.
+            bool sees = false;
+#pragma unroll 1
+            for (int i = 0; i < kKeys / 32; ++i) {
+              tmem_ld_x32_sync(s_at + 32 * i, x);
+              const uint32_t mask = mask_of(i);
+              uint32_t is = 0u;
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(fabsf(x[c]) < INFINITY)) is |= 1u << c;
+              sees |= (is & mask) != 0u;
+              is = __reduce_or_sync(0xffffffffu, is);
+              while (is != 0u) {
+                const int key = 32 * i + __ffs(is) - 1;
+                is &= is - 1u;
+                bool bad = false;
+#pragma unroll 1
+                for (int j = lane; j < kCh * 8; j += 32) {
+                  const uint32_t tile = gb * kTi + (j / 8) / L::kTileChunks;
+                  paged_wait(&kv_full[tile % kRing], (tile / kRing) & 1u, abort_flag, err, 0xA6);
+                  const uint4 v = *reinterpret_cast<const uint4*>(kv_s + (tile % kRing) * L::kTileBytes + ((j / 8) % L::kTileChunks) * L::kChunkBytes +
+                                                                  key * 128 + (j % 8) * 16);
+                  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) bad |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
+                }
+                if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll 1
+                  for (int j = lane; j < kCh * 8; j += 32) {
+                    const uint32_t tile = gb * kTi + (j / 8) / L::kTileChunks;
+                    *reinterpret_cast<uint4*>(kv_s + (tile % kRing) * L::kTileBytes + ((j / 8) % L::kTileChunks) * L::kChunkBytes + key * 128 +
+                                              (j % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                  }
+                }
+              }
+            }
+            if (sees) l0 = __int_as_float(0x7FFFFFFF);
+            fence_proxy_async_shared();
+          }
+        }
+        // the bound: raised only when exceeded by more than 2^8, behind the decision on the block before
+        if (gb > 0) paged_wait(&decided[quarter], (gb - 1) & 1u, abort_flag, err, 0xA7);
+        float before = kPgNoBound;
+        if (b > 0) before = bound_s[r];
+        float bound = before;
+        const float most = top * fabsf(to_log2);
+        if (most > before + kTcLazyLog2) bound = most;
+        bound_s[r] = bound;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&decided[quarter]);
+        const bool moved = bound != before && before != kPgNoBound;
+        if (__any_sync(0xffffffffu, used && moved)) {  // the accumulators of the blocks before follow
+          paged_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0xA3);
+          tc_fence_after_sync();
+          const float f = moved ? exp2f(before - bound) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < kTi * L::kOTile; c += 16) {
+            tmem_ld_x16(o_tmem + lane_off + c, x);
+            tmem_wait_ld_regs16(x);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] *= f;
+            tmem_st_x16(o_tmem + lane_off + c, x);
+          }
+        }
+        if (bound != l_bound) {
+          const float f = l_bound == kPgNoBound ? 0.f : exp2f(l_bound - bound);
+          l0 = l_bound == kPgNoBound && l0 == l0 ? 0.f : l0 * f;
+          l1 = l_bound == kPgNoBound ? 0.f : l1 * f;
+          l_bound = bound;
+        }
+        // weights, as bf16 in the place of the scores
+        if (used) {
+          const uint64_t neg2 = pack_f32x2(-bound, -bound);
+          uint64_t l2 = pack_f32x2(l0, l1);
+#pragma unroll 1
+          for (int i = 0; i < kKeys / 32; ++i) {
+            tmem_ld_x32_sync(s_at + 32 * i, x);
+            uint32_t pk[16];
+            const uint32_t mask = full ? 0xFFFFFFFFu : mask_of(i);
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) unpack_f32x2(fma_f32x2(pack_f32x2(x[c], x[c + 1]), to_log2_2, neg2), x[c], x[c + 1]);
+            if (!full) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if ((mask & (1u << c)) == 0u) x[c] = -INFINITY;
+            }
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              x[c] = exp2_approx(x[c]);
+              x[c + 1] = exp2_approx(x[c + 1]);
+              l2 = add_f32x2(l2, pack_f32x2(x[c], x[c + 1]));
+              const __nv_bfloat162 w = __floats2bfloat162_rn(x[c], x[c + 1]);
+              pk[c / 2] = *reinterpret_cast<const uint32_t*>(&w);
+            }
+            tmem_st_words_x16(s_at + 16 * i, pk);
+          }
+          unpack_f32x2(l2, l0, l1);
+          tmem_wait_st();
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[group]);
+      }
+      gb0 += nb;
+      // the part's end: the two threads' sums in units of the row's last bound
+      named_bar_sync(kTcEpiBar, kPgSoft);
+      // (a wait is for a phase or the one before it: both groups have seen the scores of their last blocks, so all weighted sums
+      // but the last two are done)
+      if (nb > 1) paged_wait(pv_done, (gb0 - 2) & 1u, abort_flag, err, 0xA5);
+      if (nb > 0) paged_wait(pv_done, (gb0 - 1) & 1u, abort_flag, err, 0xA5);
+      tc_fence_after_sync();
+      float bound = kPgNoBound;
+      if (nb > 0) bound = bound_s[r];
+      const float own = l0 + l1;
+      sum_s[group * N + r] = own != own ? own : (l_bound == kPgNoBound ? 0.f : own * exp2f(l_bound - bound));
+      named_bar_sync(kTcEpiBar, kPgSoft);
+      const float sum = sum_s[r] + sum_s[N + r];
+      const int way = part_s[n & 1].way;
+      const int64_t place = 2 * static_cast<int64_t>(cta) + (way == kPgHead ? 1 : 0);  // of a shared unit's part
+      float f = 1.f;
+      if (r < un.cols) {
+        if (way == kPgWhole) {
+          f = paged_factor(bound, sum, p.sink, (un.skip + r) % p.H, p.lse != nullptr && group == 0 ? p.lse + un.row0 + r : nullptr);
+        } else if (group == 0) {
+          __stcg(p.stats + place * 2 * N + r, bound);
+          __stcg(p.stats + place * 2 * N + N + r, sum);
+        }
+      }
+      if (used) {
+        // half of the dims for each of the row's two threads
+        uint16_t* out = p.out + (static_cast<int64_t>(un.row0) + r) * D;
+        float* part = p.partial + (place * N + r) * D;
+#pragma unroll 1
+        for (int d = group * (D / 2); d < (group + 1) * (D / 2); d += 16) {
+          float* o = x;
+          if (nb > 0) {
+            tmem_ld_x16(o_tmem + lane_off + d, o);
+            tmem_wait_ld_regs16(o);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = 0.f;
+          }
+          if (r < un.cols && way == kPgWhole) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const __nv_bfloat162 two = __floats2bfloat162_rn(o[j] * f, o[j + 1] * f);
+              w[j / 2] = *reinterpret_cast<const uint32_t*>(&two);
+            }
+            reinterpret_cast<uint4*>(out + d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(out + d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          } else if (r < un.cols) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) __stcg(reinterpret_cast<float4*>(part + d + j), make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]));
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(o_empty);
+        mbar_arrive(&part_empty[n & 1]);
+      }
+      named_bar_sync(kTcEpiBar, kPgSoft);  // bounds and sums are written anew by the next part
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax and output, a thread with a row of the block
     // All softmax warps take the same way: the block counts are those of a wait that succeeded for all of them, and
-    // what they decide in a block is a vote over all.  So the hardware barriers, whose wait has no limit, are passed by
-    // all or by none.
-    const int etid = threadIdx.x - 128;
-    const int quarter = warp & 3;             // tensor-memory lane quarter
-    const int cb = ((warp - 4) >> 2) * kC;    // this thread's columns [cb, cb + kC)
-    const int r = quarter * 32 + lane;        // row of the block (scores) / dim of a tile (output)
+    // what they decide in a block is a vote over all.  So the hardware barriers, whose wait has no limit,
+    // are passed by all or by none.
+    const int etid = threadIdx.x - 32 * kPgFirstSoft;
+    const int quarter = warp & 3;                                  // tensor-memory lane quarter
+    const int gc = ((warp - kPgFirstSoft) >> 2) * 32;                         // this warp's columns [gc, gc + 32)
+    constexpr int kC = 16;
+    const int cb = gc + (lane >> 4) * 16;                          // this thread's [cb, cb + kC)
+    const int r = quarter * 16 + (lane & 15);                      // its row of the block
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const float to_log2 = p.scale * 1.4426950408889634f;
-    const uint64_t to_log2_2 = pack_f32x2(to_log2, to_log2), minus = pack_f32x2(-1.f, -1.f);
-    uint8_t* p_row = p_s + (cb / 64) * (kPgKeys * 128);
+    const uint64_t to_log2_2 = pack_f32x2(to_log2, to_log2);
+    uint8_t* p_row = p_s + (cb / 64) * (kKeys * 128);
     uint32_t gb = 0;
     uint64_t lsum[kC / 2];
-    float x[kC];
+    float x[kC];          // scores or weights of its columns
+    bool p_zero = false;  // this warp's part of P is zero
     const auto load = [&](uint32_t at) {
-      if constexpr (kC == 32) {
-        tmem_ld_x32_sync(at, x);
-      } else {
-        tmem_ld_x16(at, x);
-        tmem_wait_ld_regs16(x);
-      }
+      tmem_ld_half_x16(at, x);
+      tmem_wait_ld_regs16(x);
     };
     for (int n = 0;; ++n) {
-      mbar_wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0xA0);
-      const PagedPart part = part_s[n & 1];
-      const int nb = part.blocks;
-      if (etid < N) max_s[etid] = kPgNoBound;
+      paged_wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0xA0);
+      const int nb = part_s[n & 1].blocks;
+      if (etid < N) neg_s[etid] = -kPgNoBound;
 #pragma unroll
       for (int c = 0; c < kC / 2; ++c) lsum[c] = 0ull;
-      if (bar_or(kTcEpiBar, kPgSoftThreads, *abort_flag != 0)) break;
-      if (part.unit < 0) break;
-      const PagedUnit un = paged_unit(p, part.unit, N);
-      const int* end = end_s + (n & 1) * N + cb;
-      const bool used = cb < un.cols;  // (of columns that are not, nothing is read, written or kept)
+      if (bar_or(kTcEpiBar, kPgSoft, *abort_flag != 0)) break;
+      if (__any_sync(0xffffffffu, part_s[n & 1].unit < 0)) break;
+      const int* end = end_s + (n & 1) * kPgMaxTokens;
+      bool used;  // some of this warp's columns are (of others nothing is read, written or kept)
+      int skip, i_first, i_last;  // rows before the unit's first in its token; the tokens of this warp's columns
+      {
+        const PagedUnit un = paged_unit(p, part_s[n & 1].unit);
+        used = gc < un.cols;
+        skip = un.skip;
+        i_first = (gc + skip) / p.H;
+        i_last = (min(gc + 32, un.cols) - 1 + skip) / p.H;
+      }
       for (int b = 0; b < nb; ++b, ++gb) {
         const uint32_t slot = gb % kPgSlots;
-        mbar_wait(&blk_full[slot], (gb / kPgSlots) & 1u, abort_flag, err, 0xA1);
+        paged_wait(&blk_full[slot], (gb / kPgSlots) & 1u, abort_flag, err, 0xA1);
         const PagedBlock& blk = block_s[slot];
-        const bool full = blk.full != 0;
+        const bool full = blk.full != 0, starts_run = __any_sync(0xffffffffu, blk.starts != 0) != 0;
         const int row = blk.row + r;
-        const int c0 = blk.c0 - cb, c1 = blk.c1 - cb;
+        const int i0 = max(blk.i0, i_first), i1 = min(blk.i1 - 1, i_last);
         const bool here = ((blk.pages >> (r >> p.pages.log_rows)) & 1u) != 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&blk_empty[slot]);
-        const uint32_t s_at = s_tmem + N * (gb % kSc) + lane_off + cb;
-        mbar_wait(&s_full[gb % kSc], (gb / kSc) & 1u, abort_flag, err, 0xA2);
-        tc_fence_after_sync();
-        bool odd = false;  // a score that is no number in a block that not every column sees all of
-        // scores in log2 units, minus infinity where a column does not see the row
-        const unsigned span = !here ? 0u : static_cast<unsigned>(row < p.first ? INT32_MAX : p.window);
-        const auto sees = [&](int c) {  // 0 <= end - 1 - row < span
-          return c >= c0 && c < c1 && static_cast<unsigned>(end[c] - 1 - row) < span;
-        };
-        const auto masked_scores = [&]() {
-          load(s_at);
-#pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            odd |= !(fabsf(x[c]) < INFINITY);
-            x[c] = sees(c) ? x[c] * to_log2 : -INFINITY;
-          }
-        };
-        // exponents relative to the bounds
-        const auto exponents = [&](bool bad) {
-          if (full) {
-            load(s_at);
-          } else {
-            masked_scores();
-          }
-          const uint64_t f2 = full ? to_log2_2 : pack_f32x2(1.f, 1.f);
-#pragma unroll
-          for (int c = 0; c < kC; c += 4) {
-            const float4 mv = *reinterpret_cast<const float4*>(max_s + cb + c);
-            unpack_f32x2(fma_f32x2(pack_f32x2(mv.x, mv.y), minus, fma_f32x2(pack_f32x2(x[c], x[c + 1]), f2, 0ull)), x[c], x[c + 1]);
-            unpack_f32x2(fma_f32x2(pack_f32x2(mv.z, mv.w), minus, fma_f32x2(pack_f32x2(x[c + 2], x[c + 3]), f2, 0ull)), x[c + 2],
-                         x[c + 3]);
-          }
-          if (bad) {
-#pragma unroll
-            for (int c = 0; c < kC; ++c) x[c] = -INFINITY;
-          }
-        };
-        float over = -INFINITY;
-        if (used) {
-          exponents(false);
-#pragma unroll
-          for (int c = 0; c < kC; c += 2) over = max3(over, x[c], x[c + 1]);
-        }
-        if (bar_or(kTcEpiBar, kPgSoftThreads, over > kTcLazyLog2 || odd)) {
-          // rare: a bound has to be raised, or a masked row holds what is no number
-          if (gb > 0) mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0xA3);
-          tc_fence_after_sync();
-          bool bad = false;
-          if (bar_or(kTcEpiBar, kPgSoftThreads, odd)) {
-            // 0 times such a value would still be no number in the weighted sum.  So a row that holds one is taken out of the
-            // products, and the columns that see it get a sum that is no number.
-            for (int m = 0; m < kTi; ++m) mbar_wait(&kv_full[(gb % kSt) * kTi + m], (gb / kSt) & 1u, abort_flag, err, 0xA6);
-            uint8_t* at = kv_s + (gb % kSt) * L::kStageBytes + r * 128;
-            for (int c = 0; c < kCh; ++c)
-              for (int i = 0; i < 8; ++i) {
-                const uint4 v = *reinterpret_cast<const uint4*>(at + c * L::kChunkBytes + i * 16);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) bad |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
-              }
-            named_bar_sync(kTcEpiBar, kPgSoftThreads);
-            bad = bad && !full;  // (a full block's row is seen by all columns: what comes of it is theirs)
-            if (bad) {
-              if (cb == 0)
-                for (int c = 0; c < kCh; ++c)
-                  for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<uint4*>(at + c * L::kChunkBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-              const float none = __int_as_float(0x7FFFFFFF);
-#pragma unroll
-              for (int c = 0; c < kC; c += 2) {
-                float s0, s1;
-                unpack_f32x2(lsum[c / 2], s0, s1);
-                lsum[c / 2] = pack_f32x2(sees(c) ? none : s0, sees(c + 1) ? none : s1);
-              }
-            }
-          }
-          // the largest scores of each column
-          int* top_s = reinterpret_cast<int*>(alpha_s);
-          if (etid < N) top_s[etid] = ordered(-INFINITY);
-          named_bar_sync(kTcEpiBar, kPgSoftThreads);
-          if (used) {
-            if (full) {
-              load(s_at);
-#pragma unroll
-              for (int c = 0; c < kC; ++c) x[c] *= to_log2;
-            } else {
-              masked_scores();
-            }
-            if (bad) {
-#pragma unroll
-              for (int c = 0; c < kC; ++c) x[c] = -INFINITY;
-            }
-            if constexpr (kC == 32) {
-              xpose_reduce32(x, lane, [](float v, float w) { return fmaxf(v, w); });
-              atomicMax(top_s + cb + lane, ordered(x[0]));
-            } else {
-              xpose_reduce16(x, lane, [](float v, float w) { return fmaxf(v, w); });
-              if ((lane & 1) == 0) atomicMax(top_s + cb + (lane >> 1), ordered(x[0]));
-            }
-          }
-          named_bar_sync(kTcEpiBar, kPgSoftThreads);
-          bool moved = false;
-          if (etid < N) {
-            const float bm = from_ordered(top_s[etid]), mo = max_s[etid];
-            const float mn = bm > mo + kTcLazyLog2 ? bm : mo;
-            moved = mn != mo && mo != kPgNoBound;
-            alpha_s[etid] = moved ? exp2f(mo - mn) : 1.f;
-            max_s[etid] = mn;
-          }
-          moved = bar_or(kTcEpiBar, kPgSoftThreads, moved);
-          if (moved && b > 0 && used) {
-            // sums and output accumulators of earlier blocks follow (this thread: its dim of every tile, its columns)
-#pragma unroll
-            for (int c = 0; c < kC; c += 2)
-              lsum[c / 2] = fma_f32x2(lsum[c / 2], pack_f32x2(alpha_s[cb + c], alpha_s[cb + c + 1]), 0ull);
+        const bool some = __any_sync(0xffffffffu, used && i0 <= i1) != 0;  // some of this warp's columns are the block's
+        uint32_t mask = 0xFFFFFFFFu;         // the columns that see this thread's row
+        if (!full) {
+          mask = 0u;
+          // a row is seen where 0 <= end - 1 - row < span
+          const unsigned span = !here ? 0u : static_cast<unsigned>(row < p.first ? INT32_MAX : p.window);
 #pragma unroll 1
-            for (int m = 0; m < kTi; ++m) {
-#pragma unroll
-              for (int c = 0; c < kC; c += 16) {
-                tmem_ld_x16(o_tmem + lane_off + N * m + cb + c, x);
-                tmem_wait_ld_regs16(x);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] *= alpha_s[cb + c + j];
-                tmem_st_x16(o_tmem + lane_off + N * m + cb + c, x);
-              }
-            }
-            tmem_wait_st();
+          for (int i = i0; i <= i1; ++i) {
+            const int c = i * p.H - skip - cb;  // the token's first column
+            const uint32_t bits = low_bits(min(max(c + p.H, 0), kC)) & ~low_bits(min(max(c, 0), kC));
+            if (static_cast<unsigned>(end[i] - 1 - row) < span) mask |= bits;
           }
-          if (used) exponents(bad);
         }
-        // weights, written into the bf16 row P[row r] once the weighted sum before has read P
-        if (gb > 0) mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0xA4);
-        if (used) {
+        const uint32_t s_at = s_tmem + N * (gb & 1u) + lane_off + gc;
+        paged_wait(&s_full[gb & 1u], (gb >> 1) & 1u, abort_flag, err, 0xA2);
+        tc_fence_after_sync();
+        // weights by the bounds as they are, 0 where a column does not see the row, written into the bf16 row P[row r]; x keeps
+        // them.  True where an exponent exceeds its bound by more than 2^8, or a score is no number in a block that not every
+        // column sees all of.
+        const auto weights = [&]() {
+          load(s_at);
+          uint64_t none = 0ull;  // is a number where every score is
+          if (!full) {
+#pragma unroll
+            for (int c = 0; c < kC; c += 2) none = fma_f32x2(pack_f32x2(x[c], x[c + 1]), 0ull, none);
+          }
+          float over = -INFINITY;
 #pragma unroll
           for (int c = 0; c < kC; c += 8) {
             uint32_t pk[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float e0 = exp2_approx(x[c + 2 * i]), e1 = exp2_approx(x[c + 2 * i + 1]);
-              const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
-              pk[i] = *reinterpret_cast<const uint32_t*>(&w);
-              x[c + 2 * i] = e0;
-              x[c + 2 * i + 1] = e1;
+            for (int i = 0; i < 8; i += 4) {
+              const float4 nm = *reinterpret_cast<const float4*>(neg_s + cb + c + i);
+              float y[4];
+              unpack_f32x2(fma_f32x2(pack_f32x2(x[c + i], x[c + i + 1]), to_log2_2, pack_f32x2(nm.x, nm.y)), y[0], y[1]);
+              unpack_f32x2(fma_f32x2(pack_f32x2(x[c + i + 2], x[c + i + 3]), to_log2_2, pack_f32x2(nm.z, nm.w)), y[2], y[3]);
+              if (!full) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (((mask >> (c + i + k)) & 1u) == 0u) y[k] = -INFINITY;
+              }
+              over = max3(max3(over, y[0], y[1]), y[2], y[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[c + i + k] = exp2_approx(y[k]);
+              const __nv_bfloat162 w0 = __floats2bfloat162_rn(x[c + i], x[c + i + 1]), w1 = __floats2bfloat162_rn(x[c + i + 2], x[c + i + 3]);
+              pk[i / 2] = *reinterpret_cast<const uint32_t*>(&w0);
+              pk[i / 2 + 1] = *reinterpret_cast<const uint32_t*>(&w1);
             }
             *reinterpret_cast<uint4*>(p_row + swz128(r, 2 * (cb % 64 + c))) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
+          float n0, n1;
+          unpack_f32x2(none, n0, n1);
+          return over > kTcLazyLog2 || n0 != n0 || n1 != n1;
+        };
+        // (the weighted sum before has read P)
+        if (gb > 0) paged_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0xA4);
+        bool raise = starts_run;
+        if (some && !starts_run) raise = weights();
+        if (bar_or(kTcEpiBar, kPgSoft, raise)) {
+          // A run's first block, and rarely another: a bound is raised, or a masked row holds what is no number.  The largest
+          // score of each column:
+          const auto largest = [&]() {
+            bool odd = false;
+            load(s_at);
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+              odd |= !full && !(fabsf(x[c]) < INFINITY);
+              x[c] = ((mask >> c) & 1u) != 0u ? x[c] * to_log2 : -INFINITY;
+            }
+            xpose_reduce<kC>(x, lane, [](float v, float w) { return fmaxf(v, w); });
+            atomicMax(top_s + cb + lane % kC, ordered(x[0]));
+            return odd;
+          };
+          bool odd = false;
+          if (some) odd = largest();
+          if (bar_or(kTcEpiBar, kPgSoft, odd)) {
+            // 0 times such a value would still be no number in the weighted sum.  So a row that holds one is taken out of the
+            // products, and the columns that see it get a sum that is no number.
+            bool bad = false;
+            const auto at = [&](int c) { return kv_s + ((gb * kTi + c / 2) % kRing) * L::kTileBytes + (c & 1) * L::kChunkBytes + r * 128; };
+#pragma unroll 1
+            for (int c = 0; c < kCh; ++c) {
+              const uint32_t tile = gb * kTi + c / 2;
+              paged_wait(&kv_full[tile % kRing], (tile / kRing) & 1u, abort_flag, err, 0xA6);
+#pragma unroll 1
+              for (int i = 0; i < 8; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4*>(at(c) + i * 16);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) bad |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
+              }
+            }
+            bad = bad && !full;  // (a full block's row is seen by all columns: what comes of it is theirs)
+            if (etid < N) top_s[etid] = ordered(-INFINITY);
+            named_bar_sync(kTcEpiBar, kPgSoft);
+            if (bad) {
+              if (cb == 0)
+#pragma unroll 1
+                for (int c = 0; c < kCh; ++c)
+#pragma unroll 1
+                  for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(at(c) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+              const float nan = __int_as_float(0x7FFFFFFF);
+#pragma unroll
+              for (int c = 0; c < kC; c += 2) {
+                float s0, s1;
+                unpack_f32x2(lsum[c / 2], s0, s1);
+                lsum[c / 2] = pack_f32x2(((mask >> c) & 1u) != 0u ? nan : s0, ((mask >> c) & 2u) != 0u ? nan : s1);
+              }
+              mask = 0u;
+            }
+            if (some) largest();
+            named_bar_sync(kTcEpiBar, kPgSoft);
+          }
+          bool moved = false;
+          if (etid < N) {
+            const float bm = from_ordered(top_s[etid]), mo = -neg_s[etid];
+            const float mn = bm > mo + kTcLazyLog2 ? bm : mo;
+            moved = mn != mo && mo != kPgNoBound;
+            alpha_s[etid] = moved ? exp2f(mo - mn) : 1.f;
+            neg_s[etid] = -mn;
+            top_s[etid] = ordered(-INFINITY);
+          }
+          moved = bar_or(kTcEpiBar, kPgSoft, moved);
+          if (moved && b > 0) {
+            // sums and output accumulators of earlier blocks follow
+            tc_fence_after_sync();
+            if (used) {
+#pragma unroll
+              for (int c = 0; c < kC; c += 2)
+                lsum[c / 2] = fma_f32x2(lsum[c / 2], pack_f32x2(alpha_s[cb + c], alpha_s[cb + c + 1]), 0ull);
+#pragma unroll 1
+              for (int m = 0; m < 2 * kTi; ++m) {  // (this thread: its dim of every tile, its warp's columns)
+                const int c0 = gc + (m & 1) * 16;
+                tmem_ld_x16(o_tmem + lane_off + N * (m >> 1) + c0, x);
+                tmem_wait_ld_regs16(x);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] *= alpha_s[c0 + j];
+                tmem_st_x16(o_tmem + lane_off + N * (m >> 1) + c0, x);
+              }
+              tmem_wait_st();
+            }
+          }
+          if (some) weights();
+        }
+        if (some) {
+          p_zero = false;
+        } else if (used && !p_zero) {
+          p_zero = true;
+#pragma unroll
+          for (int c = 0; c < kC; c += 8) *reinterpret_cast<uint4*>(p_row + swz128(r, 2 * (cb % 64 + c))) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_shared();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
-        if (used) {
+        if (some) {
 #pragma unroll
-          for (int c = 0; c < kC; c += 2) lsum[c / 2] = fma_f32x2(pack_f32x2(x[c], x[c + 1]), pack_f32x2(1.f, 1.f), lsum[c / 2]);
+          for (int c = 0; c < kC; c += 2) lsum[c / 2] = add_f32x2(lsum[c / 2], pack_f32x2(x[c], x[c + 1]));
         }
       }
-      // the part's end: sums over the 128 rows (P's place holds the quarters' once it is free)
-      if (nb > 0) mbar_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0xA5);
+      // the part's end: sums over the block's rows (P's place holds the quarters' once it is free)
+      if (nb > 0) paged_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0xA5);
       tc_fence_after_sync();
-      named_bar_sync(kTcEpiBar, kPgSoftThreads);
+      named_bar_sync(kTcEpiBar, kPgSoft);
       float* red_s = reinterpret_cast<float*>(p_s);  // [4][N]
-      {
+      p_zero = false;
 #pragma unroll
-        for (int c = 0; c < kC; c += 2) unpack_f32x2(lsum[c / 2], x[c], x[c + 1]);
-        if constexpr (kC == 32) {
-          xpose_reduce32(x, lane, [](float v, float w) { return v + w; });
-          red_s[quarter * N + cb + lane] = x[0];
-        } else {
-          xpose_reduce16(x, lane, [](float v, float w) { return v + w; });
-          if ((lane & 1) == 0) red_s[quarter * N + cb + (lane >> 1)] = x[0];
-        }
-      }
-      named_bar_sync(kTcEpiBar, kPgSoftThreads);
-      const int64_t row0 = static_cast<int64_t>(un.t0) * p.H + un.h0;  // the unit's first (token, head)
-      const int64_t place = 2 * static_cast<int64_t>(cta) + (part.way == kPgHead ? 1 : 0);  // of a shared unit's part
+      for (int c = 0; c < kC; c += 2) unpack_f32x2(lsum[c / 2], x[c], x[c + 1]);
+      xpose_reduce<kC>(x, lane, [](float v, float w) { return v + w; });
+      red_s[quarter * N + cb + lane % kC] = x[0];
+      named_bar_sync(kTcEpiBar, kPgSoft);
+      const PagedUnit un = paged_unit(p, part_s[n & 1].unit);  // (its place is held until the end of the part)
+      const int way = part_s[n & 1].way;
+      const int64_t place = 2 * static_cast<int64_t>(cta) + (way == kPgHead ? 1 : 0);  // of a shared unit's part
       if (etid < un.cols) {
         const float l = (red_s[etid] + red_s[N + etid]) + (red_s[2 * N + etid] + red_s[3 * N + etid]);
-        if (part.way == kPgWhole) {
-          const int h = p.groups > 1 ? un.h0 + etid : etid % p.H;
-          alpha_s[etid] = paged_factor(max_s[etid], l, p.sink, h, p.lse != nullptr ? p.lse + row0 + etid : nullptr);
+        if (way == kPgWhole) {
+          alpha_s[etid] = paged_factor(-neg_s[etid], l, p.sink, (un.skip + etid) % p.H, p.lse != nullptr ? p.lse + un.row0 + etid : nullptr);
         } else {
-          __stcg(p.stats + place * 2 * N + etid, max_s[etid]);
+          __stcg(p.stats + place * 2 * N + etid, -neg_s[etid]);
           __stcg(p.stats + place * 2 * N + N + etid, l);
         }
       }
-      named_bar_sync(kTcEpiBar, kPgSoftThreads);
-      const bool dims = D >= 128 || quarter < 2;  // (the upper half of a 64-dim row's tile is padding)
+      named_bar_sync(kTcEpiBar, kPgSoft);
+      const int dim = quarter * 32 + lane;           // of a tile
+      const bool dims = D >= 128 || quarter < 2;     // (the upper half of a 64-dim row's tile is padding)
       if (used) {
+#pragma unroll 1
         for (int m = 0; m < kTi; ++m) {
-#pragma unroll
-          for (int c = 0; c < kC; c += 16) {
+#pragma unroll 1
+          for (int c = gc; c < gc + 32; c += 16) {
             float o[16];
             if (nb > 0) {
-              tmem_ld_x16(o_tmem + lane_off + N * m + cb + c, o);
+              tmem_ld_x16(o_tmem + lane_off + N * m + c, o);
               tmem_wait_ld_regs16(o);
             } else {
 #pragma unroll
               for (int j = 0; j < 16; ++j) o[j] = 0.f;
             }
-            if (part.way != kPgWhole) {
+            if (way != kPgWhole) {
               if (dims) {
-                float* to = p.partial + (place * N + cb + c) * D + 128 * m + r;
+                float* to = p.partial + (place * N + c) * D + 128 * m + dim;
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                  if (cb + c + j < un.cols) __stcg(to + j * D, o[j]);
+                  if (c + j < un.cols) __stcg(to + j * D, o[j]);
               }
               continue;
             }
             // Neighbouring lanes (dims) trade halves of a pair of columns, so that each stores two dims of one: 64
             // contiguous bytes per column and warp.
             const bool second = (lane & 1) != 0;
-            uint16_t* dst = p.out + (row0 + cb + c + (second ? 1 : 0)) * D + 128 * m + (r & ~1);
+            uint16_t* dst = p.out + (static_cast<int64_t>(un.row0) + c + (second ? 1 : 0)) * D + 128 * m + (dim & ~1);
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
-              const float2 f = *reinterpret_cast<const float2*>(alpha_s + cb + c + j);
+              const float2 f = *reinterpret_cast<const float2*>(alpha_s + c + j);
               const __nv_bfloat162 two = __floats2bfloat162_rn(o[j] * f.x, o[j + 1] * f.y);
               const uint32_t w = *reinterpret_cast<const uint32_t*>(&two);
               const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 1);
               const uint32_t own = second ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
-              if (dims && cb + c + j + (second ? 1 : 0) < un.cols)
-                *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(j) * D) = own;
+              if (dims && c + j + (second ? 1 : 0) < un.cols) *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(j) * D) = own;
             }
           }
         }
@@ -892,7 +1261,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         mbar_arrive(o_empty);
         mbar_arrive(&part_empty[n & 1]);
       }
-      named_bar_sync(kTcEpiBar, kPgSoftThreads);  // alpha_s, max_s and P's place are written anew by the next part
+      named_bar_sync(kTcEpiBar, kPgSoft);  // alpha_s, neg_s and P's place are written anew by the next part
     }
   }
 
@@ -905,75 +1274,116 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 // ------------------------------------------------------------------------------------ shared units
 
 constexpr int kPgJoinThreads = 128;
-constexpr int kPgMaxCtas = 512;  // CTAs that may share a unit
+constexpr int kPgJoinWarps = kPgJoinThreads / 32;
+constexpr int kPgMaxCtas = 512;    // CTAs that may share a unit
+constexpr int kPgFewParts = 8;     // up to so many parts a warp joins by itself
 
-// Joins the parts of the units that several CTAs shared: block (i, j) the columns j, j + gridDim.y, ... of the i-th entry.
+// Joins the parts of the units that several CTAs shared: block (i, j) an equal share j of the i-th entry's columns and pieces of
+// 128 dims.  A warp takes one such item, four dims a lane (two at D = 64); where the parts are many, a block does, a quarter of
+// them a warp.  The loads of eight parts are in flight at a time.
 template <int D>
 __global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedAttnParams p) {
   constexpr int N = paged_cols(D);
-  __shared__ float w_s[kPgMaxCtas];
-  __shared__ float red_s[kPgJoinThreads / 32];
+  constexpr int kPieces = D >= 128 ? D / 128 : 1;
+  constexpr int kEach = D >= 128 ? 4 : 2;  // dims of a lane
+  __shared__ float acc_s[kPgJoinWarps][32 * kEach];
+  __shared__ float stat_s[kPgJoinWarps][2];
   wait_stream();
   const int4 e = __ldcg(p.shared + blockIdx.x);
   const int parts = min(e.z, kPgMaxCtas);
   if (parts <= 0) return;
-  const PagedUnit un = paged_unit(p, e.x, N);
-  const int64_t row0 = static_cast<int64_t>(un.t0) * p.H + un.h0;
+  const PagedUnit un = paged_unit(p, e.x);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // part k of the unit: the end of the first CTA's piece, the beginnings of the others'
   const auto place = [&](int k) { return 2 * (static_cast<int64_t>(e.y) + k) + (k == 0 ? 1 : 0); };
-  for (int c = blockIdx.y; c < un.cols; c += gridDim.y) {
-    float top = kPgNoBound;
-    for (int k = threadIdx.x; k < parts; k += kPgJoinThreads) {
-      const float m = __ldcg(p.stats + place(k) * 2 * N + c);
-      w_s[k] = m;
-      top = fmaxf(top, m);
-    }
+  const bool few = parts <= kPgFewParts;
+  const int k0 = few ? 0 : parts * warp / kPgJoinWarps, k1 = few ? parts : parts * (warp + 1) / kPgJoinWarps;
+  const int items = un.cols * kPieces, step = static_cast<int>(gridDim.y) * (few ? kPgJoinWarps : 1);
+  for (int item = static_cast<int>(blockIdx.y) * (few ? kPgJoinWarps : 1) + (few ? warp : 0); item < items; item += step) {
+    const int c = item / kPieces, d = (item % kPieces) * 128 + lane * kEach;
+    float top = kPgNoBound, sum = 0.f;
+    float acc[kEach];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) red_s[warp] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(red_s[0], red_s[1]), fmaxf(red_s[2], red_s[3]));
-    float sum = 0.f;
-    for (int k = threadIdx.x; k < parts; k += kPgJoinThreads) {
-      const float m = w_s[k];
-      const float f = m == kPgNoBound ? 0.f : exp2f(m - top);
-      const float l = __ldcg(p.stats + place(k) * 2 * N + N + c);
-      sum += l != l ? l : l * f;  // (a sum that is no number stays one, whatever its part weighs)
-      w_s[k] = f;
-    }
+    for (int i = 0; i < kEach; ++i) acc[i] = 0.f;
+    constexpr int kAhead = 8;
+    for (int kb = k0; kb < k1; kb += kAhead) {
+      float v[kAhead][kEach];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    __syncthreads();
-    if (lane == 0) red_s[warp] = sum;
-    __syncthreads();
-    sum = (red_s[0] + red_s[1]) + (red_s[2] + red_s[3]);
-    const int h = p.groups > 1 ? un.h0 + c : c % p.H;
-    const float f = paged_factor(top, sum, p.sink, h, p.lse != nullptr && threadIdx.x == 0 ? p.lse + row0 + c : nullptr);
-    for (int d = 4 * threadIdx.x; d < D; d += 4 * kPgJoinThreads) {
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      constexpr int kAhead = 8;  // parts in flight
-      for (int k0 = 0; k0 < parts; k0 += kAhead) {
-        float4 v[kAhead];
+      for (int k = 0; k < kAhead; ++k) {
+        if (kb + k < k1) {
+          const float* from = p.partial + (place(kb + k) * N + c) * D + d;
+          if constexpr (kEach == 4) {
+            const float4 w = __ldcg(reinterpret_cast<const float4*>(from));
+            v[k][0] = w.x, v[k][1] = w.y, v[k][2] = w.z, v[k][3] = w.w;
+          } else {
+            const float2 w = __ldcg(reinterpret_cast<const float2*>(from));
+            v[k][0] = w.x, v[k][1] = w.y;
+          }
+        } else {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (k0 + k < parts) v[k] = __ldcg(reinterpret_cast<const float4*>(p.partial + (place(k0 + k) * N + c) * D + d));
-        }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const float w = k0 + k < parts ? w_s[k0 + k] : 0.f;
-          acc.x = fmaf(v[k].x, w, acc.x);
-          acc.y = fmaf(v[k].y, w, acc.y);
-          acc.z = fmaf(v[k].z, w, acc.z);
-          acc.w = fmaf(v[k].w, w, acc.w);
+          for (int i = 0; i < kEach; ++i) v[k][i] = 0.f;
         }
       }
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f), hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-      *reinterpret_cast<uint2*>(p.out + (row0 + c) * D + d) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      // lanes 0 to 7: bounds and sums of these parts
+      float m = kPgNoBound, l = 0.f;
+      if (lane < kAhead && kb + lane < k1) {
+        m = __ldcg(p.stats + place(kb + lane) * 2 * N + c);
+        l = __ldcg(p.stats + place(kb + lane) * 2 * N + N + c);
+      }
+      float most = m;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      most = fmaxf(top, __shfl_sync(0xffffffffu, most, 0));
+      const float back = top == kPgNoBound ? 0.f : exp2f(top - most);
+      top = most;
+      const float f = m == kPgNoBound ? 0.f : exp2f(m - top);
+      float s = l != l ? l : l * f;  // (a sum that is no number stays one, whatever its part weighs)
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      sum = (sum != sum ? sum : sum * back) + __shfl_sync(0xffffffffu, s, 0);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) acc[i] *= back;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float w = __shfl_sync(0xffffffffu, f, k);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) acc[i] = fmaf(v[k][i], w, acc[i]);
+      }
     }
-    __syncthreads();
+    if (!few) {  // (the whole block is here)
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) acc_s[warp][lane * kEach + i] = acc[i];
+      if (lane == 0) {
+        stat_s[warp][0] = top;
+        stat_s[warp][1] = sum;
+      }
+      __syncthreads();
+      if (warp != 0) continue;
+      float most = kPgNoBound;
+#pragma unroll
+      for (int w = 0; w < kPgJoinWarps; ++w) most = fmaxf(most, stat_s[w][0]);
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) acc[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kPgJoinWarps; ++w) {
+        const float m = stat_s[w][0], l = stat_s[w][1];
+        const float f = m == kPgNoBound ? 0.f : exp2f(m - most);
+        sum += l != l ? l : l * f;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) acc[i] = fmaf(acc_s[w][lane * kEach + i], f, acc[i]);
+      }
+      top = most;
+    }
+    const float f = paged_factor(top, sum, p.sink, (un.skip + c) % p.H,
+                                 p.lse != nullptr && item % kPieces == 0 && lane == 0 ? p.lse + un.row0 + c : nullptr);
+    uint16_t* out = p.out + (static_cast<int64_t>(un.row0) + c) * D + d;
+#pragma unroll
+    for (int i = 0; i < kEach; i += 2) {
+      const __nv_bfloat162 two = __floats2bfloat162_rn(acc[i] * f, acc[i + 1] * f);
+      *reinterpret_cast<uint32_t*>(out + i) = *reinterpret_cast<const uint32_t*>(&two);
+    }
   }
 }
 
