@@ -32,6 +32,7 @@
 #include <cuda_bf16.h>
 
 #include "attn_kv4_kernel.cuh"
+#include "kv4_codec_kernel.cuh"
 #include "paged.cuh"
 
 namespace dsa {
@@ -39,6 +40,7 @@ namespace dsa {
 constexpr int kPgFirstSoft = 3;           // first softmax warp: the three before issue, load and scout
 constexpr int kPgSoftWarps = 8;
 constexpr int kPgSoft = 32 * kPgSoftWarps;
+constexpr int kPgQWarp = kPgFirstSoft + kPgSoftWarps;  // brings q
 constexpr int kPgSlots = 8;               // blocks whose pages are looked up ahead
 constexpr int kPgBatch = 4;               // blocks looked up at a time
 constexpr int kPgMaxTokens = 32;          // tokens of a unit: a lane of the scout each
@@ -49,7 +51,7 @@ constexpr float kPgNoBound = -3e38f;      // bound of a column without rows so f
 __host__ __device__ constexpr int paged_cols(int D) { return D == 512 ? 64 : 128; }
 __host__ __device__ constexpr int paged_block(int D) { return D == 512 ? 64 : 128; }
 // What a unit costs beside its blocks, and the least piece of the line of a CTA (joining a part takes about as long), in blocks.
-__host__ __device__ constexpr int paged_unit_cost(int D) { return D == 512 ? 3 : 2; }
+__host__ __device__ constexpr int paged_unit_cost(int D) { return 4; }
 __host__ __device__ constexpr int paged_min_piece(int D) { return D == 512 ? 4 : 2; }
 
 // What the load and softmax warps know of a block.
@@ -60,7 +62,8 @@ struct PagedBlock {
   int starts;      // the first block of its tokens here
   uint32_t pages;  // bit i: page i of the block is there
   int id[8];       // pages of the block
-  int pad[2];
+  int tail;        // rows from this on nobody sees (they may never have been written)
+  int pad[1];
 };
 
 // What the CTA does of a unit.
@@ -77,7 +80,7 @@ struct PagedLayout {
   static constexpr bool kByRow = D <= 256;                           // a softmax thread has a row of q (else a row of the block)
   static constexpr int kCols = paged_cols(D);
   static constexpr int kKeys = paged_block(D);
-  static constexpr int kThreads = 32 * (kPgFirstSoft + kPgSoftWarps);
+  static constexpr int kThreads = 32 * (kPgQWarp + 1);
   static constexpr int kChunks = D / 64;
   static constexpr int kTiles = D >= 128 ? D / 128 : 1;              // tiles of a block
   static constexpr int kTileChunks = kChunks / kTiles;
@@ -89,8 +92,8 @@ struct PagedLayout {
   static constexpr int kQBytes = kChunks * kQChunkBytes;
   static constexpr int kKv = 0;
   static constexpr int kQ = kKv + kRing * kTileBytes;
-  static constexpr int kP = kQ + kQBufs * kQBytes;                // not by row: bf16 [rows][64 columns]
-  static constexpr int kNeg = kP + (kByRow ? 0 : kKeys * kCols * 2);  // float [cols] the running bounds (log2 units); not by row: negated
+  static constexpr int kP = kQ + kQBufs * kQBytes;                // not by row: two of bf16 [rows][64 columns]
+  static constexpr int kNeg = kP + (kByRow ? 0 : 2 * kKeys * kCols * 2);  // float [cols] the running bounds (log2 units); not by row: negated
   static constexpr int kAlpha = kNeg + kCols * 4;                 // float [cols] rescale / output factors; by row: [2][cols] sums
   static constexpr int kTop = kAlpha + (kByRow ? 2 : 1) * kCols * 4;  // not by row: int [cols] largest scores, being reduced
   static constexpr int kEnd = kTop + (kByRow ? 0 : 1) * kCols * 4;    // int [2][tokens] by unit: rows below this are seen
@@ -99,15 +102,16 @@ struct PagedLayout {
   static constexpr int kPlan = kParts + 2 * static_cast<int>(sizeof(PagedPart));            // int [8]
   static constexpr int kScan = kPlan + 32;                        // int64 [warps]
   static constexpr int kBar = kScan + 96;
-  static constexpr int kNumBars = 22 + 2 * kPgSlots + 2 * kRing;
+  static constexpr int kNumBars = 25 + 2 * kPgSlots + 2 * kRing;
   static constexpr int kSmem = kBar + kNumBars * 8;
   // softmax warps that read a block, or fill a P
   static constexpr int kReaders = kByRow ? kPgSoftWarps / 2 : kPgSoftWarps;
-  // tensor memory: two S (or S^T) from column 0, O (or O^T) tile m behind them
+  // tensor memory: S (or S^T) of some blocks from column 0, O (or O^T) tile m behind them
+  static constexpr int kScores = D <= 128 ? 3 : 2;
   static constexpr int kSCols = kByRow ? kKeys : kCols;
   static constexpr int kOTile = kByRow ? (D < 128 ? D : 128) : kCols;
-  static_assert(2 * kSCols + kTiles * kOTile <= 512, "tensor memory");
-  static_assert(kRing >= 2 * kTiles, "the next block's score product goes before the last one's weighted sum");
+  static_assert(kScores * kSCols + kTiles * kOTile <= 512, "tensor memory");
+  static_assert(kRing >= kScores * kTiles, "the score products go ahead of the weighted sums");
   static_assert(kSmem <= 232448, "shared memory");
 };
 static_assert(sizeof(PagedBlock) == 64 && sizeof(PagedPart) == 16, "layout");
@@ -176,23 +180,31 @@ struct PagedRun {
   }
 };
 
-// Blocks of a unit, by one thread.
+// Blocks of a unit, by one thread (its tokens' sequences and positions are read four at a time).
 __device__ __forceinline__ int paged_blocks(const PagedAttnParams& p, const PagedUnit& u, int size) {
   int n = 0, seq = -1, a, b;
   PagedRun run;
   run.start();
 #pragma unroll 1
-  for (int i = 0; i <= u.n; ++i) {
-    int s = -1, end = 0;
-    if (i < u.n) paged_token(p, u.t0 + i, s, end);
-    if (s != seq || i == u.n) {
-      if (seq >= 0) n += run.blocks(p, size, a, b);
-      run.start();
-      seq = s;
+  for (int i0 = 0; i0 < u.n; i0 += 4) {
+    int s[4], end[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[i] = -1;
+      end[i] = 0;
+      if (i0 + i < u.n) paged_token(p, u.t0 + i0 + i, s[i], end[i]);
     }
-    if (s >= 0) run.add(p, end);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (s[i] != seq) {
+        if (seq >= 0) n += run.blocks(p, size, a, b);
+        run.start();
+        seq = s[i];
+      }
+      if (s[i] >= 0) run.add(p, end[i]);
+    }
   }
-  return n;
+  return seq >= 0 ? n + run.blocks(p, size, a, b) : n;
 }
 
 // Factor of a column's outputs whose weights' bound is m (log2 units) and whose denominator is l, in units of 2^m,
@@ -251,6 +263,28 @@ __device__ __forceinline__ void xpose_reduce(float (&v)[kN], int lane, Op op) {
   }
 }
 
+// Whether the phase of the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// Ties 32 destination registers of tensor-memory loads to the wait for them.
+__device__ __forceinline__ void tmem_wait_ld_regs32(float* v) {
+  tmem_wait_ld_regs16(v);
+  uint32_t* r = reinterpret_cast<uint32_t*>(v + 16);
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
 // tcgen05.mma kind::f16 with the A operand in tensor memory, issued where `on` is set.
 __device__ __forceinline__ void mma_f16_ts_if(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -297,17 +331,17 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t* q_full = bars + 0;      // [2]
   uint64_t* q_empty = bars + 2;     // [2]
-  uint64_t* pv_done = bars + 5;
   uint64_t* o_empty = bars + 6;
   uint64_t* drain = bars + 7;
   uint64_t* part_full = bars + 8;   // [2]
   uint64_t* part_empty = bars + 10; // [2]
-  uint64_t* s_full = bars + 12;     // [2]
-  uint64_t* p_full = bars + 16;     // [2]; not by row: [1]
+  uint64_t* s_full = bars + 12;     // [scores]
+  uint64_t* p_full = bars + 16;     // [2] of even and odd blocks
   uint64_t* decided = bars + 18;    // [4] by row: bounds of a quarter's rows
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint64_t* blk_full = bars + 22;   // [slots]
+  uint64_t* pv_done = bars + 22;    // [scores]
+  uint64_t* blk_full = bars + 25;   // [slots]
   uint64_t* blk_empty = blk_full + kPgSlots;
   uint64_t* kv_full = blk_empty + kPgSlots;  // [ring]
   uint64_t* kv_empty = kv_full + kRing;
@@ -323,22 +357,24 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   if (threadIdx.x < 2 * sizeof(PagedPart) / 4) reinterpret_cast<int*>(part_s)[threadIdx.x] = 0;
   if (!L::kByRow && threadIdx.x < N) top_s[threadIdx.x] = ordered(-INFINITY);
   if (threadIdx.x == 0) {
-    mbar_init(pv_done, 1);
     mbar_init(o_empty, kPgSoftWarps);
     mbar_init(drain, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&part_full[i], 1);
-      mbar_init(&part_empty[i], 2 + kPgSoftWarps);
+      mbar_init(&part_empty[i], 3 + kPgSoftWarps);
       mbar_init(&p_full[i], L::kReaders);
-      mbar_init(&s_full[i], 1);
-    }
+      }
     for (int i = 0; i < kPgSlots; ++i) {
       mbar_init(&blk_full[i], 1);
       mbar_init(&blk_empty[i], 1 + L::kReaders);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&decided[i], 1);
+    for (int i = 0; i < L::kScores; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&pv_done[i], 1);
+    }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
@@ -360,11 +396,21 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   // has at least one of its blocks) and belongs to those, too, whose pieces its blocks reach into.
   constexpr int kUnitCost = paged_unit_cost(D);
   int64_t* warp_scan = reinterpret_cast<int64_t*>(smem + L::kScan);  // [warps]
+  // Each unit's blocks, kept in the ring's place (where they fit: 32768 units are prompts of 65536 tokens and 64 heads).
+  constexpr int kKeep = L::kQ / 4;
+  int* blocks_s = reinterpret_cast<int*>(kv_s);
+  const bool keep = p.units <= kKeep;
+  if (keep) {
+#pragma unroll 1
+    for (int u = static_cast<int>(threadIdx.x); u < p.units; u += kThreads) blocks_s[u] = paged_blocks(p, paged_unit(p, u), kKeys);
+    __syncthreads();
+  }
+  const auto blocks_of = [&](int u) { return keep ? blocks_s[u] : paged_blocks(p, paged_unit(p, u), kKeys); };
   const int u_first = static_cast<int>(static_cast<int64_t>(p.units) * threadIdx.x / kThreads);
   const int u_last = static_cast<int>(static_cast<int64_t>(p.units) * (threadIdx.x + 1) / kThreads);
   int64_t mine = 0;
 #pragma unroll 1
-  for (int u = u_first; u < u_last; ++u) mine += paged_blocks(p, paged_unit(p, u), kKeys) + kUnitCost;
+  for (int u = u_first; u < u_last; ++u) mine += blocks_of(u) + kUnitCost;
   int64_t upto = mine;  // the line up to the end of this thread's units
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -389,7 +435,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     if (at <= from || upto >= to) {
 #pragma unroll 1
       for (int u = u_first; u < u_last; ++u) {
-        const int nb = paged_blocks(p, paged_unit(p, u), kKeys);
+        const int nb = blocks_of(u);
         const int64_t next = at + nb + kUnitCost;
         if (at <= from && from < next) {
           plan_s[0] = u;
@@ -407,12 +453,13 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       }
     }
   }
+  fence_proxy_async_shared();  // (the copies write where the blocks were)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tbase = *tmem_slot;
   const uint32_t s_tmem = tbase;
-  const uint32_t o_tmem = tbase + 2 * L::kSCols;
+  const uint32_t o_tmem = tbase + L::kScores * L::kSCols;
   const bool idle = from >= to;
   const int unit0 = idle ? 0 : plan_s[0], unit1 = idle ? -1 : plan_s[3];
   const int from_block = plan_s[1], to_block = plan_s[4];
@@ -540,6 +587,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
               blk.i1 = i1;
               blk.pages = have;
               blk.starts = k0 + j == k_first;
+              blk.tail = min(run.high - row, kKeys);
               blk.full = whole && have == want && row <= all_end - kKeys && (row >= all_low || row <= p.first - kKeys);
             }
             __syncwarp();
@@ -560,7 +608,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ load
-    uint32_t gb = 0, nq = 0;  // blocks and q's of this CTA so far
+    uint32_t gb = 0;          // blocks of this CTA so far
     uint32_t tile = 0;        // tiles whose copies were issued
     const int page_rows = 1 << p.pages.log_rows;
     const int pages = kKeys >> p.pages.log_rows > 0 ? kKeys >> p.pages.log_rows : 1;
@@ -575,17 +623,6 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       if (lane == 0) mbar_arrive(&part_empty[n & 1]);
       if (u < 0) break;
       if (nb == 0) continue;
-      // a place for q is free once the score products of the part that had it are done
-      const uint32_t qb = nq % kQb;
-      if (nq >= kQb) paged_wait(&q_empty[qb], (nq / kQb - 1) & 1u, abort_flag, err, 0x84);
-      if (gone()) break;
-      ++nq;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&q_full[qb], L::kQBytes);
-        const int y = paged_unit(p, u).row0;
-        for (int c = 0; c < kCh; ++c) tma_load_2d(q_s + qb * L::kQBytes + c * L::kQChunkBytes, &qmap, &q_full[qb], 64 * c, y);
-      }
-      __syncwarp();
       for (int b = 0; ok && b < nb; ++b, ++gb) {
         const uint32_t slot = gb % kPgSlots;
         paged_wait(&blk_full[slot], (gb / kPgSlots) & 1u, abort_flag, err, 0x85);
@@ -617,9 +654,34 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       }
     }
     if (gone()) {  // copies in flight land before the CTA ends
-      for (uint32_t i = nq > kQb ? nq - kQb : 0; i < nq; ++i) mbar_wait_drain(&q_full[i % kQb], (i / kQb) & 1u);
       for (uint32_t i = tile > kRing ? tile - kRing : 0; i < tile; ++i) mbar_wait_drain(&kv_full[i % kRing], (i / kRing) & 1u);
     }
+  } else if (warp == kPgQWarp) {
+    // ------------------------------------------------------------------ load of q
+    uint32_t nq = 0;
+    for (int n = 0;; ++n) {
+      paged_wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x87);
+      if (gone()) break;
+      const int u = part_s[n & 1].unit;
+      const int nb = part_s[n & 1].blocks;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&part_empty[n & 1]);
+      if (u < 0) break;
+      if (nb == 0) continue;
+      // a place for q is free once the score products of the part that had it are done
+      const uint32_t qb = nq % kQb;
+      if (nq >= kQb) paged_wait(&q_empty[qb], (nq / kQb - 1) & 1u, abort_flag, err, 0x84);
+      if (gone()) break;
+      ++nq;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full[qb], L::kQBytes);
+        const int y = paged_unit(p, u).row0;
+        for (int c = 0; c < kCh; ++c) tma_load_2d(q_s + qb * L::kQBytes + c * L::kQChunkBytes, &qmap, &q_full[qb], 64 * c, y);
+      }
+      __syncwarp();
+    }
+    if (gone())  // copies in flight land before the CTA ends
+      for (uint32_t i = nq > kQb ? nq - kQb : 0; i < nq; ++i) mbar_wait_drain(&q_full[i % kQb], (i / kQb) & 1u);
   } else if (warp == 0) {
     // ------------------------------------------------------------------ MMA issuer (the whole warp, one thread elected)
     const uint32_t on = elect_one();
@@ -633,102 +695,118 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     const uint64_t q_k = desc_sw128(smem_addr(q_s), 16, 1024);                  // K-major: columns x dims
     const uint64_t kv_mn = desc_sw128(smem_addr(kv_s), L::kChunkBytes, 1024);   // MN-major: dims x rows
     const uint64_t p_mn = desc_sw128(smem_addr(p_s), kKeys * 128, 1024);        // MN-major: columns x rows
-    // the score products go one block ahead of the weighted sums, across parts
-    int n = 0, left = 0;             // parts taken; blocks of the last one whose scores are still to come
-    uint32_t gs = 0, nq = 0;         // blocks scored, q's used
+    // Score products and weighted sums are issued as what they need comes in: a block's weighted sum when its weights are
+    // there, the scores of up to kScores blocks further on, across parts, when most of its rows are.
+    int n = 0, left = 0;              // parts taken; blocks of the last one whose scores are still to come
+    uint32_t gs = 0, gb = 0, nq = 0;  // blocks scored, blocks summed, q's used
+    bool fresh_q = false;
     uint32_t q_at = 0;
-    bool ended = false, failed = false;
-    int part_no = 0;                 // units so far
-    // Scores the next block; false where there is none, or where the look ahead met a part without blocks: what comes
-    // after that is made known only when the part before it is done, which takes the weighted sum still to be issued.
-    const auto score = [&](int& opens, bool ahead) -> bool {  // opens: the part's number where the block is its first, else 0
-      opens = 0;
-      while (left == 0) {
-        if (ended) return false;
-        if (!wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, 0x90)) {
-          failed = true;
-          return false;
-        }
-        const int u = __shfl_sync(0xffffffffu, part_s[n & 1].unit, 0);
-        left = __shfl_sync(0xffffffffu, part_s[n & 1].blocks, 0);
+    bool ended = false, ok = true;
+    uint32_t part_no = 0;             // units so far
+    uint32_t opens = 0;               // four bits for each scored block: whether it is its part's first, whether not of the first part, the part's parity
+    // A value of the warp by a reduction, whose result the compiler knows to be the same for all lanes: so addresses and
+    // descriptors stay in uniform registers (without it an instruction took 80 cycles to issue, longer than to run).
+    const auto uniform = [](uint32_t v) { return __reduce_max_sync(0xffffffffu, v); };
+    const auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
+    // Takes the next part, or scores the next block; false where neither can be done now.
+    const auto score = [&]() -> bool {
+      if (left == 0) {
+        if (ended || !ready(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u)) return false;
+        const int u = __reduce_max_sync(0xffffffffu, part_s[n & 1].unit);
+        left = __reduce_max_sync(0xffffffffu, part_s[n & 1].blocks);
         if (lane == 0) mbar_arrive(&part_empty[n & 1]);
         __syncwarp();
         ++n;
         if (u < 0) {
           ended = true;
-          return false;
+          left = 0;
+        } else {
+          ++part_no;
+          if (left > 0) {
+            opens |= (1u | (part_no > 1 ? 2u : 0u) | ((part_no & 1u) << 2)) << (4 * (gs - gb));
+            q_at = nq % kQb;
+            ++nq;
+            fresh_q = true;  // (its q may still have to come)
+          }
         }
-        ++part_no;
-        if (left == 0) {
-          if (ahead) return false;
-          continue;
-        }
-        q_at = nq % kQb;
-        if (!wait(&q_full[q_at], (nq / kQb) & 1u, 0x91)) {
-          failed = true;
-          return false;
-        }
-        ++nq;
-        opens = part_no;
+        return true;
       }
-      const uint32_t to = s_tmem + L::kSCols * (gs & 1u);
-      const uint64_t q = q_k + q_at * (L::kQBytes >> 4);
+      if (gs - gb >= L::kScores) return false;
+      const uint32_t t0 = gs * kTi, early = t0 + (kTi > 2 ? kTi - 2 : kTi - 1);  // a tile whose rows come among the last
+      if (!ready(&kv_full[early % kRing], (early / kRing) & 1u)) return false;
+      if (fresh_q && !ready(&q_full[q_at], ((nq - 1) / kQb) & 1u)) return false;
+      fresh_q = false;
+      const uint32_t to = uniform(s_tmem + L::kSCols * (gs % L::kScores));
+      const uint64_t q = q_k + uniform(q_at * (L::kQBytes >> 4));
 #pragma unroll
       for (int m = 0; m < kTi; ++m) {
-        const uint32_t tile = gs * kTi + m, at = tile % kRing;
-        if (!wait(&kv_full[at], (tile / kRing) & 1u, 0x92)) {
-          failed = true;
-          return false;
-        }
+        const uint32_t at = (t0 + m) % kRing;
+        if (!wait(&kv_full[at], ((t0 + m) / kRing) & 1u, 0x92)) return false;
         tc_fence_after_sync();
-        const uint64_t a = kv_k + at * (L::kTileBytes >> 4);
+        const uint64_t a = kv_k + uniform(at * (L::kTileBytes >> 4));
 #pragma unroll
-        for (int k = 0; k < (D == 64 ? 4 : 8); ++k) {
+        for (int k = 0; k < 4 * L::kTileChunks; ++k) {
           const uint64_t kv = a + (((k / 4) * L::kChunkBytes + (k % 4) * 32) >> 4);
-          const uint64_t qd = q + (((2 * m + k / 4) * L::kQChunkBytes + (k % 4) * 32) >> 4);
+          const uint64_t qd = q + (((m * L::kTileChunks + k / 4) * L::kQChunkBytes + (k % 4) * 32) >> 4);
           if (m == 0 && k == 0)
             mma_f16_if<false>(on, to, L::kByRow ? qd : kv, L::kByRow ? kv : qd, id_qk, 0u);
           else
             mma_f16_if<true>(on, to, L::kByRow ? qd : kv, L::kByRow ? kv : qd, id_qk);
         }
       }
-      mma_commit_if(on, &s_full[gs & 1u]);
+      mma_commit_if(on, &s_full[gs % L::kScores]);
       ++gs;
       if (--left == 0) mma_commit_if(on, &q_empty[q_at]);
       return true;
     };
-    uint32_t gb = 0;
-    int opens, next_opens;
-    bool more = score(opens, false);
-    while (more) {
-      more = score(next_opens, true);
-      if (failed) break;
-      if (!(L::kByRow ? wait(&p_full[gb & 1u], (gb >> 1) & 1u, 0x93) : wait(p_full, gb & 1u, 0x93))) break;
-      // a part's first weighted sum overwrites O: the output of the part before must be read
-      if (opens > 1 && !wait(o_empty, static_cast<uint32_t>(opens) & 1u, 0x94)) break;
-      tc_fence_after_sync();
-      const uint32_t add = opens != 0 ? 0u : 1u;
+    uint64_t since = 0;          // when nothing could be done first
+    uint32_t idle_rounds = 0;
+    while (ok && !(ended && gs == gb)) {
+      if (gs != gb && ready(&p_full[gb & 1u], (gb >> 1) & 1u)) {
+        // a part's first weighted sum overwrites O: the output of the part before must be read
+        if ((opens & 3u) == 3u && !wait(o_empty, (opens >> 2) & 1u, 0x94)) break;
+        tc_fence_after_sync();
+        const uint32_t add = (opens & 1u) != 0u ? 0u : 1u;
+        const uint32_t weights_at = uniform(s_tmem + L::kSCols * (gb % L::kScores));                 // by row
+        const uint64_t weights_desc = p_mn + uniform((gb & 1u) * (kKeys * 128 >> 4));                // not by row
 #pragma unroll
-      for (int m = 0; m < kTi; ++m) {
-        const uint32_t at = (gb * kTi + m) % kRing;
-        const uint64_t a = kv_mn + at * (L::kTileBytes >> 4);
+        for (int m = 0; m < kTi; ++m) {
+          const uint32_t at = (gb * kTi + m) % kRing;
+          const uint64_t a = kv_mn + uniform(at * (L::kTileBytes >> 4));
 #pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks) {
-          const uint64_t kv = a + ((ks * 16 * 128) >> 4);
-          if constexpr (L::kByRow)
-            mma_f16_ts_if(on, o_tmem + L::kOTile * m, s_tmem + L::kSCols * (gb & 1u) + 8 * ks, kv, id_pv, ks == 0 ? add : 1u);
-          else if (ks == 0)
-            mma_f16_if<false>(on, o_tmem + L::kOTile * m, kv, p_mn + ((ks * 16 * 128) >> 4), id_pv, add);
-          else
-            mma_f16_if<true>(on, o_tmem + L::kOTile * m, kv, p_mn + ((ks * 16 * 128) >> 4), id_pv);
+          for (int ks = 0; ks < kKeys / 16; ++ks) {
+            const uint64_t kv = a + ((ks * 16 * 128) >> 4);
+            if constexpr (L::kByRow) {
+              mma_f16_ts_if(on, o_tmem + L::kOTile * m, weights_at + 8 * ks, kv, id_pv, ks == 0 ? add : 1u);
+            } else {
+              const uint64_t pd = weights_desc + ((ks * 16 * 128) >> 4);
+              if (ks == 0)
+                mma_f16_if<false>(on, o_tmem + L::kOTile * m, kv, pd, id_pv, add);
+              else
+                mma_f16_if<true>(on, o_tmem + L::kOTile * m, kv, pd, id_pv);
+            }
+          }
+          mma_commit_if(on, &kv_empty[at]);
         }
-        mma_commit_if(on, &kv_empty[at]);
+        mma_commit_if(on, &pv_done[gb % L::kScores]);
+        ++gb;
+        opens >>= 4;
+        since = 0;
+      } else if (score()) {
+        since = 0;
+      } else if (++idle_rounds % 64 == 0) {  // (the timer takes long to read)
+        const uint64_t now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
+        if (since == 0) since = now;
+        if (gone()) {
+          ok = false;
+        } else if (now - since > kWaitLimitNs) {
+          if (lane == 0) {
+            record_timeout(err, 0x93);
+            *abort_flag = 1;
+          }
+          ok = false;
+        }
       }
-      mma_commit_if(on, pv_done);
-      ++gb;
-      if (!more && !ended) more = score(next_opens, false);
-      if (failed) break;
-      opens = next_opens;
     }
     // every MMA issued by this thread has completed once `drain` flips
     mma_commit_if(on, drain);
@@ -743,13 +821,13 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     const int quarter = warp & 3;               // tensor-memory lane quarter
     const int r = quarter * 32 + lane;          // the unit's row
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t s_at = s_tmem + L::kSCols * group + lane_off;
-    const float to_log2 = p.scale * 1.4426950408889634f;
+    // (a scale of 0 is taken as the least number, so that what is masked stays minus infinity)
+    const float to_log2 = p.scale == 0.f ? 1.17549435e-38f : p.scale * 1.4426950408889634f;
     const uint64_t to_log2_2 = pack_f32x2(to_log2, to_log2);
     volatile float* bound_s = neg_s;                                  // [N]
     float* sum_s = alpha_s;                                           // [2][N]
     uint32_t gb0 = 0;                                                 // blocks of the parts before
-    float x[32];
+    float x[kKeys];                                                   // the row's scores, exponents, weights
     for (int n = 0;; ++n) {
       paged_wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0xA0);
       const int nb = part_s[n & 1].blocks;
@@ -769,6 +847,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         const bool full = __any_sync(0xffffffffu, blk.full != 0) != 0;
         const bool mine = token >= blk.i0 && token < blk.i1;
         const uint32_t there = blk.pages;
+        const int tail = blk.tail;
         __syncwarp();
         if (lane == 0) mbar_arrive(&blk_empty[slot]);
         // The block's rows [32 i, 32 i + 32) that this row sees.
@@ -784,74 +863,99 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
           }
           return m;
         };
-        paged_wait(&s_full[group], (gb >> 1) & 1u, abort_flag, err, 0xA2);
+        const uint32_t s_at = s_tmem + L::kSCols * (gb % L::kScores) + lane_off;
+        paged_wait(&s_full[gb % L::kScores], (gb / L::kScores) & 1u, abort_flag, err, 0xA2);
         tc_fence_after_sync();
+        if (tail < kKeys) {  // rows that may never have been written: weights of 0 times what is no number would be none
+          for (int c = 0; c < kCh; ++c) {
+            const uint32_t tile = gb * kTi + c / L::kTileChunks;
+            uint8_t* chunk = kv_s + (tile % kRing) * L::kTileBytes + (c % L::kTileChunks) * L::kChunkBytes;
+            for (int i = tail * 128 + ((warp - kPgFirstSoft) & 3) * 512 + lane * 16; i < L::kChunkBytes; i += 2048)
+              *reinterpret_cast<uint4*>(chunk + i) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_shared();
+        }
         // the largest score
         float top = -INFINITY;
-        bool odd = false;  // a score that is no number in a block that not every row of q sees all of
         if (used) {
-#pragma unroll 1
-          for (int i = 0; i < kKeys / 32; ++i) {
-            tmem_ld_x32_sync(s_at + 32 * i, x);
-            if (!full) {
-              uint64_t none = 0ull;  // is a number where every score is
 #pragma unroll
-              for (int c = 0; c < 32; c += 2) none = fma_f32x2(pack_f32x2(x[c], x[c + 1]), 0ull, none);
-              float n0, n1;
-              unpack_f32x2(none, n0, n1);
-              odd |= n0 != n0 || n1 != n1;
-              const uint32_t mask = mask_of(i);
+          for (int i = 0; i < kKeys; i += 32) tmem_ld_x32(s_at + i, x + i);
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if ((mask & (1u << c)) == 0u) x[c] = to_log2 < 0.f ? INFINITY : -INFINITY;
+          for (int i = 0; i < kKeys; i += 32) tmem_wait_ld_regs32(x + i);
+          if (!full) {
+            if (tail < kKeys) {
+#pragma unroll
+              for (int c = 0; c < kKeys; ++c)
+                if (c >= tail) x[c] = 0.f;
             }
-            if (to_log2 < 0.f) {
+            uint64_t none = 0ull;  // is a number where every score is
 #pragma unroll
-              for (int c = 0; c < 32; ++c) x[c] = -x[c];
-            }
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) top = max3(top, x[c], x[c + 1]);
-          }
-          if (__any_sync(0xffffffffu, odd)) {
-            // Weights of 0 times values that are no numbers would still be none.  So the kv rows that hold such are zeroed (by each
-            // warp that finds them: all four of the group do), and rows of q that see such a score get a sum that is none.
-            bool sees = false;
+            for (int c = 0; c < kKeys; c += 2) none = fma_f32x2(pack_f32x2(x[c], x[c + 1]), 0ull, none);
+            float n0, n1;
+            unpack_f32x2(none, n0, n1);
+            if (__any_sync(0xffffffffu, n0 != n0 || n1 != n1)) {
+              // Weights of 0 times values that are no numbers would still be none.  So the kv rows that hold such are zeroed (by each
+              // warp that finds them: all four of the group do), and rows of q that see such a score get a sum that is none.
+              bool sees = false;
 #pragma unroll 1
-            for (int i = 0; i < kKeys / 32; ++i) {
-              tmem_ld_x32_sync(s_at + 32 * i, x);
-              const uint32_t mask = mask_of(i);
-              uint32_t is = 0u;
+              for (int i = 0; i < kKeys; i += 16) {
+                float y[16];
+                tmem_ld_x16(s_at + i, y);
+                tmem_wait_ld_regs16(y);
+                uint32_t is = 0u;
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!(fabsf(x[c]) < INFINITY)) is |= 1u << c;
-              sees |= (is & mask) != 0u;
-              is = __reduce_or_sync(0xffffffffu, is);
-              while (is != 0u) {
-                const int key = 32 * i + __ffs(is) - 1;
-                is &= is - 1u;
-                bool bad = false;
-#pragma unroll 1
-                for (int j = lane; j < kCh * 8; j += 32) {
-                  const uint32_t tile = gb * kTi + (j / 8) / L::kTileChunks;
-                  paged_wait(&kv_full[tile % kRing], (tile / kRing) & 1u, abort_flag, err, 0xA6);
-                  const uint4 v = *reinterpret_cast<const uint4*>(kv_s + (tile % kRing) * L::kTileBytes + ((j / 8) % L::kTileChunks) * L::kChunkBytes +
-                                                                  key * 128 + (j % 8) * 16);
-                  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) bad |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
-                }
-                if (__any_sync(0xffffffffu, bad)) {
+                for (int c = 0; c < 16; ++c)
+                  if (i + c < tail && !(fabsf(y[c]) < INFINITY)) is |= 1u << c;
+                sees |= (is & (mask_of(i / 32) >> (i & 16))) != 0u;
+                is = __reduce_or_sync(0xffffffffu, is);
+                while (is != 0u) {
+                  const int key = i + __ffs(is) - 1;
+                  is &= is - 1u;
+                  const auto at = [&](int j) -> uint4* {  // piece j of the row
+                    const uint32_t tile = gb * kTi + (j / 8) / L::kTileChunks;
+                    paged_wait(&kv_full[tile % kRing], (tile / kRing) & 1u, abort_flag, err, 0xA6);
+                    return reinterpret_cast<uint4*>(kv_s + (tile % kRing) * L::kTileBytes + ((j / 8) % L::kTileChunks) * L::kChunkBytes + key * 128) + j % 8;
+                  };
+                  bool bad = false;
 #pragma unroll 1
                   for (int j = lane; j < kCh * 8; j += 32) {
-                    const uint32_t tile = gb * kTi + (j / 8) / L::kTileChunks;
-                    *reinterpret_cast<uint4*>(kv_s + (tile % kRing) * L::kTileBytes + ((j / 8) % L::kTileChunks) * L::kChunkBytes + key * 128 +
-                                              (j % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 v = *at(j);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) bad |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
+                  }
+                  if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll 1
+                    for (int j = lane; j < kCh * 8; j += 32) *at(j) = make_uint4(0u, 0u, 0u, 0u);
                   }
                 }
               }
+              if (sees) l0 = __int_as_float(0x7FFFFFFF);
+              fence_proxy_async_shared();
             }
-            if (sees) l0 = __int_as_float(0x7FFFFFFF);
-            fence_proxy_async_shared();
+            const float hidden = to_log2 < 0.f ? INFINITY : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kKeys; i += 32) {
+              const uint32_t mask = mask_of(i / 32);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if ((mask & (1u << c)) == 0u) x[i + c] = hidden;
+            }
+          }
+          float t[4] = {x[0], x[1], x[2], x[3]};
+          if (to_log2 < 0.f) {
+#pragma unroll
+            for (int c = 4; c < kKeys; ++c) t[c & 3] = fminf(t[c & 3], x[c]);
+            top = -fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
+          } else {
+#pragma unroll
+            for (int c = 4; c + 8 <= kKeys; c += 8) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) t[k] = max3(t[k], x[c + k], x[c + 4 + k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[k] = fmaxf(t[k], x[kKeys - 4 + k]);
+            top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
           }
         }
         // the bound: raised only when exceeded by more than 2^8, behind the decision on the block before
@@ -866,20 +970,22 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         if (lane == 0) mbar_arrive(&decided[quarter]);
         const bool moved = bound != before && before != kPgNoBound;
         if (__any_sync(0xffffffffu, used && moved)) {  // the accumulators of the blocks before follow
-          paged_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0xA3);
+          // (these scores came behind the weighted sum kScores blocks before, so the phase waited for is the barrier's next)
+          paged_wait(&pv_done[(gb - 1) % L::kScores], ((gb - 1) / L::kScores) & 1u, abort_flag, err, 0xA3);
           tc_fence_after_sync();
-          const float f = moved ? exp2f(before - bound) : 1.f;
+          const float f = moved ? exp2_approx(before - bound) : 1.f;
 #pragma unroll 1
           for (int c = 0; c < kTi * L::kOTile; c += 16) {
-            tmem_ld_x16(o_tmem + lane_off + c, x);
-            tmem_wait_ld_regs16(x);
+            float o[16];
+            tmem_ld_x16(o_tmem + lane_off + c, o);
+            tmem_wait_ld_regs16(o);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] *= f;
-            tmem_st_x16(o_tmem + lane_off + c, x);
+            for (int j = 0; j < 16; ++j) o[j] *= f;
+            tmem_st_x16(o_tmem + lane_off + c, o);
           }
         }
         if (bound != l_bound) {
-          const float f = l_bound == kPgNoBound ? 0.f : exp2f(l_bound - bound);
+          const float f = l_bound == kPgNoBound ? 0.f : exp2_approx(l_bound - bound);
           l0 = l_bound == kPgNoBound && l0 == l0 ? 0.f : l0 * f;
           l1 = l_bound == kPgNoBound ? 0.f : l1 * f;
           l_bound = bound;
@@ -887,30 +993,22 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         // weights, as bf16 in the place of the scores
         if (used) {
           const uint64_t neg2 = pack_f32x2(-bound, -bound);
-          uint64_t l2 = pack_f32x2(l0, l1);
-#pragma unroll 1
-          for (int i = 0; i < kKeys / 32; ++i) {
-            tmem_ld_x32_sync(s_at + 32 * i, x);
+          uint64_t l2[2] = {pack_f32x2(l0, l1), 0ull};
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 32) {
             uint32_t pk[16];
-            const uint32_t mask = full ? 0xFFFFFFFFu : mask_of(i);
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) unpack_f32x2(fma_f32x2(pack_f32x2(x[c], x[c + 1]), to_log2_2, neg2), x[c], x[c + 1]);
-            if (!full) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if ((mask & (1u << c)) == 0u) x[c] = -INFINITY;
-            }
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
+            for (int c = i; c < i + 32; c += 2) {
+              unpack_f32x2(fma_f32x2(pack_f32x2(x[c], x[c + 1]), to_log2_2, neg2), x[c], x[c + 1]);
               x[c] = exp2_approx(x[c]);
               x[c + 1] = exp2_approx(x[c + 1]);
-              l2 = add_f32x2(l2, pack_f32x2(x[c], x[c + 1]));
+              l2[(c / 2) & 1] = add_f32x2(l2[(c / 2) & 1], pack_f32x2(x[c], x[c + 1]));
               const __nv_bfloat162 w = __floats2bfloat162_rn(x[c], x[c + 1]);
-              pk[c / 2] = *reinterpret_cast<const uint32_t*>(&w);
+              pk[(c - i) / 2] = *reinterpret_cast<const uint32_t*>(&w);
             }
-            tmem_st_words_x16(s_at + 16 * i, pk);
+            tmem_st_words_x16(s_at + i / 2, pk);
           }
-          unpack_f32x2(l2, l0, l1);
+          unpack_f32x2(add_f32x2(l2[0], l2[1]), l0, l1);
           tmem_wait_st();
         }
         tc_fence_before_sync();
@@ -920,10 +1018,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       gb0 += nb;
       // the part's end: the two threads' sums in units of the row's last bound
       named_bar_sync(kTcEpiBar, kPgSoft);
-      // (a wait is for a phase or the one before it: both groups have seen the scores of their last blocks, so all weighted sums
-      // but the last two are done)
-      if (nb > 1) paged_wait(pv_done, (gb0 - 2) & 1u, abort_flag, err, 0xA5);
-      if (nb > 0) paged_wait(pv_done, (gb0 - 1) & 1u, abort_flag, err, 0xA5);
+      if (nb > 0) paged_wait(&pv_done[(gb0 - 1) % L::kScores], ((gb0 - 1) / L::kScores) & 1u, abort_flag, err, 0xA5);
       tc_fence_after_sync();
       float bound = kPgNoBound;
       if (nb > 0) bound = bound_s[r];
@@ -943,12 +1038,13 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         }
       }
       if (used) {
-        // half of the dims for each of the row's two threads
+        // half of the dims for each of the row's two threads, whole sectors at a time where they are aligned
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0u;
         uint16_t* out = p.out + (static_cast<int64_t>(un.row0) + r) * D;
         float* part = p.partial + (place * N + r) * D;
 #pragma unroll 1
         for (int d = group * (D / 2); d < (group + 1) * (D / 2); d += 16) {
-          float* o = x;
+          float o[16];
           if (nb > 0) {
             tmem_ld_x16(o_tmem + lane_off + d, o);
             tmem_wait_ld_regs16(o);
@@ -963,8 +1059,12 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
               const __nv_bfloat162 two = __floats2bfloat162_rn(o[j] * f, o[j + 1] * f);
               w[j / 2] = *reinterpret_cast<const uint32_t*>(&two);
             }
-            reinterpret_cast<uint4*>(out + d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            reinterpret_cast<uint4*>(out + d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            if (wide) {
+              st_32(out + d, w);
+            } else {
+              reinterpret_cast<uint4*>(out + d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(out + d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           } else if (r < un.cols) {
 #pragma unroll
             for (int j = 0; j < 16; j += 4) __stcg(reinterpret_cast<float4*>(part + d + j), make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]));
@@ -994,11 +1094,10 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const float to_log2 = p.scale * 1.4426950408889634f;
     const uint64_t to_log2_2 = pack_f32x2(to_log2, to_log2);
-    uint8_t* p_row = p_s + (cb / 64) * (kKeys * 128);
     uint32_t gb = 0;
     uint64_t lsum[kC / 2];
     float x[kC];          // scores or weights of its columns
-    bool p_zero = false;  // this warp's part of P is zero
+    uint32_t p_zero = 0u;  // bit i: this warp's part of P of even (odd) blocks is zero
     const auto load = [&](uint32_t at) {
       tmem_ld_half_x16(at, x);
       tmem_wait_ld_regs16(x);
@@ -1029,6 +1128,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         const int row = blk.row + r;
         const int i0 = max(blk.i0, i_first), i1 = min(blk.i1 - 1, i_last);
         const bool here = ((blk.pages >> (r >> p.pages.log_rows)) & 1u) != 0;
+        const int tail = blk.tail;
         __syncwarp();
         if (lane == 0) mbar_arrive(&blk_empty[slot]);
         const bool some = __any_sync(0xffffffffu, used && i0 <= i1) != 0;  // some of this warp's columns are the block's
@@ -1045,15 +1145,23 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
           }
         }
         const uint32_t s_at = s_tmem + N * (gb & 1u) + lane_off + gc;
+        uint8_t* p_row = p_s + (gb & 1u) * (kKeys * 128);  // (the weighted sum two blocks before came before these scores)
         paged_wait(&s_full[gb & 1u], (gb >> 1) & 1u, abort_flag, err, 0xA2);
         tc_fence_after_sync();
+        if (tail < kKeys) {  // rows that may never have been written: weights of 0 times what is no number would be none
+          for (int c = 0; c < kCh; ++c) {
+            uint8_t* chunk = kv_s + ((gb * kTi + c / 2) % kRing) * L::kTileBytes + (c & 1) * L::kChunkBytes;
+            for (int i = tail * 128 + etid * 16; i < L::kChunkBytes; i += kPgSoft * 16) *reinterpret_cast<uint4*>(chunk + i) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        const bool checks = !full && r < tail;  // whether scores that are no numbers matter
         // weights by the bounds as they are, 0 where a column does not see the row, written into the bf16 row P[row r]; x keeps
         // them.  True where an exponent exceeds its bound by more than 2^8, or a score is no number in a block that not every
         // column sees all of.
         const auto weights = [&]() {
           load(s_at);
           uint64_t none = 0ull;  // is a number where every score is
-          if (!full) {
+          if (checks) {
 #pragma unroll
             for (int c = 0; c < kC; c += 2) none = fma_f32x2(pack_f32x2(x[c], x[c + 1]), 0ull, none);
           }
@@ -1079,14 +1187,12 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
               pk[i / 2] = *reinterpret_cast<const uint32_t*>(&w0);
               pk[i / 2 + 1] = *reinterpret_cast<const uint32_t*>(&w1);
             }
-            *reinterpret_cast<uint4*>(p_row + swz128(r, 2 * (cb % 64 + c))) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            *reinterpret_cast<uint4*>(p_row + swz128(r, 2 * (cb + c))) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
           float n0, n1;
           unpack_f32x2(none, n0, n1);
           return over > kTcLazyLog2 || n0 != n0 || n1 != n1;
         };
-        // (the weighted sum before has read P)
-        if (gb > 0) paged_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0xA4);
         bool raise = starts_run;
         if (some && !starts_run) raise = weights();
         if (bar_or(kTcEpiBar, kPgSoft, raise)) {
@@ -1097,7 +1203,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
             load(s_at);
 #pragma unroll
             for (int c = 0; c < kC; ++c) {
-              odd |= !full && !(fabsf(x[c]) < INFINITY);
+              odd |= checks && !(fabsf(x[c]) < INFINITY);
               x[c] = ((mask >> c) & 1u) != 0u ? x[c] * to_log2 : -INFINITY;
             }
             xpose_reduce<kC>(x, lane, [](float v, float w) { return fmaxf(v, w); });
@@ -1155,7 +1261,9 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
           }
           moved = bar_or(kTcEpiBar, kPgSoft, moved);
           if (moved && b > 0) {
-            // sums and output accumulators of earlier blocks follow
+            // sums and output accumulators of earlier blocks follow (these scores came behind the weighted sum kScores blocks
+            // before, so the phase waited for is the barrier's next)
+            paged_wait(&pv_done[(gb - 1) % L::kScores], ((gb - 1) / L::kScores) & 1u, abort_flag, err, 0xA3);
             tc_fence_after_sync();
             if (used) {
 #pragma unroll
@@ -1176,27 +1284,27 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
           if (some) weights();
         }
         if (some) {
-          p_zero = false;
-        } else if (used && !p_zero) {
-          p_zero = true;
+          p_zero &= ~(1u << (gb & 1u));
+        } else if (used && ((p_zero >> (gb & 1u)) & 1u) == 0u) {
+          p_zero |= 1u << (gb & 1u);
 #pragma unroll
-          for (int c = 0; c < kC; c += 8) *reinterpret_cast<uint4*>(p_row + swz128(r, 2 * (cb % 64 + c))) = make_uint4(0u, 0u, 0u, 0u);
+          for (int c = 0; c < kC; c += 8) *reinterpret_cast<uint4*>(p_row + swz128(r, 2 * (cb + c))) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_shared();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+        if (lane == 0) mbar_arrive(&p_full[gb & 1u]);
         if (some) {
 #pragma unroll
           for (int c = 0; c < kC; c += 2) lsum[c / 2] = add_f32x2(lsum[c / 2], pack_f32x2(x[c], x[c + 1]));
         }
       }
       // the part's end: sums over the block's rows (P's place holds the quarters' once it is free)
-      if (nb > 0) paged_wait(pv_done, (gb - 1) & 1u, abort_flag, err, 0xA5);
+      if (nb > 0) paged_wait(&pv_done[(gb - 1) % L::kScores], ((gb - 1) / L::kScores) & 1u, abort_flag, err, 0xA5);
       tc_fence_after_sync();
       named_bar_sync(kTcEpiBar, kPgSoft);
       float* red_s = reinterpret_cast<float*>(p_s);  // [4][N]
-      p_zero = false;
+      p_zero = 0u;
 #pragma unroll
       for (int c = 0; c < kC; c += 2) unpack_f32x2(lsum[c / 2], x[c], x[c + 1]);
       xpose_reduce<kC>(x, lane, [](float v, float w) { return v + w; });
