@@ -9,6 +9,10 @@
 // a run's blocks are masked for the other tokens.  (An instruction of N = 128 columns takes 64 cycles, one of 64 takes
 // 48: idle columns cost little.)
 //
+// Where sequences have several tokens each, two CTAs of a cluster take a unit of 2 N rows: their blocks are the same, and each
+// brings half of a block's rows to both (multicast).  What a block reads through L2 is otherwise the limit: 64 KB of 64 rows at
+// D = 512 for 1,900 cycles of products is 10 TB/s over all SMs.
+//
 // All blocks of all units, and for each unit a constant for its q and output, lie on one line that is cut into as
 // many equal pieces as there are CTAs; each CTA finds its piece by a scan over the units.  So one long sequence
 // uses all SMs, a batch of uneven ones keeps them equally busy, and a prompt's units go out whole but for one at
@@ -37,10 +41,10 @@
 
 namespace dsa {
 
-constexpr int kPgFirstSoft = 3;           // first softmax warp: the three before issue, load and scout
+constexpr int kPgFirstSoft = 3;           // first softmax warp: the three before issue the two products, and scout
 constexpr int kPgSoftWarps = 8;
 constexpr int kPgSoft = 32 * kPgSoftWarps;
-constexpr int kPgQWarp = kPgFirstSoft + kPgSoftWarps;  // brings q
+constexpr int kPgFirstLoad = kPgFirstSoft + kPgSoftWarps;  // first loading warp
 constexpr int kPgSlots = 8;               // blocks whose pages are looked up ahead
 constexpr int kPgBatch = 4;               // blocks looked up at a time
 constexpr int kPgMaxTokens = 32;          // tokens of a unit: a lane of the scout each
@@ -80,7 +84,8 @@ struct PagedLayout {
   static constexpr bool kByRow = D <= 256;                           // a softmax thread has a row of q (else a row of the block)
   static constexpr int kCols = paged_cols(D);
   static constexpr int kKeys = paged_block(D);
-  static constexpr int kThreads = 32 * (kPgQWarp + 1);
+  static constexpr int kLoaders = D == 512 ? 4 : 1;                  // loading warps: every kLoaders-th tile is one's
+  static constexpr int kThreads = 32 * (kPgFirstLoad + kLoaders);
   static constexpr int kChunks = D / 64;
   static constexpr int kTiles = D >= 128 ? D / 128 : 1;              // tiles of a block
   static constexpr int kTileChunks = kChunks / kTiles;
@@ -101,7 +106,7 @@ struct PagedLayout {
   static constexpr int kParts = kBlocks + kPgSlots * static_cast<int>(sizeof(PagedBlock));  // PagedPart [2]
   static constexpr int kPlan = kParts + 2 * static_cast<int>(sizeof(PagedPart));            // int [8]
   static constexpr int kScan = kPlan + 32;                        // int64 [warps]
-  static constexpr int kBar = kScan + 96;
+  static constexpr int kBar = kScan + (kThreads / 32 + 1) / 2 * 16;
   static constexpr int kNumBars = 25 + 2 * kPgSlots + 2 * kRing;
   static constexpr int kSmem = kBar + kNumBars * 8;
   // softmax warps that read a block, or fill a P
@@ -116,10 +121,23 @@ struct PagedLayout {
 };
 static_assert(sizeof(PagedBlock) == 64 && sizeof(PagedPart) == 16, "layout");
 
-// mbar_wait with its loop out of line: written out at each of the kernel's waits it made 90 KB of code, and instructions were
-// waited for.
+// mbar_wait with its loop out of line (written out at each of the kernel's waits it made 90 KB of code, and instructions were
+// waited for), and the timer, which takes some hundred cycles to read, only after some rounds.
 __device__ __noinline__ bool paged_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err, int site) {
-  return mbar_wait(bar, parity, abort, err, site);
+  uint64_t since = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    const uint64_t now = global_timer_ns();
+    if (since == 0) since = now;
+    if (now - since > kWaitLimitNs) {
+      record_timeout(err, site);
+      *abort = 1;
+      return false;
+    }
+  }
 }
 __device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err, int site) {
   return mbar_try_wait(bar, parity) || paged_wait_long(bar, parity, abort, err, site);
@@ -263,15 +281,41 @@ __device__ __forceinline__ void xpose_reduce(float (&v)[kN], int lane, Op op) {
   }
 }
 
-// Whether the phase of the given parity has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
+// tma_load_2d issued where `on` is set, by a warp whose operands are the same in all lanes (by lanes of their own, each with its
+// operands, a copy took 200 cycles to issue); kBoth: into the shared memory of both CTAs of a pair, at the same place, its bytes
+// counted on the barrier of each.
+template <bool kBoth>
+__device__ __forceinline__ void tma_load_2d_if(uint32_t on, uint32_t smem_dst, const void* map, uint32_t bar, int x, int y) {
+  if constexpr (kBoth) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4}], [%2], "
+        "%5;\n\t}" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "h"(static_cast<uint16_t>(3)), "r"(on)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(on)
+        : "memory");
+  }
+}
+
+// mbar_arrive_expect_tx where `on` is set.
+__device__ __forceinline__ void mbar_expect_if(uint32_t on, uint32_t bar, uint32_t bytes) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+               "r"(bytes), "r"(on)
+               : "memory");
+}
+
+// mma_commit_if on the barriers of both CTAs of a pair.
+__device__ __forceinline__ void mma_commit_both_if(uint32_t on, uint64_t* bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(smem_addr(bar)),
+      "r"(on), "h"(static_cast<uint16_t>(3))
       : "memory");
-  return done != 0;
 }
 
 // Ties 32 destination registers of tensor-memory loads to the wait for them.
@@ -304,7 +348,9 @@ __device__ __forceinline__ void tmem_st_words_x16(uint32_t taddr, const uint32_t
       : "memory");
 }
 
-template <int D>
+// kPair: clusters of two CTAs take units of 2 N rows, N each, whose blocks are the same: each CTA brings half of a block's
+// rows to both.
+template <int D, bool kPair>
 __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
                       const PagedAttnParams p, unsigned* err) {
@@ -332,7 +378,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   uint64_t* q_full = bars + 0;      // [2]
   uint64_t* q_empty = bars + 2;     // [2]
   uint64_t* o_empty = bars + 6;
-  uint64_t* drain = bars + 7;
+  uint64_t* drain = bars + 4;       // [2]
   uint64_t* part_full = bars + 8;   // [2]
   uint64_t* part_empty = bars + 10; // [2]
   uint64_t* s_full = bars + 12;     // [scores]
@@ -352,23 +398,34 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   }
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
+  // this CTA's rows of a unit
+  const auto own = [&](PagedUnit u) {
+    if constexpr (kPair) {
+      u.row0 += rank * N;
+      u.skip += rank * N;
+      u.cols = min(max(u.cols - rank * N, 0), N);
+    }
+    return u;
+  };
 
   if (threadIdx.x < kPgSlots * sizeof(PagedBlock) / 4) reinterpret_cast<int*>(block_s)[threadIdx.x] = 0;
   if (threadIdx.x < 2 * sizeof(PagedPart) / 4) reinterpret_cast<int*>(part_s)[threadIdx.x] = 0;
   if (!L::kByRow && threadIdx.x < N) top_s[threadIdx.x] = ordered(-INFINITY);
   if (threadIdx.x == 0) {
     mbar_init(o_empty, kPgSoftWarps);
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&part_full[i], 1);
-      mbar_init(&part_empty[i], 3 + kPgSoftWarps);
+      mbar_init(&part_empty[i], 2 + L::kLoaders + kPgSoftWarps);
       mbar_init(&p_full[i], L::kReaders);
       }
     for (int i = 0; i < kPgSlots; ++i) {
       mbar_init(&blk_full[i], 1);
-      mbar_init(&blk_empty[i], 1 + L::kReaders);
+      mbar_init(&blk_empty[i], L::kLoaders + L::kReaders);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&decided[i], 1);
     for (int i = 0; i < L::kScores; ++i) {
@@ -377,7 +434,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], kPair ? 2 : 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -426,8 +483,10 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     if (w < warp) upto += v;
     line += v;
   }
-  const int64_t ctas = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), line / paged_min_piece(D)));
-  const int cta = static_cast<int>(blockIdx.x);
+  // (of a pair: its number, and that of the pairs)
+  const int most_ctas = static_cast<int>(gridDim.x) / (kPair ? 2 : 1);
+  const int64_t ctas = max(static_cast<int64_t>(1), min(static_cast<int64_t>(most_ctas), line / paged_min_piece(D)));
+  const int cta = static_cast<int>(blockIdx.x) / (kPair ? 2 : 1);
   const int64_t from = cta < ctas ? line * cta / ctas : line, to = cta < ctas ? line * (cta + 1) / ctas : line;
   if (from < to && mine > 0 && upto > from && upto - mine < to) {
     // the threads whose units the piece starts or ends on walk over them again
@@ -457,6 +516,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  if constexpr (kPair) cluster_sync_all();  // (the other's barriers are ready, and its shared memory for copies)
   const uint32_t tbase = *tmem_slot;
   const uint32_t s_tmem = tbase;
   const uint32_t o_tmem = tbase + L::kScores * L::kSCols;
@@ -464,11 +524,11 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   const int unit0 = idle ? 0 : plan_s[0], unit1 = idle ? -1 : plan_s[3];
   const int from_block = plan_s[1], to_block = plan_s[4];
   const bool starts = plan_s[2] != 0;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && rank == 0) {
     // entries of the shared units: by unit, written by the CTA that it starts on, where there are no more than CTAs, else by CTA
     const bool shared = !idle && to_block < plan_s[6] && (unit1 > unit0 || starts);
     const int4 entry = shared ? make_int4(unit1, cta, plan_s[5] - cta + 1, 0) : make_int4(0, 0, 0, 0);
-    if (p.units > static_cast<int>(gridDim.x)) {
+    if (p.units > most_ctas) {
       p.shared[cta] = entry;
     } else {
       for (int u = starts ? unit0 : unit0 + 1; u <= unit1; ++u) p.shared[u] = u == unit1 ? entry : make_int4(0, 0, 0, 0);
@@ -556,10 +616,11 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
           const int k = min(k0 + (lane >> 3), k_end - 1);
           return (k < ra ? k : rb + k - ra) * kKeys;
         };
-        const auto look_up = [&](int k0) -> int {  // -1: no page, or none of whose rows [at, at + box) some token of the run sees
+        const int span = min(1 << p.pages.log_rows, kKeys);
+        const auto look_up = [&](int k0) -> int {  // -1: no page, or none of whose rows [at, at + span) some token of the run sees
           if (k0 >= k_end) return -1;
           const int at = first_row(k0) + off, index = at >> p.pages.log_rows;
-          const bool there = is_page && (at < run.some || (at < run.high && at - run.low > -p.box_rows));
+          const bool there = is_page && (at < run.some || (at < run.high && at - run.low > -span));
           int page = -1;
           if (there && index < p.pages.M) page = ld_after_wait(table + index);
           return page;
@@ -606,88 +667,90 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         mbar_arrive(&part_full[n & 1]);
       }
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ load
-    uint32_t gb = 0;          // blocks of this CTA so far
-    uint32_t tile = 0;        // tiles whose copies were issued
+  } else if (warp >= kPgFirstLoad) {
+    // ------------------------------------------------------------------ load (warps that elect a thread)
+    const uint32_t on = elect_one();
+    const int loader = warp - kPgFirstLoad;  // its tiles: loader, loader + kLoaders, ...; q is the first one's
+    const auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
+      return __all_sync(0xffffffffu, paged_wait(bar, parity, abort_flag, err, site)) != 0;
+    };
+    uint32_t gb = 0, nq = 0;                               // blocks and q's of this CTA so far
+    uint32_t at = static_cast<uint32_t>(loader), round = 0;  // its next tile's place in the ring, and how often that was used before
     const int page_rows = 1 << p.pages.log_rows;
-    const int pages = kKeys >> p.pages.log_rows > 0 ? kKeys >> p.pages.log_rows : 1;
+    // Copies of a block and chunk; of a pair, each CTA makes half of them: [box0, box0 + boxes).
+    const int boxes = kKeys / p.box_rows / (kPair ? 2 : 1), box0 = rank * boxes;
     const int none = max(1, p.pages.P << p.pages.log_rows);  // a row behind the last page: the copy fills in zeros
     bool ok = true;
     for (int n = 0; ok; ++n) {
-      paged_wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x83);
-      if (gone()) break;
-      const int u = part_s[n & 1].unit;
-      const int nb = part_s[n & 1].blocks;
-      __syncwarp();
+      if (!wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, 0x83)) break;
+      const int u = __reduce_max_sync(0xffffffffu, part_s[n & 1].unit);
+      const int nb = __reduce_max_sync(0xffffffffu, part_s[n & 1].blocks);
       if (lane == 0) mbar_arrive(&part_empty[n & 1]);
+      __syncwarp();
       if (u < 0) break;
-      if (nb == 0) continue;
+      if (loader == 0 && nb > 0) {
+        // a place for q is free once the score products of the part that had it are done
+        const uint32_t qb = nq % kQb;
+        if (nq >= kQb && !wait(&q_empty[qb], (nq / kQb - 1) & 1u, 0x84)) break;
+        ++nq;
+        const uint32_t bar = smem_addr(&q_full[qb]), to = smem_addr(q_s) + qb * L::kQBytes;
+        const int y = own(paged_unit(p, u)).row0;
+        mbar_expect_if(on, bar, L::kQBytes);
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) tma_load_2d_if<false>(on, to + c * L::kQChunkBytes, &qmap, bar, 64 * c, y);
+      }
       for (int b = 0; ok && b < nb; ++b, ++gb) {
         const uint32_t slot = gb % kPgSlots;
-        paged_wait(&blk_full[slot], (gb / kPgSlots) & 1u, abort_flag, err, 0x85);
-        if (gone()) {
+        if (!wait(&blk_full[slot], (gb / kPgSlots) & 1u, 0x85)) {
           ok = false;
           break;
         }
-        const PagedBlock& blk = block_s[slot];
-        const int i = lane >> 1;  // page of the block
-        int y = none;
-        if (i < pages && blk.id[i & 7] >= 0) y = (blk.id[i & 7] << p.pages.log_rows) + (blk.row & (page_rows - 1));
+        // the row of the pages of the lane's box
+        const int from = (box0 + lane % 8) * p.box_rows, page = block_s[slot].id[(from >> p.pages.log_rows) & 7];
+        const int mine = page >= 0 ? (page << p.pages.log_rows) + ((block_s[slot].row + from) & (page_rows - 1)) : none;
         __syncwarp();
         if (lane == 0) mbar_arrive(&blk_empty[slot]);
-#pragma unroll 1
-        for (int m = 0; m < kTi; ++m) {
-          const uint32_t at = tile % kRing;
-          if (tile >= kRing) paged_wait(&kv_empty[at], (tile / kRing - 1) & 1u, abort_flag, err, 0x86);
-          if (gone()) {
+#pragma unroll
+        for (int m0 = 0; m0 < kTi; m0 += L::kLoaders) {
+          if (round > 0 && !wait(&kv_empty[at], (round - 1) & 1u, 0x86)) {
             ok = false;
             break;
           }
-          ++tile;
-          if (lane == 0) mbar_arrive_expect_tx(&kv_full[at], L::kTileBytes);
-          __syncwarp();
-          const int c = 2 * m + (lane & 1);
-          if (i < pages && (lane & 1) < L::kTileChunks)
-            tma_load_2d(kv_s + at * L::kTileBytes + (lane & 1) * L::kChunkBytes + i * p.box_rows * 128, &kvmap, &kv_full[at], 64 * c, y);
+          const uint32_t bar = smem_addr(&kv_full[at]);
+          uint32_t to = smem_addr(kv_s) + at * L::kTileBytes + box0 * p.box_rows * 128;
+          mbar_expect_if(on, bar, L::kTileBytes);
+#pragma unroll 1
+          for (int i = 0; i < boxes; ++i, to += p.box_rows * 128) {
+            const int y = __shfl_sync(0xffffffffu, mine, i);
+#pragma unroll
+            for (int c = 0; c < L::kTileChunks; ++c)
+              tma_load_2d_if<kPair>(on, to + c * L::kChunkBytes, &kvmap, bar, 64 * (L::kTileChunks * (m0 + loader) + c), y);
+          }
+          at += L::kLoaders;
+          if (at >= kRing) {
+            at -= kRing;
+            ++round;
+          }
         }
       }
     }
     if (gone()) {  // copies in flight land before the CTA ends
-      for (uint32_t i = tile > kRing ? tile - kRing : 0; i < tile; ++i) mbar_wait_drain(&kv_full[i % kRing], (i / kRing) & 1u);
+      if (loader == 0)
+        for (uint32_t i = nq > kQb ? nq - kQb : 0; i < nq; ++i) mbar_wait_drain(&q_full[i % kQb], (i / kQb) & 1u);
+      const uint32_t tiles = gb * kTi;
+      for (uint32_t i = tiles > kRing ? tiles - kRing : 0; i < tiles; ++i) mbar_wait_drain(&kv_full[i % kRing], (i / kRing) & 1u);
     }
-  } else if (warp == kPgQWarp) {
-    // ------------------------------------------------------------------ load of q
-    uint32_t nq = 0;
-    for (int n = 0;; ++n) {
-      paged_wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, err, 0x87);
-      if (gone()) break;
-      const int u = part_s[n & 1].unit;
-      const int nb = part_s[n & 1].blocks;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&part_empty[n & 1]);
-      if (u < 0) break;
-      if (nb == 0) continue;
-      // a place for q is free once the score products of the part that had it are done
-      const uint32_t qb = nq % kQb;
-      if (nq >= kQb) paged_wait(&q_empty[qb], (nq / kQb - 1) & 1u, abort_flag, err, 0x84);
-      if (gone()) break;
-      ++nq;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&q_full[qb], L::kQBytes);
-        const int y = paged_unit(p, u).row0;
-        for (int c = 0; c < kCh; ++c) tma_load_2d(q_s + qb * L::kQBytes + c * L::kQChunkBytes, &qmap, &q_full[qb], 64 * c, y);
-      }
-      __syncwarp();
-    }
-    if (gone())  // copies in flight land before the CTA ends
-      for (uint32_t i = nq > kQb ? nq - kQb : 0; i < nq; ++i) mbar_wait_drain(&q_full[i % kQb], (i / kQb) & 1u);
-  } else if (warp == 0) {
-    // ------------------------------------------------------------------ MMA issuer (the whole warp, one thread elected)
+  } else if (warp < 2) {
+    // ------------------------------------------------------------------ MMA issuers (whole warps, one thread of each elected)
+    // Warp 0 issues the score products, as the rows and a place for the scores come in, warp 1 the weighted sums, as the
+    // weights do: neither waits for what the other needs, and their loops are short.
     const uint32_t on = elect_one();
     const auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
       return __all_sync(0xffffffffu, paged_wait(bar, parity, abort_flag, err, site)) != 0;
     };
+    // A value of the warp by a reduction, whose result the compiler knows to be the same for all lanes: so addresses and
+    // descriptors stay in uniform registers (without it an instruction took 80 cycles to issue, longer than to run).
+    const auto uniform = [](uint32_t v) { return __reduce_max_sync(0xffffffffu, v); };
     // by row: S = Q . KV^T and O += P . KV with P in tensor memory; else S^T = KV . Q^T and O^T += KV^T . P^T
     constexpr uint32_t id_qk = L::kByRow ? idesc_bf16(N, kKeys, false, false) : idesc_bf16(kKeys, N, false, false);
     constexpr uint32_t id_pv = L::kByRow ? idesc_bf16(N, L::kOTile, false, true) : idesc_bf16(128, N, true, true);
@@ -695,122 +758,93 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     const uint64_t q_k = desc_sw128(smem_addr(q_s), 16, 1024);                  // K-major: columns x dims
     const uint64_t kv_mn = desc_sw128(smem_addr(kv_s), L::kChunkBytes, 1024);   // MN-major: dims x rows
     const uint64_t p_mn = desc_sw128(smem_addr(p_s), kKeys * 128, 1024);        // MN-major: columns x rows
-    // Score products and weighted sums are issued as what they need comes in: a block's weighted sum when its weights are
-    // there, the scores of up to kScores blocks further on, across parts, when most of its rows are.
-    int n = 0, left = 0;              // parts taken; blocks of the last one whose scores are still to come
-    uint32_t gs = 0, gb = 0, nq = 0;  // blocks scored, blocks summed, q's used
-    bool fresh_q = false;
-    uint32_t q_at = 0;
-    bool ended = false, ok = true;
-    uint32_t part_no = 0;             // units so far
-    uint32_t opens = 0;               // four bits for each scored block: whether it is its part's first, whether not of the first part, the part's parity
-    // A value of the warp by a reduction, whose result the compiler knows to be the same for all lanes: so addresses and
-    // descriptors stay in uniform registers (without it an instruction took 80 cycles to issue, longer than to run).
-    const auto uniform = [](uint32_t v) { return __reduce_max_sync(0xffffffffu, v); };
-    const auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
-    // Takes the next part, or scores the next block; false where neither can be done now.
-    const auto score = [&]() -> bool {
-      if (left == 0) {
-        if (ended || !ready(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u)) return false;
-        const int u = __reduce_max_sync(0xffffffffu, part_s[n & 1].unit);
-        left = __reduce_max_sync(0xffffffffu, part_s[n & 1].blocks);
-        if (lane == 0) mbar_arrive(&part_empty[n & 1]);
-        __syncwarp();
-        ++n;
-        if (u < 0) {
-          ended = true;
-          left = 0;
-        } else {
-          ++part_no;
-          if (left > 0) {
-            opens |= (1u | (part_no > 1 ? 2u : 0u) | ((part_no & 1u) << 2)) << (4 * (gs - gb));
-            q_at = nq % kQb;
-            ++nq;
-            fresh_q = true;  // (its q may still have to come)
+    uint32_t gb = 0, parts = 0, nq = 0;  // blocks, units and q's so far
+    uint32_t at = 0, round = 0;          // the next tile's place in the ring, and how often it was used before
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      if (!wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, 0x90)) break;
+      const int u = __reduce_max_sync(0xffffffffu, part_s[n & 1].unit);
+      const int nb = __reduce_max_sync(0xffffffffu, part_s[n & 1].blocks);
+      if (lane == 0) mbar_arrive(&part_empty[n & 1]);
+      __syncwarp();
+      if (u < 0) break;
+      ++parts;
+      if (nb == 0) continue;
+      if (warp == 0) {
+        const uint32_t qb = nq % kQb;
+        if (!wait(&q_full[qb], (nq / kQb) & 1u, 0x91)) break;
+        ++nq;
+        const uint64_t q = q_k + uniform(qb * (L::kQBytes >> 4));
+        for (int b = 0; ok && b < nb; ++b, ++gb) {
+          // a place for the scores: by row, where the weights of the block before in it were summed; else, where they were formed
+          if (L::kByRow ? gb >= L::kScores && !wait(&pv_done[gb % L::kScores], (gb / L::kScores - 1) & 1u, 0x92)
+                        : gb >= 2 && !wait(&p_full[gb & 1u], ((gb >> 1) - 1) & 1u, 0x92)) {
+            ok = false;
+            break;
           }
-        }
-        return true;
-      }
-      if (gs - gb >= L::kScores) return false;
-      const uint32_t t0 = gs * kTi, early = t0 + (kTi > 2 ? kTi - 2 : kTi - 1);  // a tile whose rows come among the last
-      if (!ready(&kv_full[early % kRing], (early / kRing) & 1u)) return false;
-      if (fresh_q && !ready(&q_full[q_at], ((nq - 1) / kQb) & 1u)) return false;
-      fresh_q = false;
-      const uint32_t to = uniform(s_tmem + L::kSCols * (gs % L::kScores));
-      const uint64_t q = q_k + uniform(q_at * (L::kQBytes >> 4));
+          const uint32_t to = uniform(s_tmem + L::kSCols * (gb % L::kScores));
 #pragma unroll
-      for (int m = 0; m < kTi; ++m) {
-        const uint32_t at = (t0 + m) % kRing;
-        if (!wait(&kv_full[at], ((t0 + m) / kRing) & 1u, 0x92)) return false;
-        tc_fence_after_sync();
-        const uint64_t a = kv_k + uniform(at * (L::kTileBytes >> 4));
+          for (int m = 0; m < kTi; ++m) {
+            if (!wait(&kv_full[at], round & 1u, 0x93)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint64_t a = kv_k + uniform(at * (L::kTileBytes >> 4));
+            if (++at == kRing) {
+              at = 0;
+              ++round;
+            }
 #pragma unroll
-        for (int k = 0; k < 4 * L::kTileChunks; ++k) {
-          const uint64_t kv = a + (((k / 4) * L::kChunkBytes + (k % 4) * 32) >> 4);
-          const uint64_t qd = q + (((m * L::kTileChunks + k / 4) * L::kQChunkBytes + (k % 4) * 32) >> 4);
-          if (m == 0 && k == 0)
-            mma_f16_if<false>(on, to, L::kByRow ? qd : kv, L::kByRow ? kv : qd, id_qk, 0u);
-          else
-            mma_f16_if<true>(on, to, L::kByRow ? qd : kv, L::kByRow ? kv : qd, id_qk);
-        }
-      }
-      mma_commit_if(on, &s_full[gs % L::kScores]);
-      ++gs;
-      if (--left == 0) mma_commit_if(on, &q_empty[q_at]);
-      return true;
-    };
-    uint64_t since = 0;          // when nothing could be done first
-    uint32_t idle_rounds = 0;
-    while (ok && !(ended && gs == gb)) {
-      if (gs != gb && ready(&p_full[gb & 1u], (gb >> 1) & 1u)) {
-        // a part's first weighted sum overwrites O: the output of the part before must be read
-        if ((opens & 3u) == 3u && !wait(o_empty, (opens >> 2) & 1u, 0x94)) break;
-        tc_fence_after_sync();
-        const uint32_t add = (opens & 1u) != 0u ? 0u : 1u;
-        const uint32_t weights_at = uniform(s_tmem + L::kSCols * (gb % L::kScores));                 // by row
-        const uint64_t weights_desc = p_mn + uniform((gb & 1u) * (kKeys * 128 >> 4));                // not by row
-#pragma unroll
-        for (int m = 0; m < kTi; ++m) {
-          const uint32_t at = (gb * kTi + m) % kRing;
-          const uint64_t a = kv_mn + uniform(at * (L::kTileBytes >> 4));
-#pragma unroll
-          for (int ks = 0; ks < kKeys / 16; ++ks) {
-            const uint64_t kv = a + ((ks * 16 * 128) >> 4);
-            if constexpr (L::kByRow) {
-              mma_f16_ts_if(on, o_tmem + L::kOTile * m, weights_at + 8 * ks, kv, id_pv, ks == 0 ? add : 1u);
-            } else {
-              const uint64_t pd = weights_desc + ((ks * 16 * 128) >> 4);
-              if (ks == 0)
-                mma_f16_if<false>(on, o_tmem + L::kOTile * m, kv, pd, id_pv, add);
+            for (int k = 0; k < 4 * L::kTileChunks; ++k) {
+              const uint64_t kv = a + (((k / 4) * L::kChunkBytes + (k % 4) * 32) >> 4);
+              const uint64_t qd = q + (((m * L::kTileChunks + k / 4) * L::kQChunkBytes + (k % 4) * 32) >> 4);
+              if (m == 0 && k == 0)
+                mma_f16_if<false>(on, to, L::kByRow ? qd : kv, L::kByRow ? kv : qd, id_qk, 0u);
               else
-                mma_f16_if<true>(on, o_tmem + L::kOTile * m, kv, pd, id_pv);
+                mma_f16_if<true>(on, to, L::kByRow ? qd : kv, L::kByRow ? kv : qd, id_qk);
             }
           }
-          mma_commit_if(on, &kv_empty[at]);
+          if (!ok) break;
+          mma_commit_if(on, &s_full[gb % L::kScores]);
         }
-        mma_commit_if(on, &pv_done[gb % L::kScores]);
-        ++gb;
-        opens >>= 4;
-        since = 0;
-      } else if (score()) {
-        since = 0;
-      } else if (++idle_rounds % 64 == 0) {  // (the timer takes long to read)
-        const uint64_t now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
-        if (since == 0) since = now;
-        if (gone()) {
-          ok = false;
-        } else if (now - since > kWaitLimitNs) {
-          if (lane == 0) {
-            record_timeout(err, 0x93);
-            *abort_flag = 1;
+        if (ok) mma_commit_if(on, &q_empty[qb]);  // (after the part's last score product)
+      } else {
+        for (int b = 0; ok && b < nb; ++b, ++gb) {
+          // (a part's first weighted sum overwrites O: the output of the part before must be read)
+          if (!wait(&p_full[gb & 1u], (gb >> 1) & 1u, 0x94) || (b == 0 && parts > 1 && !wait(o_empty, parts & 1u, 0x95))) {
+            ok = false;
+            break;
           }
-          ok = false;
+          tc_fence_after_sync();
+          const uint32_t weights_at = uniform(s_tmem + L::kSCols * (gb % L::kScores));   // by row
+          const uint64_t weights = p_mn + uniform((gb & 1u) * (kKeys * 128 >> 4));       // not by row
+#pragma unroll
+          for (int m = 0; m < kTi; ++m) {
+            const uint64_t a = kv_mn + uniform(at * (L::kTileBytes >> 4));
+#pragma unroll
+            for (int ks = 0; ks < kKeys / 16; ++ks) {
+              const uint64_t kv = a + ((ks * 16 * 128) >> 4);
+              if constexpr (L::kByRow)
+                mma_f16_ts_if(on, o_tmem + L::kOTile * m, weights_at + 8 * ks, kv, id_pv, b > 0 || ks > 0 ? 1u : 0u);
+              else if (ks == 0)
+                mma_f16_if<false>(on, o_tmem + L::kOTile * m, kv, weights + ((ks * 16 * 128) >> 4), id_pv, b > 0 ? 1u : 0u);
+              else
+                mma_f16_if<true>(on, o_tmem + L::kOTile * m, kv, weights + ((ks * 16 * 128) >> 4), id_pv);
+            }
+            if constexpr (kPair)
+              mma_commit_both_if(on, &kv_empty[at]);
+            else
+              mma_commit_if(on, &kv_empty[at]);
+            if (++at == kRing) at = 0;
+          }
+          mma_commit_if(on, &pv_done[gb % L::kScores]);
         }
       }
     }
     // every MMA issued by this thread has completed once `drain` flips
-    mma_commit_if(on, drain);
-    mbar_wait_drain(drain, 0);
+    mma_commit_if(on, &drain[warp]);
+    mbar_wait_drain(&drain[warp], 0);
     __syncwarp();
   } else if constexpr (L::kByRow) {
     // ------------------------------------------------------------------ softmax and output, a thread with a row of q
@@ -833,7 +867,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       const int nb = part_s[n & 1].blocks;
       if (bar_or(kTcEpiBar, kPgSoft, *abort_flag != 0)) break;
       if (part_s[n & 1].unit < 0) break;
-      const PagedUnit un = paged_unit(p, part_s[n & 1].unit);
+      const PagedUnit un = own(paged_unit(p, part_s[n & 1].unit));
       const bool used = quarter * 32 < un.cols;             // (of a quarter without rows nothing is read, written or kept)
       const int token = r < un.cols ? (un.skip + r) / p.H : kPgMaxTokens;
       const int end = token < kPgMaxTokens ? end_s[(n & 1) * kPgMaxTokens + token] : 0;
@@ -970,7 +1004,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         if (lane == 0) mbar_arrive(&decided[quarter]);
         const bool moved = bound != before && before != kPgNoBound;
         if (__any_sync(0xffffffffu, used && moved)) {  // the accumulators of the blocks before follow
-          // (these scores came behind the weighted sum kScores blocks before, so the phase waited for is the barrier's next)
+          // (the last block's scores came behind the weighted sum kScores blocks before it, so the phase is the barrier's next)
           paged_wait(&pv_done[(gb - 1) % L::kScores], ((gb - 1) / L::kScores) & 1u, abort_flag, err, 0xA3);
           tc_fence_after_sync();
           const float f = moved ? exp2_approx(before - bound) : 1.f;
@@ -1027,7 +1061,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       named_bar_sync(kTcEpiBar, kPgSoft);
       const float sum = sum_s[r] + sum_s[N + r];
       const int way = part_s[n & 1].way;
-      const int64_t place = 2 * static_cast<int64_t>(cta) + (way == kPgHead ? 1 : 0);  // of a shared unit's part
+      const int64_t place = 2 * static_cast<int64_t>(blockIdx.x) + (way == kPgHead ? 1 : 0);  // of a shared unit's part
       float f = 1.f;
       if (r < un.cols) {
         if (way == kPgWhole) {
@@ -1114,7 +1148,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       bool used;  // some of this warp's columns are (of others nothing is read, written or kept)
       int skip, i_first, i_last;  // rows before the unit's first in its token; the tokens of this warp's columns
       {
-        const PagedUnit un = paged_unit(p, part_s[n & 1].unit);
+        const PagedUnit un = own(paged_unit(p, part_s[n & 1].unit));
         used = gc < un.cols;
         skip = un.skip;
         i_first = (gc + skip) / p.H;
@@ -1145,7 +1179,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
           }
         }
         const uint32_t s_at = s_tmem + N * (gb & 1u) + lane_off + gc;
-        uint8_t* p_row = p_s + (gb & 1u) * (kKeys * 128);  // (the weighted sum two blocks before came before these scores)
+        uint8_t* p_row = p_s + (gb & 1u) * (kKeys * 128);
         paged_wait(&s_full[gb & 1u], (gb >> 1) & 1u, abort_flag, err, 0xA2);
         tc_fence_after_sync();
         if (tail < kKeys) {  // rows that may never have been written: weights of 0 times what is no number would be none
@@ -1158,6 +1192,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         // weights by the bounds as they are, 0 where a column does not see the row, written into the bf16 row P[row r]; x keeps
         // them.  True where an exponent exceeds its bound by more than 2^8, or a score is no number in a block that not every
         // column sees all of.
+        if (gb >= 2) paged_wait(&pv_done[gb & 1u], ((gb >> 1) - 1) & 1u, abort_flag, err, 0xA4);  // P's place is free
         const auto weights = [&]() {
           load(s_at);
           uint64_t none = 0ull;  // is a number where every score is
@@ -1261,8 +1296,8 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
           }
           moved = bar_or(kTcEpiBar, kPgSoft, moved);
           if (moved && b > 0) {
-            // sums and output accumulators of earlier blocks follow (these scores came behind the weighted sum kScores blocks
-            // before, so the phase waited for is the barrier's next)
+            // sums and output accumulators of earlier blocks follow (the weighted sum of the block two before the last was waited for, so
+            // the phase is the barrier's next)
             paged_wait(&pv_done[(gb - 1) % L::kScores], ((gb - 1) / L::kScores) & 1u, abort_flag, err, 0xA3);
             tc_fence_after_sync();
             if (used) {
@@ -1310,9 +1345,9 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       xpose_reduce<kC>(x, lane, [](float v, float w) { return v + w; });
       red_s[quarter * N + cb + lane % kC] = x[0];
       named_bar_sync(kTcEpiBar, kPgSoft);
-      const PagedUnit un = paged_unit(p, part_s[n & 1].unit);  // (its place is held until the end of the part)
+      const PagedUnit un = own(paged_unit(p, part_s[n & 1].unit));  // (its place is held until the end of the part)
       const int way = part_s[n & 1].way;
-      const int64_t place = 2 * static_cast<int64_t>(cta) + (way == kPgHead ? 1 : 0);  // of a shared unit's part
+      const int64_t place = 2 * static_cast<int64_t>(blockIdx.x) + (way == kPgHead ? 1 : 0);  // of a shared unit's part
       if (etid < un.cols) {
         const float l = (red_s[etid] + red_s[N + etid]) + (red_s[2 * N + etid] + red_s[3 * N + etid]);
         if (way == kPgWhole) {
@@ -1377,6 +1412,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   if (warp == 0) tmem_dealloc(tbase, 512);
+  if constexpr (kPair) cluster_sync_all();  // (copies and arrivals of the other end here)
 }
 
 // ------------------------------------------------------------------------------------ shared units
@@ -1389,7 +1425,7 @@ constexpr int kPgFewParts = 8;     // up to so many parts a warp joins by itself
 // Joins the parts of the units that several CTAs shared: block (i, j) an equal share j of the i-th entry's columns and pieces of
 // 128 dims.  A warp takes one such item, four dims a lane (two at D = 64); where the parts are many, a block does, a quarter of
 // them a warp.  The loads of eight parts are in flight at a time.
-template <int D>
+template <int D, bool kPair>
 __global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedAttnParams p) {
   constexpr int N = paged_cols(D);
   constexpr int kPieces = D >= 128 ? D / 128 : 1;
@@ -1402,13 +1438,17 @@ __global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedA
   if (parts <= 0) return;
   const PagedUnit un = paged_unit(p, e.x);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // part k of the unit: the end of the first CTA's piece, the beginnings of the others'
-  const auto place = [&](int k) { return 2 * (static_cast<int64_t>(e.y) + k) + (k == 0 ? 1 : 0); };
   const bool few = parts <= kPgFewParts;
   const int k0 = few ? 0 : parts * warp / kPgJoinWarps, k1 = few ? parts : parts * (warp + 1) / kPgJoinWarps;
   const int items = un.cols * kPieces, step = static_cast<int>(gridDim.y) * (few ? kPgJoinWarps : 1);
   for (int item = static_cast<int>(blockIdx.y) * (few ? kPgJoinWarps : 1) + (few ? warp : 0); item < items; item += step) {
-    const int c = item / kPieces, d = (item % kPieces) * 128 + lane * kEach;
+    const int row = item / kPieces, d = (item % kPieces) * 128 + lane * kEach;
+    const int c = row % N;  // of the CTA that had it
+    // part k of the unit: the end of the first CTA's (pair's) piece, the beginnings of the others'
+    const auto place = [&](int k) {
+      const int64_t cta = kPair ? 2 * (static_cast<int64_t>(e.y) + k) + row / N : static_cast<int64_t>(e.y) + k;
+      return 2 * cta + (k == 0 ? 1 : 0);
+    };
     float top = kPgNoBound, sum = 0.f;
     float acc[kEach];
 #pragma unroll
@@ -1484,9 +1524,9 @@ __global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedA
       }
       top = most;
     }
-    const float f = paged_factor(top, sum, p.sink, (un.skip + c) % p.H,
-                                 p.lse != nullptr && item % kPieces == 0 && lane == 0 ? p.lse + un.row0 + c : nullptr);
-    uint16_t* out = p.out + (static_cast<int64_t>(un.row0) + c) * D + d;
+    const float f = paged_factor(top, sum, p.sink, (un.skip + row) % p.H,
+                                 p.lse != nullptr && item % kPieces == 0 && lane == 0 ? p.lse + un.row0 + row : nullptr);
+    uint16_t* out = p.out + (static_cast<int64_t>(un.row0) + row) * D + d;
 #pragma unroll
     for (int i = 0; i < kEach; i += 2) {
       const __nv_bfloat162 two = __floats2bfloat162_rn(acc[i] * f, acc[i + 1] * f);
