@@ -84,10 +84,9 @@ int sparse_attn_kv4_smem(int D);
 // How many clusters of `shares` of its CTAs this device runs at a time (0: none of that size; < 0: a CUDA error).
 int sparse_attn_kv4_clusters(int D, int shares);
 
-// bf16 paged cache: attention (D in {64, 128, 256, 512}) by `grid` CTAs and the join of the units that they share; pair:
-// clusters of two take units of twice the rows.  Its maps' boxes are [64 dims][p.box_rows] (a page's rows, paged_attn_block(D)
-// at most, of a pair half of that) and [64 dims][paged_attn_cols(D)].
-cudaError_t launch_paged_attn(int D, bool pair, int grid, const CUtensorMap& kvmap, const CUtensorMap& qmap, const PagedAttnParams& p,
+// bf16 paged cache: attention (D in {64, 128, 256, 512}) by `grid` CTAs and the join of the units that they share; its
+// maps' boxes are [64 dims][p.box_rows] (a page's rows, paged_attn_block(D) at most) and [64 dims][paged_attn_cols(D)].
+cudaError_t launch_paged_attn(int D, int grid, const CUtensorMap& kvmap, const CUtensorMap& qmap, const PagedAttnParams& p,
                               unsigned* err, cudaStream_t stream);
 int paged_attn_smem(int D);
 int paged_attn_cols(int D);   // most columns (token, head) of a unit

@@ -43,6 +43,23 @@ struct PagedAttnParams {
   int first;            // first rows that stay visible
   int box_rows;         // rows of one copy: those of a page, at most a block's
   float scale;
+  uint32_t h_mul;       // n / H = (mulhi(n, h_mul) + n) >> h_shift for 0 <= n < 2^31 (set_heads)
+  int h_shift;
+
+  // 2^h_shift >= H > 2^(h_shift - 1) and h_mul = floor(2^32 (2^h_shift - H) / H) + 1: the quotient's multiplier 2^32 + h_mul lies
+  // above 2^(32 + h_shift) / H by at most 1, which is too little to reach the next whole number for n < 2^32.
+  void set_heads(int heads) {
+    H = heads;
+    h_shift = 0;
+    while ((static_cast<int64_t>(1) << h_shift) < heads) ++h_shift;
+    h_mul = static_cast<uint32_t>((((static_cast<uint64_t>(1) << h_shift) - heads) << 32) / heads + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int by_H(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), h_mul) + static_cast<uint32_t>(n)) >> h_shift);
+  }
+  __device__ __forceinline__ int head(int n) const { return n - by_H(n) * H; }
+#endif
 };
 
 struct VerifyArgs {

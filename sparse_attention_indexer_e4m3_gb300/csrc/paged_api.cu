@@ -23,15 +23,14 @@ dsa_status check_table(PageTable* c, const int32_t* table, int R, int M, int P, 
   return DSA_OK;
 }
 
-// How the (token, head) rows of a call are cut into units of at most N rows, or 2 N.
+// How the (token, head) rows of a call are cut into units of at most N rows.
 struct Units {
   int rows, groups;
   int64_t units;
-  bool pair;  // two CTAs take a unit
 };
 Units units_of(int T, int H, int D, int R) {
   const int N = paged_attn_cols(D);
-  Units u{0, 1, 0, false};
+  Units u{0, 1, 0};
   if (H <= N && T <= R) {
     // Whole tokens: where no two share a sequence, a token in two units would have its rows walked over by both.
     u.rows = std::min(kPagedMaxTokens, N / H) * H;
@@ -40,9 +39,8 @@ Units units_of(int T, int H, int D, int R) {
     u.groups = H / N + (H % N != 0 ? 1 : 0);
     u.rows = H / u.groups + (H % u.groups != 0 ? 1 : 0);
   } else {
-    // Tokens of the same sequence: 2 N rows wherever they begin, by two CTAs (n rows lie in n / H + 2 tokens at most).
-    u.rows = static_cast<int>(std::min<int64_t>(2 * N, static_cast<int64_t>(kPagedMaxTokens - 2) * H));
-    u.pair = true;
+    // Tokens of the same sequence: N rows wherever they begin (n rows lie in n / H + 2 tokens at most).
+    u.rows = static_cast<int>(std::min<int64_t>(N, static_cast<int64_t>(kPagedMaxTokens - 2) * H));
   }
   u.units = u.groups > 1 ? static_cast<int64_t>(T) * u.groups : (static_cast<int64_t>(T) * H + u.rows - 1) / u.rows;
   return u;
@@ -134,16 +132,17 @@ dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* pages, int P, int p
   const Workspace w = workspace_of(D, dev.sms);
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < w.bytes) return DSA_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const int box = std::min(page_rows, paged_attn_block(D) / (un.pair ? 2 : 1));
+  const int box = std::min(page_rows, paged_attn_block(D));
   CUtensorMap kvmap, qmap;
   // (without pages the map is over q, of which no row of a page is read)
   if (!make_bf16_map(&kvmap, P > 0 ? pages : q, P > 0 ? static_cast<int64_t>(P) * page_rows : 1, D, box) ||
       !make_bf16_map(&qmap, q, static_cast<int64_t>(T) * H, D, paged_attn_cols(D)))
     return DSA_ERR_CUDA;
-  const PagedAttnParams p{c, seq, pos, attn_sink, out, lse, reinterpret_cast<float*>(ws + w.partial),
+  PagedAttnParams p{c, seq, pos, attn_sink, out, lse, reinterpret_cast<float*>(ws + w.partial),
                           reinterpret_cast<float*>(ws + w.stats), reinterpret_cast<int4*>(ws), T, H, un.rows, un.groups,
-                          static_cast<int>(un.units), window == 0 ? INT_MAX : window, first, box, scale};
-  return done(launch_paged_attn(D, un.pair, un.pair ? dev.sms / 2 * 2 : dev.sms, kvmap, qmap, p, dev.err, static_cast<cudaStream_t>(stream)));
+                          static_cast<int>(un.units), window == 0 ? INT_MAX : window, first, box, scale, 0u, 0};
+  p.set_heads(H);
+  return done(launch_paged_attn(D, dev.sms, kvmap, qmap, p, dev.err, static_cast<cudaStream_t>(stream)));
 }
 
 dsa_status dsa_verify_drafts(const float* target, const float* draft, const int32_t* tokens, const int32_t* count,

@@ -15,16 +15,16 @@ namespace {
 
 constexpr int kDevices = 64;
 
-template <int D, bool kPair>
-cudaError_t launch_as(int grid, const CUtensorMap& kvmap, const CUtensorMap& qmap, const PagedAttnParams& p, unsigned* err,
-                      cudaStream_t stream) {
+template <int D>
+cudaError_t launch_d(int grid, const CUtensorMap& kvmap, const CUtensorMap& qmap, const PagedAttnParams& p, unsigned* err,
+                     cudaStream_t stream) {
   static std::atomic<bool> set[kDevices];  // (setting it again, from another thread too, changes nothing)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
   if (!set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(paged_attn_kernel<D, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, PagedLayout<D>::kSmem);
+    e = cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PagedLayout<D>::kSmem);
     if (e != cudaSuccess) return e;
     set[dev].store(true, std::memory_order_release);
   }
@@ -33,30 +33,19 @@ cudaError_t launch_as(int grid, const CUtensorMap& kvmap, const CUtensorMap& qma
   c.blockDim = dim3(PagedLayout<D>::kThreads);
   c.dynamicSmemBytes = PagedLayout<D>::kSmem;
   c.stream = stream;
-  cudaLaunchAttribute attr[2] = {};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (the kernels wait for the stream themselves)
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  c.attrs = attr;
-  c.numAttrs = kPair ? 2 : 1;
-  e = cudaLaunchKernelEx(&c, paged_attn_kernel<D, kPair>, kvmap, qmap, p, err);
-  const int pieces = grid / (kPair ? 2 : 1);
-  if (e != cudaSuccess || pieces == 1) return e;  // (one CTA shares nothing)
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (the kernels wait for the stream themselves)
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  e = cudaLaunchKernelEx(&c, paged_attn_kernel<D>, kvmap, qmap, p, err);
+  if (e != cudaSuccess || grid == 1) return e;  // (one CTA shares nothing)
   // the shared units: an entry each, over enough blocks for all SMs where they are few
-  const int entries = std::min(p.units, pieces), items = p.rows * std::max(1, D / 128);
+  const int entries = std::min(p.units, grid), items = p.rows * std::max(1, D / 128);
   c.gridDim = dim3(static_cast<unsigned>(entries), static_cast<unsigned>(std::min(items, std::max(1, 8 * grid / entries))));
   c.blockDim = dim3(kPgJoinThreads);
   c.dynamicSmemBytes = 0;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, paged_join_kernel<D, kPair>, p);
-}
-
-template <int D>
-cudaError_t launch_d(bool pair, int grid, const CUtensorMap& kvmap, const CUtensorMap& qmap, const PagedAttnParams& p, unsigned* err,
-                     cudaStream_t stream) {
-  return pair ? launch_as<D, true>(grid, kvmap, qmap, p, err, stream) : launch_as<D, false>(grid, kvmap, qmap, p, err, stream);
+  return cudaLaunchKernelEx(&c, paged_join_kernel<D>, p);
 }
 
 }  // namespace
@@ -74,13 +63,13 @@ int paged_attn_smem(int D) {
   }
 }
 
-cudaError_t launch_paged_attn(int D, bool pair, int grid, const CUtensorMap& kvmap, const CUtensorMap& qmap, const PagedAttnParams& p,
+cudaError_t launch_paged_attn(int D, int grid, const CUtensorMap& kvmap, const CUtensorMap& qmap, const PagedAttnParams& p,
                               unsigned* err, cudaStream_t stream) {
   switch (D) {
-    case 64: return launch_d<64>(pair, grid, kvmap, qmap, p, err, stream);
-    case 128: return launch_d<128>(pair, grid, kvmap, qmap, p, err, stream);
-    case 256: return launch_d<256>(pair, grid, kvmap, qmap, p, err, stream);
-    case 512: return launch_d<512>(pair, grid, kvmap, qmap, p, err, stream);
+    case 64: return launch_d<64>(grid, kvmap, qmap, p, err, stream);
+    case 128: return launch_d<128>(grid, kvmap, qmap, p, err, stream);
+    case 256: return launch_d<256>(grid, kvmap, qmap, p, err, stream);
+    case 512: return launch_d<512>(grid, kvmap, qmap, p, err, stream);
     default: return cudaErrorInvalidValue;
   }
 }

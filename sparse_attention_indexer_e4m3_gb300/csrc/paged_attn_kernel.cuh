@@ -9,10 +9,6 @@
 // a run's blocks are masked for the other tokens.  (An instruction of N = 128 columns takes 64 cycles, one of 64 takes
 // 48: idle columns cost little.)
 //
-// Where sequences have several tokens each, two CTAs of a cluster take a unit of 2 N rows: their blocks are the same, and each
-// brings half of a block's rows to both (multicast).  What a block reads through L2 is otherwise the limit: 64 KB of 64 rows at
-// D = 512 for 1,900 cycles of products is 10 TB/s over all SMs.
-//
 // All blocks of all units, and for each unit a constant for its q and output, lie on one line that is cut into as
 // many equal pieces as there are CTAs; each CTA finds its piece by a scan over the units.  So one long sequence
 // uses all SMs, a batch of uneven ones keeps them equally busy, and a prompt's units go out whole but for one at
@@ -161,8 +157,8 @@ __device__ __forceinline__ PagedUnit paged_unit(const PagedAttnParams& p, int u)
     r.row0 = u * p.rows;
     r.cols = min(p.rows, p.T * p.H - r.row0);
   }
-  r.t0 = r.row0 / p.H;
-  r.n = (r.row0 + r.cols - 1) / p.H - r.t0 + 1;
+  r.t0 = p.by_H(r.row0);
+  r.n = p.by_H(r.row0 + r.cols - 1) - r.t0 + 1;
   r.skip = r.row0 - r.t0 * p.H;
   return r;
 }
@@ -282,24 +278,13 @@ __device__ __forceinline__ void xpose_reduce(float (&v)[kN], int lane, Op op) {
 }
 
 // tma_load_2d issued where `on` is set, by a warp whose operands are the same in all lanes (by lanes of their own, each with its
-// operands, a copy took 200 cycles to issue); kBoth: into the shared memory of both CTAs of a pair, at the same place, its bytes
-// counted on the barrier of each.
-template <bool kBoth>
+// operands, a copy took 200 cycles to issue).
 __device__ __forceinline__ void tma_load_2d_if(uint32_t on, uint32_t smem_dst, const void* map, uint32_t bar, int x, int y) {
-  if constexpr (kBoth) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
-        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4}], [%2], "
-        "%5;\n\t}" ::"r"(smem_dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "h"(static_cast<uint16_t>(3)), "r"(on)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(smem_dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(on)
-        : "memory");
-  }
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(smem_dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(on)
+      : "memory");
 }
 
 // mbar_arrive_expect_tx where `on` is set.
@@ -307,15 +292,6 @@ __device__ __forceinline__ void mbar_expect_if(uint32_t on, uint32_t bar, uint32
   asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
                "r"(bytes), "r"(on)
                : "memory");
-}
-
-// mma_commit_if on the barriers of both CTAs of a pair.
-__device__ __forceinline__ void mma_commit_both_if(uint32_t on, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(smem_addr(bar)),
-      "r"(on), "h"(static_cast<uint16_t>(3))
-      : "memory");
 }
 
 // Ties 32 destination registers of tensor-memory loads to the wait for them.
@@ -348,9 +324,7 @@ __device__ __forceinline__ void tmem_st_words_x16(uint32_t taddr, const uint32_t
       : "memory");
 }
 
-// kPair: clusters of two CTAs take units of 2 N rows, N each, whose blocks are the same: each CTA brings half of a block's
-// rows to both.
-template <int D, bool kPair>
+template <int D>
 __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
                       const PagedAttnParams p, unsigned* err) {
@@ -398,16 +372,6 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   }
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
-  // this CTA's rows of a unit
-  const auto own = [&](PagedUnit u) {
-    if constexpr (kPair) {
-      u.row0 += rank * N;
-      u.skip += rank * N;
-      u.cols = min(max(u.cols - rank * N, 0), N);
-    }
-    return u;
-  };
 
   if (threadIdx.x < kPgSlots * sizeof(PagedBlock) / 4) reinterpret_cast<int*>(block_s)[threadIdx.x] = 0;
   if (threadIdx.x < 2 * sizeof(PagedPart) / 4) reinterpret_cast<int*>(part_s)[threadIdx.x] = 0;
@@ -434,7 +398,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], kPair ? 2 : 1);
+      mbar_init(&kv_empty[i], 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -483,10 +447,8 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     if (w < warp) upto += v;
     line += v;
   }
-  // (of a pair: its number, and that of the pairs)
-  const int most_ctas = static_cast<int>(gridDim.x) / (kPair ? 2 : 1);
-  const int64_t ctas = max(static_cast<int64_t>(1), min(static_cast<int64_t>(most_ctas), line / paged_min_piece(D)));
-  const int cta = static_cast<int>(blockIdx.x) / (kPair ? 2 : 1);
+  const int64_t ctas = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), line / paged_min_piece(D)));
+  const int cta = static_cast<int>(blockIdx.x);
   const int64_t from = cta < ctas ? line * cta / ctas : line, to = cta < ctas ? line * (cta + 1) / ctas : line;
   if (from < to && mine > 0 && upto > from && upto - mine < to) {
     // the threads whose units the piece starts or ends on walk over them again
@@ -516,7 +478,6 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if constexpr (kPair) cluster_sync_all();  // (the other's barriers are ready, and its shared memory for copies)
   const uint32_t tbase = *tmem_slot;
   const uint32_t s_tmem = tbase;
   const uint32_t o_tmem = tbase + L::kScores * L::kSCols;
@@ -524,11 +485,11 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   const int unit0 = idle ? 0 : plan_s[0], unit1 = idle ? -1 : plan_s[3];
   const int from_block = plan_s[1], to_block = plan_s[4];
   const bool starts = plan_s[2] != 0;
-  if (threadIdx.x == 0 && rank == 0) {
+  if (threadIdx.x == 0) {
     // entries of the shared units: by unit, written by the CTA that it starts on, where there are no more than CTAs, else by CTA
     const bool shared = !idle && to_block < plan_s[6] && (unit1 > unit0 || starts);
     const int4 entry = shared ? make_int4(unit1, cta, plan_s[5] - cta + 1, 0) : make_int4(0, 0, 0, 0);
-    if (p.units > most_ctas) {
+    if (p.units > static_cast<int>(gridDim.x)) {
       p.shared[cta] = entry;
     } else {
       for (int u = starts ? unit0 : unit0 + 1; u <= unit1; ++u) p.shared[u] = u == unit1 ? entry : make_int4(0, 0, 0, 0);
@@ -677,8 +638,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     uint32_t gb = 0, nq = 0;                               // blocks and q's of this CTA so far
     uint32_t at = static_cast<uint32_t>(loader), round = 0;  // its next tile's place in the ring, and how often that was used before
     const int page_rows = 1 << p.pages.log_rows;
-    // Copies of a block and chunk; of a pair, each CTA makes half of them: [box0, box0 + boxes).
-    const int boxes = kKeys / p.box_rows / (kPair ? 2 : 1), box0 = rank * boxes;
+    const int boxes = kKeys / p.box_rows;                    // copies of a block and chunk
     const int none = max(1, p.pages.P << p.pages.log_rows);  // a row behind the last page: the copy fills in zeros
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -694,10 +654,10 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         if (nq >= kQb && !wait(&q_empty[qb], (nq / kQb - 1) & 1u, 0x84)) break;
         ++nq;
         const uint32_t bar = smem_addr(&q_full[qb]), to = smem_addr(q_s) + qb * L::kQBytes;
-        const int y = own(paged_unit(p, u)).row0;
+        const int y = paged_unit(p, u).row0;
         mbar_expect_if(on, bar, L::kQBytes);
 #pragma unroll
-        for (int c = 0; c < kCh; ++c) tma_load_2d_if<false>(on, to + c * L::kQChunkBytes, &qmap, bar, 64 * c, y);
+        for (int c = 0; c < kCh; ++c) tma_load_2d_if(on, to + c * L::kQChunkBytes, &qmap, bar, 64 * c, y);
       }
       for (int b = 0; ok && b < nb; ++b, ++gb) {
         const uint32_t slot = gb % kPgSlots;
@@ -706,7 +666,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
           break;
         }
         // the row of the pages of the lane's box
-        const int from = (box0 + lane % 8) * p.box_rows, page = block_s[slot].id[(from >> p.pages.log_rows) & 7];
+        const int from = lane % 8 * p.box_rows, page = block_s[slot].id[(from >> p.pages.log_rows) & 7];
         const int mine = page >= 0 ? (page << p.pages.log_rows) + ((block_s[slot].row + from) & (page_rows - 1)) : none;
         __syncwarp();
         if (lane == 0) mbar_arrive(&blk_empty[slot]);
@@ -717,14 +677,14 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
             break;
           }
           const uint32_t bar = smem_addr(&kv_full[at]);
-          uint32_t to = smem_addr(kv_s) + at * L::kTileBytes + box0 * p.box_rows * 128;
+          uint32_t to = smem_addr(kv_s) + at * L::kTileBytes;
           mbar_expect_if(on, bar, L::kTileBytes);
 #pragma unroll 1
           for (int i = 0; i < boxes; ++i, to += p.box_rows * 128) {
             const int y = __shfl_sync(0xffffffffu, mine, i);
 #pragma unroll
             for (int c = 0; c < L::kTileChunks; ++c)
-              tma_load_2d_if<kPair>(on, to + c * L::kChunkBytes, &kvmap, bar, 64 * (L::kTileChunks * (m0 + loader) + c), y);
+              tma_load_2d_if(on, to + c * L::kChunkBytes, &kvmap, bar, 64 * (L::kTileChunks * (m0 + loader) + c), y);
           }
           at += L::kLoaders;
           if (at >= kRing) {
@@ -832,10 +792,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
               else
                 mma_f16_if<true>(on, o_tmem + L::kOTile * m, kv, weights + ((ks * 16 * 128) >> 4), id_pv);
             }
-            if constexpr (kPair)
-              mma_commit_both_if(on, &kv_empty[at]);
-            else
-              mma_commit_if(on, &kv_empty[at]);
+            mma_commit_if(on, &kv_empty[at]);
             if (++at == kRing) at = 0;
           }
           mma_commit_if(on, &pv_done[gb % L::kScores]);
@@ -867,9 +824,9 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       const int nb = part_s[n & 1].blocks;
       if (bar_or(kTcEpiBar, kPgSoft, *abort_flag != 0)) break;
       if (part_s[n & 1].unit < 0) break;
-      const PagedUnit un = own(paged_unit(p, part_s[n & 1].unit));
+      const PagedUnit un = paged_unit(p, part_s[n & 1].unit);
       const bool used = quarter * 32 < un.cols;             // (of a quarter without rows nothing is read, written or kept)
-      const int token = r < un.cols ? (un.skip + r) / p.H : kPgMaxTokens;
+      const int token = r < un.cols ? p.by_H(un.skip + r) : kPgMaxTokens;
       const int end = token < kPgMaxTokens ? end_s[(n & 1) * kPgMaxTokens + token] : 0;
       const int low = max(0, end - p.window);
       float l0 = 0.f, l1 = 0.f, l_bound = kPgNoBound;       // this thread's sums, in units of 2^l_bound
@@ -1061,11 +1018,11 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       named_bar_sync(kTcEpiBar, kPgSoft);
       const float sum = sum_s[r] + sum_s[N + r];
       const int way = part_s[n & 1].way;
-      const int64_t place = 2 * static_cast<int64_t>(blockIdx.x) + (way == kPgHead ? 1 : 0);  // of a shared unit's part
+      const int64_t place = 2 * static_cast<int64_t>(cta) + (way == kPgHead ? 1 : 0);  // of a shared unit's part
       float f = 1.f;
       if (r < un.cols) {
         if (way == kPgWhole) {
-          f = paged_factor(bound, sum, p.sink, (un.skip + r) % p.H, p.lse != nullptr && group == 0 ? p.lse + un.row0 + r : nullptr);
+          f = paged_factor(bound, sum, p.sink, p.head(un.skip + r), p.lse != nullptr && group == 0 ? p.lse + un.row0 + r : nullptr);
         } else if (group == 0) {
           __stcg(p.stats + place * 2 * N + r, bound);
           __stcg(p.stats + place * 2 * N + N + r, sum);
@@ -1148,11 +1105,11 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       bool used;  // some of this warp's columns are (of others nothing is read, written or kept)
       int skip, i_first, i_last;  // rows before the unit's first in its token; the tokens of this warp's columns
       {
-        const PagedUnit un = own(paged_unit(p, part_s[n & 1].unit));
+        const PagedUnit un = paged_unit(p, part_s[n & 1].unit);
         used = gc < un.cols;
         skip = un.skip;
-        i_first = (gc + skip) / p.H;
-        i_last = (min(gc + 32, un.cols) - 1 + skip) / p.H;
+        i_first = p.by_H(gc + skip);
+        i_last = p.by_H(max(min(gc + 32, un.cols) - 1, 0) + skip);
       }
       for (int b = 0; b < nb; ++b, ++gb) {
         const uint32_t slot = gb % kPgSlots;
@@ -1345,13 +1302,13 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       xpose_reduce<kC>(x, lane, [](float v, float w) { return v + w; });
       red_s[quarter * N + cb + lane % kC] = x[0];
       named_bar_sync(kTcEpiBar, kPgSoft);
-      const PagedUnit un = own(paged_unit(p, part_s[n & 1].unit));  // (its place is held until the end of the part)
+      const PagedUnit un = paged_unit(p, part_s[n & 1].unit);  // (its place is held until the end of the part)
       const int way = part_s[n & 1].way;
-      const int64_t place = 2 * static_cast<int64_t>(blockIdx.x) + (way == kPgHead ? 1 : 0);  // of a shared unit's part
+      const int64_t place = 2 * static_cast<int64_t>(cta) + (way == kPgHead ? 1 : 0);  // of a shared unit's part
       if (etid < un.cols) {
         const float l = (red_s[etid] + red_s[N + etid]) + (red_s[2 * N + etid] + red_s[3 * N + etid]);
         if (way == kPgWhole) {
-          alpha_s[etid] = paged_factor(-neg_s[etid], l, p.sink, (un.skip + etid) % p.H, p.lse != nullptr ? p.lse + un.row0 + etid : nullptr);
+          alpha_s[etid] = paged_factor(-neg_s[etid], l, p.sink, p.head(un.skip + etid), p.lse != nullptr ? p.lse + un.row0 + etid : nullptr);
         } else {
           __stcg(p.stats + place * 2 * N + etid, -neg_s[etid]);
           __stcg(p.stats + place * 2 * N + N + etid, l);
@@ -1412,7 +1369,6 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   if (warp == 0) tmem_dealloc(tbase, 512);
-  if constexpr (kPair) cluster_sync_all();  // (copies and arrivals of the other end here)
 }
 
 // ------------------------------------------------------------------------------------ shared units
@@ -1425,7 +1381,7 @@ constexpr int kPgFewParts = 8;     // up to so many parts a warp joins by itself
 // Joins the parts of the units that several CTAs shared: block (i, j) an equal share j of the i-th entry's columns and pieces of
 // 128 dims.  A warp takes one such item, four dims a lane (two at D = 64); where the parts are many, a block does, a quarter of
 // them a warp.  The loads of eight parts are in flight at a time.
-template <int D, bool kPair>
+template <int D>
 __global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedAttnParams p) {
   constexpr int N = paged_cols(D);
   constexpr int kPieces = D >= 128 ? D / 128 : 1;
@@ -1438,17 +1394,13 @@ __global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedA
   if (parts <= 0) return;
   const PagedUnit un = paged_unit(p, e.x);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // part k of the unit: the end of the first CTA's piece, the beginnings of the others'
+  const auto place = [&](int k) { return 2 * (static_cast<int64_t>(e.y) + k) + (k == 0 ? 1 : 0); };
   const bool few = parts <= kPgFewParts;
   const int k0 = few ? 0 : parts * warp / kPgJoinWarps, k1 = few ? parts : parts * (warp + 1) / kPgJoinWarps;
   const int items = un.cols * kPieces, step = static_cast<int>(gridDim.y) * (few ? kPgJoinWarps : 1);
   for (int item = static_cast<int>(blockIdx.y) * (few ? kPgJoinWarps : 1) + (few ? warp : 0); item < items; item += step) {
-    const int row = item / kPieces, d = (item % kPieces) * 128 + lane * kEach;
-    const int c = row % N;  // of the CTA that had it
-    // part k of the unit: the end of the first CTA's (pair's) piece, the beginnings of the others'
-    const auto place = [&](int k) {
-      const int64_t cta = kPair ? 2 * (static_cast<int64_t>(e.y) + k) + row / N : static_cast<int64_t>(e.y) + k;
-      return 2 * cta + (k == 0 ? 1 : 0);
-    };
+    const int c = item / kPieces, d = (item % kPieces) * 128 + lane * kEach;
     float top = kPgNoBound, sum = 0.f;
     float acc[kEach];
 #pragma unroll
@@ -1524,9 +1476,9 @@ __global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedA
       }
       top = most;
     }
-    const float f = paged_factor(top, sum, p.sink, (un.skip + row) % p.H,
-                                 p.lse != nullptr && item % kPieces == 0 && lane == 0 ? p.lse + un.row0 + row : nullptr);
-    uint16_t* out = p.out + (static_cast<int64_t>(un.row0) + row) * D + d;
+    const float f = paged_factor(top, sum, p.sink, p.head(un.skip + c),
+                                 p.lse != nullptr && item % kPieces == 0 && lane == 0 ? p.lse + un.row0 + c : nullptr);
+    uint16_t* out = p.out + (static_cast<int64_t>(un.row0) + c) * D + d;
 #pragma unroll
     for (int i = 0; i < kEach; i += 2) {
       const __nv_bfloat162 two = __floats2bfloat162_rn(acc[i] * f, acc[i + 1] * f);
