@@ -495,7 +495,7 @@ DSA_API dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* pages, int 
  * accepted[r] = a, the number before the first refusal, and token[r] = the lowest v with
  *     w[0] + ... + w[v] > u[r][G] * (w[0] + ... + w[V - 1]),
  * w = max(target[r][a] - draft[r][a], 0) where a < n (target[r][a] where that is all zero), else target[r][a].
- * The sums are of whole multiples of 2^-56, to which each probability is rounded (above 1: 1; no number: 0), and so
+ * The sums are of whole multiples of 2^-55, to which each probability is rounded (above 1: 1; below 0 or no number: 0), and so
  * exact.  token[r] = -1 where w is all zero; count[r] < 0 (a place without a sequence): 0 and -1.
  * The step's sequences then grow by accepted + 1 tokens: held + added of the next dsa_step_maps, without the host.
  *   target  float [R][G + 1][V];  draft  float [R][G][V];  tokens  int32 [R][G];  count  int32 [R]

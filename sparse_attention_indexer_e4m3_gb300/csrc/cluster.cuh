@@ -13,6 +13,9 @@ namespace dsa {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Its two halves.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -26,6 +29,13 @@ __device__ __forceinline__ int32_t ld_cluster_s32(uint32_t addr, uint32_t rank) 
                : "r"(addr), "r"(rank)
                : "memory");
   return v;
+}
+
+// 64-bit word to the place of `p` (in this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ void st_cluster_u64(const void* p, uint32_t rank, uint64_t v) {
+  asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.u64 [a], %2;\n\t}" ::"r"(smem_addr(p)), "r"(rank),
+               "l"(v)
+               : "memory");
 }
 
 }  // namespace dsa

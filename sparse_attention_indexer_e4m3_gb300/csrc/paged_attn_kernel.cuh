@@ -1368,6 +1368,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the join may be made ready: it waits for this grid's end)
   if (warp == 0) tmem_dealloc(tbase, 512);
 }
 

@@ -5,6 +5,7 @@
 #include <climits>
 
 #include "kv4.cuh"
+#include "kv4_codec_kernel.cuh"
 #include "paged.cuh"
 
 namespace dsa {
@@ -117,15 +118,14 @@ constexpr int kSlotThreads = 256;
 constexpr int kSlotEach = 4;  // entries of a thread at a time
 
 // Entry v of token t names row v - start[t] of sequence seq[t].  Memory-bound but for the table, whose entries L1 and L2
-// hold: a thread takes four entries of a row, in one access each where they are aligned.
+// hold: a thread takes four entries of a row, in one access each where they are aligned.  A block takes a piece of some rows one
+// after the other (no division by the pieces of a row).
 __global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const PageTable c, const int32_t* seq, const int32_t* start,
-                                                                  const int32_t* idx, int T, int K, int32_t* slots, int pieces,
-                                                                  bool wide) {
+                                                                  const int32_t* idx, int T, int K, int32_t* slots, bool wide) {
   wait_stream();
-  const int64_t items = static_cast<int64_t>(T) * pieces;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSlotThreads + threadIdx.x; i < items;
-       i += static_cast<int64_t>(gridDim.x) * kSlotThreads) {
-    const int t = static_cast<int>(i / pieces), k = static_cast<int>(i % pieces) * kSlotEach;
+  const int64_t k = (static_cast<int64_t>(blockIdx.x) * kSlotThreads + threadIdx.x) * kSlotEach;
+  if (k >= K) return;
+  for (int t = static_cast<int>(blockIdx.y); t < T; t += static_cast<int>(gridDim.y)) {
     const int s = ld_after_wait(seq + t);
     const int64_t from = start != nullptr ? ld_after_wait(start + t) : 0;
     const int32_t* in = idx + static_cast<int64_t>(t) * K + k;
@@ -154,7 +154,9 @@ __global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const PageTabl
 
 constexpr int kStoreThreads = 256;
 
-// Row i of kv as row pos[i] of sequence seq[i], 16 bytes a thread; rows without a place are left out.
+// Row i of kv as row pos[i] of sequence seq[i], kBytes (32, or 16 where a row's place is not aligned to them) a thread; rows
+// without a place are left out.
+template <int kBytes>
 __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(const uint16_t* kv, int64_t stride, int N, int log_pieces,
                                                                  const int32_t* seq, const int32_t* pos, const int32_t* lacking,
                                                                  uint16_t* pages, const PageTable c) {
@@ -164,9 +166,18 @@ __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(const uint16_t*
   if (row >= N) return;
   if (lacking != nullptr && ld_after_wait(lacking) != 0) return;
   const int piece = static_cast<int>(i) & ((1 << log_pieces) - 1);
-  const uint4 v = ld_after_wait(reinterpret_cast<const uint4*>(kv + row * stride) + piece);
-  const int64_t slot = page_slot(c, ld_after_wait(seq + row), ld_after_wait(pos + row));
-  if (slot >= 0) reinterpret_cast<uint4*>(pages)[(slot << log_pieces) + piece] = v;
+  const uint16_t* from = kv + row * stride + piece * (kBytes / 2);
+  const int s = ld_after_wait(seq + row), at = ld_after_wait(pos + row);
+  if constexpr (kBytes == 32) {
+    uint32_t v[8];
+    ld_32(from, v);
+    const int64_t slot = page_slot(c, s, at);
+    if (slot >= 0) st_32(pages + ((slot << log_pieces) + piece) * 16, v);
+  } else {
+    const uint4 v = ld_after_wait(reinterpret_cast<const uint4*>(from));
+    const int64_t slot = page_slot(c, s, at);
+    if (slot >= 0) reinterpret_cast<uint4*>(pages)[(slot << log_pieces) + piece] = v;
+  }
 }
 
 }  // namespace dsa

@@ -103,14 +103,14 @@ def slots(table, P, rows, seq, start, idx):
     return out
 
 
-UNIT = 2 ** 56
+UNIT = 2 ** 55
 
 
 def units(p):
-    """fp32 probabilities in whole multiples of 2^-56, as Python ints."""
+    """fp32 probabilities in whole multiples of 2^-55, the nearest ones, as Python ints."""
     p = np.asarray(p, np.float32)
     p = np.where(p > 0, np.minimum(p, np.float32(1)), np.float32(0)).astype(np.float64)  # (no number: 0)
-    return [int(v) for v in np.rint(p * UNIT)]  # exact: 24 bits times a power of two, ties to even
+    return [int(v) for v in np.rint(p * UNIT)]  # (the product is exact: 24 bits times a power of two; ties to even)
 
 
 def verify(target, draft, tokens, count, u):
