@@ -222,8 +222,13 @@ __device__ __forceinline__ int paged_blocks(const PagedAttnParams& p, const Page
 }
 
 // Factor of a column's outputs whose weights' bound is m (log2 units) and whose denominator is l, in units of 2^m,
-// without the sink; writes the natural log of the whole denominator where lse is given (what is no number stays so).
+// without the sink; writes the natural log of the whole denominator where lse is given (what is no number stays so, and a
+// sink that is none makes it one).
 __device__ __forceinline__ float paged_factor(float m, float l, const float* sink, int h, float* lse) {
+  if (sink != nullptr) {
+    const float s = ld_after_wait(sink + h);
+    if (s != s) l = s;
+  }
   if (l != l) {
     if (lse != nullptr) *lse = l;
     return l;
