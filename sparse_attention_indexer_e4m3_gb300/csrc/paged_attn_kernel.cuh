@@ -16,17 +16,36 @@
 //
 // One CTA per SM; per block of B rows (128; 64 at D = 512):
 //   scout    (warp 2)      the unit's runs and blocks; the pages of the next blocks, four blocks at a time;
-//   load     (warp 1)      the rows by TMA into a ring of tiles of 128 dims, as chunks of [B rows x 128 bytes], 128-byte
+//   load     (last warps)  the rows by TMA into a ring of tiles of 128 dims, as chunks of [B rows x 128 bytes], 128-byte
 //                          swizzled, page by page (a page without a row that some token sees becomes zeros: its
-//                          memory is not read);
-//   score    (warp 0)      S^T = KV . Q^T: M = B rows, N columns, K = D (tcgen05.mma kind::f16, bf16);
-//   softmax  (warps 3 on)  thread = (row, 32 columns; 16 of them at B = 64): weights as bf16 rows P[row][column]; the
-//                          running bound of a column moves only when exceeded by more than 2^8;
-//   weighted (warp 0)      O^T += KV^T . P^T: M = 128 dims (D / 128 tiles), N columns, K = B rows.
-// The score product of the next block, of the next unit as well, is issued before the weighted sum of the last, so
-// the softmax runs beside both.  At D = 512 the accumulators of 64 columns take half of tensor memory and q and two
-// blocks of 64 rows all shared memory; an instruction reads its operands from there at 128 bytes a clock, which takes
-// (M + N) / 4 cycles: 48 for M = 128, N = 64, 34 for M = 64 (N = 128, M = 128: 64, the rate of the tensor core itself).
+//                          memory is not read); the first of these warps brings q as well;
+//   score    (warp 0)      the score product, K = D (tcgen05.mma kind::f16, bf16);
+//   softmax  (warps 3-10)  weights as bf16; a running bound moves only when exceeded by more than 2^8, so the
+//                          accumulators are rarely read back;
+//   weighted (warp 1)      the weighted sum, K = B rows.
+// Score products run ahead of the weighted sums by the places for scores, into the next unit as well.
+//
+// D <= 256: S = Q . KV^T, O += P . KV, with N = 128 rows of q in the lanes of tensor memory.  A softmax thread has a whole row:
+// largest score and sum need no other thread, and the weights go back into tensor memory over the scores, from
+// where the second product takes them.  Two groups of four warps take turns, so one block's exponentials run beside the next
+// one's.  D = 512: the accumulators of 128 rows would fill tensor memory, so S^T = KV . Q^T and O^T += KV^T . P^T with 64
+// rows of q as columns, P through shared memory, and a thread with one kv row of the block and 16 columns.  (As columns at
+// D <= 256, too, a prompt with a window took 643 us instead of 278, drafts 208 instead of 77.)
+//
+// What bounds it (times at the sizes given, GB300):
+//   - a batch of long sequences: reading them.  64 sequences of up to 65536 rows of 512, 64 heads: 382 us, 6.7 TB/s, what a copy
+//     reaches.
+//   - prompts at D = 512: the products.  Their operands come from shared memory at 128 bytes a clock, (M + N) / 4 cycles an
+//     instruction: 48 for M = 128, N = 64, 34 for M = 64; 1872 of the 2070 cycles of a block of 64 rows.  4096 tokens over 8192 rows,
+//     64 heads: 2.92 ms, 1130 TFLOP/s.
+//   - prompts and drafts at D <= 256: the places for scores.  One is taken from its score product (1000 cycles behind the
+//     products before it) over the softmax (2200) to the end of its weighted sum (1000), three of them turn over a block in 1500
+//     cycles where the products need 1024; blocks that not every row sees all of take 1800 longer, and a unit's end and beginning
+//     some 7000.  2700-token prompts with a window of 1024 at D = 128, 32 heads: 187 us.
+//   - single tokens: a chain of launch, plan, table, rows, two products and the join.  One token over 32768 rows of 512, 64
+//     heads: 22.5 us.
+// Measured and slower at D <= 256: sixteen softmax warps with half a row each (191 us for 187; window decode 24.5 for
+// 23.5), masks and outputs 32 rows or dims at a time (195 to 275 us), a place of its own for P (216).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -391,7 +410,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       mbar_init(&part_full[i], 1);
       mbar_init(&part_empty[i], 2 + L::kLoaders + kPgSoftWarps);
       mbar_init(&p_full[i], L::kReaders);
-      }
+    }
     for (int i = 0; i < kPgSlots; ++i) {
       mbar_init(&blk_full[i], 1);
       mbar_init(&blk_empty[i], L::kLoaders + L::kReaders);
@@ -910,7 +929,8 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
                   const auto at = [&](int j) -> uint4* {  // piece j of the row
                     const uint32_t tile = gb * kTi + (j / 8) / L::kTileChunks;
                     paged_wait(&kv_full[tile % kRing], (tile / kRing) & 1u, abort_flag, err, 0xA6);
-                    return reinterpret_cast<uint4*>(kv_s + (tile % kRing) * L::kTileBytes + ((j / 8) % L::kTileChunks) * L::kChunkBytes + key * 128) + j % 8;
+                    const int chunk = static_cast<int>(tile % kRing) * L::kTileBytes + ((j / 8) % L::kTileChunks) * L::kChunkBytes;
+                    return reinterpret_cast<uint4*>(kv_s + chunk + key * 128) + j % 8;
                   };
                   bool bad = false;
 #pragma unroll 1
@@ -1147,7 +1167,8 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         if (tail < kKeys) {  // rows that may never have been written: weights of 0 times what is no number would be none
           for (int c = 0; c < kCh; ++c) {
             uint8_t* chunk = kv_s + ((gb * kTi + c / 2) % kRing) * L::kTileBytes + (c & 1) * L::kChunkBytes;
-            for (int i = tail * 128 + etid * 16; i < L::kChunkBytes; i += kPgSoft * 16) *reinterpret_cast<uint4*>(chunk + i) = make_uint4(0u, 0u, 0u, 0u);
+            for (int i = tail * 128 + etid * 16; i < L::kChunkBytes; i += kPgSoft * 16)
+              *reinterpret_cast<uint4*>(chunk + i) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         const bool checks = !full && r < tail;  // whether scores that are no numbers matter
