@@ -39,12 +39,12 @@ __global__ void __launch_bounds__(kMapThreads) step_maps_kernel(const StepMapArg
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kMapTokens, t1 = min(t0 + kMapTokens, static_cast<int64_t>(a.T));
   int64_t tokens = 0, keys = 0;  // before the sequences at hand
-  for (int r0 = 0; r0 < a.R && tokens < t1; r0 += kMapSeqs) {
+  for (int64_t r0 = 0; r0 < a.R && tokens < t1; r0 += kMapSeqs) {
     int64_t add[kMapEach], both[kMapEach], sum_a = 0, sum_k = 0;
     int hold[kMapEach];
 #pragma unroll
     for (int i = 0; i < kMapEach; ++i) {
-      const int r = r0 + threadIdx.x * kMapEach + i;
+      const int64_t r = r0 + threadIdx.x * kMapEach + i;
       hold[i] = r < a.R ? max(0, ld_after_wait(a.held + r)) : 0;
       add[i] = r < a.R ? max(0, ld_after_wait(a.added + r)) : 0;
       both[i] = hold[i] + add[i];
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kMapThreads) step_maps_kernel(const StepMapArg
           hi = mid;
       }
       const int64_t pos = min(held_s[lo] + t - at_s[lo], static_cast<int64_t>(INT_MAX));
-      a.seq[t] = r0 + lo;
+      a.seq[t] = static_cast<int>(r0) + lo;
       a.pos[t] = static_cast<int>(pos);
       a.ks[t] = static_cast<int>(min(key_s[lo], static_cast<int64_t>(INT_MAX)));
       a.ke[t] = static_cast<int>(min(key_s[lo] + pos + 1, static_cast<int64_t>(INT_MAX)));
@@ -126,11 +126,11 @@ __global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const PageTabl
   wait_stream();
   const int64_t k = (static_cast<int64_t>(blockIdx.x) * kSlotThreads + threadIdx.x) * kSlotEach;
   if (k >= K) return;
-  for (int t = static_cast<int>(blockIdx.y); t < T; t += static_cast<int>(gridDim.y)) {
+  for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
     const int s = ld_after_wait(seq + t);
     const int64_t from = start != nullptr ? ld_after_wait(start + t) : 0;
-    const int32_t* in = idx + static_cast<int64_t>(t) * K + k;
-    int32_t* out = slots + static_cast<int64_t>(t) * K + k;
+    const int32_t* in = idx + t * K + k;
+    int32_t* out = slots + t * K + k;
     int v[kSlotEach];
     if (wide) {
       const int4 w = ld_after_wait(reinterpret_cast<const int4*>(in));

@@ -340,3 +340,19 @@ def test_many_tokens(D, T, H):
     assert dsa.get_device_error() == 0
     pick = np.unique(np.concatenate([np.arange(0, T, 997), np.arange(T - 40, T)]))
     PR.check_attn(out[pick], None, PR.attn(q[pick], kv, seq[pick], pos[pick], 3, 0, None, 1 / math.sqrt(D)), D)
+
+
+def test_counts_near_the_largest_int():
+    """As many lists and as many sequences as an int counts: the indexes of the last ones do not wrap."""
+    n = 2 ** 31 - 1
+    pages = torch.empty(64, 16, 1, device="cuda")
+    seq = torch.zeros(n, dtype=torch.int32, device="cuda")
+    idx = torch.zeros(n, dtype=torch.int32, device="cuda")
+    idx[-3:] = i32([17, -5, 40])
+    dsa.page_slots(pages, i32([[3, 60, -1]]), seq, idx, out=idx)
+    assert idx[-4:].tolist() == [48, 60 * 16 + 1, -1, -1] and bool((idx[:-3] == 48).all())
+    del idx
+    seq[-1], seq[5] = 2, 1  # now the added rows of each sequence; those held are as many
+    got = [x.tolist() for x in dsa.step_maps(seq, seq, 4)]
+    assert got == [[5, n - 1, n - 1, -1], [1, 2, 3, -1], [0, 2, 2, 0], [2, 5, 6, 0]]
+    assert dsa.get_device_error() == 0
