@@ -70,6 +70,8 @@ constexpr float kPgNoBound = -3e38f;      // bound of a column without rows so f
 __host__ __device__ constexpr int paged_cols(int D) { return D == 512 ? 64 : 128; }
 __host__ __device__ constexpr int paged_block(int D) { return D == 512 ? 64 : 128; }
 // What a unit costs beside its blocks, and the least piece of the line of a CTA (joining a part takes about as long), in blocks.
+// (A cost of 1: drafts 72 us, window decode 27, window prompt 200; 4: 63 to 67, 24, 188; 8: 67, 23, 188.  Least pieces of 1:
+// one token 23.2 us; these: 22.5; twice these: 25.2.)
 __host__ __device__ constexpr int paged_unit_cost(int D) { return 4; }
 __host__ __device__ constexpr int paged_min_piece(int D) { return D == 512 ? 4 : 2; }
 
@@ -1403,7 +1405,8 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
 constexpr int kPgJoinThreads = 128;
 constexpr int kPgJoinWarps = kPgJoinThreads / 32;
 constexpr int kPgMaxCtas = 512;    // CTAs that may share a unit
-constexpr int kPgFewParts = 8;     // up to so many parts a warp joins by itself
+// Up to so many parts a warp joins by itself (always: one token, of some 120 parts, 28 us; never: 22.2, but drafts 82; so: 22.5, 65).
+constexpr int kPgFewParts = 8;
 
 // Joins the parts of the units that several CTAs shared: block (i, j) an equal share j of the i-th entry's columns and pieces of
 // 128 dims.  A warp takes one such item, four dims a lane (two at D = 64); where the parts are many, a block does, a quarter of
