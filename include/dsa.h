@@ -432,7 +432,9 @@ DSA_API dsa_status dsa_copy_pages(void* pages, size_t page_bytes, int P, const i
 /*
  * The bf16 paged cache: pages uint16 (bf16 bits) [P][page_rows][D], 16-byte aligned, each row both key and value,
  * under the same tables as the 4-bit cache (page_rows a power of two in [16, 256], M * page_rows < 2^31, D in
- * {64, 128, 256, 512}; DSA_ERR_UNSUPPORTED otherwise).  The page calls above serve it as they are.
+ * {64, 128, 256, 512}; DSA_ERR_UNSUPPORTED otherwise).  The page calls above serve it as they are.  In the calls below no
+ * output may share memory with an input or another output but where that is said (DSA_ERR_INVALID_ARG where two of a call's
+ * larger arrays do).
  *
  * dsa_step_maps -- the tokens of a step from the sequences' lengths.  Sequence r holds held[r] rows and gets added[r]
  * more (below 0: 0); the added tokens lie one sequence after the other.  With A = the sum of added and K the sum of
@@ -478,7 +480,7 @@ DSA_API dsa_status dsa_store_kv(const uint16_t* kv, int64_t stride, const int32_
  *
  *   q          bf16 [T][H][D], 16-byte aligned;  seq, pos  int32 [T]
  *   attn_sink  float [H] or NULL;  window  0 (none) or more;  first  0 or more;  scale  softmax scale
- *   out        bf16 [T][H][D], 16-byte aligned   OUTPUT;  lse  float [T][H] or NULL  OUTPUT, as dsa_sparse_attn's
+ *   out        bf16 [T][H][D], 16-byte aligned   OUTPUT (may be q);  lse  float [T][H] or NULL  OUTPUT, as dsa_sparse_attn's
  *   workspace  dsa_paged_attn_workspace_size(T, H, D) bytes, 16-byte aligned; its contents on entry do not matter; two
  *              calls running at the same time must not share it.  DSA_ERR_WORKSPACE if it is missing, short or misaligned
  * T * H < 2^30, P * page_rows < 2^31 (DSA_ERR_UNSUPPORTED).

@@ -582,7 +582,8 @@ def paged_attn(q, pages, table, seq, pos, window=None, first=0, attn_sink=None, 
     """Attention over the sequences' rows in the paged cache (bf16 [P, page_rows, D], keys = values): q bf16 [T, H, D]; token
     t, at position pos[t] of sequence seq[t], sees the rows up to its own, with a window only the last `window` of them and
     the `first` first ones.  attn_sink fp32 [H] or None, scale default 1 / sqrt(D).  Returns bf16 [T, H, D] (zeros for
-    a token that sees nothing); with lse (fp32 [T, H]) given, also writes the natural log of each softmax denominator."""
+    a token that sees nothing; out may be q); with lse (fp32 [T, H]) given, also writes the natural log of each softmax
+    denominator."""
     return (_calls or _native()).paged_attn(q, pages, table, seq, pos, window, first, attn_sink, scale, out, lse, workspace,
                                             stream)
 

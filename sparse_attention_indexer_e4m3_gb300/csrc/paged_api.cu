@@ -75,6 +75,12 @@ dsa_status dsa_step_maps(const int32_t* held, const int32_t* added, int R, int T
   if (R > 0 && (!held || !aligned(held, 4) || !added || !aligned(added, 4))) return DSA_ERR_INVALID_ARG;
   if (!seq || !aligned(seq, 4) || !pos || !aligned(pos, 4) || !ks || !aligned(ks, 4) || !ke || !aligned(ke, 4))
     return DSA_ERR_INVALID_ARG;
+  int32_t* const maps[4] = {seq, pos, ks, ke};
+  for (int i = 0; i < 4; ++i) {
+    if (overlap(maps[i], T, held, R) || overlap(maps[i], T, added, R)) return DSA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(maps[i], T, maps[j], T)) return DSA_ERR_INVALID_ARG;
+  }
   return done(launch_step_maps(StepMapArgs{held, added, R, T, seq, pos, ks, ke}, static_cast<cudaStream_t>(stream)));
 }
 
@@ -87,6 +93,10 @@ dsa_status dsa_page_slots(const int32_t* table, int R, int M, int P, int page_ro
   if (static_cast<int64_t>(P) * page_rows > INT_MAX) return DSA_ERR_UNSUPPORTED;  // a row of the pages is an int
   if (T == 0 || K == 0) return DSA_OK;
   if (!seq || !aligned(seq, 4) || !idx || !aligned(idx, 4) || !slots || !aligned(slots, 4) || (start && !aligned(start, 4)))
+    return DSA_ERR_INVALID_ARG;
+  const int64_t entries = static_cast<int64_t>(T) * K;
+  if ((slots != idx && overlap(slots, entries, idx, entries)) || overlap(slots, entries, seq, T) ||
+      (start && overlap(slots, entries, start, T)) || overlap(slots, entries, table, static_cast<int64_t>(R) * M))
     return DSA_ERR_INVALID_ARG;
   return done(launch_page_slots(c, seq, start, idx, T, K, slots, static_cast<cudaStream_t>(stream)));
 }
@@ -102,6 +112,7 @@ dsa_status dsa_store_kv(const uint16_t* kv, int64_t stride, const int32_t* seq, 
   if (N == 0) return DSA_OK;
   if (!kv || !aligned(kv, 16) || !seq || !aligned(seq, 4) || !pos || !aligned(pos, 4) || (lacking && !aligned(lacking, 4)))
     return DSA_ERR_INVALID_ARG;
+  if (overlap(kv, (N - 1) * stride + D, pages, static_cast<int64_t>(P) * page_rows * D)) return DSA_ERR_INVALID_ARG;
   return done(launch_store_kv(D, kv, stride, N, seq, pos, lacking, pages, c, static_cast<cudaStream_t>(stream)));
 }
 
@@ -129,6 +140,9 @@ dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* pages, int P, int p
   // rows of q and of the pages are coordinates of the copies, which are ints
   if (static_cast<int64_t>(T) * H > INT_MAX / 2 || un.units > INT_MAX / 2 || static_cast<int64_t>(P) * page_rows > INT_MAX)
     return DSA_ERR_UNSUPPORTED;
+  const int64_t values = static_cast<int64_t>(T) * H * D;
+  if ((out != q && overlap(out, values, q, values)) || overlap(out, values, pages, static_cast<int64_t>(P) * page_rows * D))
+    return DSA_ERR_INVALID_ARG;
   DeviceFacts dev;
   if (!device_facts(&dev)) return DSA_ERR_CUDA;
   if (paged_attn_smem(D) > dev.max_smem) return DSA_ERR_UNSUPPORTED;
@@ -157,6 +171,10 @@ dsa_status dsa_verify_drafts(const float* target, const float* draft, const int3
       !token || !aligned(token, 4))
     return DSA_ERR_INVALID_ARG;
   if (G > 0 && (!draft || !aligned(draft, 4) || !tokens || !aligned(tokens, 4))) return DSA_ERR_INVALID_ARG;
+  const int64_t drafts = static_cast<int64_t>(R) * G;
+  for (int32_t* o : {accepted, token})
+    if (overlap(o, R, count, R) || overlap(o, R, tokens, drafts) || overlap(o, R, u, drafts + R)) return DSA_ERR_INVALID_ARG;
+  if (overlap(accepted, R, token, R)) return DSA_ERR_INVALID_ARG;
   DeviceFacts dev;
   if (!device_facts(&dev)) return DSA_ERR_CUDA;
   return done(launch_verify_drafts(VerifyArgs{target, draft, tokens, count, u, R, G, V, accepted, token}, dev.sms,

@@ -356,3 +356,15 @@ def test_counts_near_the_largest_int():
     got = [x.tolist() for x in dsa.step_maps(seq, seq, 4)]
     assert got == [[5, n - 1, n - 1, -1], [1, 2, 3, -1], [0, 2, 2, 0], [2, 5, 6, 0]]
     assert dsa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("D,H", [(64, 7), (128, 33), (256, 150), (512, 20)])
+def test_output_over_the_queries(D, H):
+    """out = q, with units that many CTAs share and units of several tokens."""
+    rng = np.random.default_rng(D)
+    pages, table, _ = PR.pool([2000, 300], 64, D, rng)
+    for seq, pos in (([0, 1], [1999, 299]), ([0] * 300 + [1] * 20, list(range(1700, 2000)) + list(range(280, 300)))):
+        q = torch.from_numpy(rng.standard_normal((len(seq), H, D))).to(bf16).cuda()
+        want = dsa.paged_attn(q, pages, table, i32(seq), i32(pos), window=700)
+        assert dsa.paged_attn(q, pages, table, i32(seq), i32(pos), window=700, out=q) is q and torch.equal(q, want)
+    assert dsa.get_device_error() == 0

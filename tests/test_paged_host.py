@@ -76,7 +76,7 @@ def lib():
 
 @pytest.fixture(scope="module")
 def a():
-    buf = ctypes.create_string_buffer(256)
+    buf = ctypes.create_string_buffer(4096)
     yield (ctypes.addressof(buf) + 63) // 64 * 64
     del buf
 
@@ -86,7 +86,9 @@ TOP = 2 ** 31 - 1
 
 
 def test_maps_refusals(lib, a):
-    def f(held=a, added=a, R=2, T=3, seq=a, pos=a, ks=a, ke=a):
+    at = lambda i: a + (i << 20)  # noqa: E731  (addresses apart; none is read)
+
+    def f(held=a, added=at(1), R=2, T=3, seq=at(2), pos=at(3), ks=at(4), ke=at(5)):
         return lib.dsa_step_maps(held, added, R, T, seq, pos, ks, ke, None)
 
     assert f(R=-1) == f(T=-1) == INVALID
@@ -96,7 +98,9 @@ def test_maps_refusals(lib, a):
 
 
 def test_slots_refusals(lib, a):
-    def f(table=a, R=1, M=2, P=2, rows=64, seq=a, start=None, idx=a, T=2, K=3, slots=a):
+    at = lambda i: a + (i << 20)  # noqa: E731  (addresses apart; none is read)
+
+    def f(table=a, R=1, M=2, P=2, rows=64, seq=at(1), start=None, idx=at(2), T=2, K=3, slots=at(3)):
         return lib.dsa_page_slots(table, R, M, P, rows, seq, start, idx, T, K, slots, None)
 
     assert f(rows=8) == f(rows=48) == f(rows=512) == f(M=1 << 25) == f(P=1 << 25) == UNSUPPORTED
@@ -108,7 +112,9 @@ def test_slots_refusals(lib, a):
 
 
 def test_store_refusals(lib, a):
-    def f(kv=a, stride=128, seq=a, pos=a, N=4, D=128, pages=a, P=2, rows=64, table=a, R=1, M=2, lacking=None):
+    at = lambda i: a + (i << 20)  # noqa: E731  (addresses apart; none is read)
+
+    def f(kv=a, stride=128, seq=at(1), pos=at(2), N=4, D=128, pages=at(3), P=2, rows=64, table=at(4), R=1, M=2, lacking=None):
         return lib.dsa_store_kv(kv, stride, seq, pos, N, D, pages, P, rows, table, R, M, lacking, None)
 
     assert f(D=96) == f(D=1024) == f(rows=24) == f(M=1 << 25) == UNSUPPORTED
@@ -120,7 +126,9 @@ def test_store_refusals(lib, a):
 
 
 def test_attention_refusals(lib, a):
-    def f(q=a, pages=a, P=2, rows=64, table=a, R=1, M=2, seq=a, pos=a, sink=None, T=2, H=4, D=128, window=0, first=0, out=a, lse=None):
+    at = lambda i: a + (i << 20)  # noqa: E731  (addresses apart; none is read)
+
+    def f(q=a, pages=at(1), P=2, rows=64, table=at(2), R=1, M=2, seq=at(3), pos=at(4), sink=None, T=2, H=4, D=128, window=0, first=0, out=at(5), lse=None):
         return lib.dsa_paged_attn(q, pages, P, rows, table, R, M, seq, pos, sink, T, H, D, window, first, 1.0, out, lse, None, 0, None)
 
     assert f(D=96) == f(D=1024) == f(rows=8) == f(M=1 << 25) == f(T=1 << 20, H=1 << 10) == f(P=1 << 25) == UNSUPPORTED
@@ -135,7 +143,9 @@ def test_attention_refusals(lib, a):
 
 
 def test_drafts_refusals(lib, a):
-    def f(target=a, draft=a, tokens=a, count=a, u=a, R=2, G=3, V=5, accepted=a, token=a):
+    at = lambda i: a + (i << 20)  # noqa: E731  (addresses apart; none is read)
+
+    def f(target=a, draft=at(1), tokens=at(2), count=at(3), u=at(4), R=2, G=3, V=5, accepted=at(5), token=at(6)):
         return lib.dsa_verify_drafts(target, draft, tokens, count, u, R, G, V, accepted, token, None)
 
     assert f(R=-1) == f(G=-1) == f(V=0) == f(V=-1) == INVALID
@@ -143,6 +153,31 @@ def test_drafts_refusals(lib, a):
     for k in ("target", "draft", "tokens", "count", "u", "accepted", "token"):
         assert f(**{k: None}) == INVALID and f(**{k: a + 2}) == INVALID, k
     assert f(R=0, target=None, draft=None, tokens=None, count=None, u=None, accepted=None, token=None) == OK
+
+
+def test_outputs_that_overlap(lib, a):
+    """What would be written while it is read is refused (all other arguments are right)."""
+    at = [a + 256 * i for i in range(12)]
+
+    def maps(held=at[0], added=at[1], seq=at[2], pos=at[3], ks=at[4], ke=at[5]):
+        return lib.dsa_step_maps(held, added, 4, 6, seq, pos, ks, ke, None)
+
+    assert maps(seq=at[0]) == maps(ke=at[1]) == maps(pos=at[2]) == maps(ks=at[5] + 20) == maps(seq=at[0] + 12) == INVALID
+
+    def slots(table=at[0], seq=at[1], start=at[2], idx=at[3], out=at[4]):
+        return lib.dsa_page_slots(table, 2, 2, 8, 16, seq, start, idx, 3, 5, out, None)
+
+    assert slots(out=at[3] + 4) == slots(out=at[3] - 4) == slots(out=at[1]) == slots(out=at[2]) == slots(out=at[0] + 12) == INVALID
+    store = lambda kv: lib.dsa_store_kv(kv, 64, at[0], at[0], 2, 64, at[4], 1, 16, at[1], 1, 1, None, None)  # noqa: E731
+    assert store(at[4]) == store(at[4] - 128) == store(at[11] + 240) == INVALID  # (pages: 2 KB from at[4] on)
+    attn = lambda q, out: lib.dsa_paged_attn(q, at[4], 1, 16, at[0], 1, 1, at[1], at[1], None, 1, 2, 64, 0, 0, 1.0, out, None, None, 0,  # noqa: E731
+                                             None)
+    assert attn(at[2], at[2] + 16) == attn(at[2] + 16, at[2]) == attn(at[2], at[4] + 16) == INVALID
+
+    def verify(tokens=at[0], count=at[1], u=at[2], accepted=at[3], token=at[4]):
+        return lib.dsa_verify_drafts(at[8], at[8], tokens, count, u, 2, 3, 5, accepted, token, None)
+
+    assert verify(accepted=at[1]) == verify(token=at[1]) == verify(token=at[3]) == verify(accepted=at[0] + 20) == verify(token=at[2]) == INVALID
 
 
 # ------------------------------------------------------------------------------------ what no run shows
