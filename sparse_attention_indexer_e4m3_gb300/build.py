@@ -1,5 +1,5 @@
 """Builds the CUDA library libdsa_gb300.so in-tree for sm_103a (GB300), and the native argument
-marshalling _marshal.so of the 4-bit cache's calls against the installed torch (g++).  The library needs nvcc only:
+marshalling _marshal.so of the paged caches' and the drafts' calls against the installed torch (g++).  The library needs nvcc only:
 without torch the marshalling is left out, which nothing but the Python calls on the 4-bit cache use.
 
 Plain nvcc, no CMake: each translation unit under csrc/ compiles in parallel to an object,
