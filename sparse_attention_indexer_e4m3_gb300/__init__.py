@@ -1,10 +1,11 @@
 """GB300-native FP8 lightning indexer and exact top-k selector.
 
 Python binding of the C ABI in ``include/dsa.h`` (library ``libdsa_gb300.so``, built in-tree by
-``sparse_attention_indexer_e4m3_gb300.build``; the paged caches' and the drafts' calls marshal natively, ``_marshal.so``).  This module only marshals arguments: it checks
-torch tensors, passes their device pointers and the current CUDA stream, and raises
-``DsaError`` on a non-OK status.  Every step of the computation runs in the library's kernels;
-there is no fallback path.  If the library has not been built, every call raises.
+``sparse_attention_indexer_e4m3_gb300.build``; the paged caches' and the drafts' calls marshal natively,
+``_marshal.so``).  This module only marshals arguments: it checks torch tensors, passes their device
+pointers and the current CUDA stream, and raises ``DsaError`` on a non-OK status.  Every step of the
+computation runs in the library's kernels; there is no fallback path.  If the library has not been
+built, every call raises.
 
     score[t, j] = k_scale[j] * sum_h relu(q[t, h] . k[j]) * w[t, h],   ks[t] <= j < ke[t]
     idx[t]      = the topk keys of largest score in the window, ascending, -1 padded

@@ -1,6 +1,6 @@
 """Builds the CUDA library libdsa_gb300.so in-tree for sm_103a (GB300), and the native argument
-marshalling _marshal.so of the paged caches' and the drafts' calls against the installed torch (g++).  The library needs nvcc only:
-without torch the marshalling is left out, which nothing but the Python calls on the 4-bit cache use.
+marshalling _marshal.so of the paged caches' and the drafts' calls against the installed torch (g++).  The library
+needs nvcc only: without torch the marshalling is left out, which nothing but those Python calls use.
 
 Plain nvcc, no CMake: each translation unit under csrc/ compiles in parallel to an object,
 then one shared library is linked.  The CUDA runtime is linked statically, so the library
