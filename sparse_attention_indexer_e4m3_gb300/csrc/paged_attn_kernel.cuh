@@ -124,7 +124,7 @@ struct PagedLayout {
   static constexpr int kPlan = kParts + 2 * static_cast<int>(sizeof(PagedPart));            // int [8]
   static constexpr int kScan = kPlan + 32;                        // int64 [warps]
   static constexpr int kBar = kScan + (kThreads / 32 + 1) / 2 * 16;
-  static constexpr int kNumBars = 25 + 2 * kPgSlots + 2 * kRing;
+  static constexpr int kNumBars = 28 + 2 * kPgSlots + 2 * kRing;
   static constexpr int kSmem = kBar + kNumBars * 8;
   // softmax warps that read a block, or fill a P
   static constexpr int kReaders = kByRow ? kPgSoftWarps / 2 : kPgSoftWarps;
@@ -382,12 +382,12 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   uint64_t* part_full = bars + 8;   // [2]
   uint64_t* part_empty = bars + 10; // [2]
   uint64_t* s_full = bars + 12;     // [scores]
-  uint64_t* p_full = bars + 16;     // [2] of even and odd blocks
+  uint64_t* p_full = bars + 25;     // [scores]
   uint64_t* decided = bars + 18;    // [4] by row: bounds of a quarter's rows
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint64_t* pv_done = bars + 22;    // [scores]
-  uint64_t* blk_full = bars + 25;   // [slots]
+  uint64_t* blk_full = bars + 28;   // [slots]
   uint64_t* blk_empty = blk_full + kPgSlots;
   uint64_t* kv_full = blk_empty + kPgSlots;  // [ring]
   uint64_t* kv_empty = kv_full + kRing;
@@ -411,7 +411,6 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       mbar_init(&q_empty[i], 1);
       mbar_init(&part_full[i], 1);
       mbar_init(&part_empty[i], 2 + L::kLoaders + kPgSoftWarps);
-      mbar_init(&p_full[i], L::kReaders);
     }
     for (int i = 0; i < kPgSlots; ++i) {
       mbar_init(&blk_full[i], 1);
@@ -421,6 +420,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     for (int i = 0; i < L::kScores; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&pv_done[i], 1);
+      mbar_init(&p_full[i], L::kReaders);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&kv_full[i], 1);
@@ -763,8 +763,8 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         const uint64_t q = q_k + uniform(qb * (L::kQBytes >> 4));
         for (int b = 0; ok && b < nb; ++b, ++gb) {
           // a place for the scores: by row, where the weights of the block before in it were summed; else, where they were formed
-          if (L::kByRow ? gb >= L::kScores && !wait(&pv_done[gb % L::kScores], (gb / L::kScores - 1) & 1u, 0x92)
-                        : gb >= 2 && !wait(&p_full[gb & 1u], ((gb >> 1) - 1) & 1u, 0x92)) {
+          if (gb >= L::kScores &&
+              !wait(&(L::kByRow ? pv_done : p_full)[gb % L::kScores], (gb / L::kScores - 1) & 1u, 0x92)) {
             ok = false;
             break;
           }
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       } else {
         for (int b = 0; ok && b < nb; ++b, ++gb) {
           // (a part's first weighted sum overwrites O: the output of the part before must be read)
-          if (!wait(&p_full[gb & 1u], (gb >> 1) & 1u, 0x94) || (b == 0 && parts > 1 && !wait(o_empty, parts & 1u, 0x95))) {
+          if (!wait(&p_full[gb % L::kScores], (gb / L::kScores) & 1u, 0x94) || (b == 0 && parts > 1 && !wait(o_empty, parts & 1u, 0x95))) {
             ok = false;
             break;
           }
@@ -1031,7 +1031,9 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         }
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[group]);
+        // (a barrier for each place of scores: with one for each group a warp that is a block ahead, as the third place allows, would
+        // count for one that is not done)
+        if (lane == 0) mbar_arrive(&p_full[gb % L::kScores]);
       }
       gb0 += nb;
       // the part's end: the two threads' sums in units of the row's last bound
@@ -1313,7 +1315,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         fence_proxy_async_shared();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[gb & 1u]);
+        if (lane == 0) mbar_arrive(&p_full[gb % L::kScores]);
         if (some) {
 #pragma unroll
           for (int c = 0; c < kC; c += 2) lsum[c / 2] = add_f32x2(lsum[c / 2], pack_f32x2(x[c], x[c + 1]));

@@ -159,3 +159,27 @@ def test_large_batch():
     assert dsa.get_device_error() == 0
     pick = np.arange(0, 64, 8)
     PR.check_attn(out[pick], lse[pick], PR.attn(q[pick], kv, pick, lens[pick] - 1, None, 0, None, 1 / math.sqrt(D)), D)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+@pytest.mark.parametrize("H", [8, 40, 70, 100])
+def test_warps_apart(D, H):
+    """Warps whose rows of q are few, or whose bound is raised again and again, beside others: none's weights are taken before they
+    are formed, in any of many runs."""
+    rng = np.random.default_rng(D + H)
+    n, R = 6000, 40
+    pages, table, kv = PR.pool([n], 64, D, rng)
+    seq, pos = np.zeros(R, int), rng.integers(n // 2, n, R)
+    q = torch.from_numpy(rng.standard_normal((R, H, D))).to(torch.bfloat16)
+    q[:, H // 3:H // 2] *= 6  # scores that spread: their bounds are raised in many blocks
+    q = q.cuda()
+    lse = torch.empty(R, H, device="cuda")
+    table = table.expand(R, -1).contiguous()
+    for window in (None, 900):
+        s = np.arange(R)
+        out = dsa.paged_attn(q, pages, table, i32(s), i32(pos), window=window, lse=lse)
+        PR.check_attn(out, lse, PR.attn(q, kv, seq, pos, window, 0, None, 1 / math.sqrt(D)), D)
+        for _ in range(300):
+            again = dsa.paged_attn(q, pages, table, i32(s), i32(pos), window=window)
+            assert torch.equal(out, again)
+    assert dsa.get_device_error() == 0
