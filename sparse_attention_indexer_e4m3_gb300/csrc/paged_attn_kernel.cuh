@@ -53,6 +53,7 @@
 #include "attn_kv4_kernel.cuh"
 #include "kv4_codec_kernel.cuh"
 #include "paged.cuh"
+#include "tile_ring.h"
 
 namespace dsa {
 
@@ -443,6 +444,8 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   // has at least one of its blocks) and belongs to those, too, whose pieces its blocks reach into.
   constexpr int kUnitCost = paged_unit_cost(D);
   int64_t* warp_scan = reinterpret_cast<int64_t*>(smem + L::kScan);  // [warps]
+  volatile uint32_t* issued_s = reinterpret_cast<volatile uint32_t*>(smem + L::kScan);  // later: tiles of each loading warp, and q's
+  static_assert(4 * (L::kLoaders + 1) <= L::kBar - L::kScan, "counts in the scan's place");
   // Each unit's blocks, kept in the ring's place (where they fit: 32768 units are prompts of 65536 tokens and 64 heads).
   constexpr int kKeep = L::kQ / 4;
   int* blocks_s = reinterpret_cast<int*>(kv_s);
@@ -661,8 +664,8 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     const auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
       return __all_sync(0xffffffffu, paged_wait(bar, parity, abort_flag, err, site)) != 0;
     };
-    uint32_t gb = 0, nq = 0;                               // blocks and q's of this CTA so far
-    uint32_t at = static_cast<uint32_t>(loader), round = 0;  // its next tile's place in the ring, and how often that was used before
+    uint32_t gb = 0, nq = 0;                                          // blocks and q's of this CTA so far
+    TileRing<kRing, L::kLoaders> ring(static_cast<uint32_t>(loader));  // its tiles
     const int page_rows = 1 << p.pages.log_rows;
     const int boxes = kKeys / p.box_rows;                    // copies of a block and chunk
     const int none = max(1, p.pages.P << p.pages.log_rows);  // a row behind the last page: the copy fills in zeros
@@ -698,12 +701,12 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         if (lane == 0) mbar_arrive(&blk_empty[slot]);
 #pragma unroll
         for (int m0 = 0; m0 < kTi; m0 += L::kLoaders) {
-          if (round > 0 && !wait(&kv_empty[at], (round - 1) & 1u, 0x86)) {
+          if (ring.round > 0 && !wait(&kv_empty[ring.at], (ring.round - 1) & 1u, 0x86)) {
             ok = false;
             break;
           }
-          const uint32_t bar = smem_addr(&kv_full[at]);
-          uint32_t to = smem_addr(kv_s) + at * L::kTileBytes;
+          const uint32_t bar = smem_addr(&kv_full[ring.at]);
+          uint32_t to = smem_addr(kv_s) + ring.at * L::kTileBytes;
           mbar_expect_if(on, bar, L::kTileBytes);
 #pragma unroll 1
           for (int i = 0; i < boxes; ++i, to += p.box_rows * 128) {
@@ -712,19 +715,13 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
             for (int c = 0; c < L::kTileChunks; ++c)
               tma_load_2d_if(on, to + c * L::kChunkBytes, &kvmap, bar, 64 * (L::kTileChunks * (m0 + loader) + c), y);
           }
-          at += L::kLoaders;
-          if (at >= kRing) {
-            at -= kRing;
-            ++round;
-          }
+          ring.next();
         }
       }
     }
-    if (gone()) {  // copies in flight land before the CTA ends
-      if (loader == 0)
-        for (uint32_t i = nq > kQb ? nq - kQb : 0; i < nq; ++i) mbar_wait_drain(&q_full[i % kQb], (i / kQb) & 1u);
-      const uint32_t tiles = gb * kTi;
-      for (uint32_t i = tiles > kRing ? tiles - kRing : 0; i < tiles; ++i) mbar_wait_drain(&kv_full[i % kRing], (i / kRing) & 1u);
+    if (lane == 0) {
+      issued_s[loader] = ring.issued;
+      if (loader == 0) issued_s[L::kLoaders] = nq;
     }
   } else if (warp < 2) {
     // ------------------------------------------------------------------ MMA issuers (whole warps, one thread of each elected)
@@ -1398,6 +1395,12 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  if (*abort_flag != 0 && warp == kPgFirstLoad) {
+    // Some role gave up, perhaps after the loading warps were done: copies that nobody waited for land before the CTA ends.
+    const uint32_t nq = issued_s[L::kLoaders];
+    for (uint32_t i = nq > kQb ? nq - kQb : 0; i < nq; ++i) mbar_wait_drain(&q_full[i % kQb], (i / kQb) & 1u);
+    tiles_in_flight<kRing, L::kLoaders>(issued_s, [&](uint32_t place, uint32_t parity) { mbar_wait_drain(&kv_full[place], parity); });
+  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the join may be made ready: it waits for this grid's end)
   if (warp == 0) tmem_dealloc(tbase, 512);
 }
