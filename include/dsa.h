@@ -433,8 +433,7 @@ DSA_API dsa_status dsa_copy_pages(void* pages, size_t page_bytes, int P, const i
  * The bf16 paged cache: pages uint16 (bf16 bits) [P][page_rows][D], 16-byte aligned, each row both key and value,
  * under the same tables as the 4-bit cache (page_rows a power of two in [16, 256], M * page_rows < 2^31, D in
  * {64, 128, 256, 512}; DSA_ERR_UNSUPPORTED otherwise).  The page calls above serve it as they are.  In the calls below no
- * output may share memory with an input or another output but where that is said (DSA_ERR_INVALID_ARG where two of a call's
- * larger arrays do).
+ * output or workspace may share memory with an input or another output but where that is said (DSA_ERR_INVALID_ARG).
  *
  * dsa_step_maps -- the tokens of a step from the sequences' lengths.  Sequence r holds held[r] rows and gets added[r]
  * more (below 0: 0); the added tokens lie one sequence after the other.  With A = the sum of added and K the sum of
@@ -503,7 +502,7 @@ DSA_API dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* pages, int 
  * The step's sequences then grow by accepted + 1 tokens: held + added of the next dsa_step_maps, without the host.
  *   target  float [R][G + 1][V];  draft  float [R][G][V];  tokens  int32 [R][G];  count  int32 [R]
  *   u       float [R][G + 1] in [0, 1);  accepted, token  int32 [R]   OUTPUT
- * R < 2^28 (DSA_ERR_UNSUPPORTED); V >= 1, rows whose probabilities sum to less than 256.
+ * R < 2^28, R * (G + 1) * V < 2^60 (DSA_ERR_UNSUPPORTED); V >= 1, rows whose probabilities sum to less than 256.
  */
 DSA_API dsa_status dsa_verify_drafts(const float* target, const float* draft, const int32_t* tokens, const int32_t* count,
                                      const float* u, int R, int G, int V, int32_t* accepted, int32_t* token, void* stream);

@@ -112,7 +112,10 @@ dsa_status dsa_store_kv(const uint16_t* kv, int64_t stride, const int32_t* seq, 
   if (N == 0) return DSA_OK;
   if (!kv || !aligned(kv, 16) || !seq || !aligned(seq, 4) || !pos || !aligned(pos, 4) || (lacking && !aligned(lacking, 4)))
     return DSA_ERR_INVALID_ARG;
-  if (overlap(kv, (N - 1) * stride + D, pages, static_cast<int64_t>(P) * page_rows * D)) return DSA_ERR_INVALID_ARG;
+  const int64_t held = static_cast<int64_t>(P) * page_rows * D;
+  if (overlap(pages, held, kv, (N - 1) * stride + D) || overlap(pages, held, seq, N) || overlap(pages, held, pos, N) ||
+      overlap(pages, held, table, static_cast<int64_t>(R) * M) || overlap(pages, held, lacking, lacking ? 1 : 0))
+    return DSA_ERR_INVALID_ARG;
   return done(launch_store_kv(D, kv, stride, N, seq, pos, lacking, pages, c, static_cast<cudaStream_t>(stream)));
 }
 
@@ -140,15 +143,24 @@ dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* pages, int P, int p
   // rows of q and of the pages are coordinates of the copies, which are ints
   if (static_cast<int64_t>(T) * H > INT_MAX / 2 || un.units > INT_MAX / 2 || static_cast<int64_t>(P) * page_rows > INT_MAX)
     return DSA_ERR_UNSUPPORTED;
-  const int64_t values = static_cast<int64_t>(T) * H * D;
-  if ((out != q && overlap(out, values, q, values)) || overlap(out, values, pages, static_cast<int64_t>(P) * page_rows * D))
+  const int64_t values = static_cast<int64_t>(T) * H * D, held = static_cast<int64_t>(P) * page_rows * D;
+  const int64_t logs = lse ? static_cast<int64_t>(T) * H : 0, entries = static_cast<int64_t>(R) * M, sinks = attn_sink ? H : 0;
+  if ((out != q && overlap(out, values, q, values)) || overlap(out, values, lse, logs) || overlap(lse, logs, q, values))
     return DSA_ERR_INVALID_ARG;
+  const auto taken = [&](const auto* o, int64_t n) {
+    return overlap(o, n, pages, held) || overlap(o, n, table, entries) || overlap(o, n, seq, T) || overlap(o, n, pos, T) ||
+           overlap(o, n, attn_sink, sinks);
+  };
+  if (taken(out, values) || taken(lse, logs)) return DSA_ERR_INVALID_ARG;
   DeviceFacts dev;
   if (!device_facts(&dev)) return DSA_ERR_CUDA;
   if (paged_attn_smem(D) > dev.max_smem) return DSA_ERR_UNSUPPORTED;
   const Workspace w = workspace_of(D, dev.sms);
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < w.bytes) return DSA_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int64_t bytes = static_cast<int64_t>(w.bytes);
+  if (taken(ws, bytes) || overlap(ws, bytes, q, values) || overlap(ws, bytes, out, values) || overlap(ws, bytes, lse, logs))
+    return DSA_ERR_INVALID_ARG;
   const int box = std::min(page_rows, paged_attn_block(D));
   CUtensorMap kvmap, qmap;
   // (without pages the map is over q, of which no row of a page is read)
@@ -172,8 +184,11 @@ dsa_status dsa_verify_drafts(const float* target, const float* draft, const int3
     return DSA_ERR_INVALID_ARG;
   if (G > 0 && (!draft || !aligned(draft, 4) || !tokens || !aligned(tokens, 4))) return DSA_ERR_INVALID_ARG;
   const int64_t drafts = static_cast<int64_t>(R) * G;
+  if (drafts + R > (INT64_MAX >> 3) / V) return DSA_ERR_UNSUPPORTED;  // the probabilities' bytes
   for (int32_t* o : {accepted, token})
-    if (overlap(o, R, count, R) || overlap(o, R, tokens, drafts) || overlap(o, R, u, drafts + R)) return DSA_ERR_INVALID_ARG;
+    if (overlap(o, R, count, R) || overlap(o, R, tokens, drafts) || overlap(o, R, u, drafts + R) ||
+        overlap(o, R, target, (drafts + R) * V) || overlap(o, R, draft, drafts * V))
+      return DSA_ERR_INVALID_ARG;
   if (overlap(accepted, R, token, R)) return DSA_ERR_INVALID_ARG;
   DeviceFacts dev;
   if (!device_facts(&dev)) return DSA_ERR_CUDA;
