@@ -460,7 +460,7 @@ DSA_API dsa_status dsa_page_slots(const int32_t* table, int R, int M, int P, int
 /*
  * dsa_store_kv -- writes row i of kv as row pos[i] of sequence seq[i].  A row whose place is not mapped is left out, and
  * all are where *lacking (dsa_reserve_pages' output, or NULL) is not 0.
- *   kv         bf16 (uint16 bits), row i at kv + i * stride (in values, a multiple of 8, at least D); 16-byte aligned
+ *   kv         bf16 (uint16 bits), row i at kv + i * stride (in values, a multiple of 8, at least D; N * stride < 2^61); 16-byte aligned
  *   seq, pos   int32 [N]; the same place at most once (else the rows may end up mixed)
  */
 DSA_API dsa_status dsa_store_kv(const uint16_t* kv, int64_t stride, const int32_t* seq, const int32_t* pos, int N, int D,

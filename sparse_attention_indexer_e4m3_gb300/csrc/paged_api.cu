@@ -108,7 +108,7 @@ dsa_status dsa_store_kv(const uint16_t* kv, int64_t stride, const int32_t* seq, 
   if (st != DSA_OK) return st;
   if (!paged_d(D)) return DSA_ERR_UNSUPPORTED;
   if (P > 0 && (!pages || !aligned(pages, 16))) return DSA_ERR_INVALID_ARG;
-  if (N < 0 || (N > 1 && stride < D) || stride % 8 != 0) return DSA_ERR_INVALID_ARG;
+  if (N < 0 || (N > 1 && (stride < D || stride > (INT64_MAX >> 2) / N)) || stride % 8 != 0) return DSA_ERR_INVALID_ARG;
   if (N == 0) return DSA_OK;
   if (!kv || !aligned(kv, 16) || !seq || !aligned(seq, 4) || !pos || !aligned(pos, 4) || (lacking && !aligned(lacking, 4)))
     return DSA_ERR_INVALID_ARG;

@@ -40,3 +40,9 @@ def test_drafts_over_the_probabilities(lib, at):  # noqa: F811
     for k in ("accepted", "token"):
         assert f(**{k: at[0] + 156}) == f(**{k: at[0] - 4}) == f(**{k: at[1] + 116}) == f(**{k: at[1]}) == INVALID, k
     assert f(R=2 ** 27, G=2 ** 20, V=2 ** 30) == f(R=2 ** 10, G=2 ** 20 - 1, V=2 ** 30) == UNSUPPORTED
+
+
+def test_strides_past_what_memory_holds(lib, at):  # noqa: F811
+    """A last row whose place no 64-bit count of bytes reaches: refused before it is formed."""
+    f = lambda stride, N=4: lib.dsa_store_kv(at[0], stride, at[1], at[2], N, 128, at[3], 2, 64, at[4], 1, 2, None, None)  # noqa: E731
+    assert f(2 ** 60) == f(2 ** 62) == f(2 ** 63 - 8) == f(2 ** 61 // 3 // 8 * 8 + 8, N=3) == f(2 ** 31, N=2 ** 31 - 1) == INVALID
