@@ -499,7 +499,8 @@ DSA_API dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* pages, int 
  * w = max(target[r][a] - draft[r][a], 0) where a < n (target[r][a] where that is all zero), else target[r][a].
  * The sums are of whole multiples of 2^-55, to which each probability is rounded (above 1: 1; below 0 or no number: 0), and so
  * exact.  token[r] = -1 where w is all zero; count[r] < 0 (a place without a sequence): 0 and -1.
- * The step's sequences then grow by accepted + 1 tokens: held + added of the next dsa_step_maps, without the host.
+ * A step's sequences get added = min(count, G) + 1 rows and then hold accepted + 1 more, those with count < 0 none in either:
+ * held and added of the next dsa_step_maps, without the host.
  *   target  float [R][G + 1][V];  draft  float [R][G][V];  tokens  int32 [R][G];  count  int32 [R]
  *   u       float [R][G + 1] in [0, 1);  accepted, token  int32 [R]   OUTPUT
  * R < 2^28, R * (G + 1) * V < 2^60 (DSA_ERR_UNSUPPORTED); V >= 1, rows whose probabilities sum to less than 256.
