@@ -271,6 +271,23 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// The largest of three values, no number where one of them is none.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// A value that is a number where all of 16 are.
+__device__ __forceinline__ float any_nan(const float (&o)[16]) {
+  float a = max3_nan(o[0], o[1], o[2]), b = max3_nan(o[3], o[4], o[5]);
+#pragma unroll
+  for (int j = 6; j < 14; j += 4) {
+    a = max3_nan(a, o[j], o[j + 1]);
+    b = max3_nan(b, o[j + 2], o[j + 3]);
+  }
+  return max3_nan(max3_nan(a, b, o[14]), o[15], o[15]);
+}
+
 // The low n bits (n in [0, 32]).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
@@ -908,10 +925,13 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
             float n0, n1;
             unpack_f32x2(none, n0, n1);
             if (__any_sync(0xffffffffu, mine && (n0 != n0 || n1 != n1))) {
-              // Weights of 0 times values that are no numbers would still be none.  So the kv rows that hold such are zeroed (by each
-              // warp with rows of q of the block's tokens: all of those find them), and rows of q that see such a score get a sum that
-              // is none.  (Scores of other rows of q show nothing: these may hold anything.  Four tokens over 20000 rows beside
+              // Weights of 0 times values that are no numbers would still be none.  So the kv rows that hold such are taken out (by each
+              // warp with rows of q of the block's tokens: all of those find them), and rows of q that see one get a sum that is
+              // none.  What was taken out is -0 all over, so that a warp that comes later finds it as well: a 16-byte piece of it, at
+              // least, where another is at it.  (A row that holds such a piece of its own is not written, and counts only where its
+              // score overflows.)  Scores of other rows of q show nothing: these may hold anything.  (Four tokens over 20000 rows beside
               // four places with q that is none, D = 128: 47 us with their scores looked at, 20.5 without.)
+              constexpr uint32_t kOut = 0x80008000u;
               bool sees = false;
 #pragma unroll 1
               for (int i = 0; i < kKeys; i += 16) {
@@ -922,10 +942,10 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 16; ++c)
                   if (i + c < tail && !(fabsf(y[c]) < INFINITY)) is |= 1u << c;
-                sees |= (is & (mask_of(i / 32) >> (i & 16))) != 0u;
+                const uint32_t seen = is & (mask_of(i / 32) >> (i & 16));
                 is = __reduce_or_sync(0xffffffffu, mine ? is : 0u);
                 while (is != 0u) {
-                  const int key = i + __ffs(is) - 1;
+                  const int c = __ffs(is) - 1, key = i + c;
                   is &= is - 1u;
                   const auto at = [&](int j) -> uint4* {  // piece j of the row
                     const uint32_t tile = gb * kTi + (j / 8) / L::kTileChunks;
@@ -933,18 +953,22 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
                     const int chunk = static_cast<int>(tile % kRing) * L::kTileBytes + ((j / 8) % L::kTileChunks) * L::kChunkBytes;
                     return reinterpret_cast<uint4*>(kv_s + chunk + key * 128) + j % 8;
                   };
-                  bool bad = false;
+                  uint32_t found = 0u;  // bit 0: what is no number, bit 1: what was taken out
 #pragma unroll 1
                   for (int j = lane; j < kCh * 8; j += 32) {
                     const uint4 v = *at(j);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    if (((v.x ^ kOut) | (v.y ^ kOut) | (v.z ^ kOut) | (v.w ^ kOut)) == 0u) found |= 2u;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) bad |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
+                    for (int k = 0; k < 4; ++k)
+                      if ((w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u) found |= 1u;
                   }
-                  if (__any_sync(0xffffffffu, bad)) {
+                  found = __reduce_or_sync(0xffffffffu, found);
+                  if ((found & 1u) != 0u) {
 #pragma unroll 1
-                    for (int j = lane; j < kCh * 8; j += 32) *at(j) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int j = lane; j < kCh * 8; j += 32) *at(j) = make_uint4(kOut, kOut, kOut, kOut);
                   }
+                  sees |= found != 0u && ((seen >> c) & 1u) != 0u;
                 }
               }
               if (sees) l0 = __int_as_float(0x7FFFFFFF);
@@ -1048,6 +1072,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       const int way = part_s[n & 1].way;
       const int64_t place = 2 * static_cast<int64_t>(cta) + (way == kPgHead ? 1 : 0);  // of a shared unit's part
       float f = 1.f;
+      float none = 0.f;  // no number where an output is
       if (r < un.cols) {
         if (way == kPgWhole) {
           f = paged_factor(bound, sum, p.sink, p.head(un.skip + r), p.lse != nullptr && group == 0 ? p.lse + un.row0 + r : nullptr);
@@ -1071,6 +1096,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] = 0.f;
           }
+          none = max3_nan(none, any_nan(o), 0.f);
           if (r < un.cols && way == kPgWhole) {
             uint32_t w[8];
 #pragma unroll
@@ -1097,7 +1123,25 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         mbar_arrive(o_empty);
         mbar_arrive(&part_empty[n & 1]);
       }
-      named_bar_sync(kTcEpiBar, kPgSoft);  // bounds and sums are written anew by the next part
+      // (behind it bounds and sums are written anew by the next part)
+      if (bar_or(kTcEpiBar, kPgSoft, none != none && r < un.cols)) {
+        // An infinite value of weight 0 (a score of minus infinity) in a block that every row sees: the rest of that row of outputs
+        // becomes none either, as in blocks whose masks had the value found.
+        sum_s[group * N + r] = none != none ? 1.f : 0.f;
+        named_bar_sync(kTcEpiBar, kPgSoft);
+        if (r < un.cols && sum_s[r] + sum_s[N + r] != 0.f) {
+          const float nan = __int_as_float(0x7FFFFFFF);
+          if (way == kPgWhole) {
+            uint4* to = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(un.row0) + r) * D + group * (D / 2));
+#pragma unroll 1
+            for (int d = 0; d < D / 16; ++d) to[d] = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+            if (p.lse != nullptr && group == 0) p.lse[un.row0 + r] = nan;
+          } else if (group == 0) {
+            __stcg(p.stats + place * 2 * N + N + r, nan);
+          }
+        }
+        named_bar_sync(kTcEpiBar, kPgSoft);
+      }
     }
   } else {
     // ------------------------------------------------------------------ softmax and output, a thread with a row of the block
@@ -1347,7 +1391,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       }
       named_bar_sync(kTcEpiBar, kPgSoft);
       const int dim = quarter * 32 + lane;           // of a tile
-      const bool dims = D >= 128 || quarter < 2;     // (the upper half of a 64-dim row's tile is padding)
+      uint32_t none = 0u;                            // this warp's columns with an output that is no number
       if (used) {
 #pragma unroll 1
         for (int m = 0; m < kTi; ++m) {
@@ -1361,13 +1405,17 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 16; ++j) o[j] = 0.f;
             }
-            if (way != kPgWhole) {
-              if (dims) {
-                float* to = p.partial + (place * N + c) * D + 128 * m + dim;
+            const float odd = any_nan(o);
+            if (__any_sync(0xffffffffu, odd != odd)) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (c + j < un.cols) __stcg(to + j * D, o[j]);
-              }
+              for (int j = 0; j < 16; ++j)
+                if (o[j] != o[j]) none |= 1u << (c - gc + j);
+            }
+            if (way != kPgWhole) {
+              float* to = p.partial + (place * N + c) * D + 128 * m + dim;
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (c + j < un.cols) __stcg(to + j * D, o[j]);
               continue;
             }
             // Neighbouring lanes (dims) trade halves of a pair of columns, so that each stores two dims of one: 64
@@ -1381,7 +1429,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
               const uint32_t w = *reinterpret_cast<const uint32_t*>(&two);
               const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 1);
               const uint32_t own = second ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
-              if (dims && c + j + (second ? 1 : 0) < un.cols) *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(j) * D) = own;
+              if (c + j + (second ? 1 : 0) < un.cols) *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(j) * D) = own;
             }
           }
         }
@@ -1392,7 +1440,26 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         mbar_arrive(o_empty);
         mbar_arrive(&part_empty[n & 1]);
       }
-      named_bar_sync(kTcEpiBar, kPgSoft);  // alpha_s, neg_s and P's place are written anew by the next part
+      none &= low_bits(max(un.cols - gc, 0));
+      // (behind it alpha_s, neg_s and P's place are written anew by the next part)
+      if (bar_or(kTcEpiBar, kPgSoft, none != 0u)) {
+        // As at D <= 256: the rest of a row of outputs with one that is no number becomes none either.
+        none = __reduce_or_sync(0xffffffffu, none);
+        red_s[quarter * N + gc + lane] = ((none >> lane) & 1u) != 0u ? 1.f : 0.f;
+        named_bar_sync(kTcEpiBar, kPgSoft);
+        const float nan = __int_as_float(0x7FFFFFFF);
+#pragma unroll 1
+        for (int c = gc; c < min(gc + 32, un.cols); ++c) {
+          if (red_s[c] + red_s[N + c] + red_s[2 * N + c] + red_s[3 * N + c] == 0.f) continue;
+          if (way == kPgWhole) {
+            for (int m = 0; m < kTi; ++m) p.out[(static_cast<int64_t>(un.row0) + c) * D + 128 * m + dim] = 0x7FFFu;
+            if (p.lse != nullptr && quarter == 0 && lane == 0) p.lse[un.row0 + c] = nan;
+          } else if (quarter == 0 && lane == 0) {
+            __stcg(p.stats + place * 2 * N + N + c, nan);
+          }
+        }
+        named_bar_sync(kTcEpiBar, kPgSoft);
+      }
     }
   }
 

@@ -77,3 +77,85 @@ def test_places_without_a_token_may_hold_anything(D):
     time = lambda x: best(lambda: dsa.paged_attn(x, pages, table, s, p, out=out[:7], workspace=work))  # noqa: E731
     assert time(x[:7].contiguous()) < 1.4 * time(q[:7].contiguous())
     assert dsa.get_device_error() == 0
+
+
+# Tokens whose sequence is one of 600 rows with a value that is no number in row 70, or one of 40 without; how the block of that row is
+# met: seen whole by all of a unit's rows of q, cut by a token's own position, at a window's edge, in a unit of two sequences.
+KINDS = {
+    "whole": ([0], [599], None, 0),
+    "whole, two tokens": ([0, 0], [598, 599], None, 0),
+    "own row behind": ([0, 0, 0], [100, 69, 70], None, 0),
+    "window's edge": ([0, 0], [169, 170], 100, 0),
+    "first rows": ([0, 0], [599, 595], 30, 71),
+    "two sequences": ([0, 1, 0], [599, 39, 500], None, 0),
+}
+
+
+def sees(seq, pos, window, first, at):
+    return torch.tensor([r == 0 and p >= at and (window is None or at > p - window or at < first) for r, p in zip(seq, pos)])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,H", [(64, 16), (128, 40), (256, 9), (512, 30)])
+def test_infinite_values(D, H, kind):
+    """Whatever the score of a row with infinite values is (infinite of either sign, or no number), all outputs of a token that sees it
+    and its lse are no numbers, however its block is met; other tokens' are as without it."""
+    rng = np.random.default_rng(D)
+    at, dim = 70, D // 3
+    seq, pos, window, first = KINDS[kind]
+    for values in ([math.inf], [-math.inf], [math.inf, -math.inf]):
+        pages, table, kv = PR.pool([600, 40], 32, D, rng)
+        for i, v in enumerate(values):
+            pages[int(table[0, at // 32]), at % 32, dim + i] = v
+        q = torch.from_numpy(rng.standard_normal((len(seq), H, D))).to(bf16)
+        q[:, 0, dim] = 0
+        lse = torch.empty(len(seq), H, device="cuda")
+        out = dsa.paged_attn(q.cuda(), pages, table, i32(seq), i32(pos), window=window, first=first, lse=lse)
+        hit = sees(seq, pos, window, first, at)
+        assert hit.any() and (q[hit][:, :, dim] > 0).any() and (q[hit][:, :, dim] < 0).any()
+        assert torch.isnan(out.cpu()[hit]).all() and torch.isnan(lse.cpu()[hit]).all()
+        ref = PR.attn(q, kv, seq, pos, window, first, None, 1 / math.sqrt(D))
+        PR.check_attn(out.cpu()[~hit], lse.cpu()[~hit], [x[~hit] for x in ref], D)
+    assert dsa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+def test_infinite_values_of_a_shared_unit(D):
+    """The same where many CTAs have a part of the unit, and one of them the row; and in one of two units' tokens."""
+    rng = np.random.default_rng(D)
+    H, n, at = 6, 20000, 9000
+    pages, table, kv = PR.pool([n], 64, D, rng)
+    pages[int(table[0, at // 64]), at % 64, 1] = math.inf
+    q = torch.from_numpy(rng.standard_normal((2, H, D))).to(bf16)
+    for pos in ([n - 1, at - 1], [n - 1, n - 2]):
+        lse = torch.empty(2, H, device="cuda")
+        out = dsa.paged_attn(q.cuda(), pages, table, i32([0, 0]), i32(pos), lse=lse)
+        hit = torch.tensor(pos) >= at
+        assert torch.isnan(out.cpu()[hit]).all() and torch.isnan(lse.cpu()[hit]).all()
+        ref = PR.attn(q, kv, [0, 0], pos, None, 0, None, 1 / math.sqrt(D))
+        PR.check_attn(out.cpu()[~hit], lse.cpu()[~hit], [x[~hit] for x in ref], D)
+    assert dsa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,H", [(64, 16), (128, 40), (256, 9), (512, 30)])
+def test_scores_below_fp32(D, H, kind):
+    """Finite values whose score overflows to minus infinity weigh 0, however their block is met; beside them a row that begins with
+    eight zeros of negative sign counts as any other."""
+    rng = np.random.default_rng(D)
+    at, dim = 70, D - 2
+    seq, pos, window, first = KINDS[kind]
+    pages, table, kv = PR.pool([600, 40], 32, D, rng)
+    for r, rows in enumerate(kv):
+        rows[:, dim] = 0
+        if r == 0:
+            rows[at + 1, :8] = -0.0
+            rows[at, dim] = 2.0 ** 100
+        for j in range(len(rows)):
+            pages[int(table[r, j // 32]), j % 32] = rows[j].to(bf16)
+    q = torch.from_numpy(rng.standard_normal((len(seq), H, D))).to(bf16)
+    q[:, :, dim] = -(2.0 ** 100)
+    lse = torch.empty(len(seq), H, device="cuda")
+    out = dsa.paged_attn(q.cuda(), pages, table, i32(seq), i32(pos), window=window, first=first, lse=lse)
+    PR.check_attn(out, lse, PR.attn(q, kv, seq, pos, window, first, None, 1 / math.sqrt(D), {(0, at)}), D)
+    assert dsa.get_device_error() == 0
