@@ -852,8 +852,9 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     const int quarter = warp & 3;               // tensor-memory lane quarter
     const int r = quarter * 32 + lane;          // the unit's row
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    // (a scale of 0 is taken as the least number, so that what is masked stays minus infinity)
-    const float to_log2 = p.scale == 0.f ? 1.17549435e-38f : p.scale * 1.4426950408889634f;
+    // (0 is taken as the least number, 2^-149, so that what is masked stays minus infinity: the largest score becomes 2^-21)
+    float to_log2 = p.scale * 1.4426950408889634f;
+    if (to_log2 == 0.f) to_log2 = 1.40129846e-45f;
     const uint64_t to_log2_2 = pack_f32x2(to_log2, to_log2);
     volatile float* bound_s = neg_s;                                  // [N]
     float* sum_s = alpha_s;                                           // [2][N]

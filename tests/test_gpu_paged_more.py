@@ -159,3 +159,23 @@ def test_scores_below_fp32(D, H, kind):
     out = dsa.paged_attn(q.cuda(), pages, table, i32(seq), i32(pos), window=window, first=first, lse=lse)
     PR.check_attn(out, lse, PR.attn(q, kv, seq, pos, window, first, None, 1 / math.sqrt(D), {(0, at)}), D)
     assert dsa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+def test_scale_of_zero(D):
+    """All rows weigh the same, however large their products are (2^126 and less here), in whole and in masked blocks."""
+    rng = np.random.default_rng(D)
+    n, H = 300, 4
+    pages, table, kv = PR.pool([n], 32, D, rng)
+    kv[0][:, 3] = torch.from_numpy(2.0 ** rng.integers(0, 64, n))
+    for j in range(n):
+        pages[int(table[0, j // 32]), j % 32] = kv[0][j].to(bf16)
+    q = torch.from_numpy(rng.standard_normal((3, H, D))).to(bf16)
+    q[:, :, 3] = 2.0 ** 63
+    seq, pos = [0, 0, 0], [299, 100, 0]
+    sink = torch.zeros(H, device="cuda")
+    for window in (None, 40):
+        lse = torch.empty(3, H, device="cuda")
+        out = dsa.paged_attn(q.cuda(), pages, table, i32(seq), i32(pos), window=window, attn_sink=sink, scale=0.0, lse=lse)
+        PR.check_attn(out, lse, PR.attn(q, kv, seq, pos, window, 0, sink, 0.0), D)
+    assert dsa.get_device_error() == 0
