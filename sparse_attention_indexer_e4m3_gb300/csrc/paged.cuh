@@ -25,6 +25,13 @@ struct StepMapArgs {
   int32_t* ke;
 };
 
+// How the (token, head) rows of a call are cut into units.
+struct PagedCut {
+  int rows;    // of a unit
+  int groups;  // units of a token, where a token's heads take several of their own; else 1
+  int units;
+};
+
 struct PagedAttnParams {
   PageTable pages;
   const int32_t* seq;   // [T]
@@ -34,15 +41,17 @@ struct PagedAttnParams {
   float* lse;           // [T][H] or null
   float* partial;       // [2 CTAs][N][D] partial outputs of units that several CTAs share
   float* stats;         // [2 CTAs][2][N] their bounds and sums
-  int4* shared;         // [min(units, CTAs)] the shared units: unit, first CTA, CTAs (0: none)
+  int4* shared;         // [min(units, CTAs)] the shared units: unit, first CTA, CTAs (0: none), cut
   int T, H;
-  int rows;             // (token, head) rows of a unit
-  int groups;           // units of a token, where a token's heads take several of their own; else 1
-  int units;
+  PagedCut whole;       // whole tokens, or a token's heads in equal units of their own
+  PagedCut any;         // units wherever they begin (as `whole` where there is no choice)
+  int guess;            // the cut to begin with: 0 whole, 1 any
+  float per_token;      // walks over a sequence's rows that the second cut takes more than the first: for each token,
+  float per_run;        // and for each run of tokens of one sequence
   int window;           // rows that a token sees up to its own
   int first;            // first rows that stay visible
   int box_rows;         // rows of one copy: those of a page, at most a block's
-  float scale;
+  alignas(8) float to_log2[2];  // the softmax scale in log2 units, twice
   uint32_t h_mul;       // n / H = (mulhi(n, h_mul) + n) >> h_shift for 0 <= n < 2^31 (set_heads)
   int h_shift;
 

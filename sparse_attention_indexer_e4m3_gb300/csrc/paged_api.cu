@@ -5,6 +5,8 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <limits>
+#include <numeric>
 
 #include "../../include/dsa.h"
 #include "api_checks.h"
@@ -23,30 +25,35 @@ dsa_status check_table(PageTable* c, const int32_t* table, int R, int M, int P, 
   return DSA_OK;
 }
 
-// How the (token, head) rows of a call are cut into units of at most N rows.  (N rows wherever they begin, for tokens of sequences
-// of their own, too: window decode of 20 heads 27.2 us for 23.6; 64 sequences of 4096 rows, 150 heads of 256 88 us for 71, 100
-// heads of 512 115 for 108.  Whole tokens where many share a sequence would leave columns empty: 4-token drafts of 150 heads of
-// 256, 75 columns of 128 instead of all.)
-struct Units {
-  int rows, groups;
-  int64_t units;
+// The two ways in which the (token, head) rows of a call may be cut into units of at most N rows.  Whole tokens, m a unit (or a
+// token's heads in equal units of their own): no token has its rows walked over twice, and up to half of the columns are idle.  Or
+// N rows wherever they begin: no column is idle, and a token in two units has its rows walked over by both.  A run of k tokens of
+// a sequence is walked over by (k + m - 1) / m units (k of each of its groups) or by (k H + N - gcd(H, N)) / N, on the average over its
+// place, so the better one depends on how many tokens share a sequence: the kernel counts them (places without a token, and the
+// table's height, say nothing) and takes the cut with fewer walks.  Measured, whole and anywhere: 64 sequences of 4096 rows, a token each,
+// 150 heads of 256 75 and 89 us, 100 heads of 512 112 and 118, 20 heads of 128 40.9 and 42.9; 200 tokens over 8192 rows, 150
+// heads of 256 272 and 182, 65 heads of 128 86 and 59, 40 heads of 512 207 and 144.
+struct Cuts {
+  PagedCut whole, any;
+  float per_token, per_run;
 };
-Units units_of(int T, int H, int D, int R) {
+PagedCut cut_of(int64_t rows, int groups, int T, int H) {
+  const int64_t units = groups > 1 ? static_cast<int64_t>(T) * groups : (static_cast<int64_t>(T) * H + rows - 1) / rows;
+  return {static_cast<int>(rows), groups, static_cast<int>(units)};
+}
+Cuts cuts_of(int T, int H, int D) {
   const int N = paged_attn_cols(D);
-  Units u{0, 1, 0};
-  if (H <= N && T <= R) {
-    // Whole tokens: where no two share a sequence, a token in two units would have its rows walked over by both.
-    u.rows = std::min(kPagedMaxTokens, N / H) * H;
-  } else if (T <= R) {
-    // A token's heads in equal units of their own.
-    u.groups = H / N + (H % N != 0 ? 1 : 0);
-    u.rows = H / u.groups + (H % u.groups != 0 ? 1 : 0);
-  } else {
-    // Tokens of the same sequence: N rows wherever they begin (n rows lie in n / H + 2 tokens at most).
-    u.rows = static_cast<int>(std::min<int64_t>(N, static_cast<int64_t>(kPagedMaxTokens - 2) * H));
-  }
-  u.units = u.groups > 1 ? static_cast<int64_t>(T) * u.groups : (static_cast<int64_t>(T) * H + u.rows - 1) / u.rows;
-  return u;
+  const int tokens = H <= N ? std::min(kPagedMaxTokens, N / H) : 0;  // m
+  const int groups = H <= N ? 1 : H / N + (H % N != 0 ? 1 : 0);
+  Cuts c;
+  c.whole = H <= N ? cut_of(tokens * H, 1, T, H) : cut_of(H / groups + (H % groups != 0 ? 1 : 0), groups, T, H);
+  // (no choice: a token alone, heads that fill N, more tokens than a unit of any N rows may hold: n rows lie in n / H + 2 of them)
+  const bool same = T == 1 || (H <= N && N % H == 0) || N / H + 2 > kPagedMaxTokens;
+  c.any = same ? c.whole : cut_of(N, 1, T, H);
+  const float n = static_cast<float>(N), h = static_cast<float>(H), m = static_cast<float>(tokens);
+  c.per_token = h / n - (H <= N ? 1.f / m : static_cast<float>(groups));
+  c.per_run = static_cast<float>(N - std::gcd(H, N)) / n - (H <= N ? (m - 1.f) / m : 0.f);
+  return c;
 }
 
 struct Workspace {
@@ -139,9 +146,8 @@ dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* pages, int P, int p
   if (!q || !aligned(q, 16) || !out || !aligned(out, 16) || !seq || !aligned(seq, 4) || !pos || !aligned(pos, 4))
     return DSA_ERR_INVALID_ARG;
   if ((attn_sink && !aligned(attn_sink, 4)) || (lse && !aligned(lse, 4))) return DSA_ERR_INVALID_ARG;
-  const Units un = units_of(T, H, D, R);
-  // rows of q and of the pages are coordinates of the copies, which are ints
-  if (static_cast<int64_t>(T) * H > INT_MAX / 2 || un.units > INT_MAX / 2 || static_cast<int64_t>(P) * page_rows > INT_MAX)
+  // rows of q and of the pages are coordinates of the copies, which are ints (and there are no more units than rows of q)
+  if (static_cast<int64_t>(T) * H > INT_MAX / 2 || static_cast<int64_t>(P) * page_rows > INT_MAX)
     return DSA_ERR_UNSUPPORTED;
   const int64_t values = static_cast<int64_t>(T) * H * D, held = static_cast<int64_t>(P) * page_rows * D;
   const int64_t logs = lse ? static_cast<int64_t>(T) * H : 0, entries = static_cast<int64_t>(R) * M, sinks = attn_sink ? H : 0;
@@ -167,9 +173,14 @@ dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* pages, int P, int p
   if (!make_bf16_map(&kvmap, P > 0 ? pages : q, P > 0 ? static_cast<int64_t>(P) * page_rows : 1, D, box) ||
       !make_bf16_map(&qmap, q, static_cast<int64_t>(T) * H, D, paged_attn_cols(D)))
     return DSA_ERR_CUDA;
+  const Cuts cuts = cuts_of(T, H, D);
+  // (at D <= 256 a scale of 0 is the least number, 2^-149, so that what is masked stays minus infinity: the largest score becomes 2^-21)
+  float to_log2 = scale * 1.4426950408889634f;
+  if (to_log2 == 0.f && D <= 256) to_log2 = std::numeric_limits<float>::denorm_min();
   PagedAttnParams p{c, seq, pos, attn_sink, out, lse, reinterpret_cast<float*>(ws + w.partial),
-                          reinterpret_cast<float*>(ws + w.stats), reinterpret_cast<int4*>(ws), T, H, un.rows, un.groups,
-                          static_cast<int>(un.units), window == 0 ? INT_MAX : window, first, box, scale, 0u, 0};
+                    reinterpret_cast<float*>(ws + w.stats), reinterpret_cast<int4*>(ws), T, H, cuts.whole, cuts.any,
+                    cuts.any.rows != cuts.whole.rows && T > R ? 1 : 0, cuts.per_token, cuts.per_run,
+                    window == 0 ? INT_MAX : window, first, box, {to_log2, to_log2}, 0u, 0};
   p.set_heads(H);
   return done(launch_paged_attn(D, dev.sms, kvmap, qmap, p, dev.err, static_cast<cudaStream_t>(stream)));
 }

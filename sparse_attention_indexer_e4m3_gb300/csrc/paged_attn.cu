@@ -40,9 +40,10 @@ cudaError_t launch_d(int grid, const CUtensorMap& kvmap, const CUtensorMap& qmap
   c.numAttrs = 1;
   e = cudaLaunchKernelEx(&c, paged_attn_kernel<D>, kvmap, qmap, p, err);
   if (e != cudaSuccess || grid == 1) return e;  // (one CTA shares nothing)
-  // the shared units: an entry each, over enough blocks for all SMs where they are few
-  const int entries = std::min(p.units, grid), items = p.rows * std::max(1, D / 128);
-  c.gridDim = dim3(static_cast<unsigned>(entries), static_cast<unsigned>(std::min(items, std::max(1, 8 * grid / entries))));
+  // the shared units: an entry each, over eight blocks for each SM where they are few (as many as the cut that is expected has)
+  const int entries = paged_entries(p, grid), items = std::max(p.whole.rows, p.any.rows) * std::max(1, D / 128);
+  const int units = std::min(p.guess != 0 ? p.any.units : p.whole.units, grid);
+  c.gridDim = dim3(static_cast<unsigned>(entries), static_cast<unsigned>(std::min(items, std::max(1, 8 * grid / units))));
   c.blockDim = dim3(kPgJoinThreads);
   c.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&c, paged_join_kernel<D>, p);

@@ -93,7 +93,10 @@ struct PagedPart {
   int unit;
   int blocks;   // of this CTA
   int way;      // kPgWhole: the CTA has all blocks; kPgHead: the first ones; kPgTail: later ones
-  int pad;
+  int row0;     // the unit's rows of q, and the rows of its first token before them
+  int cols;
+  int skip;
+  int pad[2];
 };
 constexpr int kPgWhole = 0, kPgHead = 1, kPgTail = 2;
 
@@ -137,7 +140,7 @@ struct PagedLayout {
   static_assert(kRing >= kScores * kTiles, "the score products go ahead of the weighted sums");
   static_assert(kSmem <= 232448, "shared memory");
 };
-static_assert(sizeof(PagedBlock) == 64 && sizeof(PagedPart) == 16, "layout");
+static_assert(sizeof(PagedBlock) == 64 && sizeof(PagedPart) == 32, "layout");
 
 // mbar_wait with its loop out of line (written out at each of the kernel's waits it made 90 KB of code, and instructions were
 // waited for), and the timer, which takes some hundred cycles to read, only after some rounds.
@@ -163,21 +166,31 @@ __device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, volat
 
 // ------------------------------------------------------------------------------------ units and runs
 
+// Entries of the shared units in the workspace: one for each unit of either cut, or for each CTA where these are fewer.
+__host__ __device__ __forceinline__ int paged_entries(const PagedAttnParams& p, int ctas) {
+  const int units = p.whole.units > p.any.units ? p.whole.units : p.any.units;
+  return units < ctas ? units : ctas;
+}
+
+constexpr int kPgCount = 4;  // places of a thread that the choice of the cut looks at
+
 struct PagedUnit {
   int row0, cols;  // its (token, head) rows
   int t0, n;       // tokens that they lie in
   int skip;        // rows of the first token before them
 };
 
-__device__ __forceinline__ PagedUnit paged_unit(const PagedAttnParams& p, int u) {
+// Unit u of the cut `any` or of `whole`.
+__device__ __forceinline__ PagedUnit paged_unit(const PagedAttnParams& p, bool any, int u) {
+  const int rows = any ? p.any.rows : p.whole.rows, groups = any ? 1 : p.whole.groups;
   PagedUnit r;
-  if (p.groups > 1) {
-    const int t = u / p.groups, h = (u % p.groups) * p.rows;
+  if (groups > 1) {
+    const int t = u / groups, h = (u % groups) * rows;
     r.row0 = t * p.H + h;
-    r.cols = min(p.rows, p.H - h);
+    r.cols = min(rows, p.H - h);
   } else {
-    r.row0 = u * p.rows;
-    r.cols = min(p.rows, p.T * p.H - r.row0);
+    r.row0 = u * rows;
+    r.cols = min(rows, p.T * p.H - r.row0);
   }
   r.t0 = p.by_H(r.row0);
   r.n = p.by_H(r.row0 + r.cols - 1) - r.t0 + 1;
@@ -466,15 +479,52 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   // Each unit's blocks, kept in the ring's place (where they fit: 32768 units are prompts of 65536 tokens and 64 heads).
   constexpr int kKeep = L::kQ / 4;
   int* blocks_s = reinterpret_cast<int*>(kv_s);
-  const bool keep = p.units <= kKeep;
-  if (keep) {
-#pragma unroll 1
-    for (int u = static_cast<int>(threadIdx.x); u < p.units; u += kThreads) blocks_s[u] = paged_blocks(p, paged_unit(p, u), kKeys);
-    __syncthreads();
+  // The cut: of these places (evenly spread ones where there are more) those with a token, and those whose next has one of the same
+  // sequence.  (Read beside the blocks of the cut that is expected; the choice takes 0.7 of window decode's 24.7 us.)
+  const bool choose = p.any.rows != p.whole.rows;
+  const int looked = min(p.T, kPgCount * kThreads);
+  int seq_of[kPgCount], seq_next[kPgCount];
+#pragma unroll
+  for (int i = 0; i < kPgCount; ++i) {
+    seq_of[i] = seq_next[i] = -1;
+    const int at = static_cast<int>(threadIdx.x) + i * kThreads;
+    if (choose && at < looked) {
+      const int t = looked == p.T ? at : static_cast<int>(static_cast<int64_t>(at) * p.T / looked);
+      seq_of[i] = ld_after_wait(p.seq + t);
+      if (t + 1 < p.T) seq_next[i] = ld_after_wait(p.seq + t + 1);
+    }
   }
-  const auto blocks_of = [&](int u) { return keep ? blocks_s[u] : paged_blocks(p, paged_unit(p, u), kKeys); };
-  const int u_first = static_cast<int>(static_cast<int64_t>(p.units) * threadIdx.x / kThreads);
-  const int u_last = static_cast<int>(static_cast<int64_t>(p.units) * (threadIdx.x + 1) / kThreads);
+  bool any = p.guess != 0, keep;
+  int units;
+#pragma unroll 1
+  for (bool chosen = !choose;; chosen = true) {
+    units = any ? p.any.units : p.whole.units;
+    keep = units <= kKeep;
+    if (keep) {  // (each entry by the thread that wrote it before)
+#pragma unroll 1
+      for (int u = static_cast<int>(threadIdx.x); u < units; u += kThreads) blocks_s[u] = paged_blocks(p, paged_unit(p, any, u), kKeys);
+    }
+    int* count_s = end_s;  // [warps]
+    static_assert(kThreads / 32 <= 2 * kPgMaxTokens && kPgCount * kThreads < 65536, "counts");
+    int n = 0;  // tokens, and in the upper half those that are joined by the next
+    if (!chosen) {
+#pragma unroll
+      for (int i = 0; i < kPgCount; ++i)
+        if (static_cast<unsigned>(seq_of[i]) < static_cast<unsigned>(p.pages.R)) n += seq_next[i] == seq_of[i] ? 65537 : 1;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0) count_s[warp] = n;
+    }
+    __syncthreads();
+    if (chosen) break;
+    n = __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? count_s[lane] : 0);
+    const int tokens = n & 0xFFFF, runs = tokens - (n >> 16);
+    const bool better = p.per_token * static_cast<float>(tokens) + p.per_run * static_cast<float>(runs) < 0.f;  // (in all threads)
+    if (better == any) break;
+    any = better;
+  }
+  const auto blocks_of = [&](int u) { return keep ? blocks_s[u] : paged_blocks(p, paged_unit(p, any, u), kKeys); };
+  const int u_first = static_cast<int>(static_cast<int64_t>(units) * threadIdx.x / kThreads);
+  const int u_last = static_cast<int>(static_cast<int64_t>(units) * (threadIdx.x + 1) / kThreads);
   int64_t mine = 0;
 #pragma unroll 1
   for (int u = u_first; u < u_last; ++u) mine += blocks_of(u) + kUnitCost;
@@ -534,13 +584,16 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   if (threadIdx.x == 0) {
     // entries of the shared units: by unit, written by the CTA that it starts on, where there are no more than CTAs, else by CTA
     const bool shared = !idle && to_block < plan_s[6] && (unit1 > unit0 || starts);
-    const int4 entry = shared ? make_int4(unit1, cta, plan_s[5] - cta + 1, 0) : make_int4(0, 0, 0, 0);
-    if (p.units > static_cast<int>(gridDim.x)) {
+    const int4 entry = shared ? make_int4(unit1, cta, plan_s[5] - cta + 1, any) : make_int4(0, 0, 0, 0);
+    if (units > static_cast<int>(gridDim.x)) {
       p.shared[cta] = entry;
     } else {
       for (int u = starts ? unit0 : unit0 + 1; u <= unit1; ++u) p.shared[u] = u == unit1 ? entry : make_int4(0, 0, 0, 0);
     }
   }
+  if (cta == 0)  // entries that the other cut would have
+    for (int u = units + static_cast<int>(threadIdx.x); u < paged_entries(p, static_cast<int>(gridDim.x)); u += kThreads)
+      p.shared[u] = make_int4(0, 0, 0, 0);
   const auto gone = [&]() -> bool { return __any_sync(0xffffffffu, *abort_flag != 0) != 0; };
 
   if (warp == 2) {
@@ -551,17 +604,17 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     static_assert(kPages * kPgBatch <= 32, "a lane for each page of a batch");
     int seq = -1, end = 0;  // of the unit's token `lane`, read a unit ahead
     if (unit0 <= unit1) {
-      const PagedUnit un = paged_unit(p, unit0);
+      const PagedUnit un = paged_unit(p, any, unit0);
       if (lane < un.n) paged_token(p, un.t0 + lane, seq, end);
     }
     bool ok = true;
     for (int u = unit0; ok && u <= unit1; ++u) {
-      const PagedUnit un = paged_unit(p, u);
+      const PagedUnit un = paged_unit(p, any, u);
       const int my_seq = seq, my_end = end;
       seq = -1;
       end = 0;
       if (u < unit1) {
-        const PagedUnit next = paged_unit(p, u + 1);
+        const PagedUnit next = paged_unit(p, any, u + 1);
         if (lane < next.n) paged_token(p, next.t0 + lane, seq, end);
       }
       // tokens that begin a run, and the runs' spans: reduced over their lanes
@@ -596,6 +649,9 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         part_s[n & 1].unit = u;
         part_s[n & 1].blocks = b1 - b0;
         part_s[n & 1].way = way;
+        part_s[n & 1].row0 = un.row0;
+        part_s[n & 1].cols = un.cols;
+        part_s[n & 1].skip = un.skip;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&part_full[n & 1]);
@@ -691,6 +747,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       if (!wait(&part_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, 0x83)) break;
       const int u = __reduce_max_sync(0xffffffffu, part_s[n & 1].unit);
       const int nb = __reduce_max_sync(0xffffffffu, part_s[n & 1].blocks);
+      const int y = __reduce_max_sync(0xffffffffu, part_s[n & 1].row0);
       if (lane == 0) mbar_arrive(&part_empty[n & 1]);
       __syncwarp();
       if (u < 0) break;
@@ -700,7 +757,6 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         if (nq >= kQb && !wait(&q_empty[qb], (nq / kQb - 1) & 1u, 0x84)) break;
         ++nq;
         const uint32_t bar = smem_addr(&q_full[qb]), to = smem_addr(q_s) + qb * L::kQBytes;
-        const int y = paged_unit(p, u).row0;
         mbar_expect_if(on, bar, L::kQBytes);
 #pragma unroll
         for (int c = 0; c < kCh; ++c) tma_load_2d_if(on, to + c * L::kQChunkBytes, &qmap, bar, 64 * c, y);
@@ -852,10 +908,8 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     const int quarter = warp & 3;               // tensor-memory lane quarter
     const int r = quarter * 32 + lane;          // the unit's row
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    // (0 is taken as the least number, 2^-149, so that what is masked stays minus infinity: the largest score becomes 2^-21)
-    float to_log2 = p.scale * 1.4426950408889634f;
-    if (to_log2 == 0.f) to_log2 = 1.40129846e-45f;
-    const uint64_t to_log2_2 = pack_f32x2(to_log2, to_log2);
+    const float to_log2 = p.to_log2[0];
+    const uint64_t to_log2_2 = *reinterpret_cast<const uint64_t*>(p.to_log2);
     volatile float* bound_s = neg_s;                                  // [N]
     float* sum_s = alpha_s;                                           // [2][N]
     uint32_t gb0 = 0;                                                 // blocks of the parts before
@@ -865,23 +919,27 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       const int nb = part_s[n & 1].blocks;
       if (bar_or(kTcEpiBar, kPgSoft, *abort_flag != 0)) break;
       if (part_s[n & 1].unit < 0) break;
-      const PagedUnit un = paged_unit(p, part_s[n & 1].unit);
-      const bool used = quarter * 32 < un.cols;             // (of a quarter without rows nothing is read, written or kept)
-      const int token = r < un.cols ? p.by_H(un.skip + r) : kPgMaxTokens;
-      const int end = token < kPgMaxTokens ? end_s[(n & 1) * kPgMaxTokens + token] : 0;
-      const int low = max(0, end - p.window);
-      float l0 = 0.f, l1 = 0.f, l_bound = kPgNoBound;       // this thread's sums, in units of 2^l_bound
-      for (int b = static_cast<int>((gb0 ^ group) & 1u); b < nb; b += 2) {
-        const uint32_t gb = gb0 + b, slot = gb % kPgSlots;
+      const bool used = quarter * 32 < part_s[n & 1].cols;  // (of a quarter without rows nothing is read, written or kept)
+      float l0 = 0.f, l_bound = kPgNoBound;                 // this thread's sum, in units of 2^l_bound
+      for (int b = static_cast<int>(gb0 + ((gb0 ^ group) & 1u)); static_cast<uint32_t>(b) < gb0 + nb; b += 2) {  // (of all blocks so far)
+        const uint32_t gb = static_cast<uint32_t>(b), slot = gb % kPgSlots;
         paged_wait(&blk_full[slot], (gb / kPgSlots) & 1u, abort_flag, err, 0xA1);
         const PagedBlock& blk = block_s[slot];
         const int row = blk.row;
         const bool full = __any_sync(0xffffffffu, blk.full != 0) != 0;
-        const bool mine = token >= blk.i0 && token < blk.i1;
+        const int i0 = blk.i0, i1 = blk.i1;
         const uint32_t there = blk.pages;
         const int tail = blk.tail;
         __syncwarp();
         if (lane == 0) mbar_arrive(&blk_empty[slot]);
+        bool mine = false;  // its token is one of the block's
+        int end = 0, low = 0;
+        if (!full && r < part_s[n & 1].cols) {
+          const int token = p.by_H(part_s[n & 1].skip + r);
+          mine = token >= i0 && token < i1;
+          end = end_s[(n & 1) * kPgMaxTokens + token];
+          low = max(0, end - p.window);
+        }
         // The block's rows [32 i, 32 i + 32) that this row sees.
         const auto mask_of = [&](int i) -> uint32_t {
           if (!mine) return 0u;
@@ -1003,7 +1061,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         // the bound: raised only when exceeded by more than 2^8, behind the decision on the block before
         if (gb > 0) paged_wait(&decided[quarter], (gb - 1) & 1u, abort_flag, err, 0xA7);
         float before = kPgNoBound;
-        if (b > 0) before = bound_s[r];
+        if (gb != gb0) before = bound_s[r];
         float bound = before;
         const float most = top * fabsf(to_log2);
         if (most > before + kTcLazyLog2) bound = most;
@@ -1029,13 +1087,12 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
         if (bound != l_bound) {
           const float f = l_bound == kPgNoBound ? 0.f : exp2_approx(l_bound - bound);
           l0 = l_bound == kPgNoBound && l0 == l0 ? 0.f : l0 * f;
-          l1 = l_bound == kPgNoBound ? 0.f : l1 * f;
           l_bound = bound;
         }
         // weights, as bf16 in the place of the scores
         if (used) {
           const uint64_t neg2 = pack_f32x2(-bound, -bound);
-          uint64_t l2[2] = {pack_f32x2(l0, l1), 0ull};
+          uint64_t l2[2] = {pack_f32x2(l0, 0.f), 0ull};
 #pragma unroll
           for (int i = 0; i < kKeys; i += 32) {
             uint32_t pk[16];
@@ -1050,7 +1107,9 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
             }
             tmem_st_words_x16(s_at + i / 2, pk);
           }
+          float l1;
           unpack_f32x2(add_f32x2(l2[0], l2[1]), l0, l1);
+          l0 += l1;
           tmem_wait_st();
         }
         tc_fence_before_sync();
@@ -1066,11 +1125,11 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       tc_fence_after_sync();
       float bound = kPgNoBound;
       if (nb > 0) bound = bound_s[r];
-      const float own = l0 + l1;
-      sum_s[group * N + r] = own != own ? own : (l_bound == kPgNoBound ? 0.f : own * exp2f(l_bound - bound));
+      sum_s[group * N + r] = l0 != l0 ? l0 : (l_bound == kPgNoBound ? 0.f : l0 * exp2f(l_bound - bound));
       named_bar_sync(kTcEpiBar, kPgSoft);
       const float sum = sum_s[r] + sum_s[N + r];
-      const int way = part_s[n & 1].way;
+      const PagedPart un = part_s[n & 1];
+      const int way = un.way;
       const int64_t place = 2 * static_cast<int64_t>(cta) + (way == kPgHead ? 1 : 0);  // of a shared unit's part
       float f = 1.f;
       float none = 0.f;  // no number where an output is
@@ -1156,8 +1215,8 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
     const int cb = gc + (lane >> 4) * 16;                          // this thread's [cb, cb + kC)
     const int r = quarter * 16 + (lane & 15);                      // its row of the block
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const float to_log2 = p.scale * 1.4426950408889634f;
-    const uint64_t to_log2_2 = pack_f32x2(to_log2, to_log2);
+    const float to_log2 = p.to_log2[0];
+    const uint64_t to_log2_2 = *reinterpret_cast<const uint64_t*>(p.to_log2);
     uint32_t gb = 0;
     uint64_t lsum[kC / 2];
     float x[kC];          // scores or weights of its columns
@@ -1178,7 +1237,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       bool used;  // some of this warp's columns are (of others nothing is read, written or kept)
       int skip, i_first, i_last;  // rows before the unit's first in its token; the tokens of this warp's columns
       {
-        const PagedUnit un = paged_unit(p, part_s[n & 1].unit);
+        const PagedPart un = part_s[n & 1];
         used = gc < un.cols;
         skip = un.skip;
         i_first = p.by_H(gc + skip);
@@ -1378,8 +1437,8 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
       xpose_reduce<kC>(x, lane, [](float v, float w) { return v + w; });
       red_s[quarter * N + cb + lane % kC] = x[0];
       named_bar_sync(kTcEpiBar, kPgSoft);
-      const PagedUnit un = paged_unit(p, part_s[n & 1].unit);  // (its place is held until the end of the part)
-      const int way = part_s[n & 1].way;
+      const PagedPart un = part_s[n & 1];  // (its place is held until the end of the part)
+      const int way = un.way;
       const int64_t place = 2 * static_cast<int64_t>(cta) + (way == kPgHead ? 1 : 0);  // of a shared unit's part
       if (etid < un.cols) {
         const float l = (red_s[etid] + red_s[N + etid]) + (red_s[2 * N + etid] + red_s[3 * N + etid]);
@@ -1479,7 +1538,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
 
 // ------------------------------------------------------------------------------------ shared units
 
-constexpr int kPgJoinThreads = 128;
+constexpr int kPgJoinThreads = 128;  // (eight blocks an SM, as the launch counts on: with registers for seven drafts took 4 us more)
 constexpr int kPgJoinWarps = kPgJoinThreads / 32;
 constexpr int kPgMaxCtas = 512;    // CTAs that may share a unit
 // Up to so many parts a warp joins by itself (always: one token, of some 120 parts, 28 us; never: 22.2, but drafts 82; so: 22.5, 65).
@@ -1489,7 +1548,7 @@ constexpr int kPgFewParts = 8;
 // 128 dims.  A warp takes one such item, four dims a lane (two at D = 64); where the parts are many, a block does, a quarter of
 // them a warp.  The loads of eight parts are in flight at a time.
 template <int D>
-__global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedAttnParams p) {
+__global__ void __launch_bounds__(kPgJoinThreads, 8) paged_join_kernel(const PagedAttnParams p) {
   constexpr int N = paged_cols(D);
   constexpr int kPieces = D >= 128 ? D / 128 : 1;
   constexpr int kEach = D >= 128 ? 4 : 2;  // dims of a lane
@@ -1499,7 +1558,7 @@ __global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedA
   const int4 e = __ldcg(p.shared + blockIdx.x);
   const int parts = min(e.z, kPgMaxCtas);
   if (parts <= 0) return;
-  const PagedUnit un = paged_unit(p, e.x);
+  const PagedUnit un = paged_unit(p, e.w != 0, e.x);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // part k of the unit: the end of the first CTA's piece, the beginnings of the others'
   const auto place = [&](int k) { return 2 * (static_cast<int64_t>(e.y) + k) + (k == 0 ? 1 : 0); };

@@ -179,3 +179,71 @@ def test_scale_of_zero(D):
         out = dsa.paged_attn(q.cuda(), pages, table, i32(seq), i32(pos), window=window, attn_sink=sink, scale=0.0, lse=lse)
         PR.check_attn(out, lse, PR.attn(q, kv, seq, pos, window, 0, sink, 0.0), D)
     assert dsa.get_device_error() == 0
+
+
+def step(D, H, lens, tokens, rows, places, seed=0):
+    """q, pages, a table of `rows` rows, seq and pos of a step: tokens (sequence, how many at its end), -1 in further places."""
+    rng = np.random.default_rng(seed)
+    M = -(-max(lens) // 64)
+    pages = torch.randn(M * len(lens), 64, D, device="cuda").to(bf16)
+    table = torch.full((rows, M), -1, dtype=torch.int32, device="cuda")
+    table[:len(lens)] = i32(rng.permutation(M * len(lens)).reshape(len(lens), M))
+    seq = np.concatenate([np.full(n, r) for r, n in tokens] + [np.full(places, -1)])
+    pos = np.concatenate([np.arange(lens[r] - n, lens[r]) for r, n in tokens] + [np.full(places, -1)])
+    q = torch.randn(len(seq), H, D, device="cuda").to(bf16)
+    return q, pages, table, i32(seq), i32(pos)
+
+
+@pytest.mark.parametrize("D,H", [(64, 100), (128, 65), (128, 20), (256, 150), (512, 40), (512, 100)])
+def test_the_table_s_height_is_no_matter(D, H):
+    """The same step, of tokens that share sequences and of some that do not, under a table with many more rows: the same bits, and the
+    references' values (200 tokens of one sequence took 1.4 to 1.5 times the time there)."""
+    for lens, tokens in (([900], [(0, 200)]), ([300, 700, 40, 333], [(0, 9), (1, 1), (2, 30), (3, 1)]), ([50, 260, 100], [(1, 1), (0, 1), (2, 1)])):
+        q, pages, table, seq, pos = step(D, H, lens, tokens, len(lens), 0)
+        want = dsa.paged_attn(q, pages, table, seq, pos)
+        kv = [pages[t].flatten(0, 1)[:n].double().cpu() for t, n in zip(table.long(), lens)]
+        PR.check_attn(want, None, PR.attn(q, kv, seq.cpu(), pos.cpu(), None, 0, None, 1 / math.sqrt(D)), D)
+        tall = torch.cat([table, torch.full((400, table.shape[1]), -1, dtype=torch.int32, device="cuda")])
+        assert torch.equal(want, dsa.paged_attn(q, pages, tall, seq, pos))
+    assert dsa.get_device_error() == 0
+
+
+def test_places_and_pairs_are_no_matter():
+    """64 sequences of 4096 rows, a token each, take their time where a place has no token and where a sequence has two, too (1.2 times,
+    cut as tokens that share a sequence are); 200 tokens of one sequence take theirs under any table (1.5 times, cut as tokens that
+    share none)."""
+    D, H = 256, 150
+    one = [(r, 1) for r in range(64)]
+
+    def time(lens, tokens, rows, places):
+        q, pages, table, seq, pos = step(D, H, lens, tokens, rows, places)
+        out, work = torch.empty_like(q), torch.empty(dsa.paged_attn_workspace_size(len(q), H, D), dtype=torch.uint8, device="cuda")
+        return best(lambda: dsa.paged_attn(q, pages, table, seq, pos, out=out, workspace=work))
+
+    plain = time([4096] * 64, one, 64, 0)
+    assert time([4096] * 64, one, 64, 1) < 1.1 * plain
+    assert time([4096] * 64, one[:63] + [(63, 2)], 64, 0) < 1.1 * plain
+    assert time([8192], [(0, 200)], 256, 0) < 1.1 * time([8192], [(0, 200)], 1, 0)
+    assert dsa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("D,H", [(64, 100), (256, 150), (512, 40)])
+def test_cuts_in_one_graph(D, H):
+    """The cut follows what the tensors hold when a captured call is replayed: tokens of one sequence, of many, and none."""
+    lens = [500] * 40
+    q, pages, table, _, _ = step(D, H, lens, [(r, 1) for r in range(40)], 40, 0)
+    seq, pos = torch.zeros(40, dtype=torch.int32, device="cuda"), torch.zeros(40, dtype=torch.int32, device="cuda")
+    work = torch.empty(dsa.paged_attn_workspace_size(40, H, D), dtype=torch.uint8, device="cuda")
+    work.fill_(255)
+    dsa.paged_attn(q, pages, table, seq, pos, workspace=work)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = dsa.paged_attn(q, pages, table, seq, pos, workspace=work)
+    kv = [pages[t].flatten(0, 1)[:500].double().cpu() for t in table.long()]
+    for s, p in ((np.zeros(40), np.arange(460, 500)), (np.arange(40), np.arange(420, 500, 2)), (np.full(40, -1), np.zeros(40)),
+                 (np.repeat(np.arange(8), 5), np.tile(np.arange(495, 500), 8))):
+        seq.copy_(i32(s)), pos.copy_(i32(p))
+        work.fill_(255)
+        g.replay()
+        PR.check_attn(out, None, PR.attn(q, kv, s, p, None, 0, None, 1 / math.sqrt(D)), D)
+    assert dsa.get_device_error() == 0
