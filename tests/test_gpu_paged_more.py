@@ -247,3 +247,35 @@ def test_cuts_in_one_graph(D, H):
         g.replay()
         PR.check_attn(out, None, PR.attn(q, kv, s, p, None, 0, None, 1 / math.sqrt(D)), D)
     assert dsa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("D,H,rows", [(64, 16, 16), (64, 5, 128), (128, 70, 256), (256, 16, 16), (256, 3, 64), (512, 16, 16), (512, 70, 32), (512, 8, 64),
+                                      (512, 8, 256)])
+def test_pages_that_are_missing(D, H, rows):
+    """Unmapped pages (negative ids, ids past the pool) at a sequence's start, in its middle and at its end, one beside another, are
+    skipped; positions behind the table see the rows of its pages."""
+    rng = np.random.default_rng(D + rows)
+    lens = [5 * rows + 3, 3 * rows, 2 * rows]
+    pages, table, kv = PR.pool(lens, rows, D, rng)
+    t = table.cpu().numpy().copy()
+    gone = [(0, 1), (0, 2), (0, 5), (1, 0), (2, 0), (2, 1)]
+    for k, (r, j) in enumerate(gone):
+        t[r, j] = (-1, -(2 ** 31), pages.shape[0], 2 ** 31 - 1)[k % 4]
+    skip = {(r, i) for r, j in gone for i in range(j * rows, (j + 1) * rows)}
+    seq = np.array([0, 0, 0, 1, 1, 1, 2, 3, -7])
+    pos = np.array([5 * rows + 2, 5 * rows - 1, 2 * rows, 3 * rows - 1, rows, rows - 1, 2 * rows - 1, 5, 5])
+    q = torch.from_numpy(rng.standard_normal((9, H, D))).to(bf16).cuda()
+    for window, first in ((None, 0), (rows + 5, rows // 2), (7, 0)):
+        for sink in (None, torch.zeros(H, device="cuda")):
+            lse = torch.empty(9, H, device="cuda")
+            out = dsa.paged_attn(q, pages, i32(t), i32(seq), i32(pos), window=window, first=first, attn_sink=sink, lse=lse)
+            PR.check_attn(out, lse, PR.attn(q, kv, seq, pos, window, first, sink, 1 / math.sqrt(D), skip), D)
+    # behind a table of three pages a sequence: all rows of those of 0 and 1, of which 0 has more
+    far = np.array([5 * rows + 2, 5 * rows - 1, 2 * rows, 2 ** 31 - 1, 2 ** 31 - 2, 10 ** 6, 2 * rows - 1, 5, 5])
+    cut = table[:, :3].contiguous()
+    kv = [x[:3 * rows] for x in kv]
+    for window, first in ((None, 0), (100, 5)):
+        lse = torch.empty(9, H, device="cuda")
+        out = dsa.paged_attn(q, pages, cut, i32(seq), i32(far), window=window, first=first, lse=lse)
+        PR.check_attn(out, lse, PR.attn(q, kv, seq, far, window, first, None, 1 / math.sqrt(D)), D)
+    assert dsa.get_device_error() == 0
