@@ -424,7 +424,12 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   uint64_t* kv_empty = kv_full + kRing;
 
   if ((smem_addr(smem) & 1023u) != 0u) {  // (the swizzle goes by addresses; nothing else lies before this memory)
-    if (threadIdx.x == 0) record_error(err, kErrPlan);
+    wait_stream();
+    if (threadIdx.x == 0) {
+      record_error(err, kErrPlan);
+      // (all CTAs are here: the join finds no shared unit, instead of what the workspace held)
+      if (static_cast<int>(blockIdx.x) < paged_entries(p, static_cast<int>(gridDim.x))) p.shared[blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
     return;
   }
   const int warp = threadIdx.x >> 5;

@@ -60,3 +60,15 @@ def test_copies_land_before_the_end():
     kernel = text[text.index("paged_attn_kernel("):text.index("paged_join_kernel(")]
     end = kernel[kernel.rindex("__syncthreads();"):]
     assert "if (*abort_flag != 0 && warp == kPgFirstLoad) {" in end and end.index("tiles_in_flight<") < end.index("tmem_dealloc")
+
+
+def test_no_early_end_leaves_the_join_stale_entries():
+    """A CTA that ends before the plan (its shared memory lies elsewhere than expected) has emptied its entry of the shared units,
+    behind the stream's earlier work, which may still read the workspace."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(SRC, "paged_attn_kernel.cuh")).read())
+    kernel = text[text.index("paged_attn_kernel("):text.index("paged_join_kernel(")]
+    start = kernel[:kernel.index("mbar_init(")]
+    assert start.count("return;") == 1
+    early = start[start.index("1023u"):start.index("return;")]
+    assert early.index("wait_stream();") < early.index("p.shared[blockIdx.x] = make_int4(0, 0, 0, 0);")
+    assert "return;" not in kernel[kernel.index("mbar_init("):]
