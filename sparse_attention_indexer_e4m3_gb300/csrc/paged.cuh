@@ -41,7 +41,7 @@ struct PagedAttnParams {
   float* lse;           // [T][H] or null
   float* partial;       // [2 CTAs][N][D] partial outputs of units that several CTAs share
   float* stats;         // [2 CTAs][2][N] their bounds and sums
-  int4* shared;         // [min(units, CTAs)] the shared units: unit, first CTA, CTAs (0: none), cut
+  int4* shared;         // [min(units, CTAs)] the shared units: first row of q, first CTA, CTAs (0: none), rows
   int T, H;
   PagedCut whole;       // whole tokens, or a token's heads in equal units of their own
   PagedCut any;         // units wherever they begin (as `whole` where there is no choice)

@@ -589,7 +589,11 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   if (threadIdx.x == 0) {
     // entries of the shared units: by unit, written by the CTA that it starts on, where there are no more than CTAs, else by CTA
     const bool shared = !idle && to_block < plan_s[6] && (unit1 > unit0 || starts);
-    const int4 entry = shared ? make_int4(unit1, cta, plan_s[5] - cta + 1, any) : make_int4(0, 0, 0, 0);
+    int4 entry = make_int4(0, 0, 0, 0);
+    if (shared) {
+      const PagedUnit un = paged_unit(p, any, unit1);
+      entry = make_int4(un.row0, cta, plan_s[5] - cta + 1, un.cols);
+    }
     if (units > static_cast<int>(gridDim.x)) {
       p.shared[cta] = entry;
     } else {
@@ -1563,13 +1567,13 @@ __global__ void __launch_bounds__(kPgJoinThreads, 8) paged_join_kernel(const Pag
   const int4 e = __ldcg(p.shared + blockIdx.x);
   const int parts = min(e.z, kPgMaxCtas);
   if (parts <= 0) return;
-  const PagedUnit un = paged_unit(p, e.w != 0, e.x);
+  const int row0 = e.x, cols = e.w;  // of the unit
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // part k of the unit: the end of the first CTA's piece, the beginnings of the others'
   const auto place = [&](int k) { return 2 * (static_cast<int64_t>(e.y) + k) + (k == 0 ? 1 : 0); };
   const bool few = parts <= kPgFewParts;
   const int k0 = few ? 0 : parts * warp / kPgJoinWarps, k1 = few ? parts : parts * (warp + 1) / kPgJoinWarps;
-  const int items = un.cols * kPieces, step = static_cast<int>(gridDim.y) * (few ? kPgJoinWarps : 1);
+  const int items = cols * kPieces, step = static_cast<int>(gridDim.y) * (few ? kPgJoinWarps : 1);
   for (int item = static_cast<int>(blockIdx.y) * (few ? kPgJoinWarps : 1) + (few ? warp : 0); item < items; item += step) {
     const int c = item / kPieces, d = (item % kPieces) * 128 + lane * kEach;
     float top = kPgNoBound, sum = 0.f;
@@ -1647,9 +1651,8 @@ __global__ void __launch_bounds__(kPgJoinThreads, 8) paged_join_kernel(const Pag
       }
       top = most;
     }
-    const float f = paged_factor(top, sum, p.sink, p.head(un.skip + c),
-                                 p.lse != nullptr && item % kPieces == 0 && lane == 0 ? p.lse + un.row0 + c : nullptr);
-    uint16_t* out = p.out + (static_cast<int64_t>(un.row0) + c) * D + d;
+    const float f = paged_factor(top, sum, p.sink, p.head(row0 + c), p.lse != nullptr && item % kPieces == 0 && lane == 0 ? p.lse + row0 + c : nullptr);
+    uint16_t* out = p.out + (static_cast<int64_t>(row0) + c) * D + d;
 #pragma unroll
     for (int i = 0; i < kEach; i += 2) {
       const __nv_bfloat162 two = __floats2bfloat162_rn(acc[i] * f, acc[i + 1] * f);
