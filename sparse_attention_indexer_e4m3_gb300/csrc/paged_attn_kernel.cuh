@@ -33,8 +33,8 @@
 // D <= 256, too, a prompt with a window took 643 us instead of 278, drafts 208 instead of 77.)
 //
 // What bounds it (times at the sizes given, GB300):
-//   - a batch of long sequences: reading them.  64 sequences of up to 65536 rows of 512, 64 heads: 382 us, 6.7 TB/s, what a copy
-//     reaches.
+//   - a batch of long sequences: reading them.  64 sequences of up to 65536 rows of 512, 64 heads: 367 to 384 us, 6.7 TB/s and
+//     more, what a copy reaches (a part stays in L2).
 //   - prompts at D = 512: the products.  Their operands come from shared memory at 128 bytes a clock, (M + N) / 4 cycles an
 //     instruction: 48 for M = 128, N = 64, 34 for M = 64; 1872 of the 2070 cycles of a block of 64 rows.  4096 tokens over 8192 rows,
 //     64 heads: 2.92 ms, 1130 TFLOP/s.
@@ -42,8 +42,8 @@
 //     products before it) over the softmax (2200) to the end of its weighted sum (1000), three of them turn over a block in 1500
 //     cycles where the products need 1024; blocks that not every row sees all of take 1800 longer, and a unit's end and beginning
 //     some 7000.  2700-token prompts with a window of 1024 at D = 128, 32 heads: 187 us.
-//   - single tokens: a chain of launch, plan, table, rows, two products and the join.  One token over 32768 rows of 512, 64
-//     heads: 22.5 us.
+//   - single tokens: a chain of launch, plan, table, rows, two products, some 128 partial outputs through L2 (as many bytes as the
+//     rows) and the join.  One token over 32768 rows of 512, 64 heads: 22.3 us.
 // Measured and slower at D <= 256: sixteen softmax warps with half a row each (191 us for 187; window decode 24.5 for
 // 23.5), masks and outputs 32 rows or dims at a time (195 to 275 us), a place of its own for P (216).
 #pragma once
@@ -73,7 +73,7 @@ __host__ __device__ constexpr int paged_block(int D) { return D == 512 ? 64 : 12
 // What a unit costs beside its blocks, and the least piece of the line of a CTA (joining a part takes about as long), in blocks.
 // (A cost of 1: drafts 72 us, window decode 27, window prompt 200; 4: 63 to 67, 24, 188; 8: 67, 23, 188.  Least pieces of 1:
 // one token 23.2 us; these: 22.5; twice these: 25.2.)
-__host__ __device__ constexpr int paged_unit_cost(int D) { return 4; }
+constexpr int kPgUnitCost = 4;
 __host__ __device__ constexpr int paged_min_piece(int D) { return D == 512 ? 4 : 2; }
 
 // What the load and softmax warps know of a block.
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
   // ------------------------------------------------------------------ the CTA's piece of the line
   // Cost of a unit: its blocks and a constant.  [from, to) of the line is this CTA's.  A unit starts on one CTA's piece (which
   // has at least one of its blocks) and belongs to those, too, whose pieces its blocks reach into.
-  constexpr int kUnitCost = paged_unit_cost(D);
+  constexpr int kUnitCost = kPgUnitCost;
   int64_t* warp_scan = reinterpret_cast<int64_t*>(smem + L::kScan);  // [warps]
   volatile uint32_t* issued_s = reinterpret_cast<volatile uint32_t*>(smem + L::kScan);  // later: tiles of each loading warp, and q's
   static_assert(4 * (L::kLoaders + 1) <= L::kBar - L::kScan, "counts in the scan's place");

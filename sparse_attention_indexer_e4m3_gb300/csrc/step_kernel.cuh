@@ -117,10 +117,10 @@ __global__ void __launch_bounds__(kMapThreads) step_maps_kernel(const StepMapArg
 constexpr int kSlotThreads = 256;
 constexpr int kSlotEach = 4;  // entries of a thread at a time
 
-// Entry v of token t names row v - start[t] of sequence seq[t].  Memory-bound but for the table, whose entries L1 and L2
-// hold: a thread takes four entries of a row, in one access each where they are aligned.  A block takes a piece of some rows one
-// after the other (no division by the pieces of a row: with one, lists of 8192 x 2048 took 31 us instead of 28).  Those 134 MB
-// move at 4.8 TB/s; 61 x 2048 entries take 3.4 us, a launch's latency.
+// Entry v of token t names row v - start[t] of sequence seq[t].  A thread takes four entries of a row, in one access each where they
+// are aligned; the table's entries come from L1 and L2.  A block takes a piece of some rows one after the other (no division by
+// the pieces of a row: with one, lists of 8192 x 2048 took 31 us instead of 28 to 29).  Those 134 MB move at 4.6 to 4.8 TB/s, 70% of
+// a copy's rate: 43 instructions an entry, in 64 bits, take some 19 us of it.  61 x 2048 entries take 3.6 us, a launch's latency.
 __global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const PageTable c, const int32_t* seq, const int32_t* start,
                                                                   const int32_t* idx, int T, int K, int32_t* slots, bool wide) {
   wait_stream();

@@ -15,8 +15,9 @@
 // the warp into whose part the drawn number falls looks for the token: first among the sums that it kept of each
 // piece of its part, then among that piece's values, which are in L2.
 // It reads two rows of V floats a row, in a chain of: counts and tokens, probabilities of the tokens, the rows, the
-// exchange, one piece again.  A row of 129280 takes 10.3 us (a launch and that chain: its bytes take 0.2), 48 rows 21.4 us,
-// 2.4 TB/s: the sums' additions, 55 instructions a pair of values on all SMs, take a third of it and the chain the rest.
+// exchange, one piece again.  A row of 131072 takes 10.3 us (a launch and that chain: its bytes take 0.2), 128 rows of 50257
+// 21.4 us, 2.4 TB/s: the sums' additions, 55 instructions a pair of values on all SMs, take about half of it (13.6 million
+// instructions of warps, some 11 us) and the chain the rest.
 // Three pieces at once a warp with 64 registers and two CTAs an SM: 21.4 us; one piece, 32 registers and four CTAs: 23.5.
 #pragma once
 
@@ -35,7 +36,7 @@ constexpr int kVerMaxCluster = 8;
 // Weights max(p - q, 0) in units of 2^-55 (what is no number or below 0 counts as 0, above 1 as 1), summed.  A probability x in [0, 1]
 // is rounded to a multiple of 2^-22 by adding 3, whose neighbours are 2^-22 apart, so that the sum's bits are 3's and that multiple;
 // what is left is exact, and rounded likewise to a multiple of 2^-44, and what is left of that to one of 2^-55.  Eight additions a
-// value, all but the bits' in fp32.  A batch of 48 rows took 23.5 us with them, 27.8 with conversions to whole numbers and
+// value, all but the bits' in fp32.  128 rows of 50257 took 23.5 us with them, 27.8 with conversions to whole numbers and
 // 24.5 with shifts of the mantissa.
 struct WeightSum {
   int part[3] = {0, 0, 0};  // of up to 2^8 weights, in units of 2^-22, 2^-44 and 2^-55
@@ -139,7 +140,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_drafts_kerne
   // the second time only where nothing is left of the target over the draft
   for (int attempt = 0; attempt < 2; ++attempt) {
     const float* q_row = n < count && attempt == 0 ? draft + static_cast<int64_t>(n) * V : nullptr;
-    // the sums of its pieces, some at a time for loads in flight (where a warp has one piece or two, one)
+    // the sums of its pieces, some at a time for loads in flight (one in the larger CTAs, whose warps have four of them at V = 131072 and
+    // one or two up to 65536)
     constexpr int kAhead = kThreads == kVerThreads ? 3 : 1;
     uint64_t mine = 0;
     for (int i = w0; i < w1; i += kAhead) {

