@@ -474,9 +474,9 @@ DSA_API dsa_status dsa_store_kv(const uint16_t* kv, int64_t stride, const int32_
  * Rows without a page are skipped; a token that sees none (seq outside [0, R), a negative position) gets zeros and an lse of its
  * sink (-inf without one).  What rows hold that a token does not see does not matter to it, no numbers included; a row that it
  * sees and that holds one (an infinite one as well, whatever its score) makes all of the token's outputs and lse no numbers, and
- * so may a product beyond fp32's range, but for a score of minus infinity, which weighs 0 (one below -2e38 may, too).  Tokens may come in any
- * order; those that share a sequence are best neighbours.  Weights enter the weighted sum as bf16; products accumulate in
- * fp32.  Deterministic.
+ * so may a product beyond fp32's range, but for a score of minus infinity, which weighs 0 (one below -2e38 may, too).  Tokens may
+ * come in any order; those that share a sequence are best neighbours.  Weights enter the weighted sum as bf16; products
+ * accumulate in fp32.  Deterministic.
  *
  *   q          bf16 [T][H][D], 16-byte aligned;  seq, pos  int32 [T]
  *   attn_sink  float [H] or NULL;  window  0 (none) or more;  first  0 or more;  scale  softmax scale

@@ -995,10 +995,10 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
             if (__any_sync(0xffffffffu, mine && (n0 != n0 || n1 != n1))) {
               // Weights of 0 times values that are no numbers would still be none.  So the kv rows that hold such are taken out (by each
               // warp with rows of q of the block's tokens: all of those find them), and rows of q that see one get a sum that is
-              // none.  What was taken out is -0 all over, so that a warp that comes later finds it as well: a 16-byte piece of it, at
-              // least, where another is at it.  (A row that holds such a piece of its own is not written, and counts only where its
-              // score overflows.)  Scores of other rows of q show nothing: these may hold anything.  (Four tokens over 20000 rows beside
-              // four places with q that is none, D = 128: 47 us with their scores looked at, 20.5 without.)
+              // none.  What was taken out is -0 all over, so that a warp that comes later finds it as well: where another is at it, each
+              // word that held one either still does or is a pair of -0.  (A row that holds such a pair of its own is not written, and
+              // counts only where its score overflows.)  Scores of other rows of q show nothing: these may hold anything.  (Four tokens
+              // over 20000 rows beside four places with q that is none, D = 128: 47 us with their scores looked at, 20.5 without.)
               constexpr uint32_t kOut = 0x80008000u;
               bool sees = false;
 #pragma unroll 1
@@ -1026,10 +1026,11 @@ __global__ void __launch_bounds__(PagedLayout<D>::kThreads, 1)
                   for (int j = lane; j < kCh * 8; j += 32) {
                     const uint4 v = *at(j);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    if (((v.x ^ kOut) | (v.y ^ kOut) | (v.z ^ kOut) | (v.w ^ kOut)) == 0u) found |= 2u;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 4; ++k) {
+                      if (w[k] == kOut) found |= 2u;
                       if ((w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u) found |= 1u;
+                    }
                   }
                   found = __reduce_or_sync(0xffffffffu, found);
                   if ((found & 1u) != 0u) {

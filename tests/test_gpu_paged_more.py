@@ -279,3 +279,26 @@ def test_pages_that_are_missing(D, H, rows):
         out = dsa.paged_attn(q, pages, cut, i32(seq), i32(far), window=window, first=first, lse=lse)
         PR.check_attn(out, lse, PR.attn(q, kv, seq, far, window, first, None, 1 / math.sqrt(D)), D)
     assert dsa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("D,H", [(64, 128), (128, 128), (256, 128)])
+def test_infinite_values_found_by_many_warps(D, H):
+    """All warps of a block find the same rows, each in its own time and perhaps while another takes them out: no run differs."""
+    rng = np.random.default_rng(D)
+    n = 2000
+    pages, table, kv = PR.pool([n], 64, D, rng)
+    for at in (5, 77, 80, 1990, 1500, 640):
+        pages[int(table[0, at // 64]), at % 64, int(rng.integers(D))] = (math.inf, -math.inf, math.nan)[at % 3]
+    pos = np.array([4, 1999, 100, 1995, 3, 60, 2, 1])
+    q = torch.from_numpy(rng.standard_normal((8, H, D))).to(bf16).cuda()
+    for window in (None, 90):
+        hit = torch.tensor([any(at <= p and (window is None or at > p - window) for at in (5, 77, 80, 1990, 1500, 640)) for p in pos])
+        assert hit.any() and not hit.all()
+        for _ in range(100):
+            lse = torch.empty(8, H, device="cuda")
+            out = dsa.paged_attn(q, pages, table, i32(np.zeros(8)), i32(pos), window=window, lse=lse)
+            assert torch.equal(torch.isnan(out).all(2).all(1).cpu(), hit) and torch.equal(torch.isnan(lse).all(1).cpu(), hit)
+            assert not torch.isnan(out[~hit.cuda()]).any() and not torch.isnan(lse[~hit.cuda()]).any()
+        ref = PR.attn(q, kv, np.zeros(8), pos, window, 0, None, 1 / math.sqrt(D))
+        PR.check_attn(out.cpu()[~hit], lse.cpu()[~hit], [x[~hit] for x in ref], D)
+    assert dsa.get_device_error() == 0
